@@ -21,7 +21,8 @@ import torch
 
 __all__ = ["topk", "topk_blocked", "topk_candidates", "compress", "compress_decode", "plan", "DTYPE_F32", "DTYPE_BF16", "load", "library_path", "LtError", "NUM_COUNTERS",
            "status_string", "version", "PlanInfo", "KERNEL_AUTO", "KERNEL_RESIDENT", "KERNEL_STREAM",
-           "KERNEL_LISTED", "plan_candidates"]
+           "KERNEL_LISTED", "plan_candidates", "DTYPE_F16", "kv4_cache", "kv4_row_bytes", "kv4_store", "kv4_load",
+           "kv4_attention", "page_extend", "page_release", "PageStep"]
 
 _LIB_PATH = Path(__file__).resolve().parent / "liblt_topk.so"
 _lib = None
@@ -90,6 +91,18 @@ def load() -> ctypes.CDLL:
     lib.lt_compress.restype = ctypes.c_int
     lib.lt_compress_decode.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, vp]
     lib.lt_compress_decode.restype = ctypes.c_int
+    lib.lt_kv4_row_bytes.argtypes = [i32]
+    lib.lt_kv4_row_bytes.restype = i32
+    lib.lt_page_release.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, i32, vp, vp, vp]
+    lib.lt_page_extend.argtypes = [vp, vp, i32, vp, i32, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.lt_kv4_store.argtypes = [vp, vp, i32, i64, i32, i32, i64, i64, i64, i64, vp, vp, i64, i32, vp]
+    lib.lt_kv4_load.argtypes = [vp, i64, i32, vp, i64, i32, i32, vp, vp, i32, vp]
+    lib.lt_kv4_attention.argtypes = [vp, i32, i64, i32, i32, i32, i64, i64, vp, i64, i32, vp, i32, vp, i32, vp, i32,
+                                     vp, i32, i32, ctypes.c_float, vp, vp, vp, i64, vp]
+    lib.lt_kv4_workspace.argtypes = [i64, i32, i32, i32, i32, i32, i32, vp]
+    for name in ("lt_page_release", "lt_page_extend", "lt_kv4_store", "lt_kv4_load", "lt_kv4_attention",
+                 "lt_kv4_workspace"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.lt_test_inject.argtypes = [i32, i32]
     lib.lt_test_inject.restype = ctypes.c_int
     lib.lt_version.argtypes = []
@@ -356,3 +369,7 @@ def plan_candidates(rows: int, row_stride: int, block: int, n_cand: int, k: int,
     return {"kernel": _KERNEL_NAMES.get(info.kernel, str(info.kernel)), "cluster": info.cluster_size,
             "threads": info.threads_per_cta, "smem": info.smem_bytes, "grid": info.grid_ctas,
             "stages": info.ring_stages, "one_round": bool(info.one_round)}
+
+
+from .kv4 import (DTYPE_F16, PageStep, kv4_attention, kv4_cache, kv4_load, kv4_row_bytes, kv4_store,  # noqa: E402
+                  page_extend, page_release)

@@ -541,6 +541,10 @@ lt_status check_dtype(int32_t dtype) {
 
 }  // namespace
 
+namespace lt {
+bool take_injected_failure() { return take_one(g_fail_launches); }
+}  // namespace lt
+
 extern "C" {
 
 lt_status lt_topk_ex(const void* scores, int32_t dtype, const int32_t* lengths, int32_t rows,

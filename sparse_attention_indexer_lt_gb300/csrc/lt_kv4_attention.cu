@@ -1,0 +1,852 @@
+// lt_kv4_attention.cu -- attention over the 4-bit cache for few query rows a
+// request (decode, drafted tokens) and for listed positions, and the join of the
+// parts of a split request.
+//
+// Rows. The query heads of one kv head, times a request's new tokens, are the
+// query rows that read the same keys and values; a CTA takes 8, 16 or 32 of them
+// (NT tiles of 8) and one chunk of the request's positions. Its four warps walk
+// the chunk's tiles of 32 positions independently, each with its own ring of
+// bulk copies, running maximum and sum, and join once at the end.
+//
+// Matrix products. At 4.5 bits a value the memory delivers 42 values a clock and
+// SM, so the work that counts is that per value: unpacking, scaling, feeding the
+// tensor core. Both products take the cache as the 16-row operand straight from
+// registers (m16n8k16, fp32 sums): S^T = K Q^T with 16 positions by 8 query rows, and
+// O^T = V^T P^T with 16 channels by 8 query rows, so a fragment register of 2
+// values serves one 16x8x16 step and the weights go from the first product's
+// result to the second's operand with one 8x8 transpose. Two value codes of
+// neighbouring positions are brought into one byte before they are converted, so the
+// conversion yields the pair that the fragment wants. The accumulator is a few
+// registers wide because the rows are few; tcgen05 would want 128 rows, and the
+// unpacked values in shared memory.
+//
+// A product of a code and its scale is an exact fp16 number, so keys and values
+// enter the products exactly. The weights are rounded to fp16 (2^-12 relative)
+// after a shift by 2^8 that keeps small ones normal; the sums that divide them are
+// fp32 and of the unrounded weights.
+
+#include <mutex>
+
+#include "lt_kv4.cuh"
+#include "lt_kv4_attention.cuh"
+
+namespace {
+
+using namespace lt::kv4;
+
+constexpr float kShift = 8.0f;  // weights are held as 2^8 exp(s - max)
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int kRow = row_bytes(D);
+  static constexpr int kTileBytes = kTile * kRow;
+  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kRing = kWarps * kStages * kTileBytes;
+  static constexpr int kJoin = kWarps * NT * 8 * (D + 4) * 4;  // the warps' sums, in the ring's place
+  static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+  static constexpr int kPerSm = D == 64 ? (NT == 4 ? 3 : 4) : D == 128 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : 2;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = lds32(a);
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+  } else {
+    static_assert(N == 4, "1, 2 or 4 words");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+  }
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Which request and chunk this CTA has: the requests' positions cut into chunks of one size, flat.
+struct Place {
+  int request, split, base, count;  // count chunks, the first with flat number base
+  int chunk;                        // positions of a chunk
+};
+
+// The requests' spans add up to `total`; with about `target` chunks wanted, a chunk has
+// total / target positions (a multiple of kTile, min_chunk at least) and request r has
+// ceil(span / chunk) of them: ragged requests come out as chunks of like work, which
+// the hardware hands to SMs as they fall free. Every CTA computes this from the
+// lengths alone.
+__device__ bool find_place(const AttentionParams& p, int flat, Place* out, int64_t* sums, Place* found) {
+  const int tid = threadIdx.x;
+  if (tid == 0) found->request = -1;
+  int64_t mine = 0;
+  for (int r = tid; r < p.requests; r += kThreads) mine += request_of(p, r).span;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(~0u, mine, d);
+  if ((tid & 31) == 0) sums[tid >> 5] = mine;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += sums[w];
+  int64_t chunk = (total + p.target - 1) / p.target;
+  chunk = (chunk + kTile - 1) / kTile * kTile;
+  if (chunk < p.min_chunk) chunk = p.min_chunk;
+  int base = 0;
+  for (int first = 0; first < p.requests; first += kThreads) {
+    const int r = first + tid;
+    int n = 0;
+    if (r < p.requests) {
+      const Request q = request_of(p, r);
+      n = q.queries > 0 ? max(1, (int)((q.span + chunk - 1) / chunk)) : 0;
+    }
+    int end = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(~0u, end, d);
+      if ((tid & 31) >= d) end += u;
+    }
+    __syncthreads();
+    if ((tid & 31) == 31) sums[tid >> 5] = end;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < (tid >> 5)) end += (int)sums[w];
+      all += (int)sums[w];
+    }
+    const int begin = base + end - n;
+    if (flat >= begin && flat < begin + n) {
+      found->request = r;
+      found->split = flat - begin;
+      found->base = begin;
+      found->count = n;
+    }
+    base += all;
+    if (base > flat) break;  // (the same for all threads)
+  }
+  __syncthreads();
+  *out = *found;
+  out->chunk = (int)(chunk > INT32_MAX ? INT32_MAX / kTile * kTile : chunk);
+  return out->request >= 0;
+}
+
+template <int D, int NT, bool kList>
+__global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(AttentionParams p) {
+  using Sh = Shape<D, NT>;
+  constexpr int kRow = Sh::kRow;
+  constexpr int kGroups = D / 32;  // scale groups of a key
+  constexpr int kWordsV = D / 64;  // words of value codes a lane takes from a position
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[kWarps][Sh::kStages];
+  __shared__ uint32_t valid_of[kWarps][Sh::kStages];
+  __shared__ float m_of[kWarps][NT * 8], l_of[kWarps][NT * 8];
+  __shared__ int64_t sums[kWarps];
+  __shared__ Place found;
+  __shared__ int gave_up;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < Sh::kStages; ++s) lt::mbar_init(&bars[warp][s], 1);
+    lt::mbar_fence_init();
+  }
+  if (tid == 0) gave_up = 0;
+  dependency_wait();
+
+  const int64_t unit = blockIdx.x;
+  const int row_tile = (int)(unit % p.row_tiles);
+  const int head = (int)(unit / p.row_tiles % p.heads);
+  const int flat = (int)(unit / p.row_tiles / p.heads);
+
+  // the request, its rows of this CTA and the range of positions (of list entries)
+  Request rq;
+  int request, count, token0, rows, from, to;
+  if constexpr (kList) {
+    token0 = flat / p.target;  // one query token
+    const int split = flat % p.target;
+    request = owner_of_token(p, token0);
+    if (request < 0) return;  // (rows past starts[requests])
+    rq = request_of(p, request);
+    count = p.target;
+    rows = p.group;
+    const int chunk = ((p.list_len + p.target - 1) / p.target + kTile - 1) / kTile * kTile;
+    from = min(split * chunk, p.list_len);
+    to = min(from + chunk, p.list_len);
+    __syncthreads();
+  } else {
+    Place pl;
+    if (!find_place(p, flat, &pl, sums, &found)) return;
+    request = pl.request;
+    rq = request_of(p, request);
+    count = pl.count;
+    token0 = rq.first;
+    rows = rq.queries * p.group;
+    if (flat == pl.base && head == 0 && row_tile == 0 && tid == 0 && p.plan != nullptr)
+      p.plan[request] = make_int2(pl.base, pl.count);
+    // chunks start on tiles: rq.low is a multiple of kTile
+    const int64_t at = rq.low + (int64_t)pl.split * pl.chunk;
+    from = (int)(at < rq.length ? at : rq.length);
+    to = (int)(at + pl.chunk < rq.length ? at + pl.chunk : rq.length);
+  }
+  const int row0 = row_tile * NT * 8;
+  if (row0 >= rows) return;
+  if constexpr (!kList) {
+    // nothing after the last row's own position, nothing before the first row's window
+    const int last = min(rows - 1, row0 + NT * 8 - 1) / p.group;
+    to = min(to, rq.length - rq.queries + last + 1);
+    if (p.window > 0) from = max(from, (rq.length - rq.queries + row0 / p.group + 1 - p.window) / kTile * kTile);
+  }
+  const int tiles = to > from ? (to - from + kTile - 1) / kTile : 0;
+
+  // ---- copies: lane i brings the tile's i-th run of positions that lie on one page
+  const uint32_t ring = lt::smem_u32(smem) + warp * Sh::kStages * Sh::kTileBytes;
+  const int run_shift = kList ? 0 : min(p.shift, 5);
+  const int32_t* table = p.table + (int64_t)request * p.width;
+  const int32_t* list = kList ? p.positions + (int64_t)token0 * p.list_len : nullptr;
+  // of the next tile to bring: the lane's position, how many, and its page's id
+  int next_pos, next_count, next_page;
+  auto look_up = [&](int tile) {
+    const int at = from + tile * kTile + (lane << run_shift);
+    next_count = tile < tiles && (lane << run_shift) < kTile ? max(0, min(to - at, 1 << run_shift)) : 0;
+    next_pos = at;
+    if constexpr (kList) {
+      if (next_count > 0) {
+        next_pos = __ldg(list + at);
+        if (next_pos < 0 || next_pos >= rq.length) next_count = 0;
+      }
+    }
+    next_page = next_count > 0 ? __ldg(table + (next_pos >> p.shift)) : -1;
+  };
+  auto bring = [&](int tile, int stage) {
+    if (next_page < 0 || next_page >= p.pages) next_count = 0;
+    const uint32_t mine = next_count > 0 ? ((next_count == 32 ? ~0u : (1u << next_count) - 1u) << ((lane << run_shift) & 31)) : 0u;
+    const uint32_t valid = __reduce_or_sync(~0u, mine);
+    if (lane == 0) {
+      valid_of[warp][stage] = valid;
+      lt::mbar_arrive_tx(&bars[warp][stage], (uint32_t)__popc(valid) * kRow);
+    }
+    __syncwarp();
+    if (next_count > 0) {
+      const uint8_t* src = p.cache + (((((int64_t)next_page * p.heads + head) << p.shift) + (next_pos & ((1 << p.shift) - 1))) * kRow);
+      bulk_in(ring + stage * Sh::kTileBytes + (lane << run_shift) * kRow, src, (uint32_t)next_count * kRow, &bars[warp][stage]);
+    }
+    look_up(tile + kWarps);
+  };
+  look_up(warp);
+#pragma unroll
+  for (int s = 0; s < Sh::kStages; ++s)
+    if (warp + s * kWarps < tiles) bring(warp + s * kWarps, s);
+
+  // ---- query fragments: lane (g, c) holds channels 32 j + 8 c .. + 7 of row g of each row tile
+  uint32_t qf[NT][kGroups][4];
+  float factor[NT][2];       // of columns 2c, 2c + 1: logits in units of log 2
+  int limit[NT][2], low[NT][2];
+  {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = min(row0 + nt * 8 + g, rows - 1);
+      const int64_t token = token0 + row / p.group;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + token * p.q_token + (int64_t)(head * p.group + row % p.group) * p.q_head;
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + 32 * j + 8 * c));
+        qf[nt][j][0] = v.x, qf[nt][j][1] = v.y, qf[nt][j][2] = v.z, qf[nt][j][3] = v.w;
+      }
+      const float inv = p.bf16 ? bf16_row_to_half<kGroups>(qf[nt]) : 1.0f;
+      factor[nt][0] = __shfl_sync(~0u, inv, 8 * c) * p.scale_log2;
+      factor[nt][1] = __shfl_sync(~0u, inv, 8 * c + 4) * p.scale_log2;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int token_of = min(row0 + nt * 8 + 2 * c + e, rows - 1) / p.group;
+        limit[nt][e] = kList ? INT32_MAX : rq.length - rq.queries + token_of + 1;
+        low[nt][e] = !kList && p.window > 0 ? limit[nt][e] - p.window : INT32_MIN;
+      }
+    }
+  }
+  const int safe_to = kList ? INT32_MAX : rq.length - rq.queries + row0 / p.group + 1;  // every row sees up to here
+  const int safe_from = !kList && p.window > 0
+                            ? rq.length - rq.queries + min(rows - 1, row0 + NT * 8 - 1) / p.group + 1 - p.window
+                            : INT32_MIN;
+
+  float acc[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[nt][t][e] = 0.0f;
+  }
+  const uint32_t pick = (g >> 2) ? 0x7632u : 0x5410u;  // this lane's value scales: upper or lower halves
+
+  bool ok = true;
+  int stage = 0;
+  uint32_t parity = 0;
+  for (int tile = warp; tile < tiles; tile += kWarps) {
+    ok = wait_bounded(&bars[warp][stage], parity) && ok;
+    const uint32_t valid = valid_of[warp][stage];
+    const uint32_t base = ring + stage * Sh::kTileBytes;
+    const int pos0 = from + tile * kTile;
+    const bool masked = valid != ~0u || (!kList && (pos0 + kTile > safe_to || pos0 < safe_from));
+
+    // S^T: 32 positions (two 16-row steps) by 8 NT rows
+    float s[2][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.0f;
+      const uint32_t ra = base + (mt * 16 + g) * kRow, rb = ra + 8 * kRow;
+      uint32_t sa[kGroups / 2], sb[kGroups / 2];
+      lds_words(ra + D, sa);
+      lds_words(rb + D, sb);
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) {
+        uint32_t ha[4], hb[4];
+        codes_to_half2(lds32(ra + (j * 4 + c) * 4), ha);
+        codes_to_half2(lds32(rb + (j * 4 + c) * 4), hb);
+        const uint32_t ka = __byte_perm(sa[j / 2], 0, j & 1 ? 0x3232 : 0x1010);
+        const uint32_t kb = __byte_perm(sb[j / 2], 0, j & 1 ? 0x3232 : 0x1010);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ha[i] = hmul2(ha[i], ka);
+          hb[i] = hmul2(hb[i], kb);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16816(s[mt][nt], ha[0], hb[0], ha[1], hb[1], qf[nt][j][0], qf[nt][j][1]);
+          mma16816(s[mt][nt], ha[2], hb[2], ha[3], hb[3], qf[nt][j][2], qf[nt][j][3]);
+        }
+      }
+    }
+
+    // logits, masks, running maximum
+    float top[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[mt][nt][e] *= factor[nt][e & 1];
+          if (masked) {
+            const int at = mt * 16 + g + (e >> 1) * 8;
+            bool sees = (valid >> at) & 1u;
+            if constexpr (!kList) sees = sees && pos0 + at < limit[nt][e & 1] && pos0 + at >= low[nt][e & 1];
+            if (!sees) s[mt][nt][e] = -INFINITY;
+          }
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float t = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+        t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
+        t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
+        top[nt][e] = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
+      }
+    }
+    bool raised = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) raised = raised || top[nt][0] > m[nt][0] || top[nt][1] > m[nt][1];
+    if (__any_sync(~0u, raised)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float a[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float now = fmaxf(m[nt][e], top[nt][e]);
+          a[e] = now == m[nt][e] ? 1.0f : exp2_fast(m[nt][e] - now);
+          m[nt][e] = now;
+          l[nt][e] *= a[e];
+        }
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) {
+          acc[nt][t][0] *= a[0];
+          acc[nt][t][1] *= a[1];
+          acc[nt][t][2] *= a[0];
+          acc[nt][t][3] *= a[1];
+        }
+      }
+    }
+
+    // weights: fp32 into the sums, fp16 into the second product
+    uint32_t pf[2][NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float ref0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0] - kShift;
+      const float ref1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1] - kShift;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const float w0 = exp2_fast(s[mt][nt][0] - ref0), w1 = exp2_fast(s[mt][nt][1] - ref1);
+        const float w2 = exp2_fast(s[mt][nt][2] - ref0), w3 = exp2_fast(s[mt][nt][3] - ref1);
+        l[nt][0] += w0 + w2;
+        l[nt][1] += w1 + w3;
+        pf[mt][nt][0] = transpose8x8(pack_half2(w0, w1));
+        pf[mt][nt][1] = transpose8x8(pack_half2(w2, w3));
+      }
+    }
+
+    // O^T += V^T P^T: channels in 16-row steps; a lane's words of a position are g and g + 8 i
+    bool poisoned = false;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      const uint32_t r0 = base + (mt * 16 + 2 * c) * kRow;
+      const uint32_t rr[4] = {r0, r0 + kRow, r0 + 8 * kRow, r0 + 9 * kRow};
+      uint32_t sv[4][kWordsV];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) lds_words(rr[t] + D + D / 16, sv[t]);
+#pragma unroll
+      for (int i = 0; i < kWordsV; ++i) {
+        uint32_t s01 = __byte_perm(sv[0][i], sv[1][i], pick), s23 = __byte_perm(sv[2][i], sv[3][i], pick);
+        if (masked) {
+          // what no row sees counts as zero, whatever it holds; a NaN that only some rows see is put
+          // into those rows below
+          const uint32_t b01 = valid >> (mt * 16 + 2 * c), b23 = b01 >> 8;
+          s01 &= ((b01 & 1u) ? 0xFFFFu : 0u) | ((b01 & 2u) ? 0xFFFF0000u : 0u);
+          s23 &= ((b23 & 1u) ? 0xFFFFu : 0u) | ((b23 & 2u) ? 0xFFFF0000u : 0u);
+          if constexpr (!kList) {
+            const uint32_t n01 = nan_halves(s01), n23 = nan_halves(s23);
+            poisoned = poisoned || (n01 | n23) != 0;
+            s01 &= ~n01;
+            s23 &= ~n23;
+          }
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t] = lds32(rr[t] + D / 2 + (g + 8 * i) * 4);
+        uint32_t e01[4], o01[4], e23[4], o23[4];
+        codes_to_half2((w[0] & 0x0F0F0F0Fu) | ((w[1] << 4) & 0xF0F0F0F0u), e01);
+        codes_to_half2(((w[0] >> 4) & 0x0F0F0F0Fu) | (w[1] & 0xF0F0F0F0u), o01);
+        codes_to_half2((w[2] & 0x0F0F0F0Fu) | ((w[3] << 4) & 0xF0F0F0F0u), e23);
+        codes_to_half2(((w[2] >> 4) & 0x0F0F0F0Fu) | (w[3] & 0xF0F0F0F0u), o23);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t a0 = hmul2(e01[b], s01), a1 = hmul2(o01[b], s01), a2 = hmul2(e23[b], s23), a3 = hmul2(o23[b], s23);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][i * 4 + b], a0, a1, a2, a3, pf[mt][nt][0], pf[mt][nt][1]);
+        }
+      }
+    }
+    if constexpr (!kList) {
+      if (masked && __any_sync(~0u, poisoned)) {
+        for (int at = 0; at < kTile; ++at) {
+          if (!((valid >> at) & 1u)) continue;
+          uint32_t sv[kWordsV];
+          lds_words(base + at * kRow + D + D / 16, sv);
+#pragma unroll
+          for (int i = 0; i < kWordsV; ++i) {
+            if (nan_halves((g >> 2) ? sv[i] >> 16 : sv[i] & 0xFFFFu) == 0) continue;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (pos0 + at < limit[nt][e & 1] && pos0 + at >= low[nt][e & 1])
+#pragma unroll
+                  for (int b = 0; b < 4; ++b) acc[nt][i * 4 + b][e] = NAN;
+          }
+        }
+      }
+    }
+    __syncwarp();  // every lane has read the stage
+    const int next = tile + Sh::kStages * kWarps;
+    if (next < tiles) bring(next, stage);
+    if (++stage == Sh::kStages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
+  dependents_launch();
+
+  // ---- join the warps
+  if (!ok && lane == 0) atomicExch(&gave_up, 1);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float t = l[nt][e];
+      t += __shfl_xor_sync(~0u, t, 4);
+      t += __shfl_xor_sync(~0u, t, 8);
+      t += __shfl_xor_sync(~0u, t, 16);
+      if (g == 0) {
+        m_of[warp][nt * 8 + 2 * c + e] = m[nt][e];
+        l_of[warp][nt * 8 + 2 * c + e] = t;
+      }
+    }
+  __syncthreads();  // (also: every warp is done with the ring)
+  float* joined = reinterpret_cast<float*>(smem);
+  constexpr int kPitch = D + 4;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float a[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = nt * 8 + 2 * c + e;
+      float top = m_of[0][row];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, m_of[w][row]);
+      a[e] = m[nt][e] == -INFINITY ? 0.0f : exp2_fast(m[nt][e] - top);
+    }
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float* to_row = joined + (warp * NT * 8 + nt * 8 + 2 * c + e) * kPitch + (g + 8 * (t / 4)) * 8 + 2 * (t % 4);
+        // (a warp that saw nothing holds zeros, or NaN that it was given)
+        *reinterpret_cast<float2*>(to_row) = make_float2(acc[nt][t][e] * a[e], acc[nt][t][e + 2] * a[e]);
+      }
+  }
+  __syncthreads();
+  const bool final_here = count == 1;
+  const int64_t part = (((int64_t)flat * p.heads + head) * p.row_tiles + row_tile) * (NT * 8);
+  for (int u = tid; u < NT * 8 * (D / 4); u += kThreads) {
+    const int row = u / (D / 4), ch = u % (D / 4) * 4;
+    if (row0 + row >= rows) break;
+    float top = m_of[0][row];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, m_of[w][row]);
+    float sum = 0.0f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = m_of[w][row];
+      // a NaN weight sum stays one
+      if (mw != -INFINITY || !(l_of[w][row] == 0.0f)) sum += l_of[w][row] * (mw == -INFINITY ? 1.0f : exp2_fast(mw - top));
+      const float4 x = *reinterpret_cast<const float4*>(joined + (w * NT * 8 + row) * kPitch + ch);
+      o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    float log2_sum = sum == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top - kShift) + __log2f(sum);
+    if (gave_up) {
+      o = make_float4(NAN, NAN, NAN, NAN);
+      log2_sum = NAN;
+    }
+    if (final_here) {
+      const int64_t token = token0 + (row0 + row) / p.group;
+      const int qh = head * p.group + (row0 + row) % p.group;
+      store4(p, (token * p.heads * p.group + qh) * D + ch, o);
+      if (p.lse != nullptr && ch == 0) p.lse[token * p.heads * p.group + qh] = log2_sum * 0.6931471805599453f;
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (part + row) * D + ch) = o;
+      if (ch == 0) p.part_lse[part + row] = log2_sum;
+    }
+  }
+}
+
+// Joins the parts of a (query, head): out = sum_i 2^(e_i - top) o_i / sum_i 2^(e_i - top), e_i
+// the parts' logarithms. Eight warps share the parts, in one fixed order whatever the timing.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionParams p, int rows_per_cta, int list) {
+  constexpr int kVec = D / 32;
+  __shared__ float o_of[kJoinThreads / 32][D];
+  __shared__ float sum_of[kJoinThreads / 32], top_of[kJoinThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  dependency_wait();
+  const int q_heads = p.heads * p.group;
+  const int64_t token = blockIdx.x / q_heads;
+  const int qh = (int)(blockIdx.x % q_heads), head = qh / p.group;
+  const int request = owner_of_token(p, (int)token);
+  if (request < 0) return;
+  int base, n, row;
+  if (list) {
+    base = (int)token * p.target;
+    n = p.target;
+    row = qh % p.group;
+  } else {
+    const int2 pl = p.plan[request];
+    base = pl.x;
+    n = pl.y;
+    const Request rq = request_of(p, request);
+    const int64_t nth = token - rq.first;
+    if (nth >= rq.queries) return;
+    row = (int)nth * p.group + qh % p.group;
+  }
+  if (n <= 1) return;  // written whole
+  const int row_tile = row / rows_per_cta, in_tile = row % rows_per_cta;
+  if (row_tile >= p.row_tiles) return;  // past max_new: not computed
+  const int64_t step = (int64_t)p.heads * p.row_tiles * rows_per_cta;
+  const int64_t first = (((int64_t)base * p.heads + head) * p.row_tiles + row_tile) * rows_per_cta + in_tile;
+
+  float top = -INFINITY;
+  bool bad = false;
+  for (int i = tid; i < n; i += kJoinThreads) {
+    const float e = p.part_lse[first + i * step];
+    top = fmaxf(top, e);
+    bad = bad || e != e;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+  if (lane == 0) top_of[warp] = top;
+  bad = __syncthreads_or(bad);
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, top_of[w]);
+
+  float o[kVec] = {}, sum = 0.0f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += kJoinThreads / 32) {
+    const float e = p.part_lse[first + i * step];
+    const float* from = p.part_o + (first + i * step) * D + lane * kVec;
+    float x[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; k += 2) *reinterpret_cast<float2*>(x + k) = *reinterpret_cast<const float2*>(from + k);
+    const float w = e == -INFINITY ? 0.0f : exp2_fast(e - top);
+    sum += w;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) o[k] += e == -INFINITY ? 0.0f : w * x[k];
+  }
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) o_of[warp][lane * kVec + k] = o[k];
+  if (lane == 0) sum_of[warp] = sum;
+  __syncthreads();
+  dependents_launch();
+  float all = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) all += sum_of[w];
+  const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+  const int64_t out_row = token * q_heads + qh;
+  if (tid < D / 4) {
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(&o_of[w][tid * 4]);
+      y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
+    }
+    y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
+    if (bad) y = make_float4(NAN, NAN, NAN, NAN);
+    store4(p, out_row * D + tid * 4, y);
+  }
+  if (p.lse != nullptr && tid == 0)
+    p.lse[out_row] = bad ? NAN : all == 0.0f ? -INFINITY : (top + __log2f(all)) * 0.6931471805599453f;
+}
+
+// ---- host side
+
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+int g_sms[kMaxDevices];
+bool g_smem_set[kMaxDevices][3][3][2];
+
+struct RowsKernel {
+  const void* func;
+  int smem, per_sm;
+};
+
+template <int D, int NT>
+RowsKernel rows_of(bool list) {
+  return {list ? reinterpret_cast<const void*>(&rows_kernel<D, NT, true>)
+               : reinterpret_cast<const void*>(&rows_kernel<D, NT, false>),
+          Shape<D, NT>::kSmem, Shape<D, NT>::kPerSm};
+}
+RowsKernel rows_kernel_of(int d, int nt, bool list) {
+  if (d == 64) return nt == 1 ? rows_of<64, 1>(list) : nt == 2 ? rows_of<64, 2>(list) : rows_of<64, 4>(list);
+  if (d == 128) return nt == 1 ? rows_of<128, 1>(list) : nt == 2 ? rows_of<128, 2>(list) : rows_of<128, 4>(list);
+  return nt == 1 ? rows_of<256, 1>(list) : rows_of<256, 2>(list);
+}
+
+// The launch for these sizes: row tiles, parts and workspace.
+struct Plan {
+  int nt, row_tiles;
+  int target;        // dense: chunks wanted over all requests; listed: parts of a list
+  int min_chunk;
+  int64_t flats;     // chunks at most
+  bool join;
+  int64_t plan_bytes, lse_bytes, o_bytes;
+  int64_t bytes() const { return join ? plan_bytes + lse_bytes + o_bytes : 0; }
+};
+
+constexpr int kMinChunk = 256;
+
+Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int requests, int max_new, int list_len) {
+  Plan a = {};
+  const int64_t rows = (int64_t)(list_len > 0 ? 1 : max_new) * group;
+  const int most = d == 256 ? 2 : 4;
+  a.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : most;
+  if (a.nt > most) a.nt = most;
+  a.row_tiles = (int)((rows + a.nt * 8 - 1) / (a.nt * 8));
+  a.min_chunk = kMinChunk;
+  const int slots = sms * rows_kernel_of(d, a.nt, list_len > 0).per_sm;
+  const int64_t units = (int64_t)heads * a.row_tiles;
+  if (list_len > 0) {
+    // parts of at least four tiles (one a warp), until the slots are full
+    int64_t parts = (slots + tokens * units - 1) / (tokens * units);
+    const int64_t tiles = (list_len + kTile * kWarps - 1) / (kTile * kWarps);
+    parts = parts > tiles ? tiles : parts;
+    a.target = (int)(parts < 1 ? 1 : parts);
+    a.flats = tokens * a.target;
+    a.join = a.target > 1;
+  } else {
+    // several chunks a slot, so that the last ones to end are short
+    int64_t target = ((int64_t)slots * 6 + units - 1) / units;
+    a.target = (int)(target < 1 ? 1 : target);
+    a.flats = a.target == 1 ? requests : a.target + (int64_t)requests;
+    a.join = a.target > 1;
+  }
+  const int64_t part_rows = a.flats * units * a.nt * 8;
+  a.plan_bytes = ((int64_t)requests * 8 + 15) / 16 * 16;
+  a.lse_bytes = (part_rows * 4 + 15) / 16 * 16;
+  a.o_bytes = part_rows * d * 4;
+  return a;
+}
+
+lt_status device_of(int* dev, int* sms) {
+  if (cudaGetDevice(dev) != cudaSuccess) return LT_ERR_CUDA;
+  if (*dev < 0 || *dev >= kMaxDevices) return LT_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_sms[*dev] == 0 && cudaDeviceGetAttribute(&g_sms[*dev], cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess)
+    return LT_ERR_CUDA;
+  *sms = g_sms[*dev];
+  return LT_OK;
+}
+
+lt_status check_sizes(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t requests,
+                      int32_t max_new, int32_t list_len) {
+  if (tokens < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || head_dim < 1 || requests < 0 ||
+      max_new < 1 || list_len < 0)
+    return LT_ERR_INVALID_ARG;
+  if (lt_kv4_row_bytes(head_dim) == 0 || tokens > INT32_MAX) return LT_ERR_UNSUPPORTED;
+  return LT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lt_status lt_kv4_workspace(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                           int32_t requests, int32_t max_new, int32_t list_len, int64_t* bytes) {
+  if (bytes == nullptr) return LT_ERR_INVALID_ARG;
+  lt_status st = check_sizes(tokens, q_heads, kv_heads, head_dim, requests, max_new, list_len);
+  if (st != LT_OK) return st;
+  *bytes = 0;
+  if (tokens == 0 || requests == 0) return LT_OK;
+  int dev = 0, sms = 0;
+  st = device_of(&dev, &sms);
+  if (st != LT_OK) return st;
+  *bytes = make_plan(sms, tokens, kv_heads, q_heads / kv_heads, head_dim, requests, max_new, list_len).bytes();
+  return LT_OK;
+}
+
+lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t q_heads,
+                           int32_t kv_heads, int32_t head_dim, int64_t q_token_stride,
+                           int64_t q_head_stride, const void* cache, int64_t pages, int32_t page_size,
+                           const int32_t* block_table, int32_t table_width, const int32_t* lengths,
+                           int32_t requests, const int32_t* starts, int32_t max_new,
+                           const int32_t* positions, int32_t list_len, int32_t window, float scale,
+                           void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+  lt_status st = check_sizes(tokens, q_heads, kv_heads, head_dim, requests, max_new, list_len);
+  if (st == LT_ERR_INVALID_ARG) return st;
+  const int shift = page_shift(page_size);
+  if (dtype != LT_DTYPE_BF16 && dtype != LT_DTYPE_F16) return LT_ERR_INVALID_ARG;
+  if (shift < 0 || pages < 0 || table_width < 1 || window < 0 || !(scale == scale) || scale - scale != 0.0f)
+    return LT_ERR_INVALID_ARG;
+  if (starts == nullptr && (tokens != requests || max_new != 1)) return LT_ERR_INVALID_ARG;
+  if (positions != nullptr && window != 0) return LT_ERR_INVALID_ARG;
+  if (positions == nullptr && list_len != 0) return LT_ERR_INVALID_ARG;
+  if (positions != nullptr && list_len == 0) return LT_ERR_INVALID_ARG;
+  if (tokens > 0 && requests > 0) {
+    if (q == nullptr || out == nullptr || block_table == nullptr || lengths == nullptr ||
+        (cache == nullptr && pages > 0))
+      return LT_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(q) % 16 || q_token_stride % 8 || q_head_stride % 8 ||
+        reinterpret_cast<uintptr_t>(cache) % 16 || reinterpret_cast<uintptr_t>(out) % 16)
+      return LT_ERR_INVALID_ARG;
+  }
+  if (st != LT_OK || pages > INT32_MAX) return LT_ERR_UNSUPPORTED;
+  if (tokens == 0 || requests == 0) return LT_OK;
+  int dev = 0, sms = 0;
+  st = device_of(&dev, &sms);
+  if (st != LT_OK) return st;
+  const int group = q_heads / kv_heads;
+  const Plan plan = make_plan(sms, tokens, kv_heads, group, head_dim, requests, max_new, list_len);
+  if (plan.join && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < plan.bytes()))
+    return LT_ERR_INVALID_ARG;
+  const int64_t grid = plan.flats * kv_heads * plan.row_tiles, joins = tokens * q_heads;
+  if (grid > INT32_MAX || joins > INT32_MAX) return LT_ERR_UNSUPPORTED;
+
+  AttentionParams p = {};
+  p.q = q;
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.table = block_table;
+  p.lengths = lengths;
+  p.starts = starts;
+  p.positions = positions;
+  p.out = out;
+  p.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (plan.join) {
+    p.plan = reinterpret_cast<int2*>(ws);
+    p.part_lse = reinterpret_cast<float*>(ws + plan.plan_bytes);
+    p.part_o = reinterpret_cast<float*>(ws + plan.plan_bytes + plan.lse_bytes);
+  }
+  p.q_token = q_token_stride;
+  p.q_head = q_head_stride;
+  p.pages = (int32_t)pages;
+  p.tokens = (int32_t)tokens;
+  p.requests = requests;
+  p.width = table_width;
+  p.heads = kv_heads;
+  p.group = group;
+  p.shift = shift;
+  p.list_len = list_len;
+  p.window = window;
+  p.target = plan.target;
+  p.min_chunk = plan.min_chunk;
+  p.row_tiles = plan.row_tiles;
+  p.bf16 = dtype == LT_DTYPE_BF16;
+  p.scale_log2 = scale * 1.4426950408889634f;
+
+  const bool list = list_len > 0;
+  const RowsKernel k = rows_kernel_of(head_dim, plan.nt, list);
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    bool& set = g_smem_set[dev][head_dim / 128][plan.nt / 2][list];
+    if (!set) {
+      if (cudaFuncSetAttribute(k.func, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess)
+        return LT_ERR_CUDA;
+      set = true;
+    }
+  }
+  st = launch(k.func, dim3((unsigned)grid), kThreads, (unsigned)k.smem, &p, stream);
+  if (st != LT_OK || !plan.join) return st;
+  if (lt::take_injected_failure()) return LT_ERR_CUDA;
+  const void* func = head_dim == 64    ? reinterpret_cast<const void*>(&join_kernel<64>)
+                     : head_dim == 128 ? reinterpret_cast<const void*>(&join_kernel<128>)
+                                       : reinterpret_cast<const void*>(&join_kernel<256>);
+  int rows_per_cta = plan.nt * 8, listed = list;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)joins);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void* a[] = {&p, &rows_per_cta, &listed};
+  return cudaLaunchKernelExC(&cfg, func, a) == cudaSuccess ? LT_OK : LT_ERR_CUDA;
+}
+
+}  // extern "C"

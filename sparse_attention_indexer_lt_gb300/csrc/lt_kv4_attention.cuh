@@ -1,0 +1,135 @@
+// lt_kv4_attention.cuh -- what the attention kernels share: their parameters, the
+// requests' ranges, query fragments and output stores.
+#pragma once
+
+#include <cmath>
+
+#include "lt_async.cuh"
+#include "lt_kv4.cuh"
+
+namespace lt {
+namespace kv4 {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 32;  // positions of a tile
+
+struct AttentionParams {
+  const void* q;
+  const uint8_t* cache;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* starts;
+  const int32_t* positions;
+  void* out;
+  float* lse;
+  int2* plan;       // [requests]: first chunk, chunks
+  float* part_lse;  // [chunk][kv head][row], in units of log 2
+  float* part_o;    // [chunk][kv head][row][D], divided by the part's own sum
+  int64_t q_token, q_head;
+  int32_t pages, tokens, requests, width, heads, group, shift, list_len, window;
+  int32_t target, min_chunk, row_tiles, bf16;
+  float scale_log2;
+};
+
+struct Request {
+  int length;   // positions in the cache
+  int first;    // its first query's row
+  int queries;
+  int low;      // the first position that any of its queries sees, rounded down to a tile
+  int span;     // length - low
+};
+
+__device__ __forceinline__ Request request_of(const AttentionParams& p, int r) {
+  Request q;
+  const int64_t most = (int64_t)p.width << p.shift;
+  const int len = max(__ldg(p.lengths + r), 0);
+  q.length = (int)(len < most ? len : most);
+  int first = r, end = r + 1;
+  if (p.starts != nullptr) {
+    first = min(max(__ldg(p.starts + r), 0), p.tokens);
+    end = min(__ldg(p.starts + r + 1), p.tokens);
+  }
+  q.first = first;
+  q.queries = max(end - first, 0);
+  q.low = 0;
+  if (p.window > 0) q.low = (int)(max((int64_t)q.length - q.queries + 1 - p.window, (int64_t)0) / kTile * kTile);
+  if (q.low > q.length) q.low = q.length / kTile * kTile;
+  q.span = q.length - q.low;
+  return q;
+}
+
+// The request that a query row belongs to; -1 past the last.
+__device__ __forceinline__ int owner_of_token(const AttentionParams& p, int token) {
+  if (p.starts == nullptr) return token < p.requests ? token : -1;
+  if (token < __ldg(p.starts) || token >= __ldg(p.starts + p.requests)) return -1;
+  int lo = 0, hi = p.requests - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.starts + mid + 1) > token)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+// Waits for a phase, a bounded number of polls; false if it gave up.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
+__device__ __forceinline__ void bulk_in(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// 0xFFFF in each half of the word that is an fp16 NaN.
+__device__ __forceinline__ uint32_t nan_halves(uint32_t h) {
+  return ((h & 0x7FFFu) > 0x7C00u ? 0xFFFFu : 0u) | ((h & 0x7FFF0000u) > 0x7C000000u ? 0xFFFF0000u : 0u);
+}
+
+// A row's eight-channel pieces, bf16 pairs spread over the four lanes of equal lane / 4, become fp16
+// pairs: times the power of two that brings the row's largest into [2^14, 2^15), so
+// nothing overflows and what lies within 2^-28 of the largest stays exact. Returns
+// the inverse of that power.
+template <int N>
+__device__ __forceinline__ float bf16_row_to_half(uint32_t (&w)[N][4]) {
+  uint32_t big = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) big = max(big, max(w[j][i] << 16 & 0x7FFF0000u, w[j][i] & 0x7FFF0000u));
+  big = max(big, __shfl_xor_sync(~0u, big, 1));
+  big = max(big, __shfl_xor_sync(~0u, big, 2));
+  const int e = (int)(big >> 23);  // biased exponent of the largest
+  // zero rows and rows with an infinity or NaN are taken as they are
+  const int up = e == 0 || e == 255 ? 127 : min(268 - e, 253);
+  const float mul = __uint_as_float((uint32_t)up << 23);
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = __uint_as_float(w[j][i] << 16) * mul, hi = __uint_as_float(w[j][i] & 0xFFFF0000u) * mul;
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j][i]) : "f"(hi), "f"(lo));
+    }
+  return __uint_as_float((uint32_t)(254 - up) << 23);
+}
+
+// Four outputs, rounded once.
+__device__ __forceinline__ void store4(const AttentionParams& p, int64_t at, float4 o) {
+  uint2 w;
+  if (p.bf16) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(o.y), "f"(o.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(o.w), "f"(o.z));
+  } else {
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(o.y), "f"(o.x));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(o.w), "f"(o.z));
+  }
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
+}
+
+}  // namespace kv4
+}  // namespace lt

@@ -29,4 +29,6 @@ const void* stream_kernel_ptr(int threads);
 // block size or thread count
 const void* listed_kernel_ptr(int threads, int block, bool bf16);
 int64_t listed_round_blocks(int block);
+// takes one of the launch failures that lt_test_inject asked for, if any is left
+bool take_injected_failure();
 }  // namespace lt

@@ -1,0 +1,500 @@
+"""GPU parity of the 4-bit cache against its 64-bit oracle.
+
+Page tables, slots, codes and scales are whole numbers or exact: they have to be
+equal. Attention is compared within a bound derived from its arithmetic, eps =
+2^-24: a logit is a sum of D exact products in fp32 on the tensor core, off by at most
+D eps reach (reach: the largest sum of |scale q k| over the visible positions) and a
+few roundings of factors (8 eps reach, and eps of the logit), so a weight by that much
+relative and 2^-21 from the exponential: together d. The weights are rounded to fp16
+(2^-11 relative, or 2^-33 of the largest where they become subnormal), the sums of n
+terms add n eps. Numerator and denominator carry d each, so, with |v| averaged by
+the weights in `size`,
+
+    |out - ref| <= size (2 d + 2^-11 + 2 n eps) + n 2^-33 max|v| + u |ref|,   |lse - ref| <= d + n eps + 2^-21 (1 + |ref|)
+
+where u is the output's rounding: 2^-8 (bf16), 2^-11 (fp16).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4 as ok
+
+pytestmark = pytest.mark.gpu
+EPS = 2.0 ** -24
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from sparse_attention_indexer_lt_gb300 import build
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+def num(t):
+    return t.detach().cpu().double().numpy()
+
+
+# ---- page tables
+
+def check_extend(lengths, new, table, free, num_free, page, max_tokens):
+    import sparse_attention_indexer_lt_gb300 as lt
+    want = ok.extend(lengths, new, table, free, num_free, page, max_tokens)
+    dev = [torch.as_tensor(np.asarray(x, np.int32)).cuda() for x in (lengths, new, table, free, [num_free])]
+    got = lt.page_extend(*dev[:2], dev[2], dev[3], dev[4], page, max_tokens)
+    torch.cuda.synchronize()
+    assert np.array_equal(got.starts.cpu().numpy(), want["starts"])
+    assert np.array_equal(got.lengths.cpu().numpy(), want["lengths"])
+    assert int(got.num_free) == want["num_free"]
+    assert np.array_equal(dev[2].cpu().numpy(), want["table"])
+    assert np.array_equal(got.slots.cpu().numpy(), want["slots"])
+    assert np.array_equal(got.positions.cpu().numpy(), want["positions"])
+    return want
+
+
+@pytest.mark.parametrize("requests", [0, 1, 2, 33, 1024, 1025, 3000])
+@pytest.mark.parametrize("page", [1, 16, 1024])
+def test_extend(requests, page):
+    rng = np.random.default_rng(requests * 7 + page)
+    lengths = rng.integers(-1, 40 if page < 1024 else 3000, requests).astype(np.int32)
+    new = rng.integers(-2, 9, requests).astype(np.int32)
+    width = max(1, (3008 if page == 1024 else 48) // page + 1)
+    pages = requests * width + 5
+    order = rng.permutation(pages).astype(np.int32)
+    table = order[:requests * width].reshape(requests, width).copy()
+    free = np.concatenate([order[requests * width:], order[:requests * width]])
+    plenty = len(free)
+    total = int(np.maximum(new, 0).sum())
+    for num_free, room in ((plenty, total + 11), (plenty, total), (plenty, max(0, total - 3)), (plenty // 9, total + 300), (0, total),
+                           (plenty + 100, total)):
+        if requests == 0 and num_free > plenty:
+            continue
+        check_extend(lengths, new, table.reshape(requests, width), free, num_free, page, room)
+
+
+def test_extend_stops_at_the_first_that_does_not_fit():
+    table = np.full((4, 2), -1, np.int32)
+    free = np.arange(10, dtype=np.int32)
+    # request 1 wants three pages of a table two wide: nothing for it and the later ones
+    want = check_extend([0, 5, 0, 0], [4, 6, 1, 1], table, free, 10, 4, 20)
+    assert want["lengths"].tolist() == [4, 5, 0, 0] and want["starts"].tolist() == [0, 4, 4, 4, 4]
+    check_extend([0, 2 ** 31 - 2, 0, 0], [4, 6, 1, 1], table, free, 10, 4, 20)
+    # a hole in an old page gives slots of -1 (nothing is stored there)
+    check_extend([2, 0, 0, 0], [2, 0, 0, 0], table, free, 10, 4, 20)
+
+
+@pytest.mark.parametrize("requests", [0, 1, 5, 1023, 2500])
+def test_release(requests):
+    import sparse_attention_indexer_lt_gb300 as lt
+    rng = np.random.default_rng(requests)
+    page, width = 8, 7
+    lengths = rng.integers(-2, 70, requests).astype(np.int32)  # some longer than their row of the table
+    done = rng.random(requests) < 0.4
+    table = rng.permutation(requests * width).astype(np.int32).reshape(requests, width)
+    for capacity, num_free in ((requests * width + 9, 3), (requests * width // 3 + 4, 1), (5, 9)):
+        free = np.full(capacity, -7, np.int32)
+        want_l, want_f, want_n = ok.release(lengths, done, table, free, num_free, page)
+        d = [torch.as_tensor(x).cuda() for x in (lengths, done, table, free, np.array([num_free], np.int32))]
+        got_l, got_n = lt.page_release(*d[:4], d[4], page)
+        torch.cuda.synchronize()
+        assert np.array_equal(got_l.cpu().numpy(), want_l) and int(got_n) == want_n
+        assert np.array_equal(d[3].cpu().numpy(), want_f)
+
+
+# ---- storing and loading
+
+def special(x):
+    """Values at the quantiser's edges in the first groups."""
+    x[0, 0, :32] = 0.0
+    x[0, 0, 32:64] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0] * 4) * torch.tensor([1.0, -1.0] * 16)
+    x[1, 0, :32] = 1e-9 * torch.arange(32)
+    x[1, 0, 32:64] = 60000.0
+    x[2, 0, 5] = float("inf")
+    x[2, 0, 40] = float("nan")
+    x[3, 0, :32] = torch.linspace(-6.0, 6.0, 32) * 2.0 ** -17
+    x[3, 0, 32:64] = -x[0, 0, 32:64] * 11 / 16
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim,heads,page", [(64, 1, 1), (64, 3, 16), (128, 2, 32), (256, 1, 8)])
+def test_store_and_load(dtype, dim, heads, page):
+    import sparse_attention_indexer_lt_gb300 as lt
+    torch.manual_seed(dim + heads)
+    tokens, pages = 37, 64 if page == 1 else 9
+    t = TYPES[dtype]
+    k = special(torch.randn(tokens, heads, dim) * 10.0 ** torch.randint(-6, 3, (tokens, heads, 1))).to(t)
+    v = special(torch.randn(tokens, heads, dim)).to(t)
+    # keys and values as views of one projection, its channels at an odd offset for the scalar loads
+    for wide in (True, False):
+        extra = 0 if wide else 1
+        both = torch.full((tokens, 2 * heads * dim + extra), 7.0, dtype=t)
+        both[:, extra:] = torch.cat([k.flatten(1), v.flatten(1)], 1)
+        both = both.cuda()
+        kd, vd = both[:, extra:extra + heads * dim].unflatten(1, (heads, dim)), both[:, extra + heads * dim:].unflatten(1, (heads, dim))
+        slots = torch.randperm(pages * page)[:tokens].long()
+        slots[4], slots[5], slots[6] = -1, pages * page, -2 ** 40
+        cache = torch.full((pages, heads, page, lt.kv4_row_bytes(dim)), 0xA5, dtype=torch.uint8, device="cuda")
+        lt.kv4_store(kd, vd, cache, slots.cuda())
+        c = cache.cpu().numpy()
+        written = np.zeros((pages, page), bool)
+        for i, s in enumerate(slots.tolist()):
+            if 0 <= s < pages * page:
+                written[s // page, s % page] = True
+                row = c[s // page, :, s % page]
+                want = ok.rows_of(num(k[i]), num(v[i]))
+                scales = slice(dim, dim + dim // 8)
+                g, w = row[:, scales].copy().view(np.float16), want[:, scales].copy().view(np.float16)
+                assert np.array_equal(g, w, equal_nan=True), f"scales of token {i}"
+                gk, wk = ok.values_of(row, dim), ok.values_of(want, dim)
+                assert np.array_equal(gk, wk, equal_nan=True), f"values of token {i}"
+        assert (c.transpose(0, 2, 1, 3)[~written] == 0xA5).all(), "rows without a slot were written"
+        for out_type in TYPES.values():
+            gk, gv = lt.kv4_load(cache, slots.cuda(), dtype=out_type)
+            for i, s in enumerate(slots.tolist()):
+                if 0 <= s < pages * page:
+                    wk, wv = ok.values_of(c[s // page, :, s % page], dim)
+                    for got, want in ((gk, wk), (gv, wv)):
+                        want = torch.as_tensor(want).to(out_type)
+                        assert torch.equal(torch.nan_to_num(got[i].cpu(), 99.0), torch.nan_to_num(want, 99.0))
+                else:
+                    assert not gk[i].any() and not gv[i].any()
+
+
+def test_store_of_many_tokens_and_a_repeat():
+    import sparse_attention_indexer_lt_gb300 as lt
+    torch.manual_seed(5)
+    tokens, heads, dim, page = 5001, 3, 128, 64
+    k, v = torch.randn(2, tokens, heads, dim, dtype=torch.bfloat16)
+    cache = lt.kv4_cache(100, heads, page, dim)
+    slots = torch.randperm(6400)[:tokens].cuda()
+    lt.kv4_store(k.cuda(), v.cuda(), cache, slots)
+    first = cache.clone()
+    lt.kv4_store(k.cuda(), v.cuda(), cache, slots)
+    assert torch.equal(first, cache)
+    gk, gv = lt.kv4_load(cache, slots, dtype=torch.float32)
+    for i in range(0, tokens, 499):
+        for got, x in ((gk, k), (gv, v)):
+            s, c = ok.quantise(num(x[i]))
+            assert np.array_equal(num(got[i]), ok.values(s, c))
+    lt.kv4_store(k[:0].cuda(), v[:0].cuda(), cache, slots[:0])
+    assert torch.equal(first, cache) and lt.kv4_load(cache, slots[:0])[0].shape == (0, heads, dim)
+
+
+# ---- attention
+
+class Problem:
+    """A filled cache with a random block table, and the oracle's view of it."""
+
+    def __init__(self, lengths, new, heads, group, dim, page, dtype, seed=0, spread=1.0, extra_width=0, positions=None, magnitude=1.0):
+        import sparse_attention_indexer_lt_gb300 as lt
+        g = torch.Generator().manual_seed(seed)
+        self.lengths, self.heads, self.dim, self.page = lengths, heads, dim, page
+        self.starts = [0]
+        for n in new:
+            self.starts.append(self.starts[-1] + n)
+        self.max_new = max(new + [1])
+        held = [-(-n // page) for n in lengths]
+        width = max(held + [1]) + extra_width
+        order = torch.randperm(sum(held) + 3, generator=g).int()
+        table = torch.full((len(lengths), width), -1, dtype=torch.int32)
+        at = 0
+        for r, n in enumerate(held):
+            table[r, :n] = order[at:at + n]
+            at += n
+        rows = lt.kv4_row_bytes(dim)
+        shape = (sum(held) + 3, heads, page)
+        # every byte random first: what no request holds is garbage, NaN scales among it
+        cache = torch.randint(0, 256, shape + (rows,), generator=g, dtype=torch.uint8)
+        scales = magnitude * 0.35 * torch.exp(0.3 * torch.randn(shape + (dim // 16,), generator=g))
+        good = (scales.half().view(torch.int16) & -4).view(torch.uint8)
+        for r, n in enumerate(lengths):
+            for p in range(n):
+                cache[table[r, p // page], :, p % page, dim:dim + dim // 8] = good[table[r, p // page], :, p % page]
+        self.table, self.cache = table, cache
+        self.q = (spread * torch.randn(self.starts[-1], heads * group, dim, generator=g)).to(TYPES[dtype])
+        self.positions = positions
+
+    def rows_at(self, r, h, p):
+        page = int(self.table[r, p // self.page])
+        if not 0 <= page < self.cache.shape[0]:
+            return None
+        if not hasattr(self, "_values"):
+            self._values = ok.values_of(self.cache.numpy(), self.dim)
+        return self._values[0][page, h, p % self.page], self._values[1][page, h, p % self.page]
+
+    def run(self, **kw):
+        import sparse_attention_indexer_lt_gb300 as lt
+        pos = None if self.positions is None else torch.as_tensor(self.positions).int().cuda()
+        starts = torch.tensor(self.starts, dtype=torch.int32).cuda()
+        args = dict(starts=starts, max_new=self.max_new, positions=pos, with_lse=True)
+        args.update(kw)
+        q = args.pop("q", None)
+        return lt.kv4_attention(self.q.cuda() if q is None else q, self.cache.cuda(), self.table.cuda(),
+                                torch.tensor(self.lengths, dtype=torch.int32).cuda(), **args)
+
+    def check(self, out, lse, window=0, scale=None):
+        want, want_lse, size, reach = ok.attention(num(self.q), self.rows_at, self.lengths, self.starts, self.heads,
+                                                   self.dim ** -0.5 if scale is None else scale, window, self.positions)
+        n = max(self.lengths + [1]) if self.positions is None else np.shape(self.positions)[1]
+        held = [self.rows_at(r, h, x) for r, n_r in enumerate(self.lengths) for h in range(self.heads) for x in range(n_r)]
+        vmax = max([float(np.abs(x[1]).max()) for x in held if x is not None] + [0.0])
+        d = (self.dim + 8) * EPS * reach + EPS * np.where(np.isfinite(want_lse), np.abs(want_lse), 0) + 2.0 ** -21
+        u = 2.0 ** -8 if self.q.dtype == torch.bfloat16 else 2.0 ** -11
+        tol = size * (2 * d[..., None] + 2.0 ** -11 + 2 * n * EPS) + n * 2.0 ** -33 * vmax + u * np.abs(want)
+        err = np.abs(num(out) - want)
+        assert np.isfinite(num(out)).all(), "not finite"
+        assert (err <= tol).all(), f"out: {int((err > tol).sum())} off, worst {float((err - tol).max()):.3g} over its bound"
+        got = num(lse)
+        empty = np.isinf(want_lse)
+        assert np.array_equal(np.isinf(got) & (got < 0), empty)
+        assert not num(out)[empty].any()
+        err = np.abs(got[~empty] - want_lse[~empty])
+        tol = (d + n * EPS + 2.0 ** -21 * (1 + np.abs(np.where(empty, 0, want_lse))))[~empty]
+        assert (err <= tol).all(), f"lse: worst {float((err / tol).max()):.3g} of its bound"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,heads,group", [(64, 2, 1), (64, 1, 3), (128, 2, 4), (128, 1, 16), (128, 1, 33), (256, 1, 8), (256, 1, 20)])
+def test_decode(dim, heads, group, dtype):
+    """One query a request: lengths of one, around the tile's 32 and a page's end, and longer."""
+    p = Problem([1, 2, 31, 32, 33, 63, 64, 65, 200], [1] * 9, heads, group, dim, 16, dtype, seed=dim + group)
+    p.check(*p.run())
+    p.check(*p.run(starts=None))
+
+
+@pytest.mark.parametrize("page", [1, 2, 8, 32, 64, 256, 1024])
+def test_page_sizes(page):
+    p = Problem([1, 77, 300], [1, 2, 3], 2, 4, 128, page, "bf16", seed=page)
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f16", 64), ("bf16", 256)])
+@pytest.mark.parametrize("window", [0, 1, 5, 32, 100, 10 ** 9])
+def test_ragged_queries_and_windows(dtype, dim, window):
+    """Requests of no, one and several new tokens; more queries than positions leave the first ones empty;
+    a request without positions."""
+    p = Problem([0, 5, 40, 130, 3, 70, 0], [1, 5, 0, 9, 6, 1, 0], 2, 3, dim, 8, dtype, seed=window % 97, extra_width=3)
+    p.check(*p.run(window=window), window=window)
+
+
+def test_many_query_rows():
+    """More query rows than one CTA takes: several row tiles a request."""
+    p = Problem([90, 150], [50, 33], 1, 5, 128, 32, "bf16", seed=3)
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("dim,heads,group,list_len", [(64, 2, 4, 1), (128, 1, 16, 33), (128, 2, 8, 512), (256, 1, 4, 100), (128, 1, 40, 130)])
+def test_listed(dim, heads, group, list_len):
+    rng = np.random.default_rng(list_len)
+    lengths, new = [400, 1, 90, 0], [3, 1, 2, 1]
+    pos = np.full((sum(new), list_len), -1)
+    t = 0
+    for n, c in zip(lengths, new):
+        for i in range(c):
+            take = rng.integers(-3, n + 9, list_len)  # pads, positions past the end, repeats
+            pos[t] = take if i != 1 else -1           # (one list is empty)
+            t += 1
+    p = Problem(lengths, new, heads, group, dim, 16, "bf16", seed=list_len, positions=pos)
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("requests", [1, 3, 130, 300])
+def test_split_requests_join_to_the_same(requests):
+    """Long requests are cut into parts and joined; more requests than a CTA's threads scan at once."""
+    lengths = [(r * 389) % 1500 + 1 if requests < 100 else (r * 37) % 90 for r in range(requests)]
+    p = Problem(lengths, [1] * requests, 1, 2, 64, 64, "f16", seed=requests)
+    out, lse = p.run(starts=None)
+    p.check(out, lse)
+    again, lse2 = p.run(starts=None)
+    assert torch.equal(out, again) and torch.equal(lse, lse2), "two runs differ"
+
+
+def test_scales_and_spreads():
+    """Peaked and flat rows, a negative and a zero scale, small and large stored values."""
+    for spread, magnitude, scale in ((30.0, 1.0, None), (1e-3, 1.0, None), (1.0, 1.0, -0.2), (1.0, 1.0, 0.0), (1.0, 1e-4, 300.0), (1.0, 3000.0, 1e-4)):
+        for dtype in ("bf16", "f16"):
+            p = Problem([50, 200], [1, 2], 1, 4, 64, 16, dtype, seed=11, spread=spread, magnitude=magnitude)
+            p.check(*p.run(scale=scale), scale=scale)
+
+
+def test_large_and_small_bf16_queries():
+    """bf16 queries outside fp16's range."""
+    for power in (-100, 100):
+        p = Problem([70], [1], 1, 4, 64, 16, "bf16", seed=12)
+        p.q = (p.q.float() * 2.0 ** power).bfloat16()
+        scale = 2.0 ** -power / 8
+        p.check(*p.run(scale=scale), scale=scale)
+
+
+def test_strided_queries_and_given_outputs():
+    import sparse_attention_indexer_lt_gb300 as lt
+    p = Problem([33, 100], [2, 3], 2, 4, 128, 16, "bf16", seed=4)
+    out, lse = p.run()
+    wide = torch.randn(5, 16 + 3, 128 + 8, device="cuda").bfloat16()
+    q = wide[:, 2:10, :128]
+    q.copy_(p.q)
+    given, given_lse = torch.empty_like(out), torch.empty_like(lse)
+    space = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    got, got_lse = p.run(q=q, out=given, out_lse=given_lse, workspace=space)
+    assert got.data_ptr() == given.data_ptr() and torch.equal(out, got) and torch.equal(lse, got_lse)
+    with pytest.raises(ValueError):
+        p.run(q=wide[:, 2:10, 4:132])  # not 16-byte aligned
+    with pytest.raises(ValueError):
+        p.run(workspace=space[:16])
+    with pytest.raises(ValueError):
+        p.run(starts=None)
+    with pytest.raises(ValueError):
+        p.run(out=given[:1])
+    with pytest.raises(ValueError):
+        p.run(window=-1)
+    with pytest.raises(TypeError):
+        p.run(q=q.float())
+    with pytest.raises(ValueError):
+        p.run(positions=torch.zeros(5, 0, dtype=torch.int32, device="cuda"))
+    assert lt.kv4_attention(q[:0], p.cache.cuda(), p.table.cuda(), torch.tensor([3, 3], dtype=torch.int32, device="cuda"),
+                            starts=torch.zeros(3, dtype=torch.int32, device="cuda")).shape == (0, 8, 128)
+
+
+def test_rows_past_the_last_request_are_not_touched():
+    p = Problem([40, 20], [2, 1], 1, 4, 64, 16, "bf16", seed=5)
+    q = torch.cat([p.q, p.q]).cuda()
+    out = torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    p.run(q=q, out=out, out_lse=lse)
+    assert (out[3:] == 7.0).all() and (lse[3:] == 7.0).all()
+    p.check(out[:3], lse[:3])
+
+
+@pytest.mark.parametrize("bad_page", [-1, -2 ** 31, 2 ** 31 - 1, None])
+def test_positions_on_pages_outside_the_cache_are_not_seen(bad_page):
+    p = Problem([100, 64], [3, 1], 1, 4, 128, 16, "bf16", seed=6)
+    p.table[0, 2] = p.cache.shape[0] if bad_page is None else bad_page
+    p.table[0, 6] = -1  # the last page, partly filled
+    p.check(*p.run())
+    pos = np.tile(np.arange(100), (4, 1))
+    p.positions = pos
+    p.check(*p.run())
+
+
+def test_nan_where_nothing_looks():
+    """NaN stored at positions that a row's mask hides leaves the row as it is; a row that sees one gets NaN
+    in that group (value) or everywhere (key)."""
+    for window in (0, 20):
+        p = Problem([70], [6], 1, 2, 128, 16, "bf16", seed=7)
+        clean, clean_lse = p.run(window=window)
+        nan = torch.tensor([0x7FFF], dtype=torch.int16).view(torch.uint8)
+
+        def poison(position, byte):
+            p.cache[p.table[0, position // 16], 0, position % 16, byte:byte + 2] = nan
+        poison(67, 128 + 8 + 2)      # value group 1 of position 67: queries 3, 4, 5 see it
+        poison(69, 128)              # key group 0 of position 69: the last query alone
+        if window:
+            poison(45, 128 + 8)      # value group 0 of position 45: queries 0 (position 64) sees it, later ones do not
+        out, lse = p.run(window=window)
+        first = 1 if window else 0
+        assert torch.equal(out[first:3], clean[first:3]) and torch.equal(lse[first:5], clean_lse[first:5])
+        if window:
+            assert torch.isnan(out[0, :, :32]).all() and torch.equal(out[0, :, 32:], clean[0, :, 32:])
+        assert torch.isnan(out[3:5, :, 32:64]).all()
+        assert torch.equal(out[3:5, :, :32], clean[3:5, :, :32]) and torch.equal(out[3:5, :, 64:], clean[3:5, :, 64:])
+        assert torch.isnan(out[5]).all() and torch.isnan(lse[5]).all()
+
+
+def test_cache_beyond_32_bit_offsets():
+    import sparse_attention_indexer_lt_gb300 as lt
+    page, heads, dim = 64, 1, 128
+    pages = (5 << 30) // (page * lt.kv4_row_bytes(dim))
+    cache = lt.kv4_cache(pages, heads, page, dim)
+    table = torch.tensor([[pages - 1, 3, pages - 7]], dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([150], dtype=torch.int32, device="cuda")
+    k, v = torch.randn(2, 150, heads, dim, device="cuda").half()
+    p = torch.arange(150, device="cuda")
+    slots = table[0].long()[p // page] * page + p % page
+    lt.kv4_store(k, v, cache, slots)
+    lk, lv = lt.kv4_load(cache, slots, dtype=torch.float32)
+    q = torch.randn(1, 4, dim, device="cuda").half()
+    for kw in ({}, {"positions": torch.arange(150, dtype=torch.int32, device="cuda")[None]}):
+        out = lt.kv4_attention(q, cache, table, lengths, **kw)
+        s = torch.einsum("hd,ld->hl", q[0].double(), lk[:, 0].double()) / dim ** 0.5
+        want = torch.softmax(s, -1) @ lv[:, 0].double()
+        assert (out[0].double() - want).abs().max() < 4e-3
+    del cache
+
+
+def test_streams_and_graphs():
+    import sparse_attention_indexer_lt_gb300 as lt
+    p = Problem([500, 90], [1, 1], 2, 4, 128, 16, "bf16", seed=9)
+    want, _ = p.run(starts=None)
+    q, cache, table = p.q.cuda(), p.cache.cuda(), p.table.cuda()
+    lengths = torch.tensor(p.lengths, dtype=torch.int32).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = lt.kv4_attention(q, cache, table, lengths, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    with torch.cuda.stream(side):
+        lt.kv4_attention(q, cache, table, lengths)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = lt.kv4_attention(q, cache, table, lengths)
+    lengths.copy_(torch.tensor([90, 33], dtype=torch.int32))
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, lt.kv4_attention(q, cache, table, lengths)) and not torch.equal(out, want)
+
+
+def test_injected_launch_failures():
+    import sparse_attention_indexer_lt_gb300 as lt
+    lib = lt.load()
+    p = Problem([50], [1], 1, 4, 64, 16, "bf16", seed=10)
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv, cache, slots = torch.zeros(1, 1, 64, device="cuda"), p.cache.cuda(), torch.zeros(1, dtype=torch.int64, device="cuda")
+    for call in (p.run, lambda: lt.kv4_store(kv, kv, cache, slots), lambda: lt.kv4_load(cache, slots),
+                 lambda: lt.page_release(z, z.bool(), z[None], z, z, 16), lambda: lt.page_extend(z, z, z[None], z, z, 16, 4)):
+        assert lib.lt_test_inject(1, 1) == 0
+        with pytest.raises(lt.LtError):
+            call()
+        call()
+    torch.cuda.synchronize()
+
+
+def test_a_serving_step_end_to_end():
+    """Extend, store, attend and release over several steps against a dense copy of what was stored."""
+    import sparse_attention_indexer_lt_gb300 as lt
+    torch.manual_seed(1)
+    n, page, width, heads, group, dim = 3, 16, 12, 2, 4, 128
+    cache = lt.kv4_cache(n * width, heads, page, dim)
+    table = torch.full((n, width), -1, dtype=torch.int32, device="cuda")
+    free = torch.randperm(n * width).int().cuda()
+    num_free = torch.tensor([n * width], dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(n, dtype=torch.int32, device="cuda")
+    kept = [([], []) for _ in range(n)]
+    for new in ([40, 1, 7], [1, 1, 1], [0, 5, 1], [1, 30, 2]):
+        tokens = sum(new) + 2  # two rows of padding
+        k, v = torch.randn(2, tokens, heads, dim, device="cuda").bfloat16()
+        q = torch.randn(tokens, heads * group, dim, device="cuda").bfloat16()
+        step = lt.page_extend(lengths, torch.tensor(new, dtype=torch.int32).cuda(), table, free, num_free, page, tokens)
+        lt.kv4_store(k, v, cache, step.slots)
+        out = lt.kv4_attention(q, cache, table, step.lengths, starts=step.starts, max_new=max(new))
+        lk, lv = lt.kv4_load(cache, step.slots, dtype=torch.float32)
+        lengths, num_free = step.lengths, step.num_free
+        at = 0
+        for r, count in enumerate(new):
+            kept[r][0].append(lk[at:at + count])
+            kept[r][1].append(lv[at:at + count])
+            kk, vv = torch.cat(kept[r][0]).double(), torch.cat(kept[r][1]).double()
+            for i in range(count):
+                upto = len(kk) - count + i + 1
+                for h in range(heads * group):
+                    s = kk[:upto, h // group] @ q[at + i, h].double() / dim ** 0.5
+                    want = torch.softmax(s, -1) @ vv[:upto, h // group]
+                    assert (out[at + i, h].double() - want).abs().max() < 3e-2
+            at += count
+    before = int(num_free)
+    lengths, num_free = lt.page_release(lengths, torch.tensor([True, False, True], device="cuda"), table, free, num_free, page)
+    held = [-(-sum(x) // page) for x in ([40, 1, 0, 1], [7, 1, 1, 2])]
+    assert int(num_free) == before + sum(held) and lengths.tolist() == [0, 37, 0]
