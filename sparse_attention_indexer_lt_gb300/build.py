@@ -18,7 +18,7 @@ BUILD = PKG / "_build"
 LIB = PKG / "liblt_topk.so"
 SOURCES = ["lt_api.cu", "lt_topk_kernels.cu", "lt_stream_kernels.cu", "lt_blocked_256_f32.cu",
            "lt_blocked_256_bf16.cu", "lt_blocked_512_f32.cu", "lt_blocked_512_bf16.cu", "lt_listed_kernels.cu", "lt_compress.cu",
-           "lt_pages.cu", "lt_kv4_cache.cu", "lt_kv4_attention.cu"]
+           "lt_pages.cu", "lt_kv4_cache.cu", "lt_kv4_attention.cu", "lt_kv4_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", f"-I{INCLUDE}"]
 

@@ -29,6 +29,7 @@
 
 #include "lt_kv4.cuh"
 #include "lt_kv4_attention.cuh"
+#include "lt_kv4_prefill.h"
 
 namespace {
 
@@ -86,71 +87,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Which request and chunk this CTA has: the requests' positions cut into chunks of one size, flat.
-struct Place {
-  int request, split, base, count;  // count chunks, the first with flat number base
-  int chunk;                        // positions of a chunk
-};
-
-// The requests' spans add up to `total`; with about `target` chunks wanted, a chunk has
-// total / target positions (a multiple of kTile, min_chunk at least) and request r has
-// ceil(span / chunk) of them: ragged requests come out as chunks of like work, which
-// the hardware hands to SMs as they fall free. Every CTA computes this from the
-// lengths alone.
-__device__ bool find_place(const AttentionParams& p, int flat, Place* out, int64_t* sums, Place* found) {
-  const int tid = threadIdx.x;
-  if (tid == 0) found->request = -1;
-  int64_t mine = 0;
-  for (int r = tid; r < p.requests; r += kThreads) mine += request_of(p, r).span;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(~0u, mine, d);
-  if ((tid & 31) == 0) sums[tid >> 5] = mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sums[w];
-  int64_t chunk = (total + p.target - 1) / p.target;
-  chunk = (chunk + kTile - 1) / kTile * kTile;
-  if (chunk < p.min_chunk) chunk = p.min_chunk;
-  int base = 0;
-  for (int first = 0; first < p.requests; first += kThreads) {
-    const int r = first + tid;
-    int n = 0;
-    if (r < p.requests) {
-      const Request q = request_of(p, r);
-      n = q.queries > 0 ? max(1, (int)((q.span + chunk - 1) / chunk)) : 0;
-    }
-    int end = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(~0u, end, d);
-      if ((tid & 31) >= d) end += u;
-    }
-    __syncthreads();
-    if ((tid & 31) == 31) sums[tid >> 5] = end;
-    __syncthreads();
-    int all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < (tid >> 5)) end += (int)sums[w];
-      all += (int)sums[w];
-    }
-    const int begin = base + end - n;
-    if (flat >= begin && flat < begin + n) {
-      found->request = r;
-      found->split = flat - begin;
-      found->base = begin;
-      found->count = n;
-    }
-    base += all;
-    if (base > flat) break;  // (the same for all threads)
-  }
-  __syncthreads();
-  *out = *found;
-  out->chunk = (int)(chunk > INT32_MAX ? INT32_MAX / kTile * kTile : chunk);
-  return out->request >= 0;
-}
-
 template <int D, int NT, bool kList>
 __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(AttentionParams p) {
   using Sh = Shape<D, NT>;
@@ -196,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
     __syncthreads();
   } else {
     Place pl;
-    if (!find_place(p, flat, &pl, sums, &found)) return;
+    if (!find_place<kThreads>(p, flat, &pl, sums, &found)) return;
     request = pl.request;
     rq = request_of(p, request);
     count = pl.count;
@@ -647,7 +583,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionParams p, i
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
-bool g_smem_set[kMaxDevices][3][3][2];
+bool g_smem_set[kMaxDevices][3][4][2];  // by head size, row tiles (3: many rows), listed
 
 struct RowsKernel {
   const void* func;
@@ -668,7 +604,8 @@ RowsKernel rows_kernel_of(int d, int nt, bool list) {
 
 // The launch for these sizes: row tiles, parts and workspace.
 struct Plan {
-  int nt, row_tiles;
+  bool prefill;        // the kernel for many query rows
+  int nt, row_tiles, cta_rows;
   int target;        // dense: chunks wanted over all requests; listed: parts of a list
   int min_chunk;
   int64_t flats;     // chunks at most
@@ -678,13 +615,37 @@ struct Plan {
 };
 
 constexpr int kMinChunk = 256;
+constexpr int kPrefillMinChunk = 512;
+constexpr int kPrefillFrom = 64;  // query rows a kv head from which the kernel for many rows is taken
+
+Plan finish_plan(Plan a, int heads, int d, int requests) {
+  // (a chunk is at least total / target long, so the requests have at most target + requests)
+  if (a.flats == 0) a.flats = a.target == 1 ? requests : a.target + (int64_t)requests;
+  a.join = a.target > 1;
+  const int64_t part_rows = a.flats * heads * a.row_tiles * a.cta_rows;
+  a.plan_bytes = ((int64_t)requests * 8 + 15) / 16 * 16;
+  a.lse_bytes = (part_rows * 4 + 15) / 16 * 16;
+  a.o_bytes = part_rows * d * 4;
+  return a;
+}
 
 Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int requests, int max_new, int list_len) {
   Plan a = {};
   const int64_t rows = (int64_t)(list_len > 0 ? 1 : max_new) * group;
+  a.prefill = list_len == 0 && d <= 128 && rows >= kPrefillFrom;
+  if (a.prefill) {
+    a.cta_rows = kPrefillRows;
+    a.row_tiles = (int)((rows + kPrefillRows - 1) / kPrefillRows);
+    a.min_chunk = kPrefillMinChunk;
+    // one CTA an SM; two waves of chunks where the row tiles alone are fewer
+    const int64_t units = (int64_t)heads * a.row_tiles;
+    a.target = (int)((2 * sms + units - 1) / units);
+    return finish_plan(a, heads, d, requests);
+  }
   const int most = d == 256 ? 2 : 4;
   a.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : most;
   if (a.nt > most) a.nt = most;
+  a.cta_rows = a.nt * 8;
   a.row_tiles = (int)((rows + a.nt * 8 - 1) / (a.nt * 8));
   a.min_chunk = kMinChunk;
   const int slots = sms * rows_kernel_of(d, a.nt, list_len > 0).per_sm;
@@ -696,19 +657,12 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
     parts = parts > tiles ? tiles : parts;
     a.target = (int)(parts < 1 ? 1 : parts);
     a.flats = tokens * a.target;
-    a.join = a.target > 1;
   } else {
     // several chunks a slot, so that the last ones to end are short
     int64_t target = ((int64_t)slots * 6 + units - 1) / units;
     a.target = (int)(target < 1 ? 1 : target);
-    a.flats = a.target == 1 ? requests : a.target + (int64_t)requests;
-    a.join = a.target > 1;
   }
-  const int64_t part_rows = a.flats * units * a.nt * 8;
-  a.plan_bytes = ((int64_t)requests * 8 + 15) / 16 * 16;
-  a.lse_bytes = (part_rows * 4 + 15) / 16 * 16;
-  a.o_bytes = part_rows * d * 4;
-  return a;
+  return finish_plan(a, heads, d, requests);
 }
 
 lt_status device_of(int* dev, int* sms) {
@@ -776,6 +730,10 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
   }
   if (st != LT_OK || pages > INT32_MAX) return LT_ERR_UNSUPPORTED;
   if (tokens == 0 || requests == 0) return LT_OK;
+  // a window as wide as the table holds every position; the kernels' sums of
+  // positions, queries and window stay within 32 bits
+  if (((int64_t)table_width << shift) <= window) window = 0;
+  if ((int64_t)window + tokens >= INT32_MAX) return LT_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   st = device_of(&dev, &sms);
   if (st != LT_OK) return st;
@@ -819,23 +777,27 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
   p.scale_log2 = scale * 1.4426950408889634f;
 
   const bool list = list_len > 0;
-  const RowsKernel k = rows_kernel_of(head_dim, plan.nt, list);
+  RowsKernel k = {};
+  if (plan.prefill)
+    k.func = prefill_kernel_ptr(head_dim, &k.smem);
+  else
+    k = rows_kernel_of(head_dim, plan.nt, list);
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    bool& set = g_smem_set[dev][head_dim / 128][plan.nt / 2][list];
+    bool& set = g_smem_set[dev][head_dim / 128][plan.prefill ? 3 : plan.nt / 2][list];
     if (!set) {
       if (cudaFuncSetAttribute(k.func, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess)
         return LT_ERR_CUDA;
       set = true;
     }
   }
-  st = launch(k.func, dim3((unsigned)grid), kThreads, (unsigned)k.smem, &p, stream);
+  st = launch(k.func, dim3((unsigned)grid), plan.prefill ? kPrefillThreads : kThreads, (unsigned)k.smem, &p, stream);
   if (st != LT_OK || !plan.join) return st;
   if (lt::take_injected_failure()) return LT_ERR_CUDA;
   const void* func = head_dim == 64    ? reinterpret_cast<const void*>(&join_kernel<64>)
                      : head_dim == 128 ? reinterpret_cast<const void*>(&join_kernel<128>)
                                        : reinterpret_cast<const void*>(&join_kernel<256>);
-  int rows_per_cta = plan.nt * 8, listed = list;
+  int rows_per_cta = plan.cta_rows, listed = list;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)joins);
   cfg.blockDim = dim3(kJoinThreads);

@@ -59,6 +59,72 @@ __device__ __forceinline__ Request request_of(const AttentionParams& p, int r) {
   return q;
 }
 
+// Which request and chunk this CTA has: the requests' positions cut into chunks of one size, flat.
+struct Place {
+  int request, split, base, count;  // count chunks, the first with flat number base
+  int chunk;                        // positions of a chunk
+};
+
+// The requests' spans add up to `total`; with about `target` chunks wanted, a chunk has
+// total / target positions (a multiple of kTile, min_chunk at least) and request r has
+// ceil(span / chunk) of them: ragged requests come out as chunks of like work, which
+// the hardware hands to SMs as they fall free. Every CTA computes this from the
+// lengths alone.
+template <int kCta>
+__device__ __forceinline__ bool find_place(const AttentionParams& p, int flat, Place* out, int64_t* sums, Place* found) {
+  const int tid = threadIdx.x;
+  if (tid == 0) found->request = -1;
+  int64_t mine = 0;
+  for (int r = tid; r < p.requests; r += kCta) mine += request_of(p, r).span;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(~0u, mine, d);
+  if ((tid & 31) == 0) sums[tid >> 5] = mine;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll 4
+  for (int w = 0; w < kCta / 32; ++w) total += sums[w];
+  int64_t chunk = (total + p.target - 1) / p.target;
+  chunk = (chunk + kTile - 1) / kTile * kTile;
+  if (chunk < p.min_chunk) chunk = p.min_chunk;
+  int base = 0;
+  for (int first = 0; first < p.requests; first += kCta) {
+    const int r = first + tid;
+    int n = 0;
+    if (r < p.requests) {
+      const Request q = request_of(p, r);
+      n = q.queries > 0 ? max(1, (int)((q.span + chunk - 1) / chunk)) : 0;
+    }
+    int end = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(~0u, end, d);
+      if ((tid & 31) >= d) end += u;
+    }
+    __syncthreads();
+    if ((tid & 31) == 31) sums[tid >> 5] = end;
+    __syncthreads();
+    int all = 0;
+#pragma unroll 4
+    for (int w = 0; w < kCta / 32; ++w) {
+      if (w < (tid >> 5)) end += (int)sums[w];
+      all += (int)sums[w];
+    }
+    const int begin = base + end - n;
+    if (flat >= begin && flat < begin + n) {
+      found->request = r;
+      found->split = flat - begin;
+      found->base = begin;
+      found->count = n;
+    }
+    base += all;
+    if (base > flat) break;  // (the same for all threads)
+  }
+  __syncthreads();
+  *out = *found;
+  out->chunk = (int)(chunk > INT32_MAX ? INT32_MAX / kTile * kTile : chunk);
+  return out->request >= 0;
+}
+
 // The request that a query row belongs to; -1 past the last.
 __device__ __forceinline__ int owner_of_token(const AttentionParams& p, int token) {
   if (p.starts == nullptr) return token < p.requests ? token : -1;
@@ -91,21 +157,13 @@ __device__ __forceinline__ uint32_t nan_halves(uint32_t h) {
   return ((h & 0x7FFFu) > 0x7C00u ? 0xFFFFu : 0u) | ((h & 0x7FFF0000u) > 0x7C000000u ? 0xFFFF0000u : 0u);
 }
 
-// A row's eight-channel pieces, bf16 pairs spread over the four lanes of equal lane / 4, become fp16
-// pairs: times the power of two that brings the row's largest into [2^14, 2^15), so
-// nothing overflows and what lies within 2^-28 of the largest stays exact. Returns
-// the inverse of that power.
+// bf16 pairs of a row whose largest magnitude has the fp32 word `big`, made fp16 pairs: times the power
+// of two that brings the largest into [2^14, 2^15), so nothing overflows and what lies
+// within 2^-28 of the largest stays exact. Returns the inverse of that power. Rows of zeros,
+// or with an infinity or NaN, are taken as they are.
 template <int N>
-__device__ __forceinline__ float bf16_row_to_half(uint32_t (&w)[N][4]) {
-  uint32_t big = 0;
-#pragma unroll
-  for (int j = 0; j < N; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) big = max(big, max(w[j][i] << 16 & 0x7FFF0000u, w[j][i] & 0x7FFF0000u));
-  big = max(big, __shfl_xor_sync(~0u, big, 1));
-  big = max(big, __shfl_xor_sync(~0u, big, 2));
-  const int e = (int)(big >> 23);  // biased exponent of the largest
-  // zero rows and rows with an infinity or NaN are taken as they are
+__device__ __forceinline__ float bf16_to_half_scaled(uint32_t (&w)[N][4], uint32_t big) {
+  const int e = (int)(big >> 23);  // biased exponent
   const int up = e == 0 || e == 255 ? 127 : min(268 - e, 253);
   const float mul = __uint_as_float((uint32_t)up << 23);
 #pragma unroll
@@ -116,6 +174,28 @@ __device__ __forceinline__ float bf16_row_to_half(uint32_t (&w)[N][4]) {
       asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j][i]) : "f"(hi), "f"(lo));
     }
   return __uint_as_float((uint32_t)(254 - up) << 23);
+}
+template <int N>
+__device__ __forceinline__ uint32_t largest_word(const uint32_t (&w)[N][4]) {
+  uint32_t big = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) big = max(big, max(w[j][i] << 16 & 0x7FFF0000u, w[j][i] & 0x7FFF0000u));
+  return big;
+}
+// A whole row in one thread.
+template <int N>
+__device__ __forceinline__ float bf16_words_to_half(uint32_t (&w)[N][4]) {
+  return bf16_to_half_scaled<N>(w, largest_word<N>(w));
+}
+// A row's pieces spread over the four lanes of equal lane / 4.
+template <int N>
+__device__ __forceinline__ float bf16_row_to_half(uint32_t (&w)[N][4]) {
+  uint32_t big = largest_word<N>(w);
+  big = max(big, __shfl_xor_sync(~0u, big, 1));
+  big = max(big, __shfl_xor_sync(~0u, big, 2));
+  return bf16_to_half_scaled<N>(w, big);
 }
 
 // Four outputs, rounded once.

@@ -285,6 +285,41 @@ def test_many_query_rows():
     p.check(*p.run())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,lengths,new,group,window", [
+    (64, [64], [64], 1, 0), (128, [64], [64], 1, 0), (64, [130], [100], 2, 0), (128, [300], [129], 1, 0), (128, [129, 5, 400], [70, 0, 33], 5, 0),
+    (64, [700, 90, 1], [100, 90, 1], 3, 50), (128, [640], [90], 3, 200), (64, [1500], [40], 4, 0), (128, [50], [80], 4, 0)])
+def test_prefill(dim, lengths, new, group, window, dtype):
+    """Many query rows a request: one and two row tiles, ragged ends, windows, requests cut into parts, more
+    queries than positions."""
+    p = Problem(lengths, new, 2, group, dim, 16, dtype, seed=sum(lengths) + dim, extra_width=1)
+    out, lse = p.run(window=window)
+    p.check(out, lse, window=window)
+    again, _ = p.run(window=window)
+    assert torch.equal(out, again), "two runs differ"
+
+
+def test_prefill_scales_and_bad_pages():
+    for spread, magnitude, scale in ((30.0, 1.0, None), (1.0, 1.0, -0.2), (1.0, 1.0, 0.0), (1.0, 1e-4, 300.0), (1.0, 3000.0, 1e-4)):
+        p = Problem([300], [40], 1, 4, 64, 16, "bf16", seed=21, spread=spread, magnitude=magnitude)
+        p.table[0, 3] = -1
+        p.table[0, 17] = 2 ** 31 - 1
+        p.check(*p.run(scale=scale), scale=scale)
+
+
+def test_prefill_nan_where_nothing_looks():
+    p = Problem([200], [80], 1, 2, 128, 16, "bf16", seed=22)
+    clean, clean_lse = p.run()
+    nan = torch.tensor([0x7FFF], dtype=torch.int16).view(torch.uint8)
+    for position, byte in ((150, 128 + 8 + 2), (199, 128)):  # value group 1 of position 150, key group 0 of the last
+        p.cache[p.table[0, position // 16], 0, position % 16, byte:byte + 2] = nan
+    out, lse = p.run()
+    assert torch.equal(out[:30], clean[:30]) and torch.equal(lse[:79], clean_lse[:79])
+    assert torch.isnan(out[30:79, :, 32:64]).all()
+    assert torch.equal(out[30:79, :, :32], clean[30:79, :, :32]) and torch.equal(out[30:79, :, 64:], clean[30:79, :, 64:])
+    assert torch.isnan(out[79]).all() and torch.isnan(lse[79]).all()
+
+
 @pytest.mark.parametrize("dim,heads,group,list_len", [(64, 2, 4, 1), (128, 1, 16, 33), (128, 2, 8, 512), (256, 1, 4, 100), (128, 1, 40, 130)])
 def test_listed(dim, heads, group, list_len):
     rng = np.random.default_rng(list_len)
