@@ -140,8 +140,17 @@ __device__ __forceinline__ int owner_of_token(const AttentionParams& p, int toke
   return lo;
 }
 
+// One poll without a time to suspend for: a phase that is complete already, the usual case of a ring that
+// runs ahead, is seen at once.
+__device__ __forceinline__ bool mbar_ready(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
 // Waits for a phase, a bounded number of polls; false if it gave up.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
+  if (mbar_ready(bar, parity)) return true;
   for (uint32_t i = 0; i < kWaitPolls; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return false;

@@ -5,16 +5,15 @@
 // range of positions in tiles of 128, with one role a warpgroup:
 //   warpgroups 0 and 1  softmax of row tile A and B: logits from tensor memory,
 //                       weights back into it as fp16, where the second product reads them
-//   warpgroup 2         unpacks: each of its warps brings 32 positions of a tile by bulk
-//                       copies, a thread turns one position's codes into fp16 keys and
+//   warpgroup 2         unpacks: a thread turns one position's codes into fp16 keys and
 //                       values, written with the 128-byte swizzle that the tensor core reads
-//   warpgroup 3         one thread issues the products
+//   warpgroup 3         one warp issues the products, another the bulk copies of packed rows
 // in the order  S_A(i) = Q_A K(i)^T,  O_B += P_B(i-1) V(i-1),  S_B(i),  O_A += P_A(i) V(i): while one row
 // tile's softmax runs, the tensor core has the other's two products.
 //
 // Keys are laid out channels inner (K-major), values are the same bytes read as
 // the transposed operand (their channels are the product's N). Unpacked tiles live in a
-// ring of three; the packed rows' pitch is an odd multiple of 16 bytes, so eight threads
+// ring of four; the packed rows' pitch is an odd multiple of 16 bytes, so eight threads
 // reading 16 bytes of eight rows touch all banks, and the swizzle does the same
 // for their stores.
 //
@@ -37,8 +36,8 @@ using namespace lt::kv4;
 
 constexpr int kCta = 512;
 constexpr int kTok = 128;    // positions of a tile
-constexpr int kSlots = 3;    // unpacked key or value tiles in shared memory
-constexpr int kRaw = 2;      // packed tiles a warp has in flight
+constexpr int kSlots = 4;    // unpacked key or value tiles in shared memory
+constexpr int kRaw = 1;      // packed tiles in shared memory: rows go on to registers, so the next one comes meanwhile
 constexpr float kShift = 6.0f;
 constexpr float kSlack = 8.0f;  // how far logits may pass the maximum (log 2) before it moves
 
@@ -49,17 +48,17 @@ struct Smem {
   static constexpr int kOperand = kHalf * (D / 64);
   static constexpr int kQ = 0;                           // two row tiles
   static constexpr int kKv = kQ + 2 * kOperand;          // kSlots
-  static constexpr int kPacked = kKv + kSlots * kOperand;  // [warp][kRaw][32 rows]
-  static constexpr int kBars = kPacked + 4 * kRaw * 32 * kRow;
+  static constexpr int kPacked = kKv + kSlots * kOperand;  // [kRaw][128 rows]
+  static constexpr int kBars = kPacked + kRaw * kTok * kRow;
   static constexpr int kTotal = kBars + 2048 + 1024;     // (slack to align the start to 1024)
 };
 
 struct Shared {
-  uint64_t packed_full[4][kRaw];
+  uint64_t packed_full[kRaw], packed_empty[kRaw];
   uint64_t kv_full[kSlots], kv_empty[kSlots];
-  uint64_t q_full, s_full[2], p_full[2], o_full[2];
-  uint32_t valid[4][4];      // [tile mod 4][warp]: positions on a page of the cache and in range
-  uint32_t nan_rows[4][4];   // positions with a NaN value scale
+  uint64_t q_full, s_full[2], p_full[2][2], o_full[2];
+  uint4 valid[4];            // [tile mod 4]: positions on a page of the cache and in range, as bits
+  uint4 nan_rows[4];         // positions with a NaN value scale
   uint8_t nan_groups[4][kTok];
   int64_t sums[kCta / 32];
   Place found;
@@ -84,16 +83,27 @@ __device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t next_c
 __device__ __forceinline__ constexpr uint32_t instruction(int n, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+// The issuing warp runs these as a whole, so that descriptors stay in uniform registers; `lead` is set in
+// one lane, which issues.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+               " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-               :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+               " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+               :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead) : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(lt::smem_u32(bar)) : "memory");
+__device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t lead) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
+               " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+               :: "r"(lt::smem_u32(bar)), "r"(lead) : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t lead;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(lead));
+  return lead;
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -143,8 +153,8 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 // Waits for a phase; gives up after kWaitPolls, or as soon as another thread has.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Shared* sh) {
   for (uint32_t i = 0; i < lt::kWaitPolls; ++i) {
-    if (lt::mbar_try_wait(bar, parity)) return true;
-    if (*(volatile int*)&sh->abort) return false;
+    if (i == 0 ? mbar_ready(bar, parity) : lt::mbar_try_wait(bar, parity)) return true;
+    if (i > 0 && *(volatile int*)&sh->abort) return false;
   }
   *(volatile int*)&sh->abort = 1;
   return false;
@@ -233,12 +243,15 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
     float* s = reinterpret_cast<float*>(raw);
 #pragma unroll
     for (int c = 0; c < kTok; c += 32) tmem_ld32(s_at + c, raw + c);
+    const uint4 valid4 = sh->valid[i & 3], nan4 = sh->nan_rows[i & 3];
+    const int pos0 = job.from + i * kTok;
+    const bool whole = (valid4.x & valid4.y & valid4.z & valid4.w) == ~0u && pos0 + kTok <= limit && pos0 >= low;
+    const bool clean = (nan4.x | nan4.y | nan4.z | nan4.w) == 0;
+    const bool plain = __all_sync(~0u, whole && clean);
     tmem_wait_ld();
 
-    const int pos0 = job.from + i * kTok;
-    const uint32_t* valid = sh->valid[i & 3];
-    const bool whole = (valid[0] & valid[1] & valid[2] & valid[3]) == ~0u && pos0 + kTok <= limit && pos0 >= low;
-    if (!__all_sync(~0u, whole)) {
+    const uint32_t valid[4] = {valid4.x, valid4.y, valid4.z, valid4.w};
+    if (!plain) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         // visible: [low, limit) of this row, as bits of the 32 positions
@@ -251,10 +264,14 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
           if (!((see >> c) & 1u)) s[32 * w + c] = -INFINITY;
       }
     }
-    if (sh->nan_rows[i & 3][0] | sh->nan_rows[i & 3][1] | sh->nan_rows[i & 3][2] | sh->nan_rows[i & 3][3]) {
-      for (int t = 0; t < kTok; ++t)
-        if ((sh->nan_rows[i & 3][t >> 5] >> (t & 31)) & 1u)
-          if (((valid[t >> 5] >> (t & 31)) & 1u) && pos0 + t < limit && pos0 + t >= low) poison |= sh->nan_groups[i & 3][t];
+    if (!clean) {
+      const uint32_t nan_rows[4] = {nan4.x, nan4.y, nan4.z, nan4.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        for (uint32_t left = nan_rows[w] & valid[w]; left != 0; left &= left - 1) {
+          const int t = 32 * w + __ffs(left) - 1;
+          if (pos0 + t < limit && pos0 + t >= low) poison |= sh->nan_groups[i & 3][t];
+        }
     }
 
     float top = s[0], top2 = s[1], top3 = s[2], top4 = s[3];
@@ -305,10 +322,10 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(x1), "f"(x0));
       }
       tmem_st32(s_at + 32 * h, pk);
+      tmem_wait_st();
+      fence_before();
+      arrive(&sh->p_full[which][h]);  // the second product starts on the first half
     }
-    tmem_wait_st();
-    fence_before();
-    arrive(&sh->p_full[which]);
   }
   ok = wait_or_abort(&sh->o_full[which], 0, sh) && ok;
   fence_after();
@@ -353,55 +370,93 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   }
 }
 
+// ---- packed rows into shared memory: one warp, a bulk copy for each run of positions on a page
+template <int D>
+__device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& job, Shared* sh, uint8_t* smem) {
+  constexpr int kRow = row_bytes(D);
+  constexpr int kMost = kTok / 32;  // runs of a lane, at pages of one position
+  const int lane = threadIdx.x & 31;
+  const uint32_t packed_at = lt::smem_u32(smem + Smem<D>::kPacked);
+  const int run_shift = min(p.shift, 7), runs = kTok >> run_shift;
+  const int32_t* table = p.table + (int64_t)job.request * p.width;
+  int page[kMost];
+  auto look_up = [&](int tile) {
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      const int run = lane + 32 * j, at = job.from + tile * kTok + (run << run_shift);
+      page[j] = tile < job.tiles && run < runs && at < job.to ? __ldg(table + (at >> p.shift)) : -1;
+    }
+  };
+  look_up(0);
+  int stage = 0;
+  uint32_t parity = 1;  // (the first round's stages are free)
+  for (int i = 0; i < job.tiles; ++i) {
+    if (!wait_or_abort(&sh->packed_empty[stage], parity, sh)) break;
+    uint32_t valid[4] = {0u, 0u, 0u, 0u};
+    int count[kMost];
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      const int first = (lane + 32 * j) << run_shift, left = job.to - (job.from + i * kTok + first);
+      count[j] = page[j] >= 0 && page[j] < p.pages ? min(left, 1 << run_shift) : 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int a = min(max(first - 32 * w, 0), 32), b = min(max(first + count[j] - 32 * w, 0), 32);
+        valid[w] |= a < b ? (b == 32 ? ~0u : (1u << b) - 1u) & (~0u << a) : 0u;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) valid[w] = __reduce_or_sync(~0u, valid[w]);
+    if (lane == 0) {
+      sh->valid[i & 3] = make_uint4(valid[0], valid[1], valid[2], valid[3]);
+      lt::mbar_arrive_tx(&sh->packed_full[stage],
+                         (uint32_t)(__popc(valid[0]) + __popc(valid[1]) + __popc(valid[2]) + __popc(valid[3])) * kRow);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kMost; ++j) {
+      const int first = (lane + 32 * j) << run_shift, at = job.from + i * kTok + first;
+      if (count[j] > 0) {
+        const uint8_t* src = p.cache + (((((int64_t)page[j] * p.heads + job.head) << p.shift) + (at & ((1 << p.shift) - 1))) * kRow);
+        bulk_in(packed_at + (stage * kTok + first) * kRow, src, (uint32_t)count[j] * kRow, &sh->packed_full[stage]);
+      }
+    }
+    look_up(i + 1);
+    if (++stage == kRaw) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
+}
+
 // ---- unpacking: a thread a position
 template <int D>
-__device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job& job, Shared* sh, uint8_t* smem) {
+__device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t* smem) {
   constexpr int kRow = row_bytes(D);
   constexpr int kGroups = D / 32;
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = warp * 32 + lane;
-  uint8_t* packed = smem + Smem<D>::kPacked + warp * kRaw * 32 * kRow;
-  const uint32_t packed_at = lt::smem_u32(packed);
-  const int run_shift = min(p.shift, 5);
-  const int32_t* table = p.table + (int64_t)job.request * p.width;
-  int next_pos, next_count, next_page;
-  auto look_up = [&](int tile) {
-    next_pos = job.from + tile * kTok + warp * 32 + (lane << run_shift);
-    next_count = tile < job.tiles && (lane << run_shift) < 32 ? max(0, min(job.to - next_pos, 1 << run_shift)) : 0;
-    next_page = next_count > 0 ? __ldg(table + (next_pos >> p.shift)) : -1;
-  };
-  uint32_t valid_of[kRaw];
-  auto bring = [&](int tile, int stage) {
-    if (next_page < 0 || next_page >= p.pages) next_count = 0;
-    const uint32_t mine = next_count > 0 ? ((next_count == 32 ? ~0u : (1u << next_count) - 1u) << ((lane << run_shift) & 31)) : 0u;
-    const uint32_t valid = __reduce_or_sync(~0u, mine);
-    if (stage == 0) valid_of[0] = valid; else valid_of[1] = valid;
-    if (lane == 0) lt::mbar_arrive_tx(&sh->packed_full[warp][stage], (uint32_t)__popc(valid) * kRow);
-    __syncwarp();
-    if (next_count > 0) {
-      const uint8_t* src = p.cache + (((((int64_t)next_page * p.heads + job.head) << p.shift) + (next_pos & ((1 << p.shift) - 1))) * kRow);
-      bulk_in(packed_at + (stage * 32 + (lane << run_shift)) * kRow, src, (uint32_t)next_count * kRow, &sh->packed_full[warp][stage]);
-    }
-    look_up(tile + 1);
-  };
-  look_up(0);
+  uint32_t chunk_at[8];  // where the row's eight 16-byte chunks lie in a swizzled 128-byte row
 #pragma unroll
-  for (int s = 0; s < kRaw; ++s)
-    if (s < job.tiles) bring(s, s);
-
+  for (int c = 0; c < 8; ++c) chunk_at[c] = lt::smem_u32(smem + Smem<D>::kKv) + row * 128 + ((c ^ (row & 7)) << 4);
   int slot = 0;
   uint32_t slot_parity = 1;  // (the first round's slots are free)
   bool ok = true;
   for (int i = 0; i < job.tiles && ok; ++i) {
-    const int stage = i & 1;
-    ok = wait_or_abort(&sh->packed_full[warp][stage], (i >> 1) & 1, sh);
+    const int stage = i % kRaw;
+    ok = wait_or_abort(&sh->packed_full[stage], (i / kRaw) & 1, sh);
     if (!ok) break;
-    const uint32_t valid = stage == 0 ? valid_of[0] : valid_of[1];
+    const uint4 valid4 = sh->valid[i & 3];
+    const uint32_t valid = warp == 0 ? valid4.x : warp == 1 ? valid4.y : warp == 2 ? valid4.z : valid4.w;
     const bool there = (valid >> lane) & 1u;
-    const uint8_t* from = packed + (stage * 32 + lane) * kRow;
-    // scales, fp16 pairs: keys, then values; a position that is not there counts as zeros
+    const uint8_t* from = smem + Smem<D>::kPacked + (stage * kTok + row) * kRow;
+    // the row's codes and scales (fp16 pairs: keys, then values; a position that is not there counts as zeros)
+    uint4 codes[D / 16];
     uint32_t sc[kGroups];
 #pragma unroll
+    for (int g = 0; g < D / 16; ++g) codes[g] = reinterpret_cast<const uint4*>(from)[g];
+#pragma unroll
     for (int g = 0; g < kGroups; ++g) sc[g] = there ? reinterpret_cast<const uint32_t*>(from + D)[g] : 0u;
+    __syncwarp();  // every lane has read the stage
+    if (lane == 0) arrive(&sh->packed_empty[stage]);
     uint32_t nan = 0;
 #pragma unroll
     for (int g = 0; g < kGroups / 2; ++g) {
@@ -410,19 +465,16 @@ __device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job&
       nan |= ((n & 1u) | ((n >> 15) & 2u)) << (2 * g);
     }
     const uint32_t nan_rows = __ballot_sync(~0u, nan != 0);
-    if (lane == 0) {
-      sh->valid[i & 3][warp] = valid;
-      sh->nan_rows[i & 3][warp] = nan_rows;
-    }
+    if (lane == 0) reinterpret_cast<uint32_t*>(&sh->nan_rows[i & 3])[warp] = nan_rows;
     if (nan_rows) sh->nan_groups[i & 3][row] = (uint8_t)nan;
 #pragma unroll
     for (int part = 0; part < 2; ++part) {  // keys, then values
       ok = ok && wait_or_abort(&sh->kv_empty[slot], slot_parity, sh);
       if (!ok) break;
-      uint8_t* to = smem + Smem<D>::kKv + slot * Smem<D>::kOperand + row * 128;
+      const uint32_t to = slot * Smem<D>::kOperand;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
-        const uint4 v = *reinterpret_cast<const uint4*>(from + part * (D / 2) + g * 16);
+        const uint4 v = codes[part * kGroups + g];
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         const uint32_t pair = sc[part * (kGroups / 2) + g / 2];
         const uint32_t scale = __byte_perm(pair, 0, g & 1 ? 0x3232 : 0x1010);
@@ -430,9 +482,9 @@ __device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job&
         for (int j = 0; j < 4; ++j) {
           uint32_t h[4];
           codes_to_half2(w[j], h);
-          const uint4 x = make_uint4(hmul2(h[0], scale), hmul2(h[1], scale), hmul2(h[2], scale), hmul2(h[3], scale));
-          const int chunk = (g & 1) * 4 + j;
-          *reinterpret_cast<uint4*>(to + (g / 2) * Smem<D>::kHalf + ((chunk ^ (row & 7)) << 4)) = x;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                       :: "r"(chunk_at[(g & 1) * 4 + j] + to + (g / 2) * Smem<D>::kHalf), "r"(hmul2(h[0], scale)),
+                          "r"(hmul2(h[1], scale)), "r"(hmul2(h[2], scale)), "r"(hmul2(h[3], scale)) : "memory");
         }
       }
       fence_async();
@@ -442,17 +494,15 @@ __device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job&
         slot_parity ^= 1u;
       }
     }
-    __syncwarp();  // every lane has read the stage
-    if (i + kRaw < job.tiles) bring(i + kRaw, stage);
   }
 }
 
-// ---- the products, issued by one thread
+// ---- the products, issued by one warp
 template <int D>
 __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t* smem) {
   constexpr uint32_t kIdescS = instruction(kTok, false), kIdescO = instruction(D, true);
   const uint32_t q_at = lt::smem_u32(smem + Smem<D>::kQ), kv_at = lt::smem_u32(smem + Smem<D>::kKv);
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0), lead = elect_one();
   bool ok = wait_or_abort(&sh->q_full, 0, sh);
   int slot = 0;
   uint32_t parity = 0;
@@ -464,55 +514,65 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   };
   // (descriptors hold addresses in units of 16 bytes; the steps' offsets are added to them, and the
   // loops stay rolled: this warpgroup runs on few registers, and a product takes 64 clocks)
+  // (descriptors hold addresses in units of 16 bytes; the steps' offsets are added to them)
   auto logits = [&](int which, int key_slot) {
     const uint64_t q = desc_k_major(q_at + which * Smem<D>::kOperand), key = desc_k_major(kv_at + key_slot * Smem<D>::kOperand);
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       const uint32_t at = ((k / 4) * Smem<D>::kHalf + (k % 4) * 32) >> 4;
-      mma_ss(tmem + which * kTok, q + at, key + at, kIdescS, k > 0);
+      mma_ss(tmem + which * kTok, q + at, key + at, kIdescS, k > 0, lead);
     }
-    mma_commit(&sh->s_full[which]);
+    mma_commit(&sh->s_full[which], lead);
   };
-  auto outputs = [&](int which, int value_slot, bool first) {
+  auto outputs = [&](int which, int value_slot, bool first, int half) {
     const uint64_t value = desc_mn_major(kv_at + value_slot * Smem<D>::kOperand, Smem<D>::kHalf);
-#pragma unroll 1
-    for (int k = 0; k < kTok / 16; ++k)
-      mma_ts(tmem + 2 * kTok + which * D, tmem + which * kTok + k * 8, value + k * (2048 >> 4), kIdescO, !first || k > 0);
+#pragma unroll
+    for (int k = half * (kTok / 32); k < (half + 1) * (kTok / 32); ++k)
+      mma_ts(tmem + 2 * kTok + which * D, tmem + which * kTok + k * 8, value + k * (2048 >> 4), kIdescO, !first || k > 0, lead);
   };
-  int before = 0;  // the slot of V(i - 1)
-  for (int i = 0; i < job.tiles && ok; ++i) {
-    ok = wait_or_abort(&sh->kv_full[slot], parity, sh);
-    if (!ok) break;
-    fence_after();
-    const int key_slot = slot;
+  // both halves of a row tile's second product
+  auto weigh = [&](int which, int value_slot, int i) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (!wait_or_abort(&sh->p_full[which][half], i & 1, sh)) return false;
+      fence_after();
+      outputs(which, value_slot, i == 0, half);
+    }
+    return true;
+  };
+  // K(i + 1) and V(i) are waited for while a product runs, so that the tensor core waits for weights only
+  auto wait_slot = [&] {
+    ok = ok && wait_or_abort(&sh->kv_full[slot], parity, sh);
+    const int at = slot;
     next_slot();
-    logits(0, key_slot);
+    return at;
+  };
+  int key = job.tiles > 0 ? wait_slot() : 0, value = 0;
+  fence_after();
+  if (job.tiles > 0 && ok) logits(0, key);
+  for (int i = 0; i < job.tiles && ok; ++i) {
+    // here S_A(i) is issued
     if (job.two) {
       if (i > 0) {
-        ok = wait_or_abort(&sh->p_full[1], (i - 1) & 1, sh);
+        ok = weigh(1, value, i - 1);
         if (!ok) break;
-        fence_after();
-        outputs(1, before, i == 1);
-        mma_commit(&sh->kv_empty[before]);
+        mma_commit(&sh->kv_empty[value], lead);
       }
-      logits(1, key_slot);
+      logits(1, key);
     }
-    mma_commit(&sh->kv_empty[key_slot]);
-    ok = wait_or_abort(&sh->kv_full[slot], parity, sh) && wait_or_abort(&sh->p_full[0], i & 1, sh);
+    mma_commit(&sh->kv_empty[key], lead);
+    value = wait_slot();
+    if (i + 1 < job.tiles) key = wait_slot();
     if (!ok) break;
     fence_after();
-    before = slot;
-    next_slot();
-    outputs(0, before, i == 0);
-    if (!job.two) mma_commit(&sh->kv_empty[before]);
+    ok = weigh(0, value, i);
+    if (!ok) break;
+    if (!job.two) mma_commit(&sh->kv_empty[value], lead);
+    if (i + 1 < job.tiles) logits(0, key);
   }
-  if (ok && job.two && job.tiles > 0) {
-    ok = wait_or_abort(&sh->p_full[1], (job.tiles - 1) & 1, sh);
-    fence_after();
-    if (ok) outputs(1, before, job.tiles == 1);
-  }
-  mma_commit(&sh->o_full[0]);
-  mma_commit(&sh->o_full[1]);
+  if (ok && job.two && job.tiles > 0) weigh(1, value, job.tiles - 1);
+  mma_commit(&sh->o_full[0], lead);
+  mma_commit(&sh->o_full[1], lead);
 }
 
 template <int D>
@@ -520,10 +580,12 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (lt::smem_u32(smem_raw) & 1023u)) & 1023u);
   Shared* sh = reinterpret_cast<Shared*>(smem + Smem<D>::kBars);
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0);
   if (tid == 0) {
-    for (int w = 0; w < 4; ++w)
-      for (int s = 0; s < kRaw; ++s) lt::mbar_init(&sh->packed_full[w][s], 1);
+    for (int s = 0; s < kRaw; ++s) {
+      lt::mbar_init(&sh->packed_full[s], 1);
+      lt::mbar_init(&sh->packed_empty[s], 4);
+    }
     for (int s = 0; s < kSlots; ++s) {
       lt::mbar_init(&sh->kv_full[s], 128);
       lt::mbar_init(&sh->kv_empty[s], 1);
@@ -531,7 +593,8 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
     lt::mbar_init(&sh->q_full, 256);
     for (int t = 0; t < 2; ++t) {
       lt::mbar_init(&sh->s_full[t], 1);
-      lt::mbar_init(&sh->p_full[t], 128);
+      lt::mbar_init(&sh->p_full[t][0], 128);
+      lt::mbar_init(&sh->p_full[t][1], 128);
       lt::mbar_init(&sh->o_full[t], 1);
     }
     sh->abort = 0;
@@ -575,16 +638,17 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   __syncthreads();
   fence_after();
 
-  // 512 threads of 128 registers are split as 2 x 192 + 88 + 40 a thread of the four warpgroups
+  // 512 threads of 128 registers are split as 2 x 184 + 80 + 64 a thread of the four warpgroups
   if (warp < 8) {
-    regs_up<192>();
+    regs_up<184>();
     softmax_role<D>(p, job, sh, smem, warp / 4);
   } else if (warp < 12) {
-    regs_down<88>();
-    unpack_role<D>(p, job, sh, smem);
+    regs_down<80>();
+    unpack_role<D>(job, sh, smem);
   } else {
-    regs_down<40>();
-    if (warp == 12 && (tid & 31) == 0) product_role<D>(job, sh, smem);
+    regs_down<64>();
+    if (warp == 12) product_role<D>(job, sh, smem);
+    if (warp == 13) copy_role<D>(p, job, sh, smem);
   }
   __syncwarp();
   fence_before();
