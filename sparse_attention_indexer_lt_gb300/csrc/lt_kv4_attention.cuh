@@ -70,9 +70,43 @@ struct Place {
 // ceil(span / chunk) of them: ragged requests come out as chunks of like work, which
 // the hardware hands to SMs as they fall free. Every CTA computes this from the
 // lengths alone.
+// For at most 32 requests a warp knows them all: no shared memory, no barrier.
+__device__ __forceinline__ bool find_place_in_warp(const AttentionParams& p, int flat, Place* out) {
+  const int lane = threadIdx.x & 31;
+  Request q = {};
+  if (lane < p.requests) q = request_of(p, lane);
+  int64_t total = q.span;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(~0u, total, d);
+  int64_t chunk = (total + p.target - 1) / p.target;
+  chunk = (chunk + kTile - 1) / kTile * kTile;
+  if (chunk < p.min_chunk) chunk = p.min_chunk;
+  const int n = q.queries > 0 ? max(1, (int)((q.span + chunk - 1) / chunk)) : 0;
+  int end = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int u = __shfl_up_sync(~0u, end, d);
+    if (lane >= d) end += u;
+  }
+  const uint32_t here = __ballot_sync(~0u, flat >= end - n && flat < end);
+  if (here == 0) return false;
+  const int r = __ffs(here) - 1;
+  out->request = r;
+  out->base = __shfl_sync(~0u, end - n, r);
+  out->count = __shfl_sync(~0u, n, r);
+  out->split = flat - out->base;
+  out->chunk = (int)(chunk > INT32_MAX ? INT32_MAX / kTile * kTile : chunk);
+  return true;
+}
+
 template <int kCta>
 __device__ __forceinline__ bool find_place(const AttentionParams& p, int flat, Place* out, int64_t* sums, Place* found) {
   const int tid = threadIdx.x;
+  if (p.requests <= 32) {
+    const bool got = find_place_in_warp(p, flat, out);
+    __syncthreads();  // (what the caller has set up before is seen by all after this, on both ways)
+    return got;
+  }
   if (tid == 0) found->request = -1;
   int64_t mine = 0;
   for (int r = tid; r < p.requests; r += kCta) mine += request_of(p, r).span;
@@ -166,23 +200,17 @@ __device__ __forceinline__ uint32_t nan_halves(uint32_t h) {
   return ((h & 0x7FFFu) > 0x7C00u ? 0xFFFFu : 0u) | ((h & 0x7FFF0000u) > 0x7C000000u ? 0xFFFF0000u : 0u);
 }
 
-// bf16 pairs of a row whose largest magnitude has the fp32 word `big`, made fp16 pairs: times the power
-// of two that brings the largest into [2^14, 2^15), so nothing overflows and what lies
-// within 2^-28 of the largest stays exact. Returns the inverse of that power. Rows of zeros,
-// or with an infinity or NaN, are taken as they are.
-template <int N>
-__device__ __forceinline__ float bf16_to_half_scaled(uint32_t (&w)[N][4], uint32_t big) {
+// bf16 rows become fp16 rows times a power of two: the one that brings the row's largest (magnitude's
+// fp32 word `big`) into [2^14, 2^15), so nothing overflows and what lies within 2^-28 of the
+// largest stays exact. Rows of zeros, or with an infinity or NaN, are taken as they are.
+__device__ __forceinline__ float bf16_row_power(uint32_t big) {
   const int e = (int)(big >> 23);  // biased exponent
-  const int up = e == 0 || e == 255 ? 127 : min(268 - e, 253);
-  const float mul = __uint_as_float((uint32_t)up << 23);
-#pragma unroll
-  for (int j = 0; j < N; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float lo = __uint_as_float(w[j][i] << 16) * mul, hi = __uint_as_float(w[j][i] & 0xFFFF0000u) * mul;
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j][i]) : "f"(hi), "f"(lo));
-    }
-  return __uint_as_float((uint32_t)(254 - up) << 23);
+  return __uint_as_float((uint32_t)(e == 0 || e == 255 ? 127 : min(268 - e, 253)) << 23);
+}
+__device__ __forceinline__ uint32_t bf16_pair_to_half(uint32_t w, float mul) {
+  const float lo = __uint_as_float(w << 16) * mul, hi = __uint_as_float(w & 0xFFFF0000u) * mul;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
 }
 template <int N>
 __device__ __forceinline__ uint32_t largest_word(const uint32_t (&w)[N][4]) {
@@ -193,31 +221,31 @@ __device__ __forceinline__ uint32_t largest_word(const uint32_t (&w)[N][4]) {
     for (int i = 0; i < 4; ++i) big = max(big, max(w[j][i] << 16 & 0x7FFF0000u, w[j][i] & 0x7FFF0000u));
   return big;
 }
-// A whole row in one thread.
-template <int N>
-__device__ __forceinline__ float bf16_words_to_half(uint32_t (&w)[N][4]) {
-  return bf16_to_half_scaled<N>(w, largest_word<N>(w));
-}
-// A row's pieces spread over the four lanes of equal lane / 4.
+// A row's pieces spread over the four lanes of equal lane / 4; returns the inverse of the power.
 template <int N>
 __device__ __forceinline__ float bf16_row_to_half(uint32_t (&w)[N][4]) {
   uint32_t big = largest_word<N>(w);
   big = max(big, __shfl_xor_sync(~0u, big, 1));
   big = max(big, __shfl_xor_sync(~0u, big, 2));
-  return bf16_to_half_scaled<N>(w, big);
+  const float mul = bf16_row_power(big);
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[j][i] = bf16_pair_to_half(w[j][i], mul);
+  return 1.0f / mul;
 }
 
-// Four outputs, rounded once.
+// Two outputs, rounded once.
+__device__ __forceinline__ uint32_t pack_out(const AttentionParams& p, float lo, float hi) {
+  uint32_t w;
+  if (p.bf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
 __device__ __forceinline__ void store4(const AttentionParams& p, int64_t at, float4 o) {
-  uint2 w;
-  if (p.bf16) {
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(o.y), "f"(o.x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(o.w), "f"(o.z));
-  } else {
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(o.y), "f"(o.x));
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(o.w), "f"(o.z));
-  }
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = w;
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_out(p, o.x, o.y), pack_out(p, o.z, o.w));
 }
 
 }  // namespace kv4

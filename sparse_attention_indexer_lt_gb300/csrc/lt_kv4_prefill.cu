@@ -37,7 +37,8 @@ using namespace lt::kv4;
 constexpr int kCta = 512;
 constexpr int kTok = 128;    // positions of a tile
 constexpr int kSlots = 4;    // unpacked key or value tiles in shared memory
-constexpr int kRaw = 1;      // packed tiles in shared memory: rows go on to registers, so the next one comes meanwhile
+constexpr int kPart = 64;    // positions of a packed stage
+constexpr int kRaw = 3;      // packed stages in shared memory or on their way there
 constexpr float kShift = 6.0f;
 constexpr float kSlack = 8.0f;  // how far logits may pass the maximum (log 2) before it moves
 
@@ -48,8 +49,8 @@ struct Smem {
   static constexpr int kOperand = kHalf * (D / 64);
   static constexpr int kQ = 0;                           // two row tiles
   static constexpr int kKv = kQ + 2 * kOperand;          // kSlots
-  static constexpr int kPacked = kKv + kSlots * kOperand;  // [kRaw][128 rows]
-  static constexpr int kBars = kPacked + kRaw * kTok * kRow;
+  static constexpr int kPacked = kKv + kSlots * kOperand;  // [kRaw][kPart rows]
+  static constexpr int kBars = kPacked + kRaw * kPart * kRow;
   static constexpr int kTotal = kBars + 2048 + 1024;     // (slack to align the start to 1024)
 };
 
@@ -57,8 +58,8 @@ struct Shared {
   uint64_t packed_full[kRaw], packed_empty[kRaw];
   uint64_t kv_full[kSlots], kv_empty[kSlots];
   uint64_t q_full, s_full[2], p_full[2][2], o_full[2];
-  uint4 valid[4];            // [tile mod 4]: positions on a page of the cache and in range, as bits
-  uint4 nan_rows[4];         // positions with a NaN value scale
+  alignas(16) uint32_t valid[4][4];     // [tile mod 4]: positions on a page of the cache and in range, as bits
+  alignas(16) uint32_t nan_rows[4][4];  // positions with a NaN value scale
   uint8_t nan_groups[4][kTok];
   int64_t sums[kCta / 32];
   Place found;
@@ -180,11 +181,6 @@ __device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
   asm("{\n .reg .b64 x, s;\n mov.b64 s, {%0, %1};\n mov.b64 x, {%2, %3};\n add.rn.f32x2 s, s, x;\n mov.b64 {%0, %1}, s;\n}"
       : "+f"(s0), "+f"(s1) : "f"(x0), "f"(x1));
 }
-template <int N>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
-
 // What a CTA works on: row0 .. of the request's query rows, positions [from, to).
 struct Job {
   Request rq;
@@ -195,32 +191,50 @@ struct Job {
 // ---- one row tile's softmax: a thread a row
 template <int D>
 __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job& job, Shared* sh, uint8_t* smem, int which) {
-  const int row_in_tile = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
+  constexpr int kHalf = Smem<D>::kHalf, kChunks = D / 8;  // 16-byte chunks of a row of 16-bit values
+  constexpr int kAtOnce = 32 / kChunks;                   // rows of one warp-wide access
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row_in_tile = warp * 32 + lane;
   const int row = job.row0 + which * 128 + row_in_tile;
   const int row_c = min(row, job.rows - 1);
-  const int64_t token = job.rq.first + row_c / p.group;
-  const int q_head = job.head * p.group + row_c % p.group;
+  uint8_t* tile = smem + Smem<D>::kQ + which * Smem<D>::kOperand;
+  // chunk c of row r of the tile, where the 128-byte swizzle puts it
+  auto chunk_of = [&](int r, int c) { return reinterpret_cast<uint4*>(tile + (c / 8) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
 
-  // the query row as fp16 into shared memory, with the power of two that keeps bf16 in range
-  float factor;
+  // the query rows into shared memory: the warp brings its rows one after the other, then each thread
+  // makes its own row fp16, with the power of two that keeps bf16 in range
+  float factor = p.scale_log2;
   {
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + token * p.q_token + (int64_t)q_head * p.q_head);
-    uint32_t w[D / 8][4];
-#pragma unroll
-    for (int j = 0; j < D / 8; ++j) {
-      const uint4 v = __ldg(q + j);
-      w[j][0] = v.x, w[j][1] = v.y, w[j][2] = v.z, w[j][3] = v.w;
+    const int chunk = lane % kChunks;
+#pragma unroll 8
+    for (int it = 0; it < 32 / kAtOnce; ++it) {
+      const int r = warp * 32 + it * kAtOnce + lane / kChunks, of = min(job.row0 + which * 128 + r, job.rows - 1);
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)(job.rq.first + of / p.group) * p.q_token +
+                          (int64_t)(job.head * p.group + of % p.group) * p.q_head;
+      *chunk_of(r, chunk) = __ldg(reinterpret_cast<const uint4*>(q) + chunk);
     }
-    factor = p.scale_log2;
-    if (p.bf16) factor *= bf16_words_to_half<D / 8>(w);
+    __syncwarp();
+    float mul = 1.0f;
+    if (p.bf16) {
+      uint32_t big = 0;
+#pragma unroll 4
+      for (int c = 0; c < kChunks; ++c) {
+        const uint4 v = *chunk_of(row_in_tile, c);
+        const uint32_t w[1][4] = {{v.x, v.y, v.z, v.w}};
+        big = max(big, largest_word<1>(w));
+      }
+      mul = bf16_row_power(big);
+      factor /= mul;  // (exact: a power of two)
+    }
     // logits are compared before they are scaled: a negative scale turns the row round instead
     const uint32_t flip = factor < 0.0f ? 0x80008000u : 0u, keep = factor == 0.0f ? 0u : ~0u;
     factor = factor == 0.0f ? 1.0f : fabsf(factor);
-    uint8_t* to = smem + Smem<D>::kQ + which * Smem<D>::kOperand + row_in_tile * 128;
+#pragma unroll 4
+    for (int c = 0; c < kChunks; ++c) {
+      uint4* at = chunk_of(row_in_tile, c);
+      uint32_t w[4] = {at->x, at->y, at->z, at->w};
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) {
-      const uint4 v = make_uint4((w[j][0] ^ flip) & keep, (w[j][1] ^ flip) & keep, (w[j][2] ^ flip) & keep, (w[j][3] ^ flip) & keep);
-      *reinterpret_cast<uint4*>(to + (j / 8) * Smem<D>::kHalf + (((j & 7) ^ (row_in_tile & 7)) << 4)) = v;
+      for (int e = 0; e < 4; ++e) w[e] = ((p.bf16 ? bf16_pair_to_half(w[e], mul) : w[e]) ^ flip) & keep;
+      *at = make_uint4(w[0], w[1], w[2], w[3]);
     }
     fence_async();
     arrive(&sh->q_full);
@@ -232,6 +246,9 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   const uint32_t lane_base = sh->tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t s_at = lane_base + which * kTok, o_at = lane_base + 2 * kTok + which * D;
 
+  // The loop reads a tile's logits twice, 64 columns at a time, once for the maximum and once for the
+  // weights: that is little against 128 exponentials a row, and the loops stay short enough
+  // for the instruction cache that four kinds of warps share.
   float m = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;  // m in units of log 2
   uint32_t poison = 0;                             // value groups in which this row is NaN
   bool ok = true;
@@ -239,52 +256,52 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
     ok = wait_or_abort(&sh->s_full[which], i & 1, sh);
     if (!ok) break;
     fence_after();
-    uint32_t raw[kTok];
-    float* s = reinterpret_cast<float*>(raw);
-#pragma unroll
-    for (int c = 0; c < kTok; c += 32) tmem_ld32(s_at + c, raw + c);
-    const uint4 valid4 = sh->valid[i & 3], nan4 = sh->nan_rows[i & 3];
     const int pos0 = job.from + i * kTok;
-    const bool whole = (valid4.x & valid4.y & valid4.z & valid4.w) == ~0u && pos0 + kTok <= limit && pos0 >= low;
-    const bool clean = (nan4.x | nan4.y | nan4.z | nan4.w) == 0;
-    const bool plain = __all_sync(~0u, whole && clean);
-    tmem_wait_ld();
-
-    const uint32_t valid[4] = {valid4.x, valid4.y, valid4.z, valid4.w};
-    if (!plain) {
-#pragma unroll
+    const uint32_t* valid = sh->valid[i & 3];
+    const uint32_t* nan_rows = sh->nan_rows[i & 3];
+    const uint4 valid4 = *reinterpret_cast<const uint4*>(valid), nan4 = *reinterpret_cast<const uint4*>(nan_rows);
+    const bool plain = (valid4.x & valid4.y & valid4.z & valid4.w) == ~0u && pos0 + kTok <= limit && pos0 >= low &&
+                       (nan4.x | nan4.y | nan4.z | nan4.w) == 0;
+    if (!__all_sync(~0u, plain)) {
+      // hide what this row does not see, in tensor memory
+#pragma unroll 1
       for (int w = 0; w < 4; ++w) {
-        // visible: [low, limit) of this row, as bits of the 32 positions
+        uint32_t x[32];
+        tmem_ld32(s_at + 32 * w, x);
         const int a = low - (pos0 + 32 * w), b = limit - (pos0 + 32 * w);  // (low >= 0: no overflow)
         uint32_t see = valid[w];
         see &= b >= 32 ? ~0u : b <= 0 ? 0u : (1u << b) - 1u;
         see &= a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a;
+        tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          if (!((see >> c) & 1u)) s[32 * w + c] = -INFINITY;
+          if (!((see >> c) & 1u)) x[c] = 0xFF800000u;
+        tmem_st32(s_at + 32 * w, x);
+        for (uint32_t left = nan_rows[w] & see; left != 0; left &= left - 1)
+          poison |= sh->nan_groups[i & 3][32 * w + __ffs(left) - 1];
+        __syncwarp();
       }
-    }
-    if (!clean) {
-      const uint32_t nan_rows[4] = {nan4.x, nan4.y, nan4.z, nan4.w};
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        for (uint32_t left = nan_rows[w] & valid[w]; left != 0; left &= left - 1) {
-          const int t = 32 * w + __ffs(left) - 1;
-          if (pos0 + t < limit && pos0 + t >= low) poison |= sh->nan_groups[i & 3][t];
-        }
+      tmem_wait_st();
     }
 
-    float top = s[0], top2 = s[1], top3 = s[2], top4 = s[3];
+    float top = -INFINITY, top2 = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t x[64];
+      const float* s = reinterpret_cast<const float*>(x);
+      tmem_ld32(s_at + 64 * h, x);
+      tmem_ld32(s_at + 64 * h + 32, x + 32);
+      tmem_wait_ld();
+      float top3 = s[0], top4 = s[1];
 #pragma unroll
-    for (int c = 4; c < kTok - 4; c += 8) {
-      top = max3(top, s[c], s[c + 1]);
-      top2 = max3(top2, s[c + 2], s[c + 3]);
-      top3 = max3(top3, s[c + 4], s[c + 5]);
-      top4 = max3(top4, s[c + 6], s[c + 7]);
+      for (int c = 2; c < 62; c += 4) {
+        top3 = max3(top3, s[c], s[c + 1]);
+        top4 = max3(top4, s[c + 2], s[c + 3]);
+      }
+      top = max3(top, top3, s[62]);
+      top2 = max3(top2, top4, s[63]);
     }
-    top = max3(top, s[kTok - 4], s[kTok - 3]);
-    top2 = max3(top2, s[kTok - 2], s[kTok - 1]);
-    top = fmaxf(max3(top, top2, top3), top4) * factor;
+    top = fmaxf(top, top2) * factor;
 
     const bool moves = top > m + kSlack || (m == -INFINITY && top > m);
     if (__any_sync(~0u, moves)) {
@@ -308,20 +325,22 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
       }
     }
     const float ref = m == -INFINITY ? 0.0f : kShift - m;
-    uint32_t pk[32];
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 2; ++h) {
+      uint32_t x[64], pk[32];
+      float* s = reinterpret_cast<float*>(x);
+      tmem_ld32(s_at + 64 * h, x);
+      tmem_ld32(s_at + 64 * h + 32, x + 32);
+      tmem_wait_ld();
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        float& x0 = s[64 * h + 2 * e];
-        float& x1 = s[64 * h + 2 * e + 1];
-        fma2(x0, x1, factor, ref);
-        x0 = exp2_fast(x0);
-        x1 = exp2_fast(x1);
-        add2(sum0, sum1, x0, x1);
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(x1), "f"(x0));
+        fma2(s[2 * e], s[2 * e + 1], factor, ref);
+        s[2 * e] = exp2_fast(s[2 * e]);
+        s[2 * e + 1] = exp2_fast(s[2 * e + 1]);
+        add2(sum0, sum1, s[2 * e], s[2 * e + 1]);
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(s[2 * e + 1]), "f"(s[2 * e]));
       }
-      tmem_st32(s_at + 32 * h, pk);
+      tmem_st32(s_at + 32 * h, pk);  // (columns whose logits have been read)
       tmem_wait_st();
       fence_before();
       arrive(&sh->p_full[which][h]);  // the second product starts on the first half
@@ -330,42 +349,62 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   ok = wait_or_abort(&sh->o_full[which], 0, sh) && ok;
   fence_after();
 
-  // epilogue: divide, write out (or the part and its logarithm)
+  // epilogue: divide, turn the rows through the query tile's place into whole lines, write out (or the
+  // part and its logarithm)
   const float sum = sum0 + sum1;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   float log2_sum = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m - kShift) + __log2f(sum);
   if (!ok) log2_sum = NAN;
-  const bool mine = row < job.rows;
-  const int64_t part = (((int64_t)job.flat * p.heads + job.head) * p.row_tiles + job.row_tile) * 256 + which * 128 + row_in_tile;
-  const int64_t out_row = token * p.heads * p.group + q_head;
+  const int64_t part = (((int64_t)job.flat * p.heads + job.head) * p.row_tiles + job.row_tile) * 256 + which * 128;
+  const int per_pass = job.final_here ? D : D / 2;  // columns that fit the tile's rows
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += per_pass) {
+#pragma unroll 1
+    for (int c = 0; c < per_pass; c += 16) {
+      uint32_t o[16];
+      if (job.tiles > 0) {
+        tmem_ld16(o_at + c0 + c, o);
+        tmem_wait_ld();
+      }
+      const bool bad = !ok || ((poison >> ((c0 + c) / 32)) & 1u);
 #pragma unroll
-  for (int c = 0; c < D; c += 32) {
-    uint32_t o[32];
-    if (job.tiles > 0) {
-      tmem_ld32(o_at + c, o);
-      tmem_wait_ld();
-    }
-    const bool bad = !ok || ((poison >> (c / 32)) & 1u);
+      for (int e = 0; e < 16; ++e) {
+        const float x = job.tiles > 0 && sum != 0.0f ? __uint_as_float(o[e]) * inv : 0.0f;
+        o[e] = __float_as_uint(bad ? NAN : x);
+      }
+      if (job.final_here) {
+        uint32_t h[8];
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (job.tiles > 0 && sum != 0.0f)
-        x = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv, __uint_as_float(o[e + 2]) * inv,
-                        __uint_as_float(o[e + 3]) * inv);
-      if (bad) x = make_float4(NAN, NAN, NAN, NAN);
-      if (mine) {
-        if (job.final_here)
-          store4(p, out_row * D + c + e, x);
-        else
-          *reinterpret_cast<float4*>(p.part_o + part * D + c + e) = x;
+        for (int e = 0; e < 8; ++e) h[e] = pack_out(p, __uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+        *chunk_of(row_in_tile, c / 8) = make_uint4(h[0], h[1], h[2], h[3]);
+        *chunk_of(row_in_tile, c / 8 + 1) = make_uint4(h[4], h[5], h[6], h[7]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *chunk_of(row_in_tile, c / 4 + e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       }
     }
+    __syncwarp();
+#pragma unroll 4
+    for (int it = 0; it < 32 / kAtOnce; ++it) {
+      const int r = warp * 32 + it * kAtOnce + lane / kChunks, of = job.row0 + which * 128 + r;
+      if (of >= job.rows) continue;
+      const uint4 v = *chunk_of(r, lane % kChunks);
+      if (job.final_here) {
+        const int64_t out_row = (int64_t)(job.rq.first + of / p.group) * p.heads * p.group + job.head * p.group + of % p.group;
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_row * D)[lane % kChunks] = v;
+      } else {
+        reinterpret_cast<uint4*>(p.part_o + (part + r) * D + c0)[lane % kChunks] = v;
+      }
+    }
+    __syncwarp();
   }
-  if (mine) {
+  if (row < job.rows) {
     if (job.final_here) {
+      const int64_t out_row = (int64_t)(job.rq.first + row / p.group) * p.heads * p.group + job.head * p.group + row % p.group;
       if (p.lse != nullptr) p.lse[out_row] = log2_sum * 0.6931471805599453f;
     } else {
-      p.part_lse[part] = log2_sum;
+      p.part_lse[part + row_in_tile] = log2_sum;
     }
   }
 }
@@ -374,53 +413,54 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
 template <int D>
 __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& job, Shared* sh, uint8_t* smem) {
   constexpr int kRow = row_bytes(D);
-  constexpr int kMost = kTok / 32;  // runs of a lane, at pages of one position
+  constexpr int kMost = kPart / 32;  // runs of a lane, at pages of one position
   const int lane = threadIdx.x & 31;
   const uint32_t packed_at = lt::smem_u32(smem + Smem<D>::kPacked);
-  const int run_shift = min(p.shift, 7), runs = kTok >> run_shift;
+  const int run_shift = min(p.shift, 6), runs = kPart >> run_shift;
   const int32_t* table = p.table + (int64_t)job.request * p.width;
+  const int stages = 2 * job.tiles;
   int page[kMost];
-  auto look_up = [&](int tile) {
+  auto look_up = [&](int n) {
 #pragma unroll
     for (int j = 0; j < kMost; ++j) {
-      const int run = lane + 32 * j, at = job.from + tile * kTok + (run << run_shift);
-      page[j] = tile < job.tiles && run < runs && at < job.to ? __ldg(table + (at >> p.shift)) : -1;
+      const int run = lane + 32 * j, at = job.from + n * kPart + (run << run_shift);
+      page[j] = n < stages && run < runs && at < job.to ? __ldg(table + (at >> p.shift)) : -1;
     }
   };
   look_up(0);
   int stage = 0;
   uint32_t parity = 1;  // (the first round's stages are free)
-  for (int i = 0; i < job.tiles; ++i) {
+#pragma unroll 1
+  for (int n = 0; n < stages; ++n) {
     if (!wait_or_abort(&sh->packed_empty[stage], parity, sh)) break;
-    uint32_t valid[4] = {0u, 0u, 0u, 0u};
+    uint32_t valid[2] = {0u, 0u};
     int count[kMost];
 #pragma unroll
     for (int j = 0; j < kMost; ++j) {
-      const int first = (lane + 32 * j) << run_shift, left = job.to - (job.from + i * kTok + first);
+      const int first = (lane + 32 * j) << run_shift, left = job.to - (job.from + n * kPart + first);
       count[j] = page[j] >= 0 && page[j] < p.pages ? min(left, 1 << run_shift) : 0;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < 2; ++w) {
         const int a = min(max(first - 32 * w, 0), 32), b = min(max(first + count[j] - 32 * w, 0), 32);
         valid[w] |= a < b ? (b == 32 ? ~0u : (1u << b) - 1u) & (~0u << a) : 0u;
       }
     }
 #pragma unroll
-    for (int w = 0; w < 4; ++w) valid[w] = __reduce_or_sync(~0u, valid[w]);
+    for (int w = 0; w < 2; ++w) valid[w] = __reduce_or_sync(~0u, valid[w]);
     if (lane == 0) {
-      sh->valid[i & 3] = make_uint4(valid[0], valid[1], valid[2], valid[3]);
-      lt::mbar_arrive_tx(&sh->packed_full[stage],
-                         (uint32_t)(__popc(valid[0]) + __popc(valid[1]) + __popc(valid[2]) + __popc(valid[3])) * kRow);
+      *reinterpret_cast<uint2*>(&sh->valid[(n >> 1) & 3][(n & 1) * 2]) = make_uint2(valid[0], valid[1]);
+      lt::mbar_arrive_tx(&sh->packed_full[stage], (uint32_t)(__popc(valid[0]) + __popc(valid[1])) * kRow);
     }
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < kMost; ++j) {
-      const int first = (lane + 32 * j) << run_shift, at = job.from + i * kTok + first;
+      const int first = (lane + 32 * j) << run_shift, at = job.from + n * kPart + first;
       if (count[j] > 0) {
         const uint8_t* src = p.cache + (((((int64_t)page[j] * p.heads + job.head) << p.shift) + (at & ((1 << p.shift) - 1))) * kRow);
-        bulk_in(packed_at + (stage * kTok + first) * kRow, src, (uint32_t)count[j] * kRow, &sh->packed_full[stage]);
+        bulk_in(packed_at + (stage * kPart + first) * kRow, src, (uint32_t)count[j] * kRow, &sh->packed_full[stage]);
       }
     }
-    look_up(i + 1);
+    look_up(n + 1);
     if (++stage == kRaw) {
       stage = 0;
       parity ^= 1u;
@@ -428,72 +468,77 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
   }
 }
 
-// ---- unpacking: a thread a position
+// ---- unpacking: a packed stage's 64 positions at a time, a thread the key (threads 0 .. 63) or the value
+// (64 .. 127) of a position
 template <int D>
 __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t* smem) {
   constexpr int kRow = row_bytes(D);
-  constexpr int kGroups = D / 32;
-  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, row = warp * 32 + lane;
+  const int t = threadIdx.x & 127, warp = t >> 5, lane = t & 31, part = t >> 6, row = t & 63;
   uint32_t chunk_at[8];  // where the row's eight 16-byte chunks lie in a swizzled 128-byte row
 #pragma unroll
   for (int c = 0; c < 8; ++c) chunk_at[c] = lt::smem_u32(smem + Smem<D>::kKv) + row * 128 + ((c ^ (row & 7)) << 4);
-  int slot = 0;
-  uint32_t slot_parity = 1;  // (the first round's slots are free)
+  int slot = part, stage = 0;                  // keys in slots 0, 2, 0, ..., values in 1, 3, 1, ...
+  uint32_t slot_parity = 1, stage_parity = 0;  // (the first round's slots are free)
   bool ok = true;
-  for (int i = 0; i < job.tiles && ok; ++i) {
-    const int stage = i % kRaw;
-    ok = wait_or_abort(&sh->packed_full[stage], (i / kRaw) & 1, sh);
+#pragma unroll 1
+  for (int i = 0; i < job.tiles; ++i) {
+    ok = wait_or_abort(&sh->kv_empty[slot], slot_parity, sh);
     if (!ok) break;
-    const uint4 valid4 = sh->valid[i & 3];
-    const uint32_t valid = warp == 0 ? valid4.x : warp == 1 ? valid4.y : warp == 2 ? valid4.z : valid4.w;
-    const bool there = (valid >> lane) & 1u;
-    const uint8_t* from = smem + Smem<D>::kPacked + (stage * kTok + row) * kRow;
-    // the row's codes and scales (fp16 pairs: keys, then values; a position that is not there counts as zeros)
-    uint4 codes[D / 16];
-    uint32_t sc[kGroups];
-#pragma unroll
-    for (int g = 0; g < D / 16; ++g) codes[g] = reinterpret_cast<const uint4*>(from)[g];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) sc[g] = there ? reinterpret_cast<const uint32_t*>(from + D)[g] : 0u;
-    __syncwarp();  // every lane has read the stage
-    if (lane == 0) arrive(&sh->packed_empty[stage]);
-    uint32_t nan = 0;
-#pragma unroll
-    for (int g = 0; g < kGroups / 2; ++g) {
-      const uint32_t n = nan_halves(sc[kGroups / 2 + g]);
-      sc[kGroups / 2 + g] &= ~n;
-      nan |= ((n & 1u) | ((n >> 15) & 2u)) << (2 * g);
-    }
-    const uint32_t nan_rows = __ballot_sync(~0u, nan != 0);
-    if (lane == 0) reinterpret_cast<uint32_t*>(&sh->nan_rows[i & 3])[warp] = nan_rows;
-    if (nan_rows) sh->nan_groups[i & 3][row] = (uint8_t)nan;
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {  // keys, then values
-      ok = ok && wait_or_abort(&sh->kv_empty[slot], slot_parity, sh);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      ok = wait_or_abort(&sh->packed_full[stage], stage_parity, sh);
       if (!ok) break;
-      const uint32_t to = slot * Smem<D>::kOperand;
+      const uint32_t valid = sh->valid[i & 3][half * 2 + (warp & 1)];
+      const bool there = (valid >> lane) & 1u;
+      const uint8_t* from = smem + Smem<D>::kPacked + (stage * kPart + row) * kRow;
+      // scales, fp16 pairs; a position that is not there counts as zeros, and so does a NaN value
+      // (noted for the rows that see it)
+      uint32_t sc[D / 64];
+      uint32_t nan = 0;
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const uint4 v = codes[part * kGroups + g];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t pair = sc[part * (kGroups / 2) + g / 2];
-        const uint32_t scale = __byte_perm(pair, 0, g & 1 ? 0x3232 : 0x1010);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t h[4];
-          codes_to_half2(w[j], h);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                       :: "r"(chunk_at[(g & 1) * 4 + j] + to + (g / 2) * Smem<D>::kHalf), "r"(hmul2(h[0], scale)),
-                          "r"(hmul2(h[1], scale)), "r"(hmul2(h[2], scale)), "r"(hmul2(h[3], scale)) : "memory");
+      for (int g = 0; g < D / 64; ++g) {
+        sc[g] = there ? reinterpret_cast<const uint32_t*>(from + D + part * (D / 16))[g] : 0u;
+        if (part == 1) {
+          const uint32_t n = nan_halves(sc[g]);
+          sc[g] &= ~n;
+          nan |= ((n & 1u) | ((n >> 15) & 2u)) << (2 * g);
         }
       }
-      fence_async();
-      arrive(&sh->kv_full[slot]);
-      if (++slot == kSlots) {
-        slot = 0;
-        slot_parity ^= 1u;
+      if (part == 1) {
+        const uint32_t nan_rows = __ballot_sync(~0u, nan != 0);
+        if (lane == 0) sh->nan_rows[i & 3][half * 2 + (warp & 1)] = nan_rows;
+        if (nan_rows) sh->nan_groups[i & 3][half * kPart + row] = (uint8_t)nan;
+      }
+      const uint32_t to = slot * Smem<D>::kOperand + half * (kPart * 128);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint4 v = reinterpret_cast<const uint4*>(from + part * (D / 2))[2 * c + g];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t scale = __byte_perm(sc[c], 0, g ? 0x3232 : 0x1010);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t h[4];
+            codes_to_half2(w[j], h);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                         :: "r"(chunk_at[g * 4 + j] + to + c * Smem<D>::kHalf), "r"(hmul2(h[0], scale)),
+                            "r"(hmul2(h[1], scale)), "r"(hmul2(h[2], scale)), "r"(hmul2(h[3], scale)) : "memory");
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (lane == 0) arrive(&sh->packed_empty[stage]);
+      if (++stage == kRaw) {
+        stage = 0;
+        stage_parity ^= 1u;
       }
     }
+    if (!ok) break;
+    fence_async();
+    arrive(&sh->kv_full[slot]);
+    slot ^= 2;
+    if (slot == part) slot_parity ^= 1u;
   }
 }
 
@@ -504,73 +549,56 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   const uint32_t q_at = lt::smem_u32(smem + Smem<D>::kQ), kv_at = lt::smem_u32(smem + Smem<D>::kKv);
   const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0), lead = elect_one();
   bool ok = wait_or_abort(&sh->q_full, 0, sh);
-  int slot = 0;
-  uint32_t parity = 0;
-  auto next_slot = [&] {
-    if (++slot == kSlots) {
-      slot = 0;
-      parity ^= 1u;
+  // One place for each product, in rolled loops: `which` alternates between the row tiles, and what goes
+  // round is short. (Descriptors hold addresses in units of 16 bytes; the steps' offsets are
+  // added to them.) Keys of tile i are in slot (i & 1) * 2, values in the next.
+  auto wait_slot = [&](int i, int part) { ok = ok && wait_or_abort(&sh->kv_full[(i & 1) * 2 + part], (i >> 1) & 1, sh); };
+  if (job.tiles > 0) wait_slot(0, 0);
+  const int steps = 2 * job.tiles + 1;  // even ones row tile A, odd ones row tile B
+#pragma unroll 1
+  for (int step = 0; step <= steps && ok && job.tiles > 0; ++step) {
+    // first the weights of tile i by its values, then the logits of tile i + 1
+    const int which = step & 1, i = (step >> 1) - 1;
+    if (which == 1 && !job.two) {
+      if (i >= 0) mma_commit(&sh->kv_empty[(i & 1) * 2 + 1], lead);
+      if (i + 1 < job.tiles) mma_commit(&sh->kv_empty[((i + 1) & 1) * 2], lead);
+      continue;
     }
-  };
-  // (descriptors hold addresses in units of 16 bytes; the steps' offsets are added to them, and the
-  // loops stay rolled: this warpgroup runs on few registers, and a product takes 64 clocks)
-  // (descriptors hold addresses in units of 16 bytes; the steps' offsets are added to them)
-  auto logits = [&](int which, int key_slot) {
-    const uint64_t q = desc_k_major(q_at + which * Smem<D>::kOperand), key = desc_k_major(kv_at + key_slot * Smem<D>::kOperand);
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t at = ((k / 4) * Smem<D>::kHalf + (k % 4) * 32) >> 4;
-      mma_ss(tmem + which * kTok, q + at, key + at, kIdescS, k > 0, lead);
+    if (which == 0 && i >= 0) {
+      // V(i) and K(i + 1) are waited for while the other row tile's product runs
+      wait_slot(i, 1);
+      if (i + 1 < job.tiles) wait_slot(i + 1, 0);
+      if (!ok) break;
     }
-    mma_commit(&sh->s_full[which], lead);
-  };
-  auto outputs = [&](int which, int value_slot, bool first, int half) {
-    const uint64_t value = desc_mn_major(kv_at + value_slot * Smem<D>::kOperand, Smem<D>::kHalf);
-#pragma unroll
-    for (int k = half * (kTok / 32); k < (half + 1) * (kTok / 32); ++k)
-      mma_ts(tmem + 2 * kTok + which * D, tmem + which * kTok + k * 8, value + k * (2048 >> 4), kIdescO, !first || k > 0, lead);
-  };
-  // both halves of a row tile's second product
-  auto weigh = [&](int which, int value_slot, int i) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (!wait_or_abort(&sh->p_full[which][half], i & 1, sh)) return false;
-      fence_after();
-      outputs(which, value_slot, i == 0, half);
-    }
-    return true;
-  };
-  // K(i + 1) and V(i) are waited for while a product runs, so that the tensor core waits for weights only
-  auto wait_slot = [&] {
-    ok = ok && wait_or_abort(&sh->kv_full[slot], parity, sh);
-    const int at = slot;
-    next_slot();
-    return at;
-  };
-  int key = job.tiles > 0 ? wait_slot() : 0, value = 0;
-  fence_after();
-  if (job.tiles > 0 && ok) logits(0, key);
-  for (int i = 0; i < job.tiles && ok; ++i) {
-    // here S_A(i) is issued
-    if (job.two) {
-      if (i > 0) {
-        ok = weigh(1, value, i - 1);
-        if (!ok) break;
-        mma_commit(&sh->kv_empty[value], lead);
-      }
-      logits(1, key);
-    }
-    mma_commit(&sh->kv_empty[key], lead);
-    value = wait_slot();
-    if (i + 1 < job.tiles) key = wait_slot();
-    if (!ok) break;
     fence_after();
-    ok = weigh(0, value, i);
-    if (!ok) break;
-    if (!job.two) mma_commit(&sh->kv_empty[value], lead);
-    if (i + 1 < job.tiles) logits(0, key);
+    if (i >= 0) {
+      const uint64_t value = desc_mn_major(kv_at + ((i & 1) * 2 + 1) * Smem<D>::kOperand, Smem<D>::kHalf);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        ok = wait_or_abort(&sh->p_full[which][half], i & 1, sh);
+        if (!ok) break;
+        fence_after();
+#pragma unroll
+        for (int k = 0; k < kTok / 32; ++k)
+          mma_ts(tmem + 2 * kTok + which * D, tmem + which * kTok + half * 32 + k * 8,
+                 value + half * ((kTok / 2 * 128) >> 4) + k * (2048 >> 4), kIdescO, i > 0 || half > 0 || k > 0, lead);
+      }
+      if (!ok) break;
+      if (which == 1) mma_commit(&sh->kv_empty[(i & 1) * 2 + 1], lead);
+    }
+    if (i + 1 < job.tiles) {
+      const uint64_t q = desc_k_major(q_at + which * Smem<D>::kOperand);
+      const uint64_t key = desc_k_major(kv_at + ((i + 1) & 1) * 2 * Smem<D>::kOperand);
+#pragma unroll 1
+      for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tmem + which * kTok, q + c * (Smem<D>::kHalf >> 4) + k * 2, key + c * (Smem<D>::kHalf >> 4) + k * 2, kIdescS,
+                 c > 0 || k > 0, lead);
+      mma_commit(&sh->s_full[which], lead);
+      if (which == 1) mma_commit(&sh->kv_empty[((i + 1) & 1) * 2], lead);
+    }
   }
-  if (ok && job.two && job.tiles > 0) weigh(1, value, job.tiles - 1);
   mma_commit(&sh->o_full[0], lead);
   mma_commit(&sh->o_full[1], lead);
 }
@@ -587,7 +615,7 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
       lt::mbar_init(&sh->packed_empty[s], 4);
     }
     for (int s = 0; s < kSlots; ++s) {
-      lt::mbar_init(&sh->kv_full[s], 128);
+      lt::mbar_init(&sh->kv_full[s], 64);
       lt::mbar_init(&sh->kv_empty[s], 1);
     }
     lt::mbar_init(&sh->q_full, 256);
@@ -638,18 +666,14 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   __syncthreads();
   fence_after();
 
-  // 512 threads of 128 registers are split as 2 x 184 + 80 + 64 a thread of the four warpgroups
-  if (warp < 8) {
-    regs_up<184>();
+  if (warp < 8)
     softmax_role<D>(p, job, sh, smem, warp / 4);
-  } else if (warp < 12) {
-    regs_down<80>();
+  else if (warp < 12)
     unpack_role<D>(job, sh, smem);
-  } else {
-    regs_down<64>();
-    if (warp == 12) product_role<D>(job, sh, smem);
-    if (warp == 13) copy_role<D>(p, job, sh, smem);
-  }
+  else if (warp == 12)
+    product_role<D>(job, sh, smem);
+  else if (warp == 13)
+    copy_role<D>(p, job, sh, smem);
   __syncwarp();
   fence_before();
   __syncthreads();
