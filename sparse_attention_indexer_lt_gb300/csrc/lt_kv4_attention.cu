@@ -773,6 +773,7 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
   p.target = plan.target;
   p.min_chunk = plan.min_chunk;
   p.row_tiles = plan.row_tiles;
+  p.align = plan.prefill ? 128 : kTile;
   p.bf16 = dtype == LT_DTYPE_BF16;
   p.scale_log2 = scale * 1.4426950408889634f;
 

@@ -29,6 +29,7 @@ struct AttentionParams {
   int64_t q_token, q_head;
   int32_t pages, tokens, requests, width, heads, group, shift, list_len, window;
   int32_t target, min_chunk, row_tiles, bf16;
+  int32_t align;    // positions at which chunks and windows start: multiples of this (32 or 128)
   float scale_log2;
 };
 
@@ -36,7 +37,7 @@ struct Request {
   int length;   // positions in the cache
   int first;    // its first query's row
   int queries;
-  int low;      // the first position that any of its queries sees, rounded down to a tile
+  int low;      // the first position that any of its queries sees, rounded down to p.align
   int span;     // length - low
 };
 
@@ -53,8 +54,8 @@ __device__ __forceinline__ Request request_of(const AttentionParams& p, int r) {
   q.first = first;
   q.queries = max(end - first, 0);
   q.low = 0;
-  if (p.window > 0) q.low = (int)(max((int64_t)q.length - q.queries + 1 - p.window, (int64_t)0) / kTile * kTile);
-  if (q.low > q.length) q.low = q.length / kTile * kTile;
+  if (p.window > 0) q.low = (int)(max((int64_t)q.length - q.queries + 1 - p.window, (int64_t)0) / p.align * p.align);
+  if (q.low > q.length) q.low = q.length / p.align * p.align;
   q.span = q.length - q.low;
   return q;
 }
@@ -66,7 +67,7 @@ struct Place {
 };
 
 // The requests' spans add up to `total`; with about `target` chunks wanted, a chunk has
-// total / target positions (a multiple of kTile, min_chunk at least) and request r has
+// total / target positions (a multiple of p.align, min_chunk at least) and request r has
 // ceil(span / chunk) of them: ragged requests come out as chunks of like work, which
 // the hardware hands to SMs as they fall free. Every CTA computes this from the
 // lengths alone.
@@ -79,7 +80,7 @@ __device__ __forceinline__ bool find_place_in_warp(const AttentionParams& p, int
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(~0u, total, d);
   int64_t chunk = (total + p.target - 1) / p.target;
-  chunk = (chunk + kTile - 1) / kTile * kTile;
+  chunk = (chunk + p.align - 1) / p.align * p.align;
   if (chunk < p.min_chunk) chunk = p.min_chunk;
   const int n = q.queries > 0 ? max(1, (int)((q.span + chunk - 1) / chunk)) : 0;
   int end = n;
@@ -95,7 +96,7 @@ __device__ __forceinline__ bool find_place_in_warp(const AttentionParams& p, int
   out->base = __shfl_sync(~0u, end - n, r);
   out->count = __shfl_sync(~0u, n, r);
   out->split = flat - out->base;
-  out->chunk = (int)(chunk > INT32_MAX ? INT32_MAX / kTile * kTile : chunk);
+  out->chunk = (int)(chunk > INT32_MAX ? INT32_MAX / 128 * 128 : chunk);
   return true;
 }
 
@@ -118,7 +119,7 @@ __device__ __forceinline__ bool find_place(const AttentionParams& p, int flat, P
 #pragma unroll 4
   for (int w = 0; w < kCta / 32; ++w) total += sums[w];
   int64_t chunk = (total + p.target - 1) / p.target;
-  chunk = (chunk + kTile - 1) / kTile * kTile;
+  chunk = (chunk + p.align - 1) / p.align * p.align;
   if (chunk < p.min_chunk) chunk = p.min_chunk;
   int base = 0;
   for (int first = 0; first < p.requests; first += kCta) {
@@ -155,7 +156,7 @@ __device__ __forceinline__ bool find_place(const AttentionParams& p, int flat, P
   }
   __syncthreads();
   *out = *found;
-  out->chunk = (int)(chunk > INT32_MAX ? INT32_MAX / kTile * kTile : chunk);
+  out->chunk = (int)(chunk > INT32_MAX ? INT32_MAX / 128 * 128 : chunk);
   return out->request >= 0;
 }
 

@@ -152,6 +152,7 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Waits for a phase; gives up after kWaitPolls, or as soon as another thread has.
+// (Per thread; a warp that goes on to .aligned instructions converges after it.)
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Shared* sh) {
   for (uint32_t i = 0; i < lt::kWaitPolls; ++i) {
     if (i == 0 ? mbar_ready(bar, parity) : lt::mbar_try_wait(bar, parity)) return true;
@@ -254,7 +255,10 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   bool ok = true;
   for (int i = 0; i < job.tiles; ++i) {
     ok = wait_or_abort(&sh->s_full[which], i & 1, sh);
-    if (!ok) break;
+    if (!__all_sync(~0u, ok)) {  // (the warp as a whole: what follows wants it converged)
+      ok = false;
+      break;
+    }
     fence_after();
     const int pos0 = job.from + i * kTok;
     const uint32_t* valid = sh->valid[i & 3];
@@ -344,9 +348,11 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
       tmem_wait_st();
       fence_before();
       arrive(&sh->p_full[which][h]);  // the second product starts on the first half
+      __syncwarp();
     }
   }
   ok = wait_or_abort(&sh->o_full[which], 0, sh) && ok;
+  __syncwarp();
   fence_after();
 
   // epilogue: divide, turn the rows through the query tile's place into whole lines, write out (or the
@@ -432,7 +438,7 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
   uint32_t parity = 1;  // (the first round's stages are free)
 #pragma unroll 1
   for (int n = 0; n < stages; ++n) {
-    if (!wait_or_abort(&sh->packed_empty[stage], parity, sh)) break;
+    if (!__all_sync(~0u, wait_or_abort(&sh->packed_empty[stage], parity, sh))) break;
     uint32_t valid[2] = {0u, 0u};
     int count[kMost];
 #pragma unroll
@@ -482,11 +488,11 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
   bool ok = true;
 #pragma unroll 1
   for (int i = 0; i < job.tiles; ++i) {
-    ok = wait_or_abort(&sh->kv_empty[slot], slot_parity, sh);
+    ok = __all_sync(~0u, wait_or_abort(&sh->kv_empty[slot], slot_parity, sh));
     if (!ok) break;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
-      ok = wait_or_abort(&sh->packed_full[stage], stage_parity, sh);
+      ok = __all_sync(~0u, wait_or_abort(&sh->packed_full[stage], stage_parity, sh));
       if (!ok) break;
       const uint32_t valid = sh->valid[i & 3][half * 2 + (warp & 1)];
       const bool there = (valid >> lane) & 1u;
@@ -548,11 +554,13 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   constexpr uint32_t kIdescS = instruction(kTok, false), kIdescO = instruction(D, true);
   const uint32_t q_at = lt::smem_u32(smem + Smem<D>::kQ), kv_at = lt::smem_u32(smem + Smem<D>::kKv);
   const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0), lead = elect_one();
-  bool ok = wait_or_abort(&sh->q_full, 0, sh);
+  bool ok = __all_sync(~0u, wait_or_abort(&sh->q_full, 0, sh));
   // One place for each product, in rolled loops: `which` alternates between the row tiles, and what goes
   // round is short. (Descriptors hold addresses in units of 16 bytes; the steps' offsets are
   // added to them.) Keys of tile i are in slot (i & 1) * 2, values in the next.
-  auto wait_slot = [&](int i, int part) { ok = ok && wait_or_abort(&sh->kv_full[(i & 1) * 2 + part], (i >> 1) & 1, sh); };
+  auto wait_slot = [&](int i, int part) {
+    ok = __all_sync(~0u, ok && wait_or_abort(&sh->kv_full[(i & 1) * 2 + part], (i >> 1) & 1, sh));
+  };
   if (job.tiles > 0) wait_slot(0, 0);
   const int steps = 2 * job.tiles + 1;  // even ones row tile A, odd ones row tile B
 #pragma unroll 1
@@ -575,7 +583,7 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
       const uint64_t value = desc_mn_major(kv_at + ((i & 1) * 2 + 1) * Smem<D>::kOperand, Smem<D>::kHalf);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        ok = wait_or_abort(&sh->p_full[which][half], i & 1, sh);
+        ok = __all_sync(~0u, wait_or_abort(&sh->p_full[which][half], i & 1, sh));
         if (!ok) break;
         fence_after();
 #pragma unroll
@@ -654,7 +662,7 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
     const int last = min(job.rows - 1, job.row0 + 255) / p.group;
     job.to = min(job.to, job.rq.length - job.rq.queries + last + 1);
     if (p.window > 0)
-      job.from = max(job.from, (job.rq.length - job.rq.queries + job.row0 / p.group + 1 - p.window) / kTile * kTile);
+      job.from = max(job.from, (job.rq.length - job.rq.queries + job.row0 / p.group + 1 - p.window) / kTok * kTok);
     job.tiles = job.to > job.from ? (job.to - job.from + kTok - 1) / kTok : 0;
   }
 

@@ -299,6 +299,14 @@ def test_prefill(dim, lengths, new, group, window, dtype):
     assert torch.equal(out, again), "two runs differ"
 
 
+@pytest.mark.parametrize("page", [1, 32, 64, 128, 1024])
+def test_prefill_page_sizes_with_parts_and_windows(page):
+    """Parts and windows that start inside a page, runs of positions longer and shorter than a page."""
+    for window in (0, 77, 300):
+        p = Problem([1100, 161], [33, 20], 1, 3, 64, page, "f16", seed=page + window)
+        p.check(*p.run(window=window), window=window)
+
+
 def test_prefill_scales_and_bad_pages():
     for spread, magnitude, scale in ((30.0, 1.0, None), (1.0, 1.0, -0.2), (1.0, 1.0, 0.0), (1.0, 1e-4, 300.0), (1.0, 3000.0, 1e-4)):
         p = Problem([300], [40], 1, 4, 64, 16, "bf16", seed=21, spread=spread, magnitude=magnitude)
