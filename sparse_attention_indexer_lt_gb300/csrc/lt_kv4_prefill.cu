@@ -109,15 +109,51 @@ __device__ __forceinline__ uint32_t elect_one() {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+// Loads from tensor memory, each with its wait in one statement: registers that are still to be written
+// must not be seen by the compiler, which would copy and reuse them.
+__device__ __forceinline__ void tmem_read16(uint32_t addr, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      :
+        "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_read32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      :
+        "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_read64(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, "
+      "%46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      :
+        "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(addr)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -129,13 +165,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
          "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
@@ -143,7 +172,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void arrive(uint64_t* bar) {
@@ -151,12 +179,19 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Waits for a phase; gives up after kWaitPolls, or as soon as another thread has.
-// (Per thread; a warp that goes on to .aligned instructions converges after it.)
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Shared* sh) {
+// A warp waits for a phase (each lane may name a barrier of its own); gives up after kWaitPolls, or as soon as
+// another warp has. Every poll ends in a vote, so the warp's control flow is uniform
+// whatever the lanes see: the callers go on to .aligned instructions, and keep descriptors
+// and counters in uniform registers, which a diverged warp would step twice.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Shared* sh) {
+  bool done = mbar_ready(bar, parity);
+  if (__all_sync(~0u, done)) return true;
+#pragma unroll 1
   for (uint32_t i = 0; i < lt::kWaitPolls; ++i) {
-    if (i == 0 ? mbar_ready(bar, parity) : lt::mbar_try_wait(bar, parity)) return true;
-    if (i > 0 && *(volatile int*)&sh->abort) return false;
+    done = done | lt::mbar_try_wait(bar, parity);
+    if (__all_sync(~0u, done)) return true;
+    const int aborted = *(volatile int*)&sh->abort;
+    if (__any_sync(~0u, aborted != 0)) return false;
   }
   *(volatile int*)&sh->abort = 1;
   return false;
@@ -247,66 +282,63 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   const uint32_t lane_base = sh->tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t s_at = lane_base + which * kTok, o_at = lane_base + 2 * kTok + which * D;
 
-  // The loop reads a tile's logits twice, 64 columns at a time, once for the maximum and once for the
-  // weights: that is little against 128 exponentials a row, and the loops stay short enough
-  // for the instruction cache that four kinds of warps share.
+  // The loop reads a tile's logits twice, once for the maximum and once for the weights: that is little
+  // against 128 exponentials a row, and the loops stay short enough for the instruction
+  // cache that four kinds of warps share.
   float m = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;  // m in units of log 2
   uint32_t poison = 0;                             // value groups in which this row is NaN
   bool ok = true;
   for (int i = 0; i < job.tiles; ++i) {
-    ok = wait_or_abort(&sh->s_full[which], i & 1, sh);
-    if (!__all_sync(~0u, ok)) {  // (the warp as a whole: what follows wants it converged)
-      ok = false;
-      break;
-    }
+    ok = wait_warp(&sh->s_full[which], i & 1, sh);
+    if (!ok) break;
     fence_after();
     const int pos0 = job.from + i * kTok;
     const uint32_t* valid = sh->valid[i & 3];
     const uint32_t* nan_rows = sh->nan_rows[i & 3];
     const uint4 valid4 = *reinterpret_cast<const uint4*>(valid), nan4 = *reinterpret_cast<const uint4*>(nan_rows);
-    const bool plain = (valid4.x & valid4.y & valid4.z & valid4.w) == ~0u && pos0 + kTok <= limit && pos0 >= low &&
-                       (nan4.x | nan4.y | nan4.z | nan4.w) == 0;
-    if (!__all_sync(~0u, plain)) {
-      // hide what this row does not see, in tensor memory
+    float top;
+    bool hidden = false;
+#pragma unroll 1
+    for (;;) {
+      float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[64];
+        tmem_read64(s_at + 64 * h, x);
+        const float* s = reinterpret_cast<const float*>(x);
+#pragma unroll
+        for (int c = 0; c < 64; c += 8) {
+          t0 = max3(t0, s[c], s[c + 1]);
+          t1 = max3(t1, s[c + 2], s[c + 3]);
+          t2 = max3(t2, s[c + 4], s[c + 5]);
+          t3 = max3(t3, s[c + 6], s[c + 7]);
+        }
+      }
+      top = fmaxf(max3(t0, t1, t2), t3) * factor;
+      // (looked at only now: the words come from shared memory, which the products keep busy)
+      const bool plain = (valid4.x & valid4.y & valid4.z & valid4.w) == ~0u && pos0 + kTok <= limit && pos0 >= low &&
+                         (nan4.x | nan4.y | nan4.z | nan4.w) == 0;
+      if (hidden || __all_sync(~0u, plain)) break;
+      // hide what this row does not see, in tensor memory, and take the maximum again
+      hidden = true;
 #pragma unroll 1
       for (int w = 0; w < 4; ++w) {
-        uint32_t x[32];
-        tmem_ld32(s_at + 32 * w, x);
+        uint32_t y[32];
+        tmem_read32(s_at + 32 * w, y);
         const int a = low - (pos0 + 32 * w), b = limit - (pos0 + 32 * w);  // (low >= 0: no overflow)
         uint32_t see = valid[w];
         see &= b >= 32 ? ~0u : b <= 0 ? 0u : (1u << b) - 1u;
         see &= a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a;
-        tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 32; ++c)
-          if (!((see >> c) & 1u)) x[c] = 0xFF800000u;
-        tmem_st32(s_at + 32 * w, x);
+          if (!((see >> c) & 1u)) y[c] = 0xFF800000u;
+        tmem_st32(s_at + 32 * w, y);
         for (uint32_t left = nan_rows[w] & see; left != 0; left &= left - 1)
           poison |= sh->nan_groups[i & 3][32 * w + __ffs(left) - 1];
         __syncwarp();
       }
       tmem_wait_st();
     }
-
-    float top = -INFINITY, top2 = -INFINITY;
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      uint32_t x[64];
-      const float* s = reinterpret_cast<const float*>(x);
-      tmem_ld32(s_at + 64 * h, x);
-      tmem_ld32(s_at + 64 * h + 32, x + 32);
-      tmem_wait_ld();
-      float top3 = s[0], top4 = s[1];
-#pragma unroll
-      for (int c = 2; c < 62; c += 4) {
-        top3 = max3(top3, s[c], s[c + 1]);
-        top4 = max3(top4, s[c + 2], s[c + 3]);
-      }
-      top = max3(top, top3, s[62]);
-      top2 = max3(top2, top4, s[63]);
-    }
-    top = fmaxf(top, top2) * factor;
-
     const bool moves = top > m + kSlack || (m == -INFINITY && top > m);
     if (__any_sync(~0u, moves)) {
       // S(i) is there, so the product O += P V of tile i - 1, issued before it, is done
@@ -319,8 +351,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           uint32_t o[16];
-          tmem_ld16(o_at + c, o);
-          tmem_wait_ld();
+          tmem_read16(o_at + c, o);
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
           tmem_st16(o_at + c, o);
@@ -332,10 +363,8 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
       uint32_t x[64], pk[32];
+      tmem_read64(s_at + 64 * h, x);
       float* s = reinterpret_cast<float*>(x);
-      tmem_ld32(s_at + 64 * h, x);
-      tmem_ld32(s_at + 64 * h + 32, x + 32);
-      tmem_wait_ld();
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         fma2(s[2 * e], s[2 * e + 1], factor, ref);
@@ -351,7 +380,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
       __syncwarp();
     }
   }
-  ok = wait_or_abort(&sh->o_full[which], 0, sh) && ok;
+  ok = wait_warp(&sh->o_full[which], 0, sh) && ok;
   __syncwarp();
   fence_after();
 
@@ -368,10 +397,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
 #pragma unroll 1
     for (int c = 0; c < per_pass; c += 16) {
       uint32_t o[16];
-      if (job.tiles > 0) {
-        tmem_ld16(o_at + c0 + c, o);
-        tmem_wait_ld();
-      }
+      if (job.tiles > 0) tmem_read16(o_at + c0 + c, o);
       const bool bad = !ok || ((poison >> ((c0 + c) / 32)) & 1u);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -438,7 +464,7 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
   uint32_t parity = 1;  // (the first round's stages are free)
 #pragma unroll 1
   for (int n = 0; n < stages; ++n) {
-    if (!__all_sync(~0u, wait_or_abort(&sh->packed_empty[stage], parity, sh))) break;
+    if (!wait_warp(&sh->packed_empty[stage], parity, sh)) break;
     uint32_t valid[2] = {0u, 0u};
     int count[kMost];
 #pragma unroll
@@ -488,29 +514,30 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
   bool ok = true;
 #pragma unroll 1
   for (int i = 0; i < job.tiles; ++i) {
-    ok = __all_sync(~0u, wait_or_abort(&sh->kv_empty[slot], slot_parity, sh));
+    ok = wait_warp(&sh->kv_empty[slot], slot_parity, sh);
     if (!ok) break;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
-      ok = __all_sync(~0u, wait_or_abort(&sh->packed_full[stage], stage_parity, sh));
+      ok = wait_warp(&sh->packed_full[stage], stage_parity, sh);
       if (!ok) break;
       const uint32_t valid = sh->valid[i & 3][half * 2 + (warp & 1)];
       const bool there = (valid >> lane) & 1u;
       const uint8_t* from = smem + Smem<D>::kPacked + (stage * kPart + row) * kRow;
       // scales, fp16 pairs; a position that is not there counts as zeros, and so does a NaN value
-      // (noted for the rows that see it)
       uint32_t sc[D / 64];
-      uint32_t nan = 0;
 #pragma unroll
       for (int g = 0; g < D / 64; ++g) {
         sc[g] = there ? reinterpret_cast<const uint32_t*>(from + D + part * (D / 16))[g] : 0u;
-        if (part == 1) {
-          const uint32_t n = nan_halves(sc[g]);
-          sc[g] &= ~n;
+        if (part == 1) sc[g] &= ~nan_halves(sc[g]);
+      }
+      if (part == 0) {
+        // the NaN values are noted here, with the keys: the softmax starts when the keys are there
+        uint32_t nan = 0;
+#pragma unroll
+        for (int g = 0; g < D / 64; ++g) {
+          const uint32_t n = there ? nan_halves(reinterpret_cast<const uint32_t*>(from + D + D / 16)[g]) : 0u;
           nan |= ((n & 1u) | ((n >> 15) & 2u)) << (2 * g);
         }
-      }
-      if (part == 1) {
         const uint32_t nan_rows = __ballot_sync(~0u, nan != 0);
         if (lane == 0) sh->nan_rows[i & 3][half * 2 + (warp & 1)] = nan_rows;
         if (nan_rows) sh->nan_groups[i & 3][half * kPart + row] = (uint8_t)nan;
@@ -554,47 +581,66 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   constexpr uint32_t kIdescS = instruction(kTok, false), kIdescO = instruction(D, true);
   const uint32_t q_at = lt::smem_u32(smem + Smem<D>::kQ), kv_at = lt::smem_u32(smem + Smem<D>::kKv);
   const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0), lead = elect_one();
-  bool ok = __all_sync(~0u, wait_or_abort(&sh->q_full, 0, sh));
-  // One place for each product, in rolled loops: `which` alternates between the row tiles, and what goes
-  // round is short. (Descriptors hold addresses in units of 16 bytes; the steps' offsets are
-  // added to them.) Keys of tile i are in slot (i & 1) * 2, values in the next.
-  auto wait_slot = [&](int i, int part) {
-    ok = __all_sync(~0u, ok && wait_or_abort(&sh->kv_full[(i & 1) * 2 + part], (i >> 1) & 1, sh));
+  bool ok = wait_warp(&sh->q_full, 0, sh);
+  // A look at a barrier takes some 250 clocks while the products keep shared memory busy. So the look at
+  // the one that is needed next is sent ahead of a product's instructions, and only a phase
+  // that was not complete then is waited for.
+  bool early = false;
+  auto look = [&](uint64_t* bar, uint32_t phase) { early = mbar_ready(bar, phase & 1); };
+  auto need = [&](uint64_t* bar, uint32_t phase) {
+    if (!__all_sync(~0u, early)) ok = wait_warp(bar, phase & 1, sh) && ok;
+    early = false;
+    return ok;
   };
-  if (job.tiles > 0) wait_slot(0, 0);
-  const int steps = 2 * job.tiles + 1;  // even ones row tile A, odd ones row tile B
+  // keys of tile i are in slot (i & 1) * 2, values in the next
+  auto key_full = [&](int i) { return &sh->kv_full[(i & 1) * 2]; };
+  auto value_full = [&](int i) { return &sh->kv_full[(i & 1) * 2 + 1]; };
+  const int tiles = ok ? job.tiles : 0;
+  if (tiles > 0) need(key_full(0), 0);
+  // One place for each product, in a rolled loop: even steps row tile A, odd ones row tile B; first the weights
+  // of tile i by its values, then the logits of tile i + 1. (Descriptors hold addresses in
+  // units of 16 bytes; the steps' offsets are added to them.)
 #pragma unroll 1
-  for (int step = 0; step <= steps && ok && job.tiles > 0; ++step) {
-    // first the weights of tile i by its values, then the logits of tile i + 1
+  for (int step = 0; step <= 2 * tiles + 1 && ok && tiles > 0; ++step) {
     const int which = step & 1, i = (step >> 1) - 1;
+    const bool weights = i >= 0, keys = i + 1 < tiles;
+    uint64_t* const value_empty = &sh->kv_empty[(i & 1) * 2 + 1];
+    uint64_t* const key_empty = &sh->kv_empty[((i + 1) & 1) * 2];
     if (which == 1 && !job.two) {
-      if (i >= 0) mma_commit(&sh->kv_empty[(i & 1) * 2 + 1], lead);
-      if (i + 1 < job.tiles) mma_commit(&sh->kv_empty[((i + 1) & 1) * 2], lead);
+      if (weights) mma_commit(value_empty, lead);
+      if (keys) mma_commit(key_empty, lead);
       continue;
     }
-    if (which == 0 && i >= 0) {
-      // V(i) and K(i + 1) are waited for while the other row tile's product runs
-      wait_slot(i, 1);
-      if (i + 1 < job.tiles) wait_slot(i + 1, 0);
-      if (!ok) break;
-    }
-    fence_after();
-    if (i >= 0) {
+    if (weights) {
+      if (which == 0) {
+        if (!need(value_full(i), i >> 1)) break;
+        look(&sh->p_full[0][0], i);
+      }
       const uint64_t value = desc_mn_major(kv_at + ((i & 1) * 2 + 1) * Smem<D>::kOperand, Smem<D>::kHalf);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        ok = __all_sync(~0u, wait_or_abort(&sh->p_full[which][half], i & 1, sh));
-        if (!ok) break;
+        if (!need(&sh->p_full[which][half], i)) break;
         fence_after();
+        if (half == 0)
+          look(&sh->p_full[which][1], i);
+        else if (which == 0 && keys)
+          look(key_full(i + 1), (i + 1) >> 1);
 #pragma unroll
         for (int k = 0; k < kTok / 32; ++k)
           mma_ts(tmem + 2 * kTok + which * D, tmem + which * kTok + half * 32 + k * 8,
                  value + half * ((kTok / 2 * 128) >> 4) + k * (2048 >> 4), kIdescO, i > 0 || half > 0 || k > 0, lead);
       }
       if (!ok) break;
-      if (which == 1) mma_commit(&sh->kv_empty[(i & 1) * 2 + 1], lead);
+      if (which == 1) mma_commit(value_empty, lead);
     }
-    if (i + 1 < job.tiles) {
+    if (keys) {
+      if (which == 0 && weights && !need(key_full(i + 1), (i + 1) >> 1)) break;
+      fence_after();
+      // what the next step begins with
+      if (which == 1 || !job.two)
+        look(value_full(i + 1), (i + 1) >> 1);
+      else if (weights)
+        look(&sh->p_full[1][0], i);
       const uint64_t q = desc_k_major(q_at + which * Smem<D>::kOperand);
       const uint64_t key = desc_k_major(kv_at + ((i + 1) & 1) * 2 * Smem<D>::kOperand);
 #pragma unroll 1
@@ -604,7 +650,7 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
           mma_ss(tmem + which * kTok, q + c * (Smem<D>::kHalf >> 4) + k * 2, key + c * (Smem<D>::kHalf >> 4) + k * 2, kIdescS,
                  c > 0 || k > 0, lead);
       mma_commit(&sh->s_full[which], lead);
-      if (which == 1) mma_commit(&sh->kv_empty[((i + 1) & 1) * 2], lead);
+      if (which == 1) mma_commit(key_empty, lead);
     }
   }
   mma_commit(&sh->o_full[0], lead);
