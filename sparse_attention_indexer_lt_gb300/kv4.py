@@ -16,11 +16,12 @@ and, over the positions that the indexer's top-k kept,
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
 
-from . import DTYPE_BF16, DTYPE_F32, LtError, _ptr, load
+from . import DTYPE_BF16, DTYPE_F32, LtError, load
 
 DTYPE_F16 = 2
 _ALL = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
@@ -36,31 +37,47 @@ class PageStep(NamedTuple):
     num_free: torch.Tensor   # int32 [1]
 
 
-def _stream(stream, dev):
-    return ctypes.c_void_p((stream or torch.cuda.current_stream(dev)).cuda_stream)
+# The checks are on the path of every decode step, whose kernels take a few microseconds: devices are
+# compared by their index, the stream is taken by its handle, outputs are made with new_empty.
 
 
-def _want(name, t, dtype, dev=None, shape=None):
+def _raw_stream(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _call(name, index, *args):
+    """Calls the library with the tensors' device current; raises on an error status."""
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args)
+    if st != 0:
+        raise LtError(name, st)
+
+
+def _want(name, t, dtype, index=None, shape=None):
     """A contiguous CUDA tensor of this type (and shape), on this device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
     if t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
     return t
 
 
-def _result(name, t, shape, dtype, dev, stream):
+def _result(name, t, shape, dtype, like, stream):
     """The caller's output tensor, or a new one whose memory belongs to the stream that writes it."""
     if t is not None:
-        return _want(name, t, dtype, dev, shape)
+        return _want(name, t, dtype, like.get_device(), shape)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _int32(name, x, least):
@@ -93,11 +110,19 @@ def kv4_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, device=N
 
 
 def _check_cache(cache):
-    """(pages, kv_heads, page_size, head_dim) of a cache."""
+    """(pages, kv_heads, page_size, head_dim, device index) of a cache."""
     _want("cache", cache, torch.uint8)
     if cache.dim() != 4 or cache.shape[3] not in _DIM_OF_ROW:
         raise ValueError("cache must be [pages, kv_heads, page_size, row bytes], as kv4_cache makes it")
-    return cache.shape[0], cache.shape[1], _check_page_size(cache.shape[2]), _DIM_OF_ROW[cache.shape[3]]
+    pages, heads, page_size, row = cache.shape
+    return pages, heads, _check_page_size(page_size), _DIM_OF_ROW[row], cache.get_device()
+
+
+def _check_table(block_table, index, n):
+    _want("block_table", block_table, torch.int32, index)
+    if block_table.dim() != 2 or block_table.shape[0] != n or block_table.shape[1] < 1:
+        raise ValueError("block_table must be [requests, pages a request]")
+    return block_table.shape[1]
 
 
 def page_release(lengths: torch.Tensor, finished: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -105,30 +130,21 @@ def page_release(lengths: torch.Tensor, finished: torch.Tensor, block_table: tor
                  out_num_free: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
     """Gives the pages of finished requests (bool or uint8 [requests]) back to free_pages (in place);
     returns (lengths, num_free): 0 for the finished requests, and the new number of free pages."""
-    lib = load()
     _want("lengths", lengths, torch.int32)
-    dev, n = lengths.device, lengths.numel()
+    index, n = lengths.get_device(), lengths.numel()
     if not isinstance(finished, torch.Tensor) or finished.dtype not in (torch.bool, torch.uint8):
         raise TypeError("finished must be a bool or uint8 tensor")
-    _want("finished", finished, finished.dtype, dev, (n,))
-    _check_table(block_table, dev, n)
-    _want("free_pages", free_pages, torch.int32, dev)
-    _want("num_free", num_free, torch.int32, dev, (1,))
-    out_lengths = _result("out_lengths", out_lengths, (n,), torch.int32, dev, stream)
-    out_num_free = _result("out_num_free", out_num_free, (1,), torch.int32, dev, stream)
-    with torch.cuda.device(dev):
-        st = lib.lt_page_release(_ptr(lengths), _ptr(finished), n, _ptr(block_table), block_table.shape[1],
-                                 _ptr(free_pages), free_pages.numel(), _ptr(num_free), _check_page_size(page_size),
-                                 _ptr(out_lengths), _ptr(out_num_free), _stream(stream, dev))
-    if st != 0:
-        raise LtError("lt_page_release", st)
+    _want("finished", finished, finished.dtype, index, (n,))
+    width = _check_table(block_table, index, n)
+    _want("free_pages", free_pages, torch.int32, index)
+    _want("num_free", num_free, torch.int32, index, (1,))
+    page_size = _check_page_size(page_size)
+    out_lengths = _result("out_lengths", out_lengths, (n,), torch.int32, lengths, stream)
+    out_num_free = _result("out_num_free", out_num_free, (1,), torch.int32, lengths, stream)
+    _call("lt_page_release", index, lengths.data_ptr(), finished.data_ptr(), n, block_table.data_ptr(), width,
+          free_pages.data_ptr(), free_pages.numel(), num_free.data_ptr(), page_size, out_lengths.data_ptr(),
+          out_num_free.data_ptr(), _raw_stream(stream, index))
     return out_lengths, out_num_free
-
-
-def _check_table(block_table, dev, n):
-    _want("block_table", block_table, torch.int32, dev)
-    if block_table.dim() != 2 or block_table.shape[0] != n or block_table.shape[1] < 1:
-        raise ValueError("block_table must be [requests, pages a request]")
 
 
 def page_extend(lengths: torch.Tensor, new_tokens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -138,31 +154,28 @@ def page_extend(lengths: torch.Tensor, new_tokens: torch.Tensor, block_table: to
                 stream: torch.cuda.Stream | None = None) -> PageStep:
     """Places the new tokens of a step: takes pages from the top of free_pages, writes them into
     block_table (in place) and returns slots, positions, starts, lengths and the pages left."""
-    lib = load()
     _want("lengths", lengths, torch.int32)
-    dev, n = lengths.device, lengths.numel()
-    _want("new_tokens", new_tokens, torch.int32, dev, (n,))
-    _check_table(block_table, dev, n)
-    _want("free_pages", free_pages, torch.int32, dev)
-    _want("num_free", num_free, torch.int32, dev, (1,))
+    index, n = lengths.get_device(), lengths.numel()
+    _want("new_tokens", new_tokens, torch.int32, index, (n,))
+    width = _check_table(block_table, index, n)
+    _want("free_pages", free_pages, torch.int32, index)
+    _want("num_free", num_free, torch.int32, index, (1,))
+    page_size = _check_page_size(page_size)
     max_tokens = _int32("max_tokens", max_tokens, 0)
-    step = PageStep(_result("out_slots", out_slots, (max_tokens,), torch.int64, dev, stream),
-                    _result("out_positions", out_positions, (max_tokens,), torch.int32, dev, stream),
-                    _result("out_starts", out_starts, (n + 1,), torch.int32, dev, stream),
-                    _result("out_lengths", out_lengths, (n,), torch.int32, dev, stream),
-                    _result("out_num_free", out_num_free, (1,), torch.int32, dev, stream))
-    with torch.cuda.device(dev):
-        st = lib.lt_page_extend(_ptr(lengths), _ptr(new_tokens), n, _ptr(block_table), block_table.shape[1],
-                                _ptr(free_pages), free_pages.numel(), _ptr(num_free), _check_page_size(page_size),
-                                max_tokens, _ptr(step.slots), _ptr(step.positions), _ptr(step.starts),
-                                _ptr(step.lengths), _ptr(step.num_free), _stream(stream, dev))
-    if st != 0:
-        raise LtError("lt_page_extend", st)
-    return step
+    slots = _result("out_slots", out_slots, (max_tokens,), torch.int64, lengths, stream)
+    positions = _result("out_positions", out_positions, (max_tokens,), torch.int32, lengths, stream)
+    starts = _result("out_starts", out_starts, (n + 1,), torch.int32, lengths, stream)
+    out_lengths = _result("out_lengths", out_lengths, (n,), torch.int32, lengths, stream)
+    out_num_free = _result("out_num_free", out_num_free, (1,), torch.int32, lengths, stream)
+    _call("lt_page_extend", index, lengths.data_ptr(), new_tokens.data_ptr(), n, block_table.data_ptr(), width,
+          free_pages.data_ptr(), free_pages.numel(), num_free.data_ptr(), page_size, max_tokens, slots.data_ptr(),
+          positions.data_ptr(), starts.data_ptr(), out_lengths.data_ptr(), out_num_free.data_ptr(),
+          _raw_stream(stream, index))
+    return PageStep(slots, positions, starts, out_lengths, out_num_free)
 
 
-def _check_slots(slots, dev, tokens):
-    _want("slots", slots, torch.int64, dev)
+def _check_slots(slots, index, tokens):
+    _want("slots", slots, torch.int64, index)
     if slots.dim() != 1 or (tokens is not None and slots.numel() != tokens):
         raise ValueError("slots must be int64 [tokens]")
 
@@ -171,26 +184,21 @@ def kv4_store(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torc
               stream: torch.cuda.Stream | None = None) -> None:
     """Quantises k, v [tokens, kv_heads, head_dim] (float32, bfloat16 or float16; any strides of tokens
     and heads) into the cache rows that slots (int64 [tokens]; -1 skips) name."""
-    lib = load()
-    pages, heads, page_size, dim = _check_cache(cache)
-    dev = cache.device
+    pages, heads, page_size, dim, index = _check_cache(cache)
     for name, t in (("k", k), ("v", v)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-        if t.device != dev or t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
-            raise ValueError(f"{name} must be [tokens, {heads}, {dim}] on {dev}")
-        if t.numel() > 0 and t.stride(2) != 1:
-            raise ValueError(f"the channels of {name} must be contiguous")
-    if k.dtype not in _ALL or v.dtype != k.dtype or v.shape != k.shape:
+        if t.get_device() != index or t.dim() != 3 or t.shape[1:] != (heads, dim):
+            raise ValueError(f"{name} must be [tokens, {heads}, {dim}] on cuda:{index}")
+    dtype, tokens = _ALL.get(k.dtype), k.shape[0]
+    if dtype is None or v.dtype != k.dtype or v.shape != k.shape:
         raise ValueError("k and v must have one shape and one type: float32, bfloat16 or float16")
-    tokens = k.shape[0]
-    _check_slots(slots, dev, tokens)
-    with torch.cuda.device(dev):
-        st = lib.lt_kv4_store(_ptr(k), _ptr(v), _ALL[k.dtype], tokens, heads, dim, k.stride(0), k.stride(1),
-                              v.stride(0), v.stride(1), _ptr(slots), _ptr(cache), pages, page_size,
-                              _stream(stream, dev))
-    if st != 0:
-        raise LtError("lt_kv4_store", st)
+    ks, vs = k.stride(), v.stride()
+    if tokens > 0 and (ks[2] != 1 or vs[2] != 1):
+        raise ValueError("the channels of k and v must be contiguous")
+    _check_slots(slots, index, tokens)
+    _call("lt_kv4_store", index, k.data_ptr(), v.data_ptr(), dtype, tokens, heads, dim, ks[0], ks[1], vs[0], vs[1],
+          slots.data_ptr(), cache.data_ptr(), pages, page_size, _raw_stream(stream, index))
 
 
 def kv4_load(cache: torch.Tensor, slots: torch.Tensor, *, dtype: torch.dtype = torch.float16,
@@ -198,21 +206,25 @@ def kv4_load(cache: torch.Tensor, slots: torch.Tensor, *, dtype: torch.dtype = t
              stream: torch.cuda.Stream | None = None):
     """The numbers that the slots stand for: (k, v), each [tokens, kv_heads, head_dim]; zeros for a slot
     outside the cache."""
-    lib = load()
-    pages, heads, page_size, dim = _check_cache(cache)
-    dev = cache.device
+    pages, heads, page_size, dim, index = _check_cache(cache)
     if dtype not in _ALL:
         raise ValueError("dtype must be float32, bfloat16 or float16")
-    _check_slots(slots, dev, None)
-    shape = (slots.numel(), heads, dim)
-    out_k = _result("out_k", out_k, shape, dtype, dev, stream)
-    out_v = _result("out_v", out_v, shape, dtype, dev, stream)
-    with torch.cuda.device(dev):
-        st = lib.lt_kv4_load(_ptr(cache), pages, page_size, _ptr(slots), slots.numel(), heads, dim, _ptr(out_k),
-                             _ptr(out_v), _ALL[dtype], _stream(stream, dev))
-    if st != 0:
-        raise LtError("lt_kv4_load", st)
+    _check_slots(slots, index, None)
+    tokens = slots.shape[0]
+    out_k = _result("out_k", out_k, (tokens, heads, dim), dtype, cache, stream)
+    out_v = _result("out_v", out_v, (tokens, heads, dim), dtype, cache, stream)
+    _call("lt_kv4_load", index, cache.data_ptr(), pages, page_size, slots.data_ptr(), tokens, heads, dim,
+          out_k.data_ptr(), out_v.data_ptr(), _ALL[dtype], _raw_stream(stream, index))
     return out_k, out_v
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(index, tokens, q_heads, kv_heads, head_dim, requests, max_new, list_len):
+    """lt_kv4_workspace's answer: it goes by these sizes and the device alone."""
+    need = ctypes.c_int64(0)
+    _call("lt_kv4_workspace", index, tokens, q_heads, kv_heads, head_dim, requests, max_new, list_len,
+          ctypes.byref(need))
+    return need.value
 
 
 def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor, *,
@@ -231,56 +243,50 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     workspace (uint8) replaces the scratch memory that a call takes from torch's allocator for its
     stream; see lt_kv4_workspace for its size.
     """
-    lib = load()
-    pages, heads, page_size, dim = _check_cache(cache)
-    dev = cache.device
+    pages, heads, page_size, dim, index = _check_cache(cache)
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise TypeError("q must be a CUDA tensor")
-    if q.dtype not in (torch.bfloat16, torch.float16):
+    dtype = q.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float16:
         raise TypeError("q must be bfloat16 or float16")
-    if q.device != dev or q.dim() != 3 or q.shape[2] != dim or q.shape[1] % heads or q.shape[1] < 1:
-        raise ValueError(f"q must be [tokens, a multiple of {heads} heads, {dim}] on {dev}")
+    if q.get_device() != index or q.dim() != 3 or q.shape[2] != dim or q.shape[1] % heads or q.shape[1] < 1:
+        raise ValueError(f"q must be [tokens, a multiple of {heads} heads, {dim}] on cuda:{index}")
     tokens, q_heads, _ = q.shape
-    if q.numel() > 0 and (q.stride(2) != 1 or q.stride(0) % 8 or q.stride(1) % 8 or q.data_ptr() % 16):
+    token_stride, head_stride, channel_stride = q.stride()
+    q_ptr = q.data_ptr()
+    if tokens > 0 and (channel_stride != 1 or token_stride % 8 or head_stride % 8 or q_ptr % 16):
         raise ValueError("q must have contiguous channels, strides that are multiples of 8 and a 16-byte aligned start")
-    _want("lengths", lengths, torch.int32, dev)
+    _want("lengths", lengths, torch.int32, index)
     n = lengths.numel()
-    _check_table(block_table, dev, n)
+    width = _check_table(block_table, index, n)
     max_new = _int32("max_new", max_new, 1)
     if starts is None:
         if tokens != n or max_new != 1:
             raise ValueError("without starts, q must have one row a request")
     else:
-        _want("starts", starts, torch.int32, dev, (n + 1,))
+        _want("starts", starts, torch.int32, index, (n + 1,))
     window = _int32("window", window, 0)
-    if window and positions is not None:
-        raise ValueError("window is not used with positions")
     list_len = 0
     if positions is not None:
-        _want("positions", positions, torch.int32, dev)
+        if window:
+            raise ValueError("window is not used with positions")
+        _want("positions", positions, torch.int32, index)
         if positions.dim() != 2 or positions.shape[0] != tokens or positions.shape[1] < 1:
             raise ValueError("positions must be int32 [tokens, at least one]")
         list_len = positions.shape[1]
-    out = _result("out", out, (tokens, q_heads, dim), q.dtype, dev, stream)
-    lse = _result("out_lse", out_lse, (tokens, q_heads), torch.float32, dev, stream) if with_lse else None
-    scale = dim ** -0.5 if scale is None else float(scale)
-    with torch.cuda.device(dev):
-        need = ctypes.c_int64(0)
-        st = lib.lt_kv4_workspace(tokens, q_heads, heads, dim, n, max_new, list_len, ctypes.byref(need))
-        if st != 0:
-            raise LtError("lt_kv4_workspace", st)
-        s = stream or torch.cuda.current_stream(dev)
-        if workspace is None and need.value > 0:
-            workspace = _result("workspace", None, (need.value,), torch.uint8, dev, stream)
-        elif workspace is not None:
-            _want("workspace", workspace, torch.uint8, dev)
-            if workspace.numel() < need.value:
-                raise ValueError(f"workspace must have at least {need.value} bytes")
-        st = lib.lt_kv4_attention(_ptr(q), _ALL[q.dtype], tokens, q_heads, heads, dim, q.stride(0), q.stride(1),
-                                  _ptr(cache), pages, page_size, _ptr(block_table), block_table.shape[1],
-                                  _ptr(lengths), n, _ptr(starts), max_new, _ptr(positions), list_len, window,
-                                  scale, _ptr(out), _ptr(lse), _ptr(workspace),
-                                  0 if workspace is None else workspace.numel(), ctypes.c_void_p(s.cuda_stream))
-    if st != 0:
-        raise LtError("lt_kv4_attention", st)
+    out = _result("out", out, (tokens, q_heads, dim), dtype, q, stream)
+    lse = _result("out_lse", out_lse, (tokens, q_heads), torch.float32, q, stream) if with_lse else None
+    need = _workspace_bytes(index, tokens, q_heads, heads, dim, n, max_new, list_len)
+    if workspace is not None:
+        _want("workspace", workspace, torch.uint8, index)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace must have at least {need} bytes")
+    elif need > 0:
+        workspace = _result("workspace", None, (need,), torch.uint8, q, stream)
+    _call("lt_kv4_attention", index, q_ptr, _ALL[dtype], tokens, q_heads, heads, dim, token_stride, head_stride,
+          cache.data_ptr(), pages, page_size, block_table.data_ptr(), width, lengths.data_ptr(), n,
+          None if starts is None else starts.data_ptr(), max_new, None if positions is None else positions.data_ptr(),
+          list_len, window, dim ** -0.5 if scale is None else scale, out.data_ptr(),
+          None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.numel(), _raw_stream(stream, index))
     return (out, lse) if with_lse else out
