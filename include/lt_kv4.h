@@ -156,7 +156,7 @@ lt_status lt_kv4_load(const void* cache, int64_t pages, int32_t page_size, const
  *   positions  int32 [tokens][list_len] or NULL
  *   out        [tokens][q_heads][head_dim] of `dtype`, contiguous
  *   lse        float [tokens][q_heads] or NULL
- *   workspace  lt_kv4_workspace() bytes, 16-byte aligned; no contents kept
+ *   workspace  lt_kv4_workspace() bytes, 16-byte aligned (NULL if 0); no contents kept
  * q_heads is a multiple of kv_heads; head_dim 64, 128 or 256.
  */
 lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t q_heads,
@@ -169,9 +169,11 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
                            void* stream);
 
 /* Bytes of workspace that lt_kv4_attention needs for these sizes on the current
- * device (list_len 0: without positions). */
+ * device: 0 where a request's parts are joined within the launch. list_len 0:
+ * without positions (else window is 0); positions = table_width * page_size. */
 lt_status lt_kv4_workspace(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                           int32_t requests, int32_t max_new, int32_t list_len, int64_t* bytes);
+                           int32_t requests, int32_t max_new, int32_t list_len, int64_t positions,
+                           int32_t window, int64_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -99,7 +99,7 @@ def load() -> ctypes.CDLL:
     lib.lt_kv4_load.argtypes = [vp, i64, i32, vp, i64, i32, i32, vp, vp, i32, vp]
     lib.lt_kv4_attention.argtypes = [vp, i32, i64, i32, i32, i32, i64, i64, vp, i64, i32, vp, i32, vp, i32, vp, i32,
                                      vp, i32, i32, ctypes.c_float, vp, vp, vp, i64, vp]
-    lib.lt_kv4_workspace.argtypes = [i64, i32, i32, i32, i32, i32, i32, vp]
+    lib.lt_kv4_workspace.argtypes = [i64, i32, i32, i32, i32, i32, i32, i64, i32, vp]
     for name in ("lt_page_release", "lt_page_extend", "lt_kv4_store", "lt_kv4_load", "lt_kv4_attention",
                  "lt_kv4_workspace"):
         getattr(lib, name).restype = ctypes.c_int

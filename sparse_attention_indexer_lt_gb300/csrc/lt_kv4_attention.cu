@@ -87,6 +87,22 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive;\n barrier.cluster.wait;" ::: "memory");
+}
+__device__ __forceinline__ float peer_f32(uint32_t addr, int rank) {
+  float v;
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}"
+               : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_f32x4(uint32_t addr, int rank) {
+  float4 v;
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %4, %5;\n ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr), "r"(rank) : "memory");
+  return v;
+}
+
 template <int D, int NT, bool kList>
 __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(AttentionParams p) {
   using Sh = Shape<D, NT>;
@@ -96,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][Sh::kStages];
   __shared__ uint32_t valid_of[kWarps][Sh::kStages];
-  __shared__ float m_of[kWarps][NT * 8], l_of[kWarps][NT * 8];
+  __shared__ float m_of[kWarps][NT * 8], l_of[kWarps][NT * 8], part_log2[NT * 8];
   __shared__ int64_t sums[kWarps];
   __shared__ Place found;
   __shared__ int gave_up;
@@ -110,7 +126,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   if (tid == 0) gave_up = 0;
   dependency_wait();
 
-  const int64_t unit = blockIdx.x;
+  // with p.parts > 0 a request (a list) is cut into that many parts, the CTAs of one cluster
+  const int rank = p.parts > 0 ? (int)(blockIdx.x % p.parts) : 0;
+  const int64_t unit = p.parts > 0 ? blockIdx.x / p.parts : blockIdx.x;
   const int row_tile = (int)(unit % p.row_tiles);
   const int head = (int)(unit / p.row_tiles % p.heads);
   const int flat = (int)(unit / p.row_tiles / p.heads);
@@ -119,16 +137,23 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   Request rq;
   int request, count, token0, rows, from, to;
   if constexpr (kList) {
-    token0 = flat / p.target;  // one query token
-    const int split = flat % p.target;
+    token0 = flat;  // one query token
     request = owner_of_token(p, token0);
     if (request < 0) return;  // (rows past starts[requests])
     rq = request_of(p, request);
-    count = p.target;
     rows = p.group;
-    const int chunk = ((p.list_len + p.target - 1) / p.target + kTile - 1) / kTile * kTile;
-    from = min(split * chunk, p.list_len);
-    to = min(from + chunk, p.list_len);
+    from = 0;
+    to = p.list_len;
+    count = 1;
+    __syncthreads();
+  } else if (p.parts > 0) {
+    request = flat;
+    rq = request_of(p, request);
+    rows = rq.queries * p.group;
+    token0 = rq.first;
+    from = rq.low;
+    to = rq.length;
+    count = 1;
     __syncthreads();
   } else {
     Place pl;
@@ -152,6 +177,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
     const int last = min(rows - 1, row0 + NT * 8 - 1) / p.group;
     to = min(to, rq.length - rq.queries + last + 1);
     if (p.window > 0) from = max(from, (rq.length - rq.queries + row0 / p.group + 1 - p.window) / kTile * kTile);
+  }
+  if (p.parts > 1) {
+    // the cluster's CTAs take equal runs of tiles
+    const int all = to > from ? (to - from + kTile - 1) / kTile : 0, mine = (all + p.parts - 1) / p.parts * kTile;
+    const int64_t at = from + (int64_t)rank * mine;
+    from = (int)(at < to ? at : to);
+    to = (int)(at + mine < to ? at + mine : to);
   }
   const int tiles = to > from ? (to - from + kTile - 1) / kTile : 0;
 
@@ -242,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   int stage = 0;
   uint32_t parity = 0;
   for (int tile = warp; tile < tiles; tile += kWarps) {
-    ok = wait_bounded(&bars[warp][stage], parity) && ok;
+    ok = wait_bounded(&bars[warp][stage], parity) && ok;  // (the warp votes: it stays converged)
     const uint32_t valid = valid_of[warp][stage];
     const uint32_t base = ring + stage * Sh::kTileBytes;
     const int pos0 = from + tile * kTile;
@@ -455,6 +487,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   __syncthreads();
   const bool final_here = count == 1;
   const int64_t part = (((int64_t)flat * p.heads + head) * p.row_tiles + row_tile) * (NT * 8);
+  auto write_out = [&](int row, int ch, float4 o, float log2_sum) {
+    const int64_t out_row = (int64_t)(token0 + (row0 + row) / p.group) * p.heads * p.group + head * p.group + (row0 + row) % p.group;
+    store4(p, out_row * D + ch, o);
+    if (p.lse != nullptr && ch == 0) p.lse[out_row] = log2_sum * 0.6931471805599453f;
+  };
   for (int u = tid; u < NT * 8 * (D / 4); u += kThreads) {
     const int row = u / (D / 4), ch = u % (D / 4) * 4;
     if (row0 + row >= rows) break;
@@ -478,15 +515,47 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
       o = make_float4(NAN, NAN, NAN, NAN);
       log2_sum = NAN;
     }
-    if (final_here) {
-      const int64_t token = token0 + (row0 + row) / p.group;
-      const int qh = head * p.group + (row0 + row) % p.group;
-      store4(p, (token * p.heads * p.group + qh) * D + ch, o);
-      if (p.lse != nullptr && ch == 0) p.lse[token * p.heads * p.group + qh] = log2_sum * 0.6931471805599453f;
+    if (p.parts > 1) {
+      // this thread alone has read the element's place: the part stays here for the cluster to read
+      *reinterpret_cast<float4*>(joined + row * kPitch + ch) = o;
+      if (ch == 0) part_log2[row] = log2_sum;
+    } else if (final_here) {
+      write_out(row, ch, o, log2_sum);
     } else {
       *reinterpret_cast<float4*>(p.part_o + (part + row) * D + ch) = o;
       if (ch == 0) p.part_lse[part + row] = log2_sum;
     }
+  }
+  if (p.parts > 1) {
+    // join the cluster's parts over distributed shared memory, each CTA a share of the elements
+    cluster_sync();
+    const uint32_t o_at = lt::smem_u32(joined), l_at = lt::smem_u32(part_log2);
+    for (int u = rank * kThreads + tid; u < NT * 8 * (D / 4); u += p.parts * kThreads) {
+      const int row = u / (D / 4), ch = u % (D / 4) * 4;
+      if (row0 + row >= rows) break;
+      float top = -INFINITY;
+      bool bad = false;
+      for (int r = 0; r < p.parts; ++r) {
+        const float e = peer_f32(l_at + row * 4, r);
+        top = fmaxf(top, e);
+        bad = bad || e != e;
+      }
+      float sum = 0.0f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int r = 0; r < p.parts; ++r) {
+        const float e = peer_f32(l_at + row * 4, r);
+        const float4 x = peer_f32x4(o_at + (row * kPitch + ch) * 4, r);
+        const float w = e == -INFINITY ? 0.0f : exp2_fast(e - top);
+        sum += w;
+        if (e != -INFINITY) o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+      if (bad) o = make_float4(NAN, NAN, NAN, NAN);
+      write_out(row, ch, o, bad ? NAN : sum == 0.0f ? -INFINITY : top + __log2f(sum));
+    }
+    cluster_sync();  // (a CTA's shared memory stays until its peers have read it)
   }
 }
 
@@ -495,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
 constexpr int kJoinThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionParams p, int rows_per_cta, int list) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionParams p, int rows_per_cta) {
   constexpr int kVec = D / 32;
   __shared__ float o_of[kJoinThreads / 32][D];
   __shared__ float sum_of[kJoinThreads / 32], top_of[kJoinThreads / 32];
@@ -506,20 +575,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionParams p, i
   const int qh = (int)(blockIdx.x % q_heads), head = qh / p.group;
   const int request = owner_of_token(p, (int)token);
   if (request < 0) return;
-  int base, n, row;
-  if (list) {
-    base = (int)token * p.target;
-    n = p.target;
-    row = qh % p.group;
-  } else {
-    const int2 pl = p.plan[request];
-    base = pl.x;
-    n = pl.y;
-    const Request rq = request_of(p, request);
-    const int64_t nth = token - rq.first;
-    if (nth >= rq.queries) return;
-    row = (int)nth * p.group + qh % p.group;
-  }
+  const int2 pl = p.plan[request];
+  const int base = pl.x, n = pl.y;
+  const Request rq = request_of(p, request);
+  const int64_t nth = token - rq.first;
+  if (nth >= rq.queries) return;
+  const int row = (int)nth * p.group + qh % p.group;
   if (n <= 1) return;  // written whole
   const int row_tile = row / rows_per_cta, in_tile = row % rows_per_cta;
   if (row_tile >= p.row_tiles) return;  // past max_new: not computed
@@ -606,22 +667,25 @@ RowsKernel rows_kernel_of(int d, int nt, bool list) {
 struct Plan {
   bool prefill;        // the kernel for many query rows
   int nt, row_tiles, cta_rows;
-  int target;        // dense: chunks wanted over all requests; listed: parts of a list
+  int parts;           // > 0: every request (list) in that many parts, a cluster; 0: chunks of like work
+  int target;          // chunks wanted over all requests
   int min_chunk;
-  int64_t flats;     // chunks at most
-  bool join;
+  int64_t flats;       // chunks, or requests (lists) at most
+  bool join;           // chunks are joined by a second launch
   int64_t plan_bytes, lse_bytes, o_bytes;
   int64_t bytes() const { return join ? plan_bytes + lse_bytes + o_bytes : 0; }
 };
 
 constexpr int kMinChunk = 256;
 constexpr int kPrefillMinChunk = 512;
-constexpr int kPrefillFrom = 64;  // query rows a kv head from which the kernel for many rows is taken
+constexpr int kPrefillFrom = 64;    // query rows a kv head from which the kernel for many rows is taken
+constexpr int kMaxParts = 8;        // CTAs of a portable cluster
+constexpr int kPartPositions = 2048;  // positions of a part up to which requests are cut into equal numbers of parts
 
 Plan finish_plan(Plan a, int heads, int d, int requests) {
   // (a chunk is at least total / target long, so the requests have at most target + requests)
   if (a.flats == 0) a.flats = a.target == 1 ? requests : a.target + (int64_t)requests;
-  a.join = a.target > 1;
+  a.join = a.parts == 0 && a.target > 1;
   const int64_t part_rows = a.flats * heads * a.row_tiles * a.cta_rows;
   a.plan_bytes = ((int64_t)requests * 8 + 15) / 16 * 16;
   a.lse_bytes = (part_rows * 4 + 15) / 16 * 16;
@@ -629,7 +693,9 @@ Plan finish_plan(Plan a, int heads, int d, int requests) {
   return a;
 }
 
-Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int requests, int max_new, int list_len) {
+// positions: the most that a request can have by its row of the table
+Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int requests, int max_new, int list_len,
+               int64_t positions, int window) {
   Plan a = {};
   const int64_t rows = (int64_t)(list_len > 0 ? 1 : max_new) * group;
   a.prefill = list_len == 0 && d <= 128 && rows >= kPrefillFrom;
@@ -650,18 +716,21 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
   a.min_chunk = kMinChunk;
   const int slots = sms * rows_kernel_of(d, a.nt, list_len > 0).per_sm;
   const int64_t units = (int64_t)heads * a.row_tiles;
-  if (list_len > 0) {
-    // parts of at least four tiles (one a warp), until the slots are full
-    int64_t parts = (slots + tokens * units - 1) / (tokens * units);
-    const int64_t tiles = (list_len + kTile * kWarps - 1) / (kTile * kWarps);
-    parts = parts > tiles ? tiles : parts;
-    a.target = (int)(parts < 1 ? 1 : parts);
-    a.flats = tokens * a.target;
-  } else {
-    // several chunks a slot, so that the last ones to end are short
-    int64_t target = ((int64_t)slots * 6 + units - 1) / units;
-    a.target = (int)(target < 1 ? 1 : target);
+  // what one query (a request's queries) can see
+  int64_t seen = list_len > 0 ? list_len : positions;
+  if (list_len == 0 && window > 0 && (int64_t)window + max_new + kTile < seen) seen = (int64_t)window + max_new + kTile;
+  const int64_t whole = (list_len > 0 ? tokens : (int64_t)requests) * units;
+  // parts while the CTAs do not fill the slots twice and a part is at least a tile for every warp
+  int parts = 1;
+  while (parts < kMaxParts && whole * parts < 2 * slots && seen > (int64_t)parts * kTile * kWarps) parts *= 2;
+  if (list_len > 0 || seen <= (int64_t)parts * kPartPositions) {
+    a.parts = parts;
+    a.flats = list_len > 0 ? tokens : requests;
+    return finish_plan(a, heads, d, requests);
   }
+  // several chunks a slot, so that the last ones to end are short
+  const int64_t target = ((int64_t)slots * 6 + units - 1) / units;
+  a.target = (int)(target < 1 ? 1 : target);
   return finish_plan(a, heads, d, requests);
 }
 
@@ -689,16 +758,19 @@ lt_status check_sizes(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t
 extern "C" {
 
 lt_status lt_kv4_workspace(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
-                           int32_t requests, int32_t max_new, int32_t list_len, int64_t* bytes) {
+                           int32_t requests, int32_t max_new, int32_t list_len, int64_t positions,
+                           int32_t window, int64_t* bytes) {
   if (bytes == nullptr) return LT_ERR_INVALID_ARG;
   lt_status st = check_sizes(tokens, q_heads, kv_heads, head_dim, requests, max_new, list_len);
+  if (st == LT_OK && (positions < 0 || window < 0)) st = LT_ERR_INVALID_ARG;
   if (st != LT_OK) return st;
   *bytes = 0;
   if (tokens == 0 || requests == 0) return LT_OK;
   int dev = 0, sms = 0;
   st = device_of(&dev, &sms);
   if (st != LT_OK) return st;
-  *bytes = make_plan(sms, tokens, kv_heads, q_heads / kv_heads, head_dim, requests, max_new, list_len).bytes();
+  *bytes = make_plan(sms, tokens, kv_heads, q_heads / kv_heads, head_dim, requests, max_new, list_len,
+                     positions, window >= positions ? 0 : window).bytes();
   return LT_OK;
 }
 
@@ -738,10 +810,11 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
   st = device_of(&dev, &sms);
   if (st != LT_OK) return st;
   const int group = q_heads / kv_heads;
-  const Plan plan = make_plan(sms, tokens, kv_heads, group, head_dim, requests, max_new, list_len);
+  const Plan plan = make_plan(sms, tokens, kv_heads, group, head_dim, requests, max_new, list_len,
+                              (int64_t)table_width << shift, window);
   if (plan.join && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < plan.bytes()))
     return LT_ERR_INVALID_ARG;
-  const int64_t grid = plan.flats * kv_heads * plan.row_tiles, joins = tokens * q_heads;
+  const int64_t grid = plan.flats * kv_heads * plan.row_tiles * (plan.parts > 1 ? plan.parts : 1), joins = tokens * q_heads;
   if (grid > INT32_MAX || joins > INT32_MAX) return LT_ERR_UNSUPPORTED;
 
   AttentionParams p = {};
@@ -770,6 +843,7 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
   p.shift = shift;
   p.list_len = list_len;
   p.window = window;
+  p.parts = plan.parts;
   p.target = plan.target;
   p.min_chunk = plan.min_chunk;
   p.row_tiles = plan.row_tiles;
@@ -792,13 +866,14 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
       set = true;
     }
   }
-  st = launch(k.func, dim3((unsigned)grid), plan.prefill ? kPrefillThreads : kThreads, (unsigned)k.smem, &p, stream);
+  st = launch(k.func, dim3((unsigned)grid), plan.prefill ? kPrefillThreads : kThreads, (unsigned)k.smem, &p, stream,
+              plan.parts > 1 ? plan.parts : 1);
   if (st != LT_OK || !plan.join) return st;
   if (lt::take_injected_failure()) return LT_ERR_CUDA;
   const void* func = head_dim == 64    ? reinterpret_cast<const void*>(&join_kernel<64>)
                      : head_dim == 128 ? reinterpret_cast<const void*>(&join_kernel<128>)
                                        : reinterpret_cast<const void*>(&join_kernel<256>);
-  int rows_per_cta = plan.cta_rows, listed = list;
+  int rows_per_cta = plan.cta_rows;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)joins);
   cfg.blockDim = dim3(kJoinThreads);
@@ -808,7 +883,7 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  void* a[] = {&p, &rows_per_cta, &listed};
+  void* a[] = {&p, &rows_per_cta};
   return cudaLaunchKernelExC(&cfg, func, a) == cudaSuccess ? LT_OK : LT_ERR_CUDA;
 }
 

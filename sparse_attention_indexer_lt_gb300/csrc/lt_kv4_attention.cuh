@@ -28,7 +28,7 @@ struct AttentionParams {
   float* part_o;    // [chunk][kv head][row][D], divided by the part's own sum
   int64_t q_token, q_head;
   int32_t pages, tokens, requests, width, heads, group, shift, list_len, window;
-  int32_t target, min_chunk, row_tiles, bf16;
+  int32_t parts, target, min_chunk, row_tiles, bf16;
   int32_t align;    // positions at which chunks and windows start: multiples of this (32 or 128)
   float scale_log2;
 };
@@ -183,11 +183,16 @@ __device__ __forceinline__ bool mbar_ready(uint64_t* bar, uint32_t parity) {
                : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
   return ok != 0;
 }
-// Waits for a phase, a bounded number of polls; false if it gave up.
+// A warp waits for a phase, a bounded number of polls; false if it gave up. Every poll ends in a vote, so
+// the warp goes on converged.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
-  if (mbar_ready(bar, parity)) return true;
-  for (uint32_t i = 0; i < kWaitPolls; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+  if (__all_sync(~0u, mbar_ready(bar, parity))) return true;
+  bool done = false;
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    done = done | mbar_try_wait(bar, parity);
+    if (__all_sync(~0u, done)) return true;
+  }
   return false;
 }
 

@@ -38,7 +38,7 @@ class PageStep(NamedTuple):
 
 
 # The checks are on the path of every decode step, whose kernels take a few microseconds: devices are
-# compared by their index, the stream is taken by its handle, outputs are made with new_empty.
+# compared by their index, the stream is taken by its handle.
 
 
 def _raw_stream(stream, index):
@@ -75,9 +75,9 @@ def _result(name, t, shape, dtype, like, stream):
     if t is not None:
         return _want(name, t, dtype, like.get_device(), shape)
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _int32(name, x, least):
@@ -219,11 +219,11 @@ def kv4_load(cache: torch.Tensor, slots: torch.Tensor, *, dtype: torch.dtype = t
 
 
 @functools.lru_cache(maxsize=4096)
-def _workspace_bytes(index, tokens, q_heads, kv_heads, head_dim, requests, max_new, list_len):
+def _workspace_bytes(index, tokens, q_heads, kv_heads, head_dim, requests, max_new, list_len, positions, window):
     """lt_kv4_workspace's answer: it goes by these sizes and the device alone."""
     need = ctypes.c_int64(0)
     _call("lt_kv4_workspace", index, tokens, q_heads, kv_heads, head_dim, requests, max_new, list_len,
-          ctypes.byref(need))
+          positions, window, ctypes.byref(need))
     return need.value
 
 
@@ -276,7 +276,7 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         list_len = positions.shape[1]
     out = _result("out", out, (tokens, q_heads, dim), dtype, q, stream)
     lse = _result("out_lse", out_lse, (tokens, q_heads), torch.float32, q, stream) if with_lse else None
-    need = _workspace_bytes(index, tokens, q_heads, heads, dim, n, max_new, list_len)
+    need = _workspace_bytes(index, tokens, q_heads, heads, dim, n, max_new, list_len, width * page_size, window)
     if workspace is not None:
         _want("workspace", workspace, torch.uint8, index)
         if workspace.numel() < need:

@@ -354,6 +354,15 @@ def test_split_requests_join_to_the_same(requests):
     assert torch.equal(out, again) and torch.equal(lse, lse2), "two runs differ"
 
 
+@pytest.mark.parametrize("lengths,new", [([20000], [1]), ([17000, 3, 0, 9000], [2, 1, 1, 0]), ([300] * 40 + [17001], [1] * 41)])
+def test_long_tables_are_cut_into_chunks(lengths, new):
+    """Tables too long for parts of one size: chunks of like work over all requests, and a second launch."""
+    p = Problem(lengths, new, 1, 2, 64, 64, "bf16", seed=len(lengths))
+    out, lse = p.run()
+    p.check(out, lse)
+    assert torch.equal(out, p.run()[0])
+
+
 def test_scales_and_spreads():
     """Peaked and flat rows, a negative and a zero scale, small and large stored values."""
     for spread, magnitude, scale in ((30.0, 1.0, None), (1e-3, 1.0, None), (1.0, 1.0, -0.2), (1.0, 1.0, 0.0), (1.0, 1e-4, 300.0), (1.0, 3000.0, 1e-4)):
@@ -384,8 +393,10 @@ def test_strided_queries_and_given_outputs():
     assert got.data_ptr() == given.data_ptr() and torch.equal(out, got) and torch.equal(lse, got_lse)
     with pytest.raises(ValueError):
         p.run(q=wide[:, 2:10, 4:132])  # not 16-byte aligned
+    assert torch.equal(out, p.run(q=q, workspace=space[:16])[0])  # (short requests need none)
+    long = Problem([40000], [1], 1, 4, 64, 64, "bf16", seed=4)
     with pytest.raises(ValueError):
-        p.run(workspace=space[:16])
+        long.run(workspace=space[:16])
     with pytest.raises(ValueError):
         p.run(starts=None)
     with pytest.raises(ValueError):

@@ -193,10 +193,12 @@ def test_attention_of_nothing(lib):
     assert _attend(lib, tokens=0, n=0) == 0
     assert _attend(lib, tokens=0, n=3, starts=FAKE, new=4) == 0
     need = ctypes.c_int64(-1)
-    assert lib.lt_kv4_workspace(0, 8, 2, 128, 0, 1, 0, ctypes.byref(need)) == 0 and need.value == 0
-    assert lib.lt_kv4_workspace(4, 8, 2, 128, 4, 1, 0, None) == 1
-    assert lib.lt_kv4_workspace(4, 8, 3, 128, 4, 1, 0, ctypes.byref(need)) == 1
-    assert lib.lt_kv4_workspace(4, 8, 2, 80, 4, 1, 0, ctypes.byref(need)) == 2
+    assert lib.lt_kv4_workspace(0, 8, 2, 128, 0, 1, 0, 64, 0, ctypes.byref(need)) == 0 and need.value == 0
+    assert lib.lt_kv4_workspace(4, 8, 2, 128, 4, 1, 0, 64, 0, None) == 1
+    assert lib.lt_kv4_workspace(4, 8, 3, 128, 4, 1, 0, 64, 0, ctypes.byref(need)) == 1
+    assert lib.lt_kv4_workspace(4, 8, 2, 128, 4, 1, 0, -64, 0, ctypes.byref(need)) == 1
+    assert lib.lt_kv4_workspace(4, 8, 2, 128, 4, 1, 0, 64, -1, ctypes.byref(need)) == 1
+    assert lib.lt_kv4_workspace(4, 8, 2, 80, 4, 1, 0, 64, 0, ctypes.byref(need)) == 2
 
 
 def test_valid_calls_without_a_device_report_a_cuda_error(lib):
