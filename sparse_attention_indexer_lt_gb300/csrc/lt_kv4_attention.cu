@@ -22,7 +22,7 @@
 //
 // A product of a code and its scale is an exact fp16 number, so keys and values
 // enter the products exactly. The weights are rounded to fp16 (2^-12 relative)
-// after a shift by 2^8 that keeps small ones normal; the sums that divide them are
+// after a shift by 2^6 that keeps small ones normal; the sums that divide them are
 // fp32 and of the unrounded weights.
 
 #include <mutex>
@@ -35,17 +35,18 @@ namespace {
 
 using namespace lt::kv4;
 
-constexpr float kShift = 8.0f;  // weights are held as 2^8 exp(s - max)
+constexpr float kShift = 6.0f;  // weights are held as 2^6 exp(s - max)
+constexpr float kSlack = 8.0f;  // how far logits may pass the maximum (log 2) before it moves: weights stay below 2^14
 
 template <int D, int NT>
 struct Shape {
   static constexpr int kRow = row_bytes(D);
   static constexpr int kTileBytes = kTile * kRow;
-  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
   static constexpr int kRing = kWarps * kStages * kTileBytes;
   static constexpr int kJoin = kWarps * NT * 8 * (D + 4) * 4;  // the warps' sums, in the ring's place
   static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
-  static constexpr int kPerSm = D == 64 ? (NT == 4 ? 3 : 4) : D == 128 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : 2;
+  static constexpr int kPerSm = D == 64 ? (NT == 4 ? 3 : 4) : D == 128 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : NT == 1 ? 3 : 2;
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -87,6 +88,14 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+// This thread's copies so far arrive on the barrier when they are done.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(lt::smem_u32(bar)) : "memory");
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive;\n barrier.cluster.wait;" ::: "memory");
 }
@@ -120,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   if (lane == 0) {
 #pragma unroll
-    for (int s = 0; s < Sh::kStages; ++s) lt::mbar_init(&bars[warp][s], 1);
+    for (int s = 0; s < Sh::kStages; ++s) lt::mbar_init(&bars[warp][s], kList ? 32 : 1);
     lt::mbar_fence_init();
   }
   if (tid == 0) gave_up = 0;
@@ -210,6 +219,23 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
     if (next_page < 0 || next_page >= p.pages) next_count = 0;
     const uint32_t mine = next_count > 0 ? ((next_count == 32 ? ~0u : (1u << next_count) - 1u) << ((lane << run_shift) & 31)) : 0u;
     const uint32_t valid = __reduce_or_sync(~0u, mine);
+    if constexpr (kList) {
+      // one row a position: 16-byte copies, the lanes along the rows (a bulk copy for each row is slower, by
+      // the rate at which such copies start)
+      if (lane == 0) valid_of[warp][stage] = valid;
+      const int64_t at = (((int64_t)next_page * p.heads + head) << p.shift) + (next_pos & ((1 << p.shift) - 1));
+      constexpr int kChunks = kRow / 16;
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const int id = k * 32 + lane, of = id / kChunks, chunk = id % kChunks;
+        const int64_t row = __shfl_sync(~0u, at, of);
+        if ((valid >> of) & 1u)
+          copy16(ring + stage * Sh::kTileBytes + id * 16, p.cache + row * kRow + chunk * 16);
+      }
+      copies_arrive(&bars[warp][stage]);
+      look_up(tile + kWarps);
+      return;
+    }
     if (lane == 0) {
       valid_of[warp][stage] = valid;
       lt::mbar_arrive_tx(&bars[warp][stage], (uint32_t)__popc(valid) * kRow);
@@ -310,10 +336,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
       }
     }
 
-    // logits, masks, running maximum
-    float top[NT][2];
+    // logits, masks, running maximum: it moves only when a logit passes it by 2^kSlack (always at first), so
+    // most tiles need neither the maximum over the lanes nor a new scale of the sums
+    bool raised = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -327,23 +354,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
           }
         }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float t = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
-        t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
-        t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
-        top[nt][e] = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
-      }
-    }
-    bool raised = false;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) raised = raised || top[nt][0] > m[nt][0] || top[nt][1] > m[nt][1];
+      for (int e = 0; e < 2; ++e)
+        raised = raised || fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2])) > m[nt][e] + kSlack;
     if (__any_sync(~0u, raised)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float a[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float now = fmaxf(m[nt][e], top[nt][e]);
+          float t = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
+          t = fmaxf(t, __shfl_xor_sync(~0u, t, 4));
+          t = fmaxf(t, __shfl_xor_sync(~0u, t, 8));
+          t = fmaxf(t, __shfl_xor_sync(~0u, t, 16));
+          const float now = fmaxf(m[nt][e], t);
           a[e] = now == m[nt][e] ? 1.0f : exp2_fast(m[nt][e] - now);
           m[nt][e] = now;
           l[nt][e] *= a[e];
