@@ -36,6 +36,7 @@ namespace {
 using namespace lt::kv4;
 
 constexpr float kShift = 6.0f;  // weights are held as 2^6 exp(s - max)
+constexpr int kMaxParts = 8;    // CTAs of a portable cluster
 constexpr float kSlack = 8.0f;  // how far logits may pass the maximum (log 2) before it moves: weights stay below 2^14
 
 template <int D, int NT>
@@ -121,7 +122,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][Sh::kStages];
   __shared__ uint32_t valid_of[kWarps][Sh::kStages];
-  __shared__ float m_of[kWarps][NT * 8], l_of[kWarps][NT * 8], part_log2[NT * 8];
+  __shared__ float m_of[kMaxParts][NT * 8];  // a warp's maximum; at the end a part's weight
+  __shared__ float l_of[kWarps][NT * 8], part_log2[NT * 8];
+  __shared__ int64_t out_of[NT * 8];
   __shared__ int64_t sums[kWarps];
   __shared__ Place found;
   __shared__ int gave_up;
@@ -201,81 +204,99 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   const int run_shift = kList ? 0 : min(p.shift, 5);
   const int32_t* table = p.table + (int64_t)request * p.width;
   const int32_t* list = kList ? p.positions + (int64_t)token0 * p.list_len : nullptr;
-  // of the next tile to bring: the lane's position, how many, and its page's id
-  int next_pos, next_count, next_page;
-  auto look_up = [&](int tile) {
-    const int at = from + tile * kTile + (lane << run_shift);
-    next_count = tile < tiles && (lane << run_shift) < kTile ? max(0, min(to - at, 1 << run_shift)) : 0;
-    next_pos = at;
+  // The lane's position in a tile (of its run's first one), -1 for none; and the page that a position lies on.
+  auto position_of = [&](int tile) {
+    const int at = from + tile * kTile + (run_shift == 5 ? 0 : lane << run_shift);
+    if (tile >= tiles || at >= to || at >= from + (tile + 1) * kTile) return -1;
     if constexpr (kList) {
-      if (next_count > 0) {
-        next_pos = __ldg(list + at);
-        if (next_pos < 0 || next_pos >= rq.length) next_count = 0;
-      }
+      const int pos = __ldg(list + at);
+      return pos < rq.length ? pos : -1;
     }
-    next_page = next_count > 0 ? __ldg(table + (next_pos >> p.shift)) : -1;
+    return at;
   };
-  auto bring = [&](int tile, int stage) {
-    if (next_page < 0 || next_page >= p.pages) next_count = 0;
-    const uint32_t mine = next_count > 0 ? ((next_count == 32 ? ~0u : (1u << next_count) - 1u) << ((lane << run_shift) & 31)) : 0u;
-    const uint32_t valid = __reduce_or_sync(~0u, mine);
+  auto page_of = [&](int pos) { return pos >= 0 ? __ldg(table + (pos >> p.shift)) : -1; };
+  auto row_at = [&](int page, int pos) { return (((int64_t)page * p.heads + head) << p.shift) + (pos & ((1 << p.shift) - 1)); };
+  auto bring = [&](int stage, int pos, int page) {
+    const bool there = pos >= 0 && page >= 0 && page < p.pages;
+    const uint32_t tile_at = ring + stage * Sh::kTileBytes;
     if constexpr (kList) {
-      // one row a position: 16-byte copies, the lanes along the rows (a bulk copy for each row is slower, by
-      // the rate at which such copies start)
+      // one row a position: 16-byte copies, the lanes along the rows
+      const uint32_t valid = __ballot_sync(~0u, there);
       if (lane == 0) valid_of[warp][stage] = valid;
-      const int64_t at = (((int64_t)next_page * p.heads + head) << p.shift) + (next_pos & ((1 << p.shift) - 1));
+      const int64_t at = there ? row_at(page, pos) : 0;
       constexpr int kChunks = kRow / 16;
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
         const int id = k * 32 + lane, of = id / kChunks, chunk = id % kChunks;
         const int64_t row = __shfl_sync(~0u, at, of);
-        if ((valid >> of) & 1u)
-          copy16(ring + stage * Sh::kTileBytes + id * 16, p.cache + row * kRow + chunk * 16);
+        if ((valid >> of) & 1u) copy16(tile_at + id * 16, p.cache + row * kRow + chunk * 16);
       }
       copies_arrive(&bars[warp][stage]);
-      look_up(tile + kWarps);
-      return;
+    } else if (run_shift == 5) {
+      // the tile lies on one page: one copy, and all lanes know its size
+      const int count = there ? min(to - pos, kTile) : 0;
+      if (lane == 0) {
+        valid_of[warp][stage] = count == kTile ? ~0u : (1u << count) - 1u;
+        lt::mbar_arrive_tx(&bars[warp][stage], (uint32_t)count * kRow);
+        if (count > 0) bulk_in(tile_at, p.cache + row_at(page, pos) * kRow, (uint32_t)count * kRow, &bars[warp][stage]);
+      }
+      __syncwarp();
+    } else {
+      const int count = there ? min(to - pos, 1 << run_shift) : 0;
+      const uint32_t mine = count > 0 ? ((1u << count) - 1u) << (lane << run_shift) : 0u;
+      const uint32_t valid = __reduce_or_sync(~0u, mine);
+      if (lane == 0) {
+        valid_of[warp][stage] = valid;
+        lt::mbar_arrive_tx(&bars[warp][stage], (uint32_t)__popc(valid) * kRow);
+      }
+      __syncwarp();
+      if (count > 0)
+        bulk_in(tile_at + (lane << run_shift) * kRow, p.cache + row_at(page, pos) * kRow, (uint32_t)count * kRow, &bars[warp][stage]);
     }
-    if (lane == 0) {
-      valid_of[warp][stage] = valid;
-      lt::mbar_arrive_tx(&bars[warp][stage], (uint32_t)__popc(valid) * kRow);
-    }
-    __syncwarp();
-    if (next_count > 0) {
-      const uint8_t* src = p.cache + (((((int64_t)next_page * p.heads + head) << p.shift) + (next_pos & ((1 << p.shift) - 1))) * kRow);
-      bulk_in(ring + stage * Sh::kTileBytes + (lane << run_shift) * kRow, src, (uint32_t)next_count * kRow, &bars[warp][stage]);
-    }
-    look_up(tile + kWarps);
   };
-  look_up(warp);
-#pragma unroll
-  for (int s = 0; s < Sh::kStages; ++s)
-    if (warp + s * kWarps < tiles) bring(warp + s * kWarps, s);
 
+  // Everything that the start waits for from far away is asked for together: the queries, the first tiles'
+  // positions, then their pages, then their rows. Later, positions are looked up two tiles and
+  // pages one tile before their rows are brought.
   // ---- query fragments: lane (g, c) holds channels 32 j + 8 c .. + 7 of row g of each row tile
   uint32_t qf[NT][kGroups][4];
-  float factor[NT][2];       // of columns 2c, 2c + 1: logits in units of log 2
-  int limit[NT][2], low[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = min(row0 + nt * 8 + g, rows - 1);
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + (int64_t)(token0 + row / p.group) * p.q_token +
+                        (int64_t)(head * p.group + row % p.group) * p.q_head;
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + 32 * j + 8 * c));
+      qf[nt][j][0] = v.x, qf[nt][j][1] = v.y, qf[nt][j][2] = v.z, qf[nt][j][3] = v.w;
+    }
+  }
+  int next_pos, next_page, later_pos;
   {
+    int pos[Sh::kStages], page[Sh::kStages];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = min(row0 + nt * 8 + g, rows - 1);
-      const int64_t token = token0 + row / p.group;
-      const uint16_t* q = static_cast<const uint16_t*>(p.q) + token * p.q_token + (int64_t)(head * p.group + row % p.group) * p.q_head;
+    for (int s = 0; s < Sh::kStages; ++s) pos[s] = position_of(warp + s * kWarps);
+    next_pos = position_of(warp + Sh::kStages * kWarps);
+    later_pos = position_of(warp + (Sh::kStages + 1) * kWarps);
 #pragma unroll
-      for (int j = 0; j < kGroups; ++j) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + 32 * j + 8 * c));
-        qf[nt][j][0] = v.x, qf[nt][j][1] = v.y, qf[nt][j][2] = v.z, qf[nt][j][3] = v.w;
-      }
-      const float inv = p.bf16 ? bf16_row_to_half<kGroups>(qf[nt]) : 1.0f;
-      factor[nt][0] = __shfl_sync(~0u, inv, 8 * c) * p.scale_log2;
-      factor[nt][1] = __shfl_sync(~0u, inv, 8 * c + 4) * p.scale_log2;
+    for (int s = 0; s < Sh::kStages; ++s) page[s] = page_of(pos[s]);
+    next_page = page_of(next_pos);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int token_of = min(row0 + nt * 8 + 2 * c + e, rows - 1) / p.group;
-        limit[nt][e] = kList ? INT32_MAX : rq.length - rq.queries + token_of + 1;
-        low[nt][e] = !kList && p.window > 0 ? limit[nt][e] - p.window : INT32_MIN;
-      }
+    for (int s = 0; s < Sh::kStages; ++s)
+      if (warp + s * kWarps < tiles) bring(s, pos[s], page[s]);
+  }
+  float factor[NT][2];  // of columns 2c, 2c + 1: logits in units of log 2
+  int limit[NT][2], low[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float inv = p.bf16 ? bf16_row_to_half<kGroups>(qf[nt]) : 1.0f;
+    factor[nt][0] = __shfl_sync(~0u, inv, 8 * c) * p.scale_log2;
+    factor[nt][1] = __shfl_sync(~0u, inv, 8 * c + 4) * p.scale_log2;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int token_of = min(row0 + nt * 8 + 2 * c + e, rows - 1) / p.group;
+      limit[nt][e] = kList ? INT32_MAX : rq.length - rq.queries + token_of + 1;
+      low[nt][e] = !kList && p.window > 0 ? limit[nt][e] - p.window : INT32_MIN;
     }
   }
   const int safe_to = kList ? INT32_MAX : rq.length - rq.queries + row0 / p.group + 1;  // every row sees up to here
@@ -321,17 +342,31 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
         uint32_t ha[4], hb[4];
         codes_to_half2(lds32(ra + (j * 4 + c) * 4), ha);
         codes_to_half2(lds32(rb + (j * 4 + c) * 4), hb);
-        const uint32_t ka = __byte_perm(sa[j / 2], 0, j & 1 ? 0x3232 : 0x1010);
-        const uint32_t kb = __byte_perm(sb[j / 2], 0, j & 1 ? 0x3232 : 0x1010);
+        if constexpr (NT == 1) {
+          // with one row tile the scale of the group is cheaper on the product's four results than on eight
+          // operand registers
+          const __half2 pa = *reinterpret_cast<const __half2*>(&sa[j / 2]), pb = *reinterpret_cast<const __half2*>(&sb[j / 2]);
+          const float fa = j & 1 ? __high2float(pa) : __low2float(pa), fb = j & 1 ? __high2float(pb) : __low2float(pb);
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma16816(d, ha[0], hb[0], ha[1], hb[1], qf[0][j][0], qf[0][j][1]);
+          mma16816(d, ha[2], hb[2], ha[3], hb[3], qf[0][j][2], qf[0][j][3]);
+          s[mt][0][0] = fmaf(d[0], fa, s[mt][0][0]);
+          s[mt][0][1] = fmaf(d[1], fa, s[mt][0][1]);
+          s[mt][0][2] = fmaf(d[2], fb, s[mt][0][2]);
+          s[mt][0][3] = fmaf(d[3], fb, s[mt][0][3]);
+        } else {
+          const uint32_t ka = __byte_perm(sa[j / 2], 0, j & 1 ? 0x3232 : 0x1010);
+          const uint32_t kb = __byte_perm(sb[j / 2], 0, j & 1 ? 0x3232 : 0x1010);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ha[i] = hmul2(ha[i], ka);
-          hb[i] = hmul2(hb[i], kb);
-        }
+          for (int i = 0; i < 4; ++i) {
+            ha[i] = hmul2(ha[i], ka);
+            hb[i] = hmul2(hb[i], kb);
+          }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816(s[mt][nt], ha[0], hb[0], ha[1], hb[1], qf[nt][j][0], qf[nt][j][1]);
-          mma16816(s[mt][nt], ha[2], hb[2], ha[3], hb[3], qf[nt][j][2], qf[nt][j][3]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(s[mt][nt], ha[0], hb[0], ha[1], hb[1], qf[nt][j][0], qf[nt][j][1]);
+            mma16816(s[mt][nt], ha[2], hb[2], ha[3], hb[3], qf[nt][j][2], qf[nt][j][3]);
+          }
         }
       }
     }
@@ -462,8 +497,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
       }
     }
     __syncwarp();  // every lane has read the stage
-    const int next = tile + Sh::kStages * kWarps;
-    if (next < tiles) bring(next, stage);
+    if (tile + Sh::kStages * kWarps < tiles) {
+      bring(stage, next_pos, next_page);
+      next_pos = later_pos;
+      next_page = page_of(next_pos);
+      later_pos = position_of(tile + (Sh::kStages + 2) * kWarps);
+    }
     if (++stage == Sh::kStages) {
       stage = 0;
       parity ^= 1u;
@@ -487,101 +526,103 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
       }
     }
   __syncthreads();  // (also: every warp is done with the ring)
+  if (tid < NT * 8) {
+    // a thread a row: what each warp's sums are to be multiplied by, where the row goes
+    float top = m_of[0][tid], sum = 0.0f;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, m_of[w][tid]);
+    float a[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      a[w] = m_of[w][tid] == -INFINITY ? 0.0f : exp2_fast(m_of[w][tid] - top);
+      sum += m_of[w][tid] == -INFINITY ? l_of[w][tid] : l_of[w][tid] * a[w];  // (0, or NaN, where a warp saw nothing else)
+    }
+    const float inv = gave_up ? NAN : sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) l_of[w][tid] = inv != inv ? inv : a[w] * inv;
+    part_log2[tid] = gave_up ? NAN : sum == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top - kShift) + __log2f(sum);
+    const int row = min(row0 + tid, rows - 1);
+    out_of[tid] = (int64_t)(token0 + row / p.group) * p.heads * p.group + head * p.group + row % p.group;
+  }
+  __syncthreads();
   float* joined = reinterpret_cast<float*>(smem);
   constexpr int kPitch = D + 4;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float a[2];
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int row = nt * 8 + 2 * c + e;
-      float top = m_of[0][row];
+      const float a = l_of[warp][nt * 8 + 2 * c + e];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, m_of[w][row]);
-      a[e] = m[nt][e] == -INFINITY ? 0.0f : exp2_fast(m[nt][e] - top);
-    }
-#pragma unroll
-    for (int t = 0; t < D / 16; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int t = 0; t < D / 16; ++t) {
         float* to_row = joined + (warp * NT * 8 + nt * 8 + 2 * c + e) * kPitch + (g + 8 * (t / 4)) * 8 + 2 * (t % 4);
-        // (a warp that saw nothing holds zeros, or NaN that it was given)
-        *reinterpret_cast<float2*>(to_row) = make_float2(acc[nt][t][e] * a[e], acc[nt][t][e + 2] * a[e]);
+        *reinterpret_cast<float2*>(to_row) = make_float2(acc[nt][t][e] * a, acc[nt][t][e + 2] * a);
       }
-  }
+    }
   __syncthreads();
-  const bool final_here = count == 1;
+  const int here = min(NT * 8, rows - row0) * (D / 4);  // groups of four channels
   const int64_t part = (((int64_t)flat * p.heads + head) * p.row_tiles + row_tile) * (NT * 8);
-  auto write_out = [&](int row, int ch, float4 o, float log2_sum) {
-    const int64_t out_row = (int64_t)(token0 + (row0 + row) / p.group) * p.heads * p.group + head * p.group + (row0 + row) % p.group;
-    store4(p, out_row * D + ch, o);
-    if (p.lse != nullptr && ch == 0) p.lse[out_row] = log2_sum * 0.6931471805599453f;
-  };
-  for (int u = tid; u < NT * 8 * (D / 4); u += kThreads) {
+  for (int u = tid; u < here; u += kThreads) {
     const int row = u / (D / 4), ch = u % (D / 4) * 4;
-    if (row0 + row >= rows) break;
-    float top = m_of[0][row];
+    float4 o = *reinterpret_cast<const float4*>(joined + row * kPitch + ch);
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, m_of[w][row]);
-    float sum = 0.0f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float mw = m_of[w][row];
-      // a NaN weight sum stays one
-      if (mw != -INFINITY || !(l_of[w][row] == 0.0f)) sum += l_of[w][row] * (mw == -INFINITY ? 1.0f : exp2_fast(mw - top));
+    for (int w = 1; w < kWarps; ++w) {
       const float4 x = *reinterpret_cast<const float4*>(joined + (w * NT * 8 + row) * kPitch + ch);
       o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-    float log2_sum = sum == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top - kShift) + __log2f(sum);
-    if (gave_up) {
-      o = make_float4(NAN, NAN, NAN, NAN);
-      log2_sum = NAN;
-    }
-    if (p.parts > 1) {
-      // this thread alone has read the element's place: the part stays here for the cluster to read
+    if (p.parts > 1)
+      // (this thread alone has read the place: the part stays here for the cluster to read)
       *reinterpret_cast<float4*>(joined + row * kPitch + ch) = o;
-      if (ch == 0) part_log2[row] = log2_sum;
-    } else if (final_here) {
-      write_out(row, ch, o, log2_sum);
-    } else {
+    else if (count == 1)
+      store4(p, out_of[row] * D + ch, o);
+    else
       *reinterpret_cast<float4*>(p.part_o + (part + row) * D + ch) = o;
-      if (ch == 0) p.part_lse[part + row] = log2_sum;
-    }
   }
-  if (p.parts > 1) {
-    // join the cluster's parts over distributed shared memory, each CTA a share of the elements
-    cluster_sync();
-    const uint32_t o_at = lt::smem_u32(joined), l_at = lt::smem_u32(part_log2);
-    for (int u = rank * kThreads + tid; u < NT * 8 * (D / 4); u += p.parts * kThreads) {
-      const int row = u / (D / 4), ch = u % (D / 4) * 4;
-      if (row0 + row >= rows) break;
-      float top = -INFINITY;
-      bool bad = false;
-      for (int r = 0; r < p.parts; ++r) {
-        const float e = peer_f32(l_at + row * 4, r);
-        top = fmaxf(top, e);
-        bad = bad || e != e;
-      }
-      float sum = 0.0f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int r = 0; r < p.parts; ++r) {
-        const float e = peer_f32(l_at + row * 4, r);
-        const float4 x = peer_f32x4(o_at + (row * kPitch + ch) * 4, r);
-        const float w = e == -INFINITY ? 0.0f : exp2_fast(e - top);
-        sum += w;
-        if (e != -INFINITY) o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
-      }
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-      if (bad) o = make_float4(NAN, NAN, NAN, NAN);
-      write_out(row, ch, o, bad ? NAN : sum == 0.0f ? -INFINITY : top + __log2f(sum));
+  if (p.parts <= 1) {
+    if (tid < NT * 8 && row0 + tid < rows) {
+      if (count > 1)
+        p.part_lse[part + tid] = part_log2[tid];
+      else if (p.lse != nullptr)
+        p.lse[out_of[tid]] = part_log2[tid] * 0.6931471805599453f;
     }
-    cluster_sync();  // (a CTA's shared memory stays until its peers have read it)
+    return;
   }
+  // ---- join the cluster's parts over distributed shared memory: the weights of the parts by a thread a row,
+  // then each CTA a share of the elements
+  cluster_sync();
+  const uint32_t o_at = lt::smem_u32(joined), l_at = lt::smem_u32(part_log2);
+  float(*weight)[NT * 8] = m_of;
+  if (tid < NT * 8) {
+    float e[kMaxParts], top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kMaxParts; ++r) e[r] = r < p.parts ? peer_f32(l_at + tid * 4, r) : -INFINITY;
+#pragma unroll
+    for (int r = 0; r < kMaxParts; ++r) top = fmaxf(top, e[r]);
+#pragma unroll
+    for (int r = 0; r < kMaxParts; ++r) {
+      const float x = e[r];
+      e[r] = x == -INFINITY ? 0.0f : exp2_fast(x - top);  // (NaN stays NaN)
+      sum += e[r];
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int r = 0; r < kMaxParts; ++r) weight[r][tid] = inv != inv ? inv : e[r] * inv;
+    if (rank == 0 && p.lse != nullptr && row0 + tid < rows)
+      p.lse[out_of[tid]] = sum == 0.0f ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
+  }
+  __syncthreads();
+  for (int u = rank * kThreads + tid; u < here; u += p.parts * kThreads) {
+    const int row = u / (D / 4), ch = u % (D / 4) * 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int r = 0; r < kMaxParts; ++r) {
+      if (r >= p.parts) break;
+      const float4 x = peer_f32x4(o_at + (row * kPitch + ch) * 4, r);
+      const float w = weight[r][row];
+      o.x += w * x.x, o.y += w * x.y, o.z += w * x.z, o.w += w * x.w;
+    }
+    store4(p, out_of[row] * D + ch, o);
+  }
+  cluster_sync();  // (a CTA's shared memory stays until its peers have read it)
 }
 
 // Joins the parts of a (query, head): out = sum_i 2^(e_i - top) o_i / sum_i 2^(e_i - top), e_i
@@ -704,7 +745,6 @@ struct Plan {
 constexpr int kMinChunk = 256;
 constexpr int kPrefillMinChunk = 512;
 constexpr int kPrefillFrom = 64;    // query rows a kv head from which the kernel for many rows is taken
-constexpr int kMaxParts = 8;        // CTAs of a portable cluster
 constexpr int kPartPositions = 2048;  // positions of a part up to which requests are cut into equal numbers of parts
 
 Plan finish_plan(Plan a, int heads, int d, int requests) {
@@ -728,9 +768,10 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
     a.cta_rows = kPrefillRows;
     a.row_tiles = (int)((rows + kPrefillRows - 1) / kPrefillRows);
     a.min_chunk = kPrefillMinChunk;
-    // one CTA an SM; two waves of chunks where the row tiles alone are fewer
+    // one CTA an SM: chunks only where the row tiles alone do not fill the SMs (their joins cost more than an
+    // uneven second wave: 256 row tiles of 16384 positions take 511 us whole, 690 us in halves)
     const int64_t units = (int64_t)heads * a.row_tiles;
-    a.target = (int)((2 * sms + units - 1) / units);
+    a.target = (int)((sms + units - 1) / units);
     return finish_plan(a, heads, d, requests);
   }
   const int most = d == 256 ? 2 : 4;
@@ -745,16 +786,19 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
   int64_t seen = list_len > 0 ? list_len : positions;
   if (list_len == 0 && window > 0 && (int64_t)window + max_new + kTile < seen) seen = (int64_t)window + max_new + kTile;
   const int64_t whole = (list_len > 0 ? tokens : (int64_t)requests) * units;
-  // parts while the CTAs do not fill the slots twice and a part is at least a tile for every warp
+  // parts while the CTAs do not fill the slots and a part is at least a tile for every warp (filling them twice
+  // costs the drafted step 55 us instead of 46)
   int parts = 1;
-  while (parts < kMaxParts && whole * parts < 2 * slots && seen > (int64_t)parts * kTile * kWarps) parts *= 2;
+  while (parts < kMaxParts && whole * parts < slots && seen > (int64_t)parts * kTile * kWarps) parts *= 2;
   if (list_len > 0 || seen <= (int64_t)parts * kPartPositions) {
     a.parts = parts;
     a.flats = list_len > 0 ? tokens : requests;
     return finish_plan(a, heads, d, requests);
   }
-  // several chunks a slot, so that the last ones to end are short
-  const int64_t target = ((int64_t)slots * 6 + units - 1) / units;
+  // Several chunks a slot where requests differ in length, so that the last ones to end are short (64 ragged
+  // requests: 324, 279, 271, 269 us with 1, 2, 3, 4); one request's chunks are alike, and one
+  // wave of them has the fewest starts and joins (262144 positions at D = 256: 82 us, 96 with 2).
+  const int64_t target = ((int64_t)slots * (requests == 1 ? 1 : 4) + units - 1) / units;
   a.target = (int)(target < 1 ? 1 : target);
   return finish_plan(a, heads, d, requests);
 }
