@@ -35,79 +35,97 @@ struct CacheParams {
   void* out_v;
   const int64_t* slots;
   uint8_t* cache;
-  int64_t items;  // tokens * kv_heads
+  int64_t tokens;
   int64_t slot_end;
   int64_t k_token, k_head, v_token, v_head;
   int32_t heads;
   int32_t shift;
 };
 
-// The smallest scale >= amax / 6 with 9 significant bits, a multiple of 2^-23 (amax finite).
-// The quotient rounded up to fp32 has the same successors on that grid as the exact one,
-// since the grid's numbers are fp32 numbers; from 2^-15 on its 9 bits are the word's upper
-// ones, below it the multiples of 2^-23.
-__device__ __forceinline__ float scale_of(float amax) {
-  const float t = __fdiv_ru(amax, 6.0f);
+// The smallest scale >= amax / 6 with 9 significant bits, a multiple of 2^-23 (amax finite), from a `t` near
+// amax / 6: the next number of the grid at or above t; from 2^-15 on its 9 bits are the word's
+// upper ones, below it the grid is the multiples of 2^-23.
+__device__ __forceinline__ float scale_above(float t) {
   const float s = t >= 0x1p-15f ? __uint_as_float((__float_as_uint(t) + 0x7FFFu) & ~0x7FFFu) : ceilf(t * 0x1p23f) * 0x1p-23f;
   return fminf(s, kScaleMax);
 }
 
+// Eight channels as they lie in memory, and what is asked of them.
 template <class S>
-__device__ __forceinline__ void load8(const S* p, bool wide, float (&x)[8]);
-
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, bool wide, float (&x)[8]) {
-  if (wide) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
+struct Eight {  // 16-bit types: pairs in words
+  uint32_t w[4];
+  __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ __forceinline__ void load(const S* p, bool wide) {
+    if (wide) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+    } else {
+      const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __ldg(p + i);
-  }
-}
-template <class S>
-__device__ __forceinline__ float widen(uint16_t b) {
-  if constexpr (std::is_same<S, __nv_bfloat16>::value)
-    return __uint_as_float((uint32_t)b << 16);
-  else
-    return __half2float(__ushort_as_half(b));
-}
-template <class S>
-__device__ __forceinline__ void load8_16(const S* p, bool wide, float (&x)[8]) {
-  const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
-  if (wide) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = widen<S>((uint16_t)w[i]);
-      x[2 * i + 1] = widen<S>((uint16_t)(w[i] >> 16));
+      for (int i = 0; i < 4; ++i) w[i] = __ldg(u + 2 * i) | ((uint32_t)__ldg(u + 2 * i + 1) << 16);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = widen<S>(__ldg(u + i));
   }
-}
-template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, bool wide, float (&x)[8]) { load8_16(p, wide, x); }
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, bool wide, float (&x)[8]) {
-  load8_16(p, wide, x);
-}
-
-// The codes of eight channels of a group with this scale (finite inputs).
-template <class S>
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float s) {
-  if constexpr (sizeof(S) == 2) {
-    const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+  // The largest magnitude's bits; an infinity's bits or more where one is not finite (they order as integers).
+  __device__ __forceinline__ uint32_t largest() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+    return max(m & 0xFFFFu, m >> 16);
+  }
+  static __device__ __forceinline__ bool finite(uint32_t bits) { return bits < (std::is_same<S, __half>::value ? 0x7C00u : 0x7F80u); }
+  static __device__ __forceinline__ float number(uint32_t bits) {
+    if constexpr (std::is_same<S, __half>::value)
+      return __half2float(__ushort_as_half((uint16_t)bits));
+    else
+      return __uint_as_float(bits << 16);
+  }
+  // t: amax / 6 times 1 - 2^-18 or so. amax has at most 11 bits, so amax / 6 is a number of the grid or at
+  // least 2^-13 of itself away from one: the next number above t is the next at or above amax / 6.
+  static __device__ __forceinline__ float scale(float amax) { return scale_above(amax * 0x1.55550p-3f); }
+  // y = x / s as q + r / s with the exact remainder r = x - q s: exact where the quotient is a level border
+  // (inv within 2^-22 of 1 / s will do).
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    inv = s > 0.0f ? inv : 0.0f;
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float q = x[i] * inv;
-      y[i] = fmaf(fmaf(-q, s, x[i]), inv, q);
+      const float x = number(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+      const float q = x * inv;
+      y[i] = fmaf(fmaf(-q, s, x), inv, q);
     }
     return lt::kv4::codes_of(y);
-  } else {
+  }
+};
+
+template <>
+struct Eight<float> {
+  float x[8];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+  }
+  __device__ __forceinline__ void load(const float* p, bool wide) {
+    if (wide) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __ldg(p + i);
+    }
+  }
+  __device__ __forceinline__ uint32_t largest() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+    return m;
+  }
+  static __device__ __forceinline__ bool finite(uint32_t bits) { return bits < 0x7F800000u; }
+  static __device__ __forceinline__ float number(uint32_t bits) { return __uint_as_float(bits); }
+  // The quotient rounded up to fp32 has the same next number of the grid as the exact one, since the grid's
+  // numbers are fp32 numbers.
+  static __device__ __forceinline__ float scale(float amax) { return scale_above(__fdiv_ru(amax, 6.0f)); }
+  // (fp32 may lie nearer to a border than a rounded quotient tells; border * s has at most 12 bits)
+  __device__ __forceinline__ uint32_t codes(float s) const {
     uint32_t w = 0;
     if (s > 0.0f) {
 #pragma unroll
@@ -120,57 +138,62 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float s) {
     }
     return w;
   }
-}
+};
 
-// One warp-wide step covers 256 channels: lanes walk the 2 * D channels (key, then value) of an
-// item, 16 (D = 64) or 32 (D = 128) lanes an item; D = 256 takes two steps of a warp.
+// A step of a warp covers 256 channels: lanes walk the 2 * D channels (key, then value) of an item, 16
+// (D = 64) or 32 (D = 128) lanes an item; D = 256 takes two warps. A CTA has one head, so no
+// index is divided. A thread has kAhead steps in flight: their slots and values are asked
+// for before the first is worked on (the values of a token without a slot are read in
+// vain, which is rare and in bounds).
+constexpr int kAhead = 4;
+
 template <class S, int D>
 __global__ void __launch_bounds__(kThreads) store_kernel(CacheParams p, bool wide) {
   constexpr int kLanes = 2 * D / 8;  // lanes of an item
+  constexpr int kTokens = kThreads / kLanes;
   constexpr int kRow = row_bytes(D);
+  const int part = threadIdx.x % kLanes, head = blockIdx.y;  // part: eight of the item's channels, keys first
+  const bool is_v = part >= kLanes / 2;
+  const int c = part % (kLanes / 2) * 8;
+  const int64_t step = is_v ? p.v_token : p.k_token;
+  const S* from = is_v ? static_cast<const S*>(p.v) + head * p.v_head + c : static_cast<const S*>(p.k) + head * p.k_head + c;
+  const int64_t stride = (int64_t)gridDim.x * kTokens;
   lt::kv4::dependency_wait();
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < (p.items + 3) / 4 * 4 * kLanes; u += stride) {
-    // (items rounded up to four keep whole warps in step for the shuffles)
-    const int64_t item = u / kLanes;
-    const int part = (int)(u % kLanes);  // of the item's channels: eight each, keys first
-    const bool is_v = part >= kLanes / 2;
-    const int c = (part % (kLanes / 2)) * 8;
-    int64_t slot = -1;
-    float x[8] = {};
-    const int64_t token = item / p.heads;
-    const int head = (int)(item % p.heads);
-    if (item < p.items) {
-      slot = __ldg(p.slots + token);
-      if (slot >= p.slot_end) slot = -1;
-    }
-    if (slot >= 0) {
-      const S* from = is_v ? static_cast<const S*>(p.v) + token * p.v_token + head * p.v_head
-                           : static_cast<const S*>(p.k) + token * p.k_token + head * p.k_head;
-      load8<S>(from + c, wide, x);
-    }
-    float amax = 0.0f;
-    bool finite = true;
+  for (int64_t base = (int64_t)blockIdx.x * kTokens; base < p.tokens; base += kAhead * stride) {
+    Eight<S> x[kAhead];
+    int64_t slot[kAhead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      amax = fmaxf(amax, fabsf(x[i]));
-      finite = finite && fabsf(x[i]) <= FLT_MAX;
+    for (int k = 0; k < kAhead; ++k) {
+      const int64_t t = base + k * stride + threadIdx.x / kLanes;
+      slot[k] = -1;
+      x[k].clear();
+      if (t < p.tokens) {
+        slot[k] = __ldg(p.slots + t);
+        x[k].load(from + t * step, wide);
+      }
     }
-    if (!finite) amax = INFINITY;  // a NaN is lost in fmaxf: both are carried as infinity
-    amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
-    if (slot < 0) continue;  // (only after the shuffles)
-    const bool bad = !(amax <= FLT_MAX);
-    const float s = bad ? 0.0f : scale_of(amax);
-    const uint32_t codes = bad ? 0u : quantise8<S>(x, s);
-    uint8_t* row = p.cache + ((((slot >> p.shift) * p.heads + head) << p.shift) + (slot & ((1 << p.shift) - 1))) * (int64_t)kRow;
-    *reinterpret_cast<uint32_t*>(row + part * 4) = codes;
-    if ((part & 3) == 0) {
-      const uint16_t h = bad ? (uint16_t)0x7FFF : __half_as_ushort(__float2half_rn(s));
-      *reinterpret_cast<uint16_t*>(row + D + part / 4 * 2) = h;
-    }
-    if constexpr (kRow > D + D / 8) {
-      if (part == 0) *reinterpret_cast<uint2*>(row + D + D / 8) = make_uint2(0u, 0u);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (base + k * stride >= p.tokens) break;  // (the same for the whole CTA)
+      uint32_t largest = x[k].largest();
+      largest = max(largest, __shfl_xor_sync(~0u, largest, 1));
+      largest = max(largest, __shfl_xor_sync(~0u, largest, 2));
+      const int64_t at = slot[k];
+      if (at >= 0 && at < p.slot_end) {
+        const bool bad = !Eight<S>::finite(largest);
+        const float s = bad ? 0.0f : Eight<S>::scale(Eight<S>::number(largest));
+        const uint32_t codes = bad ? 0u : x[k].codes(s);
+        uint8_t* row = p.cache + ((((at >> p.shift) * p.heads + head) << p.shift) + (at & ((1 << p.shift) - 1))) * (int64_t)kRow;
+        *reinterpret_cast<uint32_t*>(row + part * 4) = codes;
+        if ((part & 3) == 0) {
+          const uint16_t h = bad ? (uint16_t)0x7FFF : __half_as_ushort(__float2half_rn(s));
+          *reinterpret_cast<uint16_t*>(row + D + part / 4 * 2) = h;
+        }
+        if constexpr (kRow > D + D / 8) {
+          if (part == 0) *reinterpret_cast<uint2*>(row + D + D / 8) = make_uint2(0u, 0u);
+        }
+      }
+      __syncwarp();
     }
   }
   lt::kv4::dependents_launch();
@@ -205,39 +228,48 @@ __device__ __forceinline__ void put8<__nv_bfloat16>(__nv_bfloat16* p, const uint
 template <class S, int D>
 __global__ void __launch_bounds__(kThreads) load_kernel(CacheParams p) {
   constexpr int kLanes = 2 * D / 8;
+  constexpr int kTokens = kThreads / kLanes;
   constexpr int kRow = row_bytes(D);
+  const int part = threadIdx.x % kLanes, head = blockIdx.y;
+  S* to = static_cast<S*>(part >= kLanes / 2 ? p.out_v : p.out_k) + (int64_t)head * D + part % (kLanes / 2) * 8;
+  const int64_t stride = (int64_t)gridDim.x * kTokens, step = (int64_t)p.heads * D;
   lt::kv4::dependency_wait();
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < p.items * kLanes; u += stride) {
-    const int64_t item = u / kLanes;
-    const int part = (int)(u % kLanes);
-    const int64_t token = item / p.heads;
-    const int head = (int)(item % p.heads);
-    const int64_t slot = __ldg(p.slots + token);
-    uint32_t h[4] = {};
-    if (slot >= 0 && slot < p.slot_end) {
-      const uint8_t* row =
-          p.cache + ((((slot >> p.shift) * p.heads + head) << p.shift) + (slot & ((1 << p.shift) - 1))) * (int64_t)kRow;
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(row + part * 4);
-      const uint32_t s = *reinterpret_cast<const uint16_t*>(row + D + part / 4 * 2);
-      lt::kv4::codes_to_half2(w, h);
+  for (int64_t base = (int64_t)blockIdx.x * kTokens + threadIdx.x / kLanes; base < p.tokens; base += kAhead * stride) {
+    int64_t slot[kAhead];
+    uint32_t codes[kAhead], scale[kAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = lt::kv4::hmul2(h[i], s | (s << 16));
+    for (int k = 0; k < kAhead; ++k) slot[k] = base + k * stride < p.tokens ? __ldg(p.slots + base + k * stride) : -1;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      codes[k] = scale[k] = 0u;
+      if (slot[k] >= 0 && slot[k] < p.slot_end) {
+        const uint8_t* row = p.cache + ((((slot[k] >> p.shift) * p.heads + head) << p.shift) + (slot[k] & ((1 << p.shift) - 1))) * (int64_t)kRow;
+        codes[k] = *reinterpret_cast<const uint32_t*>(row + part * 4);
+        scale[k] = *reinterpret_cast<const uint16_t*>(row + D + part / 4 * 2);
+      }
     }
-    const bool is_v = part >= kLanes / 2;
-    S* to = static_cast<S*>(is_v ? p.out_v : p.out_k) + item * D + (part % (kLanes / 2)) * 8;
-    put8<S>(to, h);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (base + k * stride >= p.tokens) break;
+      uint32_t h[4];
+      lt::kv4::codes_to_half2(codes[k], h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = lt::kv4::hmul2(h[i], scale[k] | (scale[k] << 16));
+      put8<S>(to + (base + k * stride) * step, h);
+    }
   }
   lt::kv4::dependents_launch();
 }
 
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// Enough CTAs for a few rounds of every SM; the kernels walk the items grid-stride.
-unsigned grid_for(int64_t threads) {
-  int64_t g = (threads + kThreads - 1) / kThreads;
-  const int64_t most = 152 * 32;
-  return (unsigned)(g < 1 ? 1 : g > most ? most : g);
+// A CTA for each head and run of tokens. While there are few, a thread has one step; with more than fill
+// the SMs it takes up to kAhead, and beyond a few rounds of CTAs it walks the tokens.
+dim3 grid_for(int64_t tokens, int heads, int d) {
+  const int64_t per = kThreads / (d / 4), once = (152 * 8 + heads - 1) / heads, most = (152 * 32 + heads - 1) / heads;
+  int64_t g = (tokens + per - 1) / per;
+  if (g > once) g = (g + kAhead - 1) / kAhead > once ? (g + kAhead - 1) / kAhead : once;
+  return dim3((unsigned)(g < 1 ? 1 : g > most ? most : g), (unsigned)heads);
 }
 
 template <class S>
@@ -260,7 +292,7 @@ lt_status check(const void* k, const void* v, int32_t dtype, int64_t tokens, int
   if (tokens > 0 && (k == nullptr || v == nullptr || slots == nullptr || (cache == nullptr && pages > 0)))
     return LT_ERR_INVALID_ARG;
   if (head_dim < 1 || !aligned(cache, 16)) return LT_ERR_INVALID_ARG;
-  if (lt_kv4_row_bytes(head_dim) == 0) return LT_ERR_UNSUPPORTED;
+  if (lt_kv4_row_bytes(head_dim) == 0 || kv_heads > 65535) return LT_ERR_UNSUPPORTED;
   return LT_OK;
 }
 
@@ -286,7 +318,7 @@ lt_status lt_kv4_store(const void* k, const void* v, int32_t dtype, int64_t toke
   p.v = v;
   p.slots = slots;
   p.cache = static_cast<uint8_t*>(cache);
-  p.items = tokens * kv_heads;
+  p.tokens = tokens;
   p.slot_end = pages * page_size;
   p.k_token = k_token_stride;
   p.k_head = k_head_stride;
@@ -302,7 +334,7 @@ lt_status lt_kv4_store(const void* k, const void* v, int32_t dtype, int64_t toke
                                               : store_ptr<__half>(head_dim);
   if (lt::take_injected_failure()) return LT_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid_for((p.items + 3) / 4 * 4 * (head_dim / 4)));
+  cfg.gridDim = grid_for(tokens, kv_heads, head_dim);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr;
@@ -326,14 +358,14 @@ lt_status lt_kv4_load(const void* cache, int64_t pages, int32_t page_size, const
   p.out_v = v;
   p.slots = slots;
   p.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
-  p.items = tokens * kv_heads;
+  p.tokens = tokens;
   p.slot_end = pages * page_size;
   p.heads = kv_heads;
   p.shift = lt::kv4::page_shift(page_size);
   const void* func = dtype == LT_DTYPE_F32    ? load_ptr<float>(head_dim)
                      : dtype == LT_DTYPE_BF16 ? load_ptr<__nv_bfloat16>(head_dim)
                                               : load_ptr<__half>(head_dim);
-  return lt::kv4::launch(func, dim3(grid_for(p.items * (head_dim / 4))), kThreads, 0, &p, stream);
+  return lt::kv4::launch(func, grid_for(tokens, kv_heads, head_dim), kThreads, 0, &p, stream);
 }
 
 }  // extern "C"

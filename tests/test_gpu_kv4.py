@@ -162,6 +162,28 @@ def test_store_and_load(dtype, dim, heads, page):
                     assert not gk[i].any() and not gv[i].any()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_every_16_bit_magnitude_as_the_largest_of_a_group(dtype):
+    """The scale of each finite magnitude, and codes of values spread below it, on either side of the borders."""
+    import sparse_attention_indexer_lt_gb300 as lt
+    t = TYPES[dtype]
+    bits = torch.arange(0x7F80 if dtype == "bf16" else 0x7C00, dtype=torch.int32).to(torch.int16)
+    top = bits.view(t)
+    rows = (top.numel() + 7) // 8  # eight groups a token: key and value of D = 128
+    top = torch.cat([top, top.new_zeros(rows * 8 - top.numel())]).view(rows, 8, 1)
+    x = (top.float() * torch.linspace(-1.0, 1.0, 32)).to(t)
+    x[..., 31] = top[..., 0]
+    k, v = x[:, :4].reshape(rows, 1, 128), x[:, 4:].reshape(rows, 1, 128)
+    cache = lt.kv4_cache((rows + 63) // 64, 1, 64, 128)
+    slots = torch.arange(rows, device="cuda")
+    lt.kv4_store(k.cuda(), v.cuda(), cache, slots)
+    got = cache.view(-1, 144)[:rows].cpu().numpy()
+    for i in range(0, rows, 7 if dtype == "bf16" else 5):
+        want = ok.rows_of(num(k[i, 0]), num(v[i, 0]))
+        assert np.array_equal(got[i, 128:], want[128:]), f"scales of row {i}"
+        assert np.array_equal(ok.values_of(got[i], 128), ok.values_of(want, 128)), f"values of row {i}"
+
+
 def test_store_of_many_tokens_and_a_repeat():
     import sparse_attention_indexer_lt_gb300 as lt
     torch.manual_seed(5)
