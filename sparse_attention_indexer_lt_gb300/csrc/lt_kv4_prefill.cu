@@ -86,14 +86,21 @@ __device__ __forceinline__ constexpr uint32_t instruction(int n, bool b_mn_major
 }
 // The issuing warp runs these as a whole, so that descriptors stay in uniform registers; `lead` is set in
 // one lane, which issues.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
-               " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+// Four products in a row, 16 of the inner dimension each; only the first may start a new sum.
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
+  asm volatile("{\n .reg .pred p, q, t;\n .reg .b64 a, b;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n setp.eq.u32 t, 0, 0;\n"
+               " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+               " add.s64 a, %1, 2;\n add.s64 b, %2, 2;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+               " add.s64 a, %1, 4;\n add.s64 b, %2, 4;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+               " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}"
                :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
-               " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
+  asm volatile("{\n .reg .pred p, q, t;\n .reg .b32 a;\n .reg .b64 b;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n setp.eq.u32 t, 0, 0;\n"
+               " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+               " add.s32 a, %1, 8;\n add.s64 b, %2, 128;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+               " add.s32 a, %1, 16;\n add.s64 b, %2, 256;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+               " add.s32 a, %1, 24;\n add.s64 b, %2, 384;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}"
                :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead) : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t lead) {
@@ -625,10 +632,8 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
           look(&sh->p_full[which][1], i);
         else if (which == 0 && keys)
           look(key_full(i + 1), (i + 1) >> 1);
-#pragma unroll
-        for (int k = 0; k < kTok / 32; ++k)
-          mma_ts(tmem + 2 * kTok + which * D, tmem + which * kTok + half * 32 + k * 8,
-                 value + half * ((kTok / 2 * 128) >> 4) + k * (2048 >> 4), kIdescO, i > 0 || half > 0 || k > 0, lead);
+        mma_ts4(tmem + 2 * kTok + which * D, tmem + which * kTok + half * 32, value + half * ((kTok / 2 * 128) >> 4), kIdescO,
+                i > 0 || half > 0, lead);
       }
       if (!ok) break;
       if (which == 1) mma_commit(value_empty, lead);
@@ -643,12 +648,9 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
         look(&sh->p_full[1][0], i);
       const uint64_t q = desc_k_major(q_at + which * Smem<D>::kOperand);
       const uint64_t key = desc_k_major(kv_at + ((i + 1) & 1) * 2 * Smem<D>::kOperand);
-#pragma unroll 1
-      for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss(tmem + which * kTok, q + c * (Smem<D>::kHalf >> 4) + k * 2, key + c * (Smem<D>::kHalf >> 4) + k * 2, kIdescS,
-                 c > 0 || k > 0, lead);
+      for (int c = 0; c < D / 64; ++c)
+        mma_ss4(tmem + which * kTok, q + c * (Smem<D>::kHalf >> 4), key + c * (Smem<D>::kHalf >> 4), kIdescS, c > 0, lead);
       mma_commit(&sh->s_full[which], lead);
       if (which == 1) mma_commit(key_empty, lead);
     }
