@@ -56,15 +56,15 @@ struct Smem {
 
 struct Shared {
   uint64_t packed_full[kRaw], packed_empty[kRaw];
-  uint64_t kv_full[kSlots], kv_empty[kSlots];
-  uint64_t q_full, s_full[2], p_full[2][2], o_full[2];
+  uint64_t kv_empty[kSlots];
+  uint64_t q_full, s_full[2], o_full[2];
   alignas(16) uint32_t valid[4][4];     // [tile mod 4]: positions on a page of the cache and in range, as bits
   alignas(16) uint32_t nan_rows[4][4];  // positions with a NaN value scale
   uint8_t nan_groups[4][kTok];
   int64_t sums[kCta / 32];
   Place found;
   uint32_t tmem;
-  int abort;
+  int gave_up;
 };
 static_assert(sizeof(Shared) <= 2048, "shared state");
 
@@ -186,10 +186,10 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// A warp waits for a phase (each lane may name a barrier of its own); gives up after kWaitPolls, or as soon as
-// another warp has. Every poll ends in a vote, so the warp's control flow is uniform
-// whatever the lanes see: the callers go on to .aligned instructions, and keep descriptors
-// and counters in uniform registers, which a diverged warp would step twice.
+// A warp waits for a phase, kWaitPolls polls at most; a wait that gives up marks the CTA, whose outputs are NaN
+// then, and the warp goes on: the roles keep their steps, so nobody waits for one that has
+// left. Every poll ends in a vote, so the warp's control flow is uniform: the callers go on to .aligned
+// instructions.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Shared* sh) {
   bool done = mbar_ready(bar, parity);
   if (__all_sync(~0u, done)) return true;
@@ -197,12 +197,25 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Shared
   for (uint32_t i = 0; i < lt::kWaitPolls; ++i) {
     done = done | lt::mbar_try_wait(bar, parity);
     if (__all_sync(~0u, done)) return true;
-    const int aborted = *(volatile int*)&sh->abort;
-    if (__any_sync(~0u, aborted != 0)) return false;
   }
-  *(volatile int*)&sh->abort = 1;
+  *(volatile int*)&sh->gave_up = 1;
   return false;
 }
+
+// What the issuing warp waits for comes over the CTA's named barriers: it sees them within some 50 clocks, where
+// a look at an mbarrier takes 250 and more while the products keep shared memory busy. A named
+// barrier's wait has no limit of its own; it ends because every role keeps its steps, also
+// after a wait that gave up.
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  asm volatile("barrier.cta.arrive %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ int weights_ready(int which, int half) { return 1 + 2 * which + half; }
+constexpr int kWeightsThreads = 128 + 32;
+__device__ __forceinline__ int slot_ready(int slot) { return 5 + slot; }
+constexpr int kSlotThreads = 64 + 32;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -294,10 +307,8 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   // cache that four kinds of warps share.
   float m = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;  // m in units of log 2
   uint32_t poison = 0;                             // value groups in which this row is NaN
-  bool ok = true;
   for (int i = 0; i < job.tiles; ++i) {
-    ok = wait_warp(&sh->s_full[which], i & 1, sh);
-    if (!ok) break;
+    wait_warp(&sh->s_full[which], i & 1, sh);
     fence_after();
     const int pos0 = job.from + i * kTok;
     const uint32_t* valid = sh->valid[i & 3];
@@ -383,11 +394,11 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
       tmem_st32(s_at + 32 * h, pk);  // (columns whose logits have been read)
       tmem_wait_st();
       fence_before();
-      arrive(&sh->p_full[which][h]);  // the second product starts on the first half
+      named_arrive(weights_ready(which, h), kWeightsThreads);  // the second product starts on the first half
       __syncwarp();
     }
   }
-  ok = wait_warp(&sh->o_full[which], 0, sh) && ok;
+  const bool ok = wait_warp(&sh->o_full[which], 0, sh) && *(volatile int*)&sh->gave_up == 0;
   __syncwarp();
   fence_after();
 
@@ -471,7 +482,7 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
   uint32_t parity = 1;  // (the first round's stages are free)
 #pragma unroll 1
   for (int n = 0; n < stages; ++n) {
-    if (!wait_warp(&sh->packed_empty[stage], parity, sh)) break;
+    wait_warp(&sh->packed_empty[stage], parity, sh);
     uint32_t valid[2] = {0u, 0u};
     int count[kMost];
 #pragma unroll
@@ -518,15 +529,13 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
   for (int c = 0; c < 8; ++c) chunk_at[c] = lt::smem_u32(smem + Smem<D>::kKv) + row * 128 + ((c ^ (row & 7)) << 4);
   int slot = part, stage = 0;                  // keys in slots 0, 2, 0, ..., values in 1, 3, 1, ...
   uint32_t slot_parity = 1, stage_parity = 0;  // (the first round's slots are free)
-  bool ok = true;
+  bool fed = true;
 #pragma unroll 1
   for (int i = 0; i < job.tiles; ++i) {
-    ok = wait_warp(&sh->kv_empty[slot], slot_parity, sh);
-    if (!ok) break;
+    wait_warp(&sh->kv_empty[slot], slot_parity, sh);
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
-      ok = wait_warp(&sh->packed_full[stage], stage_parity, sh);
-      if (!ok) break;
+      fed = fed && wait_warp(&sh->packed_full[stage], stage_parity, sh);  // (once in vain is enough)
       const uint32_t valid = sh->valid[i & 3][half * 2 + (warp & 1)];
       const bool there = (valid >> lane) & 1u;
       const uint8_t* from = smem + Smem<D>::kPacked + (stage * kPart + row) * kRow;
@@ -574,9 +583,8 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
         stage_parity ^= 1u;
       }
     }
-    if (!ok) break;
     fence_async();
-    arrive(&sh->kv_full[slot]);
+    named_arrive(slot_ready(slot), kSlotThreads);
     slot ^= 2;
     if (slot == part) slot_parity ^= 1u;
   }
@@ -588,71 +596,45 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   constexpr uint32_t kIdescS = instruction(kTok, false), kIdescO = instruction(D, true);
   const uint32_t q_at = lt::smem_u32(smem + Smem<D>::kQ), kv_at = lt::smem_u32(smem + Smem<D>::kKv);
   const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0), lead = elect_one();
-  bool ok = wait_warp(&sh->q_full, 0, sh);
-  // A look at a barrier takes some 250 clocks while the products keep shared memory busy. So the look at
-  // the one that is needed next is sent ahead of a product's instructions, and only a phase
-  // that was not complete then is waited for.
-  bool early = false;
-  auto look = [&](uint64_t* bar, uint32_t phase) { early = mbar_ready(bar, phase & 1); };
-  auto need = [&](uint64_t* bar, uint32_t phase) {
-    if (!__all_sync(~0u, early)) ok = wait_warp(bar, phase & 1, sh) && ok;
-    early = false;
-    return ok;
-  };
+  wait_warp(&sh->q_full, 0, sh);
   // keys of tile i are in slot (i & 1) * 2, values in the next
-  auto key_full = [&](int i) { return &sh->kv_full[(i & 1) * 2]; };
-  auto value_full = [&](int i) { return &sh->kv_full[(i & 1) * 2 + 1]; };
-  const int tiles = ok ? job.tiles : 0;
-  if (tiles > 0) need(key_full(0), 0);
+  const int tiles = job.tiles;
+  if (tiles > 0) named_sync(slot_ready(0), kSlotThreads);
   // One place for each product, in a rolled loop: even steps row tile A, odd ones row tile B; first the weights
   // of tile i by its values, then the logits of tile i + 1. (Descriptors hold addresses in
   // units of 16 bytes; the steps' offsets are added to them.)
 #pragma unroll 1
-  for (int step = 0; step <= 2 * tiles + 1 && ok && tiles > 0; ++step) {
+  for (int step = 0; step <= 2 * tiles + 1 && tiles > 0; ++step) {
     const int which = step & 1, i = (step >> 1) - 1;
     const bool weights = i >= 0, keys = i + 1 < tiles;
-    uint64_t* const value_empty = &sh->kv_empty[(i & 1) * 2 + 1];
-    uint64_t* const key_empty = &sh->kv_empty[((i + 1) & 1) * 2];
+    const int value_slot = (i & 1) * 2 + 1, key_slot = ((i + 1) & 1) * 2;
     if (which == 1 && !job.two) {
-      if (weights) mma_commit(value_empty, lead);
-      if (keys) mma_commit(key_empty, lead);
+      if (weights) mma_commit(&sh->kv_empty[value_slot], lead);
+      if (keys) mma_commit(&sh->kv_empty[key_slot], lead);
       continue;
     }
     if (weights) {
-      if (which == 0) {
-        if (!need(value_full(i), i >> 1)) break;
-        look(&sh->p_full[0][0], i);
-      }
-      const uint64_t value = desc_mn_major(kv_at + ((i & 1) * 2 + 1) * Smem<D>::kOperand, Smem<D>::kHalf);
-#pragma unroll 1
+      if (which == 0) named_sync(slot_ready(value_slot), kSlotThreads);
+      const uint64_t value = desc_mn_major(kv_at + value_slot * Smem<D>::kOperand, Smem<D>::kHalf);
+#pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (!need(&sh->p_full[which][half], i)) break;
+        named_sync(weights_ready(which, half), kWeightsThreads);
         fence_after();
-        if (half == 0)
-          look(&sh->p_full[which][1], i);
-        else if (which == 0 && keys)
-          look(key_full(i + 1), (i + 1) >> 1);
         mma_ts4(tmem + 2 * kTok + which * D, tmem + which * kTok + half * 32, value + half * ((kTok / 2 * 128) >> 4), kIdescO,
                 i > 0 || half > 0, lead);
       }
-      if (!ok) break;
-      if (which == 1) mma_commit(value_empty, lead);
+      if (which == 1) mma_commit(&sh->kv_empty[value_slot], lead);
     }
     if (keys) {
-      if (which == 0 && weights && !need(key_full(i + 1), (i + 1) >> 1)) break;
+      if (which == 0 && weights) named_sync(slot_ready(key_slot), kSlotThreads);
       fence_after();
-      // what the next step begins with
-      if (which == 1 || !job.two)
-        look(value_full(i + 1), (i + 1) >> 1);
-      else if (weights)
-        look(&sh->p_full[1][0], i);
       const uint64_t q = desc_k_major(q_at + which * Smem<D>::kOperand);
-      const uint64_t key = desc_k_major(kv_at + ((i + 1) & 1) * 2 * Smem<D>::kOperand);
+      const uint64_t key = desc_k_major(kv_at + key_slot * Smem<D>::kOperand);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
         mma_ss4(tmem + which * kTok, q + c * (Smem<D>::kHalf >> 4), key + c * (Smem<D>::kHalf >> 4), kIdescS, c > 0, lead);
       mma_commit(&sh->s_full[which], lead);
-      if (which == 1) mma_commit(key_empty, lead);
+      if (which == 1) mma_commit(&sh->kv_empty[key_slot], lead);
     }
   }
   mma_commit(&sh->o_full[0], lead);
@@ -671,17 +653,14 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
       lt::mbar_init(&sh->packed_empty[s], 4);
     }
     for (int s = 0; s < kSlots; ++s) {
-      lt::mbar_init(&sh->kv_full[s], 64);
       lt::mbar_init(&sh->kv_empty[s], 1);
     }
     lt::mbar_init(&sh->q_full, 256);
     for (int t = 0; t < 2; ++t) {
       lt::mbar_init(&sh->s_full[t], 1);
-      lt::mbar_init(&sh->p_full[t][0], 128);
-      lt::mbar_init(&sh->p_full[t][1], 128);
       lt::mbar_init(&sh->o_full[t], 1);
     }
-    sh->abort = 0;
+    sh->gave_up = 0;
     lt::mbar_fence_init();
   }
   dependency_wait();
