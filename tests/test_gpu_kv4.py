@@ -574,3 +574,17 @@ def test_a_serving_step_end_to_end():
     lengths, num_free = lt.page_release(lengths, torch.tensor([True, False, True], device="cuda"), table, free, num_free, page)
     held = [-(-sum(x) // page) for x in ([40, 1, 0, 1], [7, 1, 1, 2])]
     assert int(num_free) == before + sum(held) and lengths.tolist() == [0, 37, 0]
+
+
+def test_the_example_runs_and_is_right():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "sparse_step.py")
+    spec = importlib.util.spec_from_file_location("sparse_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    for kw in ({"tokens": 400, "steps": 9}, {"tokens": 64, "steps": 4, "k": 100, "head_dim": 64, "kv_heads": 1}):
+        results, held, free, pages = example.run(**kw)
+        # outputs are averages of values of unit size, rounded to bf16 and with fp16 weights
+        assert example.check(results, held) < 2.0 ** -8 * 4 + 2.0 ** -9 * 4
+        assert free == pages and len(results) == kw["steps"]
