@@ -124,7 +124,7 @@ lt_status lt_kv4_load(const void* cache, int64_t pages, int32_t page_size, const
 /*
  * lt_kv4_attention -- attention of new tokens over the cache.
  *
- * Request r has lengths[r] positions in the cache; its queries are the rows
+ * Request r has lengths[r] positions in the cache (at most its table row's, and 2^31 - 1024); its queries are the rows
  * q[starts[r] .. starts[r + 1]), the last of those positions: query i of n lies
  * at position lengths[r] - n + i. Query head h reads kv head
  * h / (q_heads / kv_heads). For each query and head, over its visible positions:

@@ -178,9 +178,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
     if (flat == pl.base && head == 0 && row_tile == 0 && tid == 0 && p.plan != nullptr)
       p.plan[request] = make_int2(pl.base, pl.count);
     // chunks start on tiles: rq.low is a multiple of kTile
-    const int64_t at = rq.low + (int64_t)pl.split * pl.chunk;
+    const int64_t at = rq.low + pl.split * chunk_of(p, rq, pl.count), end = at + chunk_of(p, rq, pl.count);
     from = (int)(at < rq.length ? at : rq.length);
-    to = (int)(at + pl.chunk < rq.length ? at + pl.chunk : rq.length);
+    to = (int)(end < rq.length ? end : rq.length);
   }
   const int row0 = row_tile * NT * 8;
   if (row0 >= rows) return;
@@ -744,7 +744,11 @@ struct Plan {
 
 constexpr int kMinChunk = 256;
 constexpr int kPrefillMinChunk = 512;
-constexpr int kPrefillFrom = 64;    // query rows a kv head from which the kernel for many rows is taken
+// Query rows a kv head from which the kernel for many rows is taken, each side's us with 8 kv heads of D:
+//   1 request of 8192 positions, D = 128: 26 there, 25 here with 16 rows, 28 and 37 with 32, 36 and 74 with 256
+//   16 requests of 4096, D = 128: 81 and 74 with 32 rows, 87 and 119 with 64; D = 64: 68 and 59, 73 and 57
+// so from two row tiles of this kernel on (D = 64: from three), and with few CTAs from 17 rows.
+int prefill_from(int d, bool few) { return few ? 17 : d == 64 ? 65 : 33; }
 constexpr int kPartPositions = 2048;  // positions of a part up to which requests are cut into equal numbers of parts
 
 Plan finish_plan(Plan a, int heads, int d, int requests) {
@@ -763,7 +767,7 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
                int64_t positions, int window) {
   Plan a = {};
   const int64_t rows = (int64_t)(list_len > 0 ? 1 : max_new) * group;
-  a.prefill = list_len == 0 && d <= 128 && rows >= kPrefillFrom;
+  a.prefill = list_len == 0 && d <= 128 && rows >= prefill_from(d, (int64_t)requests * heads * 4 <= sms);
   if (a.prefill) {
     a.cta_rows = kPrefillRows;
     a.row_tiles = (int)((rows + kPrefillRows - 1) / kPrefillRows);

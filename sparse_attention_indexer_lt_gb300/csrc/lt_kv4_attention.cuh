@@ -43,7 +43,7 @@ struct Request {
 
 __device__ __forceinline__ Request request_of(const AttentionParams& p, int r) {
   Request q;
-  const int64_t most = (int64_t)p.width << p.shift;
+  const int64_t most = min((int64_t)p.width << p.shift, (int64_t)INT32_MAX - 1023);  // (sums of a few tiles stay in 32 bits)
   const int len = max(__ldg(p.lengths + r), 0);
   q.length = (int)(len < most ? len : most);
   int first = r, end = r + 1;
@@ -63,10 +63,14 @@ __device__ __forceinline__ Request request_of(const AttentionParams& p, int r) {
 // Which request and chunk this CTA has: the requests' positions cut into chunks of one size, flat.
 struct Place {
   int request, split, base, count;  // count chunks, the first with flat number base
-  int chunk;                        // positions of a chunk
 };
 
-// The requests' spans add up to `total`; with about `target` chunks wanted, a chunk has
+// The positions of each of a request's chunks: alike, and multiples of p.align.
+__device__ __forceinline__ int64_t chunk_of(const AttentionParams& p, const Request& q, int count) {
+  return ((int64_t)(q.span + count - 1) / count + p.align - 1) / p.align * p.align;
+}
+
+// The requests' spans add up to `total`; with about `target` chunks wanted, a chunk has at most
 // total / target positions (a multiple of p.align, min_chunk at least) and request r has
 // ceil(span / chunk) of them: ragged requests come out as chunks of like work, which
 // the hardware hands to SMs as they fall free. Every CTA computes this from the
@@ -96,7 +100,6 @@ __device__ __forceinline__ bool find_place_in_warp(const AttentionParams& p, int
   out->base = __shfl_sync(~0u, end - n, r);
   out->count = __shfl_sync(~0u, n, r);
   out->split = flat - out->base;
-  out->chunk = (int)(chunk > INT32_MAX ? INT32_MAX / 128 * 128 : chunk);
   return true;
 }
 
@@ -156,7 +159,6 @@ __device__ __forceinline__ bool find_place(const AttentionParams& p, int flat, P
   }
   __syncthreads();
   *out = *found;
-  out->chunk = (int)(chunk > INT32_MAX ? INT32_MAX / 128 * 128 : chunk);
   return out->request >= 0;
 }
 

@@ -683,9 +683,9 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   if (job.row0 >= job.rows) return;
   job.two = job.rows - job.row0 > 128;
   {
-    const int64_t at = job.rq.low + (int64_t)pl.split * pl.chunk;
+    const int64_t at = job.rq.low + pl.split * chunk_of(p, job.rq, pl.count), end = at + chunk_of(p, job.rq, pl.count);
     job.from = (int)(at < job.rq.length ? at : job.rq.length);
-    job.to = (int)(at + pl.chunk < job.rq.length ? at + pl.chunk : job.rq.length);
+    job.to = (int)(end < job.rq.length ? end : job.rq.length);
     const int last = min(job.rows - 1, job.row0 + 255) / p.group;
     job.to = min(job.to, job.rq.length - job.rq.queries + last + 1);
     if (p.window > 0)

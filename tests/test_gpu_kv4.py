@@ -329,6 +329,13 @@ def test_prefill_page_sizes_with_parts_and_windows(page):
         p.check(*p.run(window=window), window=window)
 
 
+def test_prefill_of_empty_and_of_many_requests():
+    p = Problem([0, 200, 0], [90, 70, 64], 1, 1, 64, 16, "f16", seed=31, extra_width=1)
+    p.check(*p.run())
+    p = Problem([64 + (r * 7) % 40 for r in range(40)], [64 + r % 3 for r in range(40)], 1, 1, 64, 16, "bf16", seed=32)
+    p.check(*p.run())
+
+
 def test_prefill_scales_and_bad_pages():
     for spread, magnitude, scale in ((30.0, 1.0, None), (1.0, 1.0, -0.2), (1.0, 1.0, 0.0), (1.0, 1e-4, 300.0), (1.0, 3000.0, 1e-4)):
         p = Problem([300], [40], 1, 4, 64, 16, "bf16", seed=21, spread=spread, magnitude=magnitude)
@@ -348,6 +355,14 @@ def test_prefill_nan_where_nothing_looks():
     assert torch.isnan(out[30:79, :, 32:64]).all()
     assert torch.equal(out[30:79, :, :32], clean[30:79, :, :32]) and torch.equal(out[30:79, :, 64:], clean[30:79, :, 64:])
     assert torch.isnan(out[79]).all() and torch.isnan(lse[79]).all()
+
+
+@pytest.mark.parametrize("dim,group,most", [(64, 5, 5), (128, 5, 5), (64, 10, 6), (256, 10, 3)])
+def test_many_requests_of_some_query_rows(dim, group, most):
+    """Row tiles of 32 (16 for D = 256), two of them for some requests, where there are CTAs for every SM."""
+    p = Problem([1 + (r * 11) % 70 for r in range(45)], [1 + r % most for r in range(45)], 1, group, dim, 16, "bf16", seed=dim + most)
+    for window in (0, 9):
+        p.check(*p.run(window=window), window=window)
 
 
 @pytest.mark.parametrize("dim,heads,group,list_len", [(64, 2, 4, 1), (128, 1, 16, 33), (128, 2, 8, 512), (256, 1, 4, 100), (128, 1, 40, 130)])
