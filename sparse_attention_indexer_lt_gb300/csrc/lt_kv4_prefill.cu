@@ -666,21 +666,23 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   dependency_wait();
 
   Job job;
-  const int64_t unit = blockIdx.x;
-  // the last rows see the most positions: they start first
-  job.row_tile = p.row_tiles - 1 - (int)(unit % p.row_tiles);
-  job.head = (int)(unit / p.row_tiles % p.heads);
-  job.flat = (int)(unit / p.row_tiles / p.heads);
+  // A request's last rows see the most positions: every request's last row tile comes first, then their last
+  // but one, so the long CTAs start early and the short ones fill in.
+  const int units = gridDim.x / p.row_tiles;
+  const int nth = blockIdx.x / units, unit = blockIdx.x % units;
+  job.head = unit % p.heads;
+  job.flat = unit / p.heads;
   Place pl;
   if (!find_place<kCta>(p, job.flat, &pl, sh->sums, &sh->found)) return;
   job.request = pl.request;
   job.rq = request_of(p, pl.request);
   job.rows = job.rq.queries * p.group;
+  job.row_tile = min((job.rows + 255) / 256, p.row_tiles) - 1 - nth;
+  if (job.row_tile < 0) return;
   job.final_here = pl.count == 1;
   if (job.flat == pl.base && job.head == 0 && job.row_tile == 0 && tid == 0 && p.plan != nullptr)
     p.plan[pl.request] = make_int2(pl.base, pl.count);
   job.row0 = job.row_tile * 256;
-  if (job.row0 >= job.rows) return;
   job.two = job.rows - job.row0 > 128;
   {
     const int64_t at = job.rq.low + pl.split * chunk_of(p, job.rq, pl.count), end = at + chunk_of(p, job.rq, pl.count);
