@@ -1,7 +1,7 @@
 // lt_kv4_prefill.cu -- attention over the 4-bit cache for many query rows a
 // request (prefill chunks): tcgen05 with the sums in tensor memory.
 //
-// A CTA takes 256 query rows of one kv head (two tiles of 128, one thread a row) and a
+// A CTA takes 256 query rows of one kv head (two tiles of 128, a thread a row) and a
 // range of positions in tiles of 128, with one role a warpgroup:
 //   warpgroups 0 and 1  softmax of row tile A and B: logits from tensor memory,
 //                       weights back into it as fp16, where the second product reads them
@@ -20,6 +20,19 @@
 // The running maximum moves only when a row's logits pass it by 2^8 (the sums are
 // then rescaled in tensor memory, seldom); weights are held as 2^6 exp(s - max) at
 // most 2^14, so fp16 neither overflows nor goes subnormal above 2^-20.
+//
+// What bounds it: the chain softmax, second product, next first product of a row tile.
+// An iteration (both row tiles by 128 positions of D = 128) takes some 3100 clocks, the
+// products alone 2048 (64 each, in every operand mode); the softmax's part is some 1700 from the logits'
+// arrival to the weights'. What the chain gave up on the way, on a chunk of 2048 tokens
+// behind 14336 positions (32 query heads on 8 kv heads): 941 us with one lane issuing, 716
+// with the warp issuing and copies in a warp of their own, 650 with short loops and whole-line
+// queries and outputs, 511 without cutting requests that fill the SMs, 494 with four
+// products a statement, 424 with named barriers, 410 with the longest row tiles first: 1.26
+// PFLOP/s, 65% of cuBLAS's burst; 84% is the most that two waves of 256 CTAs on 152 SMs
+// allow. Measured and dropped: a quarter, a third or half of the exponentials on the FMA
+// pipes (541, 557, 621 us against 511), two threads a row (541), the first half's weights taken
+// before the tile's maximum is known (804 against 716).
 //
 // A value that is NaN is unpacked as zero, and the rows that see it note the group:
 // a row's output is NaN there whatever its weight, and rows that do not see it stay clean.

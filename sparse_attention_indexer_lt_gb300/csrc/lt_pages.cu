@@ -8,6 +8,10 @@
 // CTA) in segments of kSegment, and then writes its share of the segment's
 // tokens and pages, finding an item's request by a binary search in the
 // scanned sums. No CTA waits for another one, and one launch does the step.
+//
+// Bound by latency: release and extend take some 5 us each in a graph for 64 requests, and 6
+// for 1000 requests with 128000 token slots (1.6 MB, a quarter of a microsecond at
+// HBM's rate).
 
 #include <cuda_runtime.h>
 
