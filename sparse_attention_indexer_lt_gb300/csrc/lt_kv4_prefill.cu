@@ -5,8 +5,8 @@
 // range of positions in tiles of 128, with one role a warpgroup:
 //   warpgroups 0 and 1  softmax of row tile A and B: logits from tensor memory,
 //                       weights back into it as fp16, where the second product reads them
-//   warpgroup 2         unpacks: a thread turns one position's codes into fp16 keys and
-//                       values, written with the 128-byte swizzle that the tensor core reads
+//   warpgroup 2         unpacks: a thread turns one position's key or value codes into fp16,
+//                       written with the 128-byte swizzle that the tensor core reads
 //   warpgroup 3         one warp issues the products, another the bulk copies of packed rows
 // in the order  S_A(i) = Q_A K(i)^T,  O_B += P_B(i-1) V(i-1),  S_B(i),  O_A += P_A(i) V(i): while one row
 // tile's softmax runs, the tensor core has the other's two products.
