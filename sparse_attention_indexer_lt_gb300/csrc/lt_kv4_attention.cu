@@ -803,7 +803,11 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
   // costs the drafted step 55 us instead of 46)
   int parts = 1;
   while (parts < kMaxParts && whole * parts < slots && seen > (int64_t)parts * kTile * kWarps) parts *= 2;
-  if (list_len > 0 || seen <= (int64_t)parts * kPartPositions) {
+  // Requests stay whole, too, where they are so many that the hardware evens them out and none can be long
+  // (us whole against chunks, 8 kv heads of 128: 256 requests to 8192 positions 287 and 303, 1024
+  // 956 and 1083; but 128 to 8192 176 and 168, 128 to 32768 638 and 498, 512 of 4 heads 1051 and 998).
+  const bool whole_ones = parts == 1 && ((whole >= 3 * slots && seen <= 8192) || (whole >= 8 * slots && seen <= 32768));
+  if (list_len > 0 || whole_ones || seen <= (int64_t)parts * kPartPositions) {
     a.parts = parts;
     a.flats = list_len > 0 ? tokens : requests;
     return finish_plan(a, heads, d, requests);

@@ -400,6 +400,26 @@ def test_long_tables_are_cut_into_chunks(lengths, new):
     assert torch.equal(out, p.run()[0])
 
 
+def test_a_great_many_requests_stay_whole():
+    """More requests than chunks would serve, of tables longer than a part: rows against the same rows alone."""
+    import sparse_attention_indexer_lt_gb300 as lt
+    torch.manual_seed(3)
+    n, heads, page, width = 700, 8, 64, 40
+    cache = torch.randint(0, 256, (300, heads, page, 80), dtype=torch.uint8, device="cuda")
+    scales = (0.35 * torch.exp(0.3 * torch.randn(300, heads, page, 4, device="cuda"))).half().view(torch.int16) & -4
+    cache[..., 64:72] = scales.view(torch.uint8)
+    table = torch.randint(0, 300, (n, width), dtype=torch.int32, device="cuda")
+    lengths = torch.randint(0, width * page + 1, (n,), dtype=torch.int32, device="cuda")
+    lengths[:3] = torch.tensor([0, 1, width * page])
+    q = torch.randn(n, heads * 2, 64, device="cuda").half()
+    out, lse = lt.kv4_attention(q, cache, table, lengths, with_lse=True)
+    for r in (0, 1, 2, 350, 699):
+        one, one_lse = lt.kv4_attention(q[r:r + 1], cache, table[r:r + 1], lengths[r:r + 1].clone(), with_lse=True)
+        # the same sums in another order: fp32 sums of up to 2560 terms, outputs rounded to fp16
+        assert (one.float() - out[r:r + 1].float()).abs().max() <= 2.0 ** -10 * 6 and torch.allclose(one_lse, lse[r:r + 1], atol=1e-4, rtol=0)
+    assert not out[0].any() and torch.isinf(lse[0]).all()
+
+
 def test_scales_and_spreads():
     """Peaked and flat rows, a negative and a zero scale, small and large stored values."""
     for spread, magnitude, scale in ((30.0, 1.0, None), (1e-3, 1.0, None), (1.0, 1.0, -0.2), (1.0, 1.0, 0.0), (1.0, 1e-4, 300.0), (1.0, 3000.0, 1e-4)):
