@@ -776,10 +776,10 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
                int64_t positions, int window) {
   Plan a = {};
   const int64_t rows = (int64_t)(list_len > 0 ? 1 : max_new) * group;
-  a.prefill = list_len == 0 && d <= 128 && rows >= prefill_from(d, (int64_t)requests * heads * 4 <= sms);
+  a.prefill = list_len == 0 && rows >= prefill_from(d, (int64_t)requests * heads * 4 <= sms);
   if (a.prefill) {
-    a.cta_rows = kPrefillRows;
-    a.row_tiles = (int)((rows + kPrefillRows - 1) / kPrefillRows);
+    a.cta_rows = prefill_rows(d);
+    a.row_tiles = (int)((rows + a.cta_rows - 1) / a.cta_rows);
     a.min_chunk = kPrefillMinChunk;
     // one CTA an SM: chunks only where the row tiles alone do not fill the SMs (their joins cost more than an
     // uneven second wave: 256 row tiles of 16384 positions take 511 us whole, 690 us in halves)

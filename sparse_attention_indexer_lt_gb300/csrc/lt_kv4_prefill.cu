@@ -1,8 +1,8 @@
 // lt_kv4_prefill.cu -- attention over the 4-bit cache for many query rows a
 // request (prefill chunks): tcgen05 with the sums in tensor memory.
 //
-// A CTA takes 256 query rows of one kv head (two tiles of 128, a thread a row) and a
-// range of positions in tiles of 128, with one role a warpgroup:
+// A CTA takes 256 query rows of one kv head (two tiles of 128, a thread a row; one tile
+// with heads of 256) and a range of positions in tiles of 128, with one role a warpgroup:
 //   warpgroups 0 and 1  softmax of row tile A and B: logits from tensor memory,
 //                       weights back into it as fp16, where the second product reads them
 //   warpgroup 2         unpacks: a thread turns one position's key or value codes into fp16,
@@ -49,19 +49,23 @@ using namespace lt::kv4;
 
 constexpr int kCta = 512;
 constexpr int kTok = 128;    // positions of a tile
-constexpr int kSlots = 4;    // unpacked key or value tiles in shared memory
-constexpr int kPart = 64;    // positions of a packed stage
-constexpr int kRaw = 3;      // packed stages in shared memory or on their way there
+constexpr int kMaxSlots = 4;  // unpacked key or value tiles in shared memory
+constexpr int kRaw = 3;       // packed stages in shared memory or on their way there
 constexpr float kShift = 6.0f;
 constexpr float kSlack = 8.0f;  // how far logits may pass the maximum (log 2) before it moves
 
 template <int D>
 struct Smem {
   static constexpr int kRow = row_bytes(D);
+  // heads of 256 leave room for one row tile, a key and a value tile
+  static constexpr int kRowTiles = D == 256 ? 1 : 2;
+  static constexpr int kSlots = D == 256 ? 2 : 4;
+  static constexpr int kPart = D == 256 ? 32 : 64;       // positions of a packed stage
+  static constexpr int kParts = kTok / kPart;
   static constexpr int kHalf = kTok * 128;               // 128 rows by 64 channels, swizzled
   static constexpr int kOperand = kHalf * (D / 64);
-  static constexpr int kQ = 0;                           // two row tiles
-  static constexpr int kKv = kQ + 2 * kOperand;          // kSlots
+  static constexpr int kQ = 0;                           // kRowTiles
+  static constexpr int kKv = kQ + kRowTiles * kOperand;  // kSlots
   static constexpr int kPacked = kKv + kSlots * kOperand;  // [kRaw][kPart rows]
   static constexpr int kBars = kPacked + kRaw * kPart * kRow;
   static constexpr int kTotal = kBars + 2048 + 1024;     // (slack to align the start to 1024)
@@ -69,7 +73,7 @@ struct Smem {
 
 struct Shared {
   uint64_t packed_full[kRaw], packed_empty[kRaw];
-  uint64_t kv_empty[kSlots];
+  uint64_t kv_empty[kMaxSlots];
   uint64_t q_full, s_full[2], o_full[2];
   alignas(16) uint32_t valid[4][4];     // [tile mod 4]: positions on a page of the cache and in range, as bits
   alignas(16) uint32_t nan_rows[4][4];  // positions with a NaN value scale
@@ -269,6 +273,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   // chunk c of row r of the tile, where the 128-byte swizzle puts it
   auto chunk_of = [&](int r, int c) { return reinterpret_cast<uint4*>(tile + (c / 8) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
 
+  if (which >= Smem<D>::kRowTiles) return;
   // the query rows into shared memory: the warp brings its rows one after the other, then each thread
   // makes its own row fp16, with the power of two that keeps bf16 in range
   float factor = p.scale_log2;
@@ -421,7 +426,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   float log2_sum = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m - kShift) + __log2f(sum);
   if (!ok) log2_sum = NAN;
-  const int64_t part = (((int64_t)job.flat * p.heads + job.head) * p.row_tiles + job.row_tile) * 256 + which * 128;
+  const int64_t part = (((int64_t)job.flat * p.heads + job.head) * p.row_tiles + job.row_tile) * (Smem<D>::kRowTiles * 128) + which * 128;
   const int per_pass = job.final_here ? D : D / 2;  // columns that fit the tile's rows
 #pragma unroll 1
   for (int c0 = 0; c0 < D; c0 += per_pass) {
@@ -476,12 +481,13 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
 template <int D>
 __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& job, Shared* sh, uint8_t* smem) {
   constexpr int kRow = row_bytes(D);
-  constexpr int kMost = kPart / 32;  // runs of a lane, at pages of one position
+  constexpr int kPart = Smem<D>::kPart, kParts = Smem<D>::kParts;
+  constexpr int kMost = kPart / 32;  // runs of a lane, at pages of one position; words of a stage's valid bits
   const int lane = threadIdx.x & 31;
   const uint32_t packed_at = lt::smem_u32(smem + Smem<D>::kPacked);
-  const int run_shift = min(p.shift, 6), runs = kPart >> run_shift;
+  const int run_shift = min(p.shift, kPart == 64 ? 6 : 5), runs = kPart >> run_shift;
   const int32_t* table = p.table + (int64_t)job.request * p.width;
-  const int stages = 2 * job.tiles;
+  const int stages = kParts * job.tiles;
   int page[kMost];
   auto look_up = [&](int n) {
 #pragma unroll
@@ -496,23 +502,28 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
 #pragma unroll 1
   for (int n = 0; n < stages; ++n) {
     wait_warp(&sh->packed_empty[stage], parity, sh);
-    uint32_t valid[2] = {0u, 0u};
+    uint32_t valid[kMost] = {};
     int count[kMost];
 #pragma unroll
     for (int j = 0; j < kMost; ++j) {
       const int first = (lane + 32 * j) << run_shift, left = job.to - (job.from + n * kPart + first);
       count[j] = page[j] >= 0 && page[j] < p.pages ? min(left, 1 << run_shift) : 0;
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
+      for (int w = 0; w < kMost; ++w) {
         const int a = min(max(first - 32 * w, 0), 32), b = min(max(first + count[j] - 32 * w, 0), 32);
         valid[w] |= a < b ? (b == 32 ? ~0u : (1u << b) - 1u) & (~0u << a) : 0u;
       }
     }
+    uint32_t there = 0;
 #pragma unroll
-    for (int w = 0; w < 2; ++w) valid[w] = __reduce_or_sync(~0u, valid[w]);
+    for (int w = 0; w < kMost; ++w) {
+      valid[w] = __reduce_or_sync(~0u, valid[w]);
+      there += __popc(valid[w]);
+    }
     if (lane == 0) {
-      *reinterpret_cast<uint2*>(&sh->valid[(n >> 1) & 3][(n & 1) * 2]) = make_uint2(valid[0], valid[1]);
-      lt::mbar_arrive_tx(&sh->packed_full[stage], (uint32_t)(__popc(valid[0]) + __popc(valid[1])) * kRow);
+#pragma unroll
+      for (int w = 0; w < kMost; ++w) sh->valid[(n / kParts) & 3][n % kParts * kMost + w] = valid[w];
+      lt::mbar_arrive_tx(&sh->packed_full[stage], there * kRow);
     }
     __syncwarp();
 #pragma unroll
@@ -531,35 +542,39 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
   }
 }
 
-// ---- unpacking: a packed stage's 64 positions at a time, a thread the key (threads 0 .. 63) or the value
-// (64 .. 127) of a position
+// ---- unpacking: a packed stage's positions at a time, a thread the key or the value of a position (with
+// D = 256 half of its channels); 64 threads have keys, 64 values
 template <int D>
 __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t* smem) {
   constexpr int kRow = row_bytes(D);
-  const int t = threadIdx.x & 127, warp = t >> 5, lane = t & 31, part = t >> 6, row = t & 63;
+  constexpr int kPart = Smem<D>::kPart, kParts = Smem<D>::kParts, kSlots = Smem<D>::kSlots;
+  constexpr int kBlocks = D / 64 / (64 / kPart);  // 64-channel blocks of a thread
+  const int t = threadIdx.x & 127, lane = t & 31, row = t % kPart, part = t / kPart & 1;
+  const int block0 = t / (2 * kPart) * kBlocks;
   uint32_t chunk_at[8];  // where the row's eight 16-byte chunks lie in a swizzled 128-byte row
 #pragma unroll
   for (int c = 0; c < 8; ++c) chunk_at[c] = lt::smem_u32(smem + Smem<D>::kKv) + row * 128 + ((c ^ (row & 7)) << 4);
-  int slot = part, stage = 0;                  // keys in slots 0, 2, 0, ..., values in 1, 3, 1, ...
+  int slot = part, stage = 0;                  // keys in slots 0, 2, 0, ..., values in 1, 3, 1, ... (or 0 and 1)
   uint32_t slot_parity = 1, stage_parity = 0;  // (the first round's slots are free)
   bool fed = true;
 #pragma unroll 1
   for (int i = 0; i < job.tiles; ++i) {
     wait_warp(&sh->kv_empty[slot], slot_parity, sh);
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < kParts; ++half) {
       fed = fed && wait_warp(&sh->packed_full[stage], stage_parity, sh);  // (once in vain is enough)
-      const uint32_t valid = sh->valid[i & 3][half * 2 + (warp & 1)];
+      const int word = half * (kPart / 32) + row / 32;  // (the warp's rows are one word's)
+      const uint32_t valid = sh->valid[i & 3][word];
       const bool there = (valid >> lane) & 1u;
       const uint8_t* from = smem + Smem<D>::kPacked + (stage * kPart + row) * kRow;
       // scales, fp16 pairs; a position that is not there counts as zeros, and so does a NaN value
-      uint32_t sc[D / 64];
+      uint32_t sc[kBlocks];
 #pragma unroll
-      for (int g = 0; g < D / 64; ++g) {
-        sc[g] = there ? reinterpret_cast<const uint32_t*>(from + D + part * (D / 16))[g] : 0u;
+      for (int g = 0; g < kBlocks; ++g) {
+        sc[g] = there ? reinterpret_cast<const uint32_t*>(from + D + part * (D / 16))[block0 + g] : 0u;
         if (part == 1) sc[g] &= ~nan_halves(sc[g]);
       }
-      if (part == 0) {
+      if (part == 0 && block0 == 0) {
         // the NaN values are noted here, with the keys: the softmax starts when the keys are there
         uint32_t nan = 0;
 #pragma unroll
@@ -568,15 +583,15 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
           nan |= ((n & 1u) | ((n >> 15) & 2u)) << (2 * g);
         }
         const uint32_t nan_rows = __ballot_sync(~0u, nan != 0);
-        if (lane == 0) sh->nan_rows[i & 3][half * 2 + (warp & 1)] = nan_rows;
+        if (lane == 0) sh->nan_rows[i & 3][word] = nan_rows;
         if (nan_rows) sh->nan_groups[i & 3][half * kPart + row] = (uint8_t)nan;
       }
       const uint32_t to = slot * Smem<D>::kOperand + half * (kPart * 128);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
+      for (int c = 0; c < kBlocks; ++c) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const uint4 v = reinterpret_cast<const uint4*>(from + part * (D / 2))[2 * c + g];
+          const uint4 v = reinterpret_cast<const uint4*>(from + part * (D / 2))[2 * (block0 + c) + g];
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           const uint32_t scale = __byte_perm(sc[c], 0, g ? 0x3232 : 0x1010);
 #pragma unroll
@@ -584,7 +599,7 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
             uint32_t h[4];
             codes_to_half2(w[j], h);
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                         :: "r"(chunk_at[g * 4 + j] + to + c * Smem<D>::kHalf), "r"(hmul2(h[0], scale)),
+                         :: "r"(chunk_at[g * 4 + j] + to + (block0 + c) * Smem<D>::kHalf), "r"(hmul2(h[0], scale)),
                             "r"(hmul2(h[1], scale)), "r"(hmul2(h[2], scale)), "r"(hmul2(h[3], scale)) : "memory");
           }
         }
@@ -598,7 +613,7 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
     }
     fence_async();
     named_arrive(slot_ready(slot), kSlotThreads);
-    slot ^= 2;
+    if constexpr (kSlots == 4) slot ^= 2;
     if (slot == part) slot_parity ^= 1u;
   }
 }
@@ -610,7 +625,8 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   const uint32_t q_at = lt::smem_u32(smem + Smem<D>::kQ), kv_at = lt::smem_u32(smem + Smem<D>::kKv);
   const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0), lead = elect_one();
   wait_warp(&sh->q_full, 0, sh);
-  // keys of tile i are in slot (i & 1) * 2, values in the next
+  // keys of tile i are in slot (i & 1) * 2 (of two slots: 0), values in the next
+  constexpr int kTurn = Smem<D>::kSlots == 4 ? 1 : 0;
   const int tiles = job.tiles;
   if (tiles > 0) named_sync(slot_ready(0), kSlotThreads);
   // One place for each product, in a rolled loop: even steps row tile A, odd ones row tile B; first the weights
@@ -620,12 +636,12 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   for (int step = 0; step <= 2 * tiles + 1 && tiles > 0; ++step) {
     const int which = step & 1, i = (step >> 1) - 1;
     const bool weights = i >= 0, keys = i + 1 < tiles;
-    const int value_slot = (i & 1) * 2 + 1, key_slot = ((i + 1) & 1) * 2;
-    if (which == 1 && !job.two) {
-      if (weights) mma_commit(&sh->kv_empty[value_slot], lead);
-      if (keys) mma_commit(&sh->kv_empty[key_slot], lead);
-      continue;
-    }
+    const int value_slot = (i & kTurn) * 2 + 1, key_slot = ((i + 1) & kTurn) * 2;
+    if (which == 1 && !job.two) continue;
+    // A slot is free when the last row tile's product has read it. The values' is given back before the next keys
+    // are waited for: with two slots those come only after it (keys and values of a tile are
+    // unpacked from the same packed stages).
+    const bool last = which == 1 || !job.two;
     if (weights) {
       if (which == 0) named_sync(slot_ready(value_slot), kSlotThreads);
       const uint64_t value = desc_mn_major(kv_at + value_slot * Smem<D>::kOperand, Smem<D>::kHalf);
@@ -636,7 +652,7 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
         mma_ts4(tmem + 2 * kTok + which * D, tmem + which * kTok + half * 32, value + half * ((kTok / 2 * 128) >> 4), kIdescO,
                 i > 0 || half > 0, lead);
       }
-      if (which == 1) mma_commit(&sh->kv_empty[value_slot], lead);
+      if (last) mma_commit(&sh->kv_empty[value_slot], lead);
     }
     if (keys) {
       if (which == 0 && weights) named_sync(slot_ready(key_slot), kSlotThreads);
@@ -647,7 +663,7 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
       for (int c = 0; c < D / 64; ++c)
         mma_ss4(tmem + which * kTok, q + c * (Smem<D>::kHalf >> 4), key + c * (Smem<D>::kHalf >> 4), kIdescS, c > 0, lead);
       mma_commit(&sh->s_full[which], lead);
-      if (which == 1) mma_commit(&sh->kv_empty[key_slot], lead);
+      if (last) mma_commit(&sh->kv_empty[key_slot], lead);
     }
   }
   mma_commit(&sh->o_full[0], lead);
@@ -665,10 +681,8 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
       lt::mbar_init(&sh->packed_full[s], 1);
       lt::mbar_init(&sh->packed_empty[s], 4);
     }
-    for (int s = 0; s < kSlots; ++s) {
-      lt::mbar_init(&sh->kv_empty[s], 1);
-    }
-    lt::mbar_init(&sh->q_full, 256);
+    for (int s = 0; s < kMaxSlots; ++s) lt::mbar_init(&sh->kv_empty[s], 1);
+    lt::mbar_init(&sh->q_full, Smem<D>::kRowTiles * 128);
     for (int t = 0; t < 2; ++t) {
       lt::mbar_init(&sh->s_full[t], 1);
       lt::mbar_init(&sh->o_full[t], 1);
@@ -690,18 +704,19 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   job.request = pl.request;
   job.rq = request_of(p, pl.request);
   job.rows = job.rq.queries * p.group;
-  job.row_tile = min((job.rows + 255) / 256, p.row_tiles) - 1 - nth;
+  constexpr int kRows = Smem<D>::kRowTiles * 128;
+  job.row_tile = min((job.rows + kRows - 1) / kRows, p.row_tiles) - 1 - nth;
   if (job.row_tile < 0) return;
   job.final_here = pl.count == 1;
   if (job.flat == pl.base && job.head == 0 && job.row_tile == 0 && tid == 0 && p.plan != nullptr)
     p.plan[pl.request] = make_int2(pl.base, pl.count);
-  job.row0 = job.row_tile * 256;
-  job.two = job.rows - job.row0 > 128;
+  job.row0 = job.row_tile * kRows;
+  job.two = kRows > 128 && job.rows - job.row0 > 128;
   {
     const int64_t at = job.rq.low + pl.split * chunk_of(p, job.rq, pl.count), end = at + chunk_of(p, job.rq, pl.count);
     job.from = (int)(at < job.rq.length ? at : job.rq.length);
     job.to = (int)(end < job.rq.length ? end : job.rq.length);
-    const int last = min(job.rows - 1, job.row0 + 255) / p.group;
+    const int last = min(job.rows - 1, job.row0 + kRows - 1) / p.group;
     job.to = min(job.to, job.rq.length - job.rq.queries + last + 1);
     if (p.window > 0)
       job.from = max(job.from, (job.rq.length - job.rq.queries + job.row0 / p.group + 1 - p.window) / kTok * kTok);
@@ -746,7 +761,8 @@ const void* prefill_kernel_ptr(int head_dim, int* smem) {
     *smem = Smem<128>::kTotal;
     return reinterpret_cast<const void*>(&prefill_kernel<128>);
   }
-  return nullptr;
+  *smem = Smem<256>::kTotal;
+  return reinterpret_cast<const void*>(&prefill_kernel<256>);
 }
 
 }  // namespace kv4

@@ -5,9 +5,10 @@ namespace lt {
 namespace kv4 {
 
 constexpr int kPrefillThreads = 512;
-constexpr int kPrefillRows = 256;  // query rows of a CTA
+// query rows of a CTA
+inline int prefill_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
 
-// nullptr for a head size that it does not take; *smem: its dynamic shared memory.
+// head_dim 64, 128 or 256; *smem: its dynamic shared memory.
 const void* prefill_kernel_ptr(int head_dim, int* smem);
 
 }  // namespace kv4

@@ -310,7 +310,8 @@ def test_many_query_rows():
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("dim,lengths,new,group,window", [
     (64, [64], [64], 1, 0), (128, [64], [64], 1, 0), (64, [130], [100], 2, 0), (128, [300], [129], 1, 0), (128, [129, 5, 400], [70, 0, 33], 5, 0),
-    (64, [700, 90, 1], [100, 90, 1], 3, 50), (128, [640], [90], 3, 200), (64, [1500], [40], 4, 0), (128, [50], [80], 4, 0)])
+    (64, [700, 90, 1], [100, 90, 1], 3, 50), (128, [640], [90], 3, 200), (64, [1500], [40], 4, 0), (128, [50], [80], 4, 0),
+    (256, [100], [70], 1, 0), (256, [300, 0, 5, 33], [129, 70, 0, 33], 1, 0), (256, [700, 64], [40, 17], 4, 150), (256, [1300], [33], 2, 0)])
 def test_prefill(dim, lengths, new, group, window, dtype):
     """Many query rows a request: one and two row tiles, ragged ends, windows, requests cut into parts, more
     queries than positions."""
@@ -324,8 +325,8 @@ def test_prefill(dim, lengths, new, group, window, dtype):
 @pytest.mark.parametrize("page", [1, 32, 64, 128, 1024])
 def test_prefill_page_sizes_with_parts_and_windows(page):
     """Parts and windows that start inside a page, runs of positions longer and shorter than a page."""
-    for window in (0, 77, 300):
-        p = Problem([1100, 161], [33, 20], 1, 3, 64, page, "f16", seed=page + window)
+    for window, dim in ((0, 64), (77, 64), (300, 64), (77, 256)):
+        p = Problem([1100, 161], [33, 20], 1, 3, dim, page, "f16", seed=page + window)
         p.check(*p.run(window=window), window=window)
 
 
@@ -344,11 +345,12 @@ def test_prefill_scales_and_bad_pages():
         p.check(*p.run(scale=scale), scale=scale)
 
 
-def test_prefill_nan_where_nothing_looks():
-    p = Problem([200], [80], 1, 2, 128, 16, "bf16", seed=22)
+@pytest.mark.parametrize("dim", [128, 256])
+def test_prefill_nan_where_nothing_looks(dim):
+    p = Problem([200], [80], 1, 2, dim, 16, "bf16", seed=22)
     clean, clean_lse = p.run()
     nan = torch.tensor([0x7FFF], dtype=torch.int16).view(torch.uint8)
-    for position, byte in ((150, 128 + 8 + 2), (199, 128)):  # value group 1 of position 150, key group 0 of the last
+    for position, byte in ((150, dim + dim // 16 + 2), (199, dim)):  # value group 1 of position 150, key group 0 of the last
         p.cache[p.table[0, position // 16], 0, position % 16, byte:byte + 2] = nan
     out, lse = p.run()
     assert torch.equal(out[:30], clean[:30]) and torch.equal(lse[:79], clean_lse[:79])
