@@ -57,16 +57,21 @@ constexpr float kSlack = 8.0f;  // how far logits may pass the maximum (log 2) b
 template <int D>
 struct Smem {
   static constexpr int kRow = row_bytes(D);
-  // heads of 256 leave room for one row tile, a key and a value tile
-  static constexpr int kRowTiles = D == 256 ? 1 : 2;
-  static constexpr int kSlots = D == 256 ? 2 : 4;
+  // Heads of 256 leave room for one row tile, and its queries are in tensor memory (128 columns, beside 128 of
+  // logits and 256 of sums), so that three key and value tiles fit: keys and values of the next
+  // tile are unpacked while the softmax of this one runs.
+  static constexpr bool kQInTmem = D == 256;
+  static constexpr int kRowTiles = kQInTmem ? 1 : 2;
+  static constexpr int kSlots = kQInTmem ? 3 : 4;
   static constexpr int kPart = D == 256 ? 32 : 64;       // positions of a packed stage
   static constexpr int kParts = kTok / kPart;
   static constexpr int kHalf = kTok * 128;               // 128 rows by 64 channels, swizzled
   static constexpr int kOperand = kHalf * (D / 64);
-  static constexpr int kQ = 0;                           // kRowTiles
-  static constexpr int kKv = kQ + kRowTiles * kOperand;  // kSlots
-  static constexpr int kPacked = kKv + kSlots * kOperand;  // [kRaw][kPart rows]
+  static constexpr int kKv = kQInTmem ? 0 : kRowTiles * kOperand;  // kSlots
+  // row tiles; where the queries are in tensor memory, the last slot is what they and the outputs are turned
+  // round in, before its first keys and after the last product
+  static constexpr int kQ = kQInTmem ? kKv + (kSlots - 1) * kOperand : 0;
+  static constexpr int kPacked = kKv + kSlots * kOperand;          // [kRaw][kPart rows]
   static constexpr int kBars = kPacked + kRaw * kPart * kRow;
   static constexpr int kTotal = kBars + 2048 + 1024;     // (slack to align the start to 1024)
 };
@@ -112,13 +117,16 @@ __device__ __forceinline__ void mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint
                " add.s64 a, %1, 6;\n add.s64 b, %2, 6;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}"
                :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead) : "memory");
 }
+// (kStep: from one 16 of the inner dimension to the next in B, in units of 16 bytes)
+template <int kStep>
 __device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t lead) {
   asm volatile("{\n .reg .pred p, q, t;\n .reg .b32 a;\n .reg .b64 b;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n setp.eq.u32 t, 0, 0;\n"
                " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-               " add.s32 a, %1, 8;\n add.s64 b, %2, 128;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-               " add.s32 a, %1, 16;\n add.s64 b, %2, 256;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-               " add.s32 a, %1, 24;\n add.s64 b, %2, 384;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}"
-               :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead) : "memory");
+               " add.s32 a, %1, 8;\n add.s64 b, %2, %6;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+               " add.s32 a, %1, 16;\n add.s64 b, %2, %7;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+               " add.s32 a, %1, 24;\n add.s64 b, %2, %8;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}"
+               :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(lead), "n"(kStep), "n"(2 * kStep), "n"(3 * kStep)
+               : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t* bar, uint32_t lead) {
   asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %1, 0;\n"
@@ -302,16 +310,28 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
     // logits are compared before they are scaled: a negative scale turns the row round instead
     const uint32_t flip = factor < 0.0f ? 0x80008000u : 0u, keep = factor == 0.0f ? 0u : ~0u;
     factor = factor == 0.0f ? 1.0f : fabsf(factor);
-#pragma unroll 4
-    for (int c = 0; c < kChunks; ++c) {
-      uint4* at = chunk_of(row_in_tile, c);
-      uint32_t w[4] = {at->x, at->y, at->z, at->w};
+#pragma unroll 1
+    for (int c0 = 0; c0 < kChunks; c0 += 4) {
+      uint32_t w[16];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = ((p.bf16 ? bf16_pair_to_half(w[e], mul) : w[e]) ^ flip) & keep;
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int c = 0; c < 4; ++c) {
+        uint4* at = chunk_of(row_in_tile, c0 + c);
+        const uint4 v = *at;
+        w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
+#pragma unroll
+        for (int e = 4 * c; e < 4 * c + 4; ++e) w[e] = ((p.bf16 ? bf16_pair_to_half(w[e], mul) : w[e]) ^ flip) & keep;
+        if (!Smem<D>::kQInTmem) *at = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+      }
+      if constexpr (Smem<D>::kQInTmem) tmem_st16(sh->tmem + ((uint32_t)(warp * 32) << 16) + kTok + c0 * 4, w);
     }
-    fence_async();
+    if constexpr (Smem<D>::kQInTmem) {
+      tmem_wait_st();
+      fence_before();
+    } else {
+      fence_async();
+    }
     arrive(&sh->q_full);
+    __syncwarp();
   }
   if (which == 1 && !job.two) return;
 
@@ -554,12 +574,14 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
   uint32_t chunk_at[8];  // where the row's eight 16-byte chunks lie in a swizzled 128-byte row
 #pragma unroll
   for (int c = 0; c < 8; ++c) chunk_at[c] = lt::smem_u32(smem + Smem<D>::kKv) + row * 128 + ((c ^ (row & 7)) << 4);
-  int slot = part, stage = 0;                  // keys in slots 0, 2, 0, ..., values in 1, 3, 1, ... (or 0 and 1)
+  // the slots go round: keys of tile i in slot 2 i mod kSlots, values in the next
+  int slot = part, stage = 0;
   uint32_t slot_parity = 1, stage_parity = 0;  // (the first round's slots are free)
   bool fed = true;
 #pragma unroll 1
   for (int i = 0; i < job.tiles; ++i) {
     wait_warp(&sh->kv_empty[slot], slot_parity, sh);
+    if (Smem<D>::kQInTmem && i == 1) wait_warp(&sh->q_full, 0, sh);  // until then the queries are in the last slot
 #pragma unroll 1
     for (int half = 0; half < kParts; ++half) {
       fed = fed && wait_warp(&sh->packed_full[stage], stage_parity, sh);  // (once in vain is enough)
@@ -613,8 +635,11 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
     }
     fence_async();
     named_arrive(slot_ready(slot), kSlotThreads);
-    if constexpr (kSlots == 4) slot ^= 2;
-    if (slot == part) slot_parity ^= 1u;
+    slot += 2;
+    if (slot >= kSlots) {
+      slot -= kSlots;
+      slot_parity ^= 1u;
+    }
   }
 }
 
@@ -625,8 +650,7 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   const uint32_t q_at = lt::smem_u32(smem + Smem<D>::kQ), kv_at = lt::smem_u32(smem + Smem<D>::kKv);
   const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0), lead = elect_one();
   wait_warp(&sh->q_full, 0, sh);
-  // keys of tile i are in slot (i & 1) * 2 (of two slots: 0), values in the next
-  constexpr int kTurn = Smem<D>::kSlots == 4 ? 1 : 0;
+  constexpr int kSlots = Smem<D>::kSlots;
   const int tiles = job.tiles;
   if (tiles > 0) named_sync(slot_ready(0), kSlotThreads);
   // One place for each product, in a rolled loop: even steps row tile A, odd ones row tile B; first the weights
@@ -636,12 +660,9 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   for (int step = 0; step <= 2 * tiles + 1 && tiles > 0; ++step) {
     const int which = step & 1, i = (step >> 1) - 1;
     const bool weights = i >= 0, keys = i + 1 < tiles;
-    const int value_slot = (i & kTurn) * 2 + 1, key_slot = ((i + 1) & kTurn) * 2;
+    const int value_slot = (uint32_t)(2 * i + 1) % kSlots, key_slot = (uint32_t)(2 * i + 2) % kSlots;
     if (which == 1 && !job.two) continue;
-    // A slot is free when the last row tile's product has read it. The values' is given back before the next keys
-    // are waited for: with two slots those come only after it (keys and values of a tile are
-    // unpacked from the same packed stages).
-    const bool last = which == 1 || !job.two;
+    const bool last = which == 1 || !job.two;  // the product after which a slot is free
     if (weights) {
       if (which == 0) named_sync(slot_ready(value_slot), kSlotThreads);
       const uint64_t value = desc_mn_major(kv_at + value_slot * Smem<D>::kOperand, Smem<D>::kHalf);
@@ -649,8 +670,8 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
       for (int half = 0; half < 2; ++half) {
         named_sync(weights_ready(which, half), kWeightsThreads);
         fence_after();
-        mma_ts4(tmem + 2 * kTok + which * D, tmem + which * kTok + half * 32, value + half * ((kTok / 2 * 128) >> 4), kIdescO,
-                i > 0 || half > 0, lead);
+        mma_ts4<128>(tmem + 2 * kTok + which * D, tmem + which * kTok + half * 32, value + half * ((kTok / 2 * 128) >> 4), kIdescO,
+                     i > 0 || half > 0, lead);
       }
       if (last) mma_commit(&sh->kv_empty[value_slot], lead);
     }
@@ -660,8 +681,13 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
       const uint64_t q = desc_k_major(q_at + which * Smem<D>::kOperand);
       const uint64_t key = desc_k_major(kv_at + key_slot * Smem<D>::kOperand);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        mma_ss4(tmem + which * kTok, q + c * (Smem<D>::kHalf >> 4), key + c * (Smem<D>::kHalf >> 4), kIdescS, c > 0, lead);
+      for (int c = 0; c < D / 64; ++c) {
+        const uint64_t k = key + c * (Smem<D>::kHalf >> 4);
+        if constexpr (Smem<D>::kQInTmem)
+          mma_ts4<2>(tmem, tmem + kTok + c * 32, k, kIdescS, c > 0, lead);
+        else
+          mma_ss4(tmem + which * kTok, q + c * (Smem<D>::kHalf >> 4), k, kIdescS, c > 0, lead);
+      }
       mma_commit(&sh->s_full[which], lead);
       if (last) mma_commit(&sh->kv_empty[key_slot], lead);
     }
