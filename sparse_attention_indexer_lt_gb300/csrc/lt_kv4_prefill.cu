@@ -63,6 +63,7 @@ struct Smem {
   static constexpr bool kQInTmem = D == 256;
   static constexpr int kRowTiles = kQInTmem ? 1 : 2;
   static constexpr int kSlots = kQInTmem ? 3 : 4;
+  static constexpr int kUnpackers = kQInTmem ? 256 : 128;  // threads that unpack: row tile B's warpgroup is free to
   static constexpr int kPart = D == 256 ? 32 : 64;       // positions of a packed stage
   static constexpr int kParts = kTok / kPart;
   static constexpr int kHalf = kTok * 128;               // 128 rows by 64 channels, swizzled
@@ -240,7 +241,8 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 __device__ __forceinline__ int weights_ready(int which, int half) { return 1 + 2 * which + half; }
 constexpr int kWeightsThreads = 128 + 32;
 __device__ __forceinline__ int slot_ready(int slot) { return 5 + slot; }
-constexpr int kSlotThreads = 64 + 32;
+template <int D>
+constexpr int kSlotThreads = Smem<D>::kUnpackers / 2 + 32;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -281,7 +283,6 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   // chunk c of row r of the tile, where the 128-byte swizzle puts it
   auto chunk_of = [&](int r, int c) { return reinterpret_cast<uint4*>(tile + (c / 8) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
 
-  if (which >= Smem<D>::kRowTiles) return;
   // the query rows into shared memory: the warp brings its rows one after the other, then each thread
   // makes its own row fp16, with the power of two that keeps bf16 in range
   float factor = p.scale_log2;
@@ -563,13 +564,13 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
 }
 
 // ---- unpacking: a packed stage's positions at a time, a thread the key or the value of a position (with
-// D = 256 half of its channels); 64 threads have keys, 64 values
+// D = 256 a quarter of its channels); half of the threads have keys, half values
 template <int D>
 __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t* smem) {
   constexpr int kRow = row_bytes(D);
   constexpr int kPart = Smem<D>::kPart, kParts = Smem<D>::kParts, kSlots = Smem<D>::kSlots;
-  constexpr int kBlocks = D / 64 / (64 / kPart);  // 64-channel blocks of a thread
-  const int t = threadIdx.x & 127, lane = t & 31, row = t % kPart, part = t / kPart & 1;
+  constexpr int kBlocks = D / 64 * 2 * kPart / Smem<D>::kUnpackers;  // 64-channel blocks of a thread
+  const int t = threadIdx.x - (384 - Smem<D>::kUnpackers), lane = t & 31, row = t % kPart, part = t / kPart & 1;
   const int block0 = t / (2 * kPart) * kBlocks;
   uint32_t chunk_at[8];  // where the row's eight 16-byte chunks lie in a swizzled 128-byte row
 #pragma unroll
@@ -634,7 +635,7 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
       }
     }
     fence_async();
-    named_arrive(slot_ready(slot), kSlotThreads);
+    named_arrive(slot_ready(slot), kSlotThreads<D>);
     slot += 2;
     if (slot >= kSlots) {
       slot -= kSlots;
@@ -652,7 +653,7 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   wait_warp(&sh->q_full, 0, sh);
   constexpr int kSlots = Smem<D>::kSlots;
   const int tiles = job.tiles;
-  if (tiles > 0) named_sync(slot_ready(0), kSlotThreads);
+  if (tiles > 0) named_sync(slot_ready(0), kSlotThreads<D>);
   // One place for each product, in a rolled loop: even steps row tile A, odd ones row tile B; first the weights
   // of tile i by its values, then the logits of tile i + 1. (Descriptors hold addresses in
   // units of 16 bytes; the steps' offsets are added to them.)
@@ -664,7 +665,7 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
     if (which == 1 && !job.two) continue;
     const bool last = which == 1 || !job.two;  // the product after which a slot is free
     if (weights) {
-      if (which == 0) named_sync(slot_ready(value_slot), kSlotThreads);
+      if (which == 0) named_sync(slot_ready(value_slot), kSlotThreads<D>);
       const uint64_t value = desc_mn_major(kv_at + value_slot * Smem<D>::kOperand, Smem<D>::kHalf);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -676,7 +677,7 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
       if (last) mma_commit(&sh->kv_empty[value_slot], lead);
     }
     if (keys) {
-      if (which == 0 && weights) named_sync(slot_ready(key_slot), kSlotThreads);
+      if (which == 0 && weights) named_sync(slot_ready(key_slot), kSlotThreads<D>);
       fence_after();
       const uint64_t q = desc_k_major(q_at + which * Smem<D>::kOperand);
       const uint64_t key = desc_k_major(kv_at + key_slot * Smem<D>::kOperand);
@@ -705,7 +706,7 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   if (tid == 0) {
     for (int s = 0; s < kRaw; ++s) {
       lt::mbar_init(&sh->packed_full[s], 1);
-      lt::mbar_init(&sh->packed_empty[s], 4);
+      lt::mbar_init(&sh->packed_empty[s], Smem<D>::kUnpackers / 32);
     }
     for (int s = 0; s < kMaxSlots; ++s) lt::mbar_init(&sh->kv_empty[s], 1);
     lt::mbar_init(&sh->q_full, Smem<D>::kRowTiles * 128);
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   __syncthreads();
   fence_after();
 
-  if (warp < 8)
+  if (warp < 4 * Smem<D>::kRowTiles)
     softmax_role<D>(p, job, sh, smem, warp / 4);
   else if (warp < 12)
     unpack_role<D>(job, sh, smem);
