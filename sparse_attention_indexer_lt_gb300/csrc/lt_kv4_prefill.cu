@@ -48,42 +48,51 @@ namespace {
 using namespace lt::kv4;
 
 constexpr int kCta = 512;
-constexpr int kTok = 128;    // positions of a tile
-constexpr int kMaxSlots = 4;  // unpacked key or value tiles in shared memory
-constexpr int kRaw = 3;       // packed stages in shared memory or on their way there
+constexpr int kSlots = 4;    // unpacked key or value tiles in shared memory
+constexpr int kPart = 64;    // positions of a packed stage
+constexpr int kMaxRaw = 5;   // packed stages in shared memory or on their way there
+// columns of tensor memory: logits and weights first, two tiles
+constexpr int kQueryColumn = 128;  // queries, with heads of 256
+constexpr int kSumColumn = 256;
 constexpr float kShift = 6.0f;
 constexpr float kSlack = 8.0f;  // how far logits may pass the maximum (log 2) before it moves
 
 template <int D>
 struct Smem {
   static constexpr int kRow = row_bytes(D);
-  // Heads of 256 leave room for one row tile, and its queries are in tensor memory (128 columns, beside 128 of
-  // logits and 256 of sums), so that three key and value tiles fit: keys and values of the next
-  // tile are unpacked while the softmax of this one runs.
-  static constexpr bool kQInTmem = D == 256;
-  static constexpr int kRowTiles = kQInTmem ? 1 : 2;
-  static constexpr int kSlots = kQInTmem ? 3 : 4;
-  static constexpr int kUnpackers = kQInTmem ? 256 : 128;  // threads that unpack: row tile B's warpgroup is free to
-  static constexpr int kPart = D == 256 ? 32 : 64;       // positions of a packed stage
+  // Heads of 256 leave room for one row tile. Its queries are in tensor memory, and its position tiles are
+  // of 64: two of logits (128 columns), the queries (128) and the sums (256) fit, so that the next
+  // tile's logits are there when the softmax of this one ends, and shared memory has room for five packed stages.
+  static constexpr bool kOne = D == 256;
+  static constexpr int kRowTiles = kOne ? 1 : 2;
+  static constexpr int kTok = kOne ? 64 : 128;             // positions of a tile
+  static constexpr int kRaw = kOne ? 5 : 3;
+  static constexpr int kUnpackers = kOne ? 256 : 128;      // threads that unpack: row tile B's warpgroup is free to
   static constexpr int kParts = kTok / kPart;
-  static constexpr int kHalf = kTok * 128;               // 128 rows by 64 channels, swizzled
+  static constexpr int kRing = 512 / kTok;                 // tiles whose notes are kept
+  static constexpr int kQHalf = 128 * 128;                 // 128 rows by 64 channels, swizzled
+  static constexpr int kQTile = kQHalf * (D / 64);
+  static constexpr int kHalf = kTok * 128;                 // a tile's positions by 64 channels
   static constexpr int kOperand = kHalf * (D / 64);
-  static constexpr int kKv = kQInTmem ? 0 : kRowTiles * kOperand;  // kSlots
-  // row tiles; where the queries are in tensor memory, the last slot is what they and the outputs are turned
-  // round in, before its first keys and after the last product
-  static constexpr int kQ = kQInTmem ? kKv + (kSlots - 1) * kOperand : 0;
-  static constexpr int kPacked = kKv + kSlots * kOperand;          // [kRaw][kPart rows]
+  static constexpr int kKv = kOne ? 0 : kRowTiles * kQTile;  // kSlots
+  // row tiles; where the queries are in tensor memory, the last slots are what they and the outputs are turned
+  // round in, before their first keys and after the last product
+  static constexpr int kQ = kOne ? kKv + kSlots * kOperand - kQTile : 0;
+  static constexpr int kPacked = kKv + kSlots * kOperand;  // [kRaw][kPart rows]
   static constexpr int kBars = kPacked + kRaw * kPart * kRow;
   static constexpr int kTotal = kBars + 2048 + 1024;     // (slack to align the start to 1024)
 };
 
 struct Shared {
-  uint64_t packed_full[kRaw], packed_empty[kRaw];
-  uint64_t kv_empty[kMaxSlots];
+  uint64_t packed_full[kMaxRaw], packed_empty[kMaxRaw];
+  uint64_t kv_empty[kSlots];
   uint64_t q_full, s_full[2], o_full[2];
-  alignas(16) uint32_t valid[4][4];     // [tile mod 4]: positions on a page of the cache and in range, as bits
-  alignas(16) uint32_t nan_rows[4][4];  // positions with a NaN value scale
-  uint8_t nan_groups[4][kTok];
+  uint64_t o_tile;  // with one row tile: a position tile's second product is done
+  // notes of the tiles in work, a ring of 512 positions (they are made at most three tiles of 128, or six of
+  // 64, ahead of the softmax: slots that its products give back hold the rest up)
+  alignas(16) uint32_t valid[16];     // positions on a page of the cache and in range, as bits
+  alignas(16) uint32_t nan_rows[16];  // positions with a NaN value scale
+  uint8_t nan_groups[512];
   int64_t sums[kCta / 32];
   Place found;
   uint32_t tmem;
@@ -274,12 +283,13 @@ struct Job {
 // ---- one row tile's softmax: a thread a row
 template <int D>
 __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job& job, Shared* sh, uint8_t* smem, int which) {
-  constexpr int kHalf = Smem<D>::kHalf, kChunks = D / 8;  // 16-byte chunks of a row of 16-bit values
+  constexpr int kHalf = Smem<D>::kQHalf, kTok = Smem<D>::kTok, kRing = Smem<D>::kRing;
+  constexpr int kChunks = D / 8;                          // 16-byte chunks of a row of 16-bit values
   constexpr int kAtOnce = 32 / kChunks;                   // rows of one warp-wide access
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, row_in_tile = warp * 32 + lane;
   const int row = job.row0 + which * 128 + row_in_tile;
   const int row_c = min(row, job.rows - 1);
-  uint8_t* tile = smem + Smem<D>::kQ + which * Smem<D>::kOperand;
+  uint8_t* tile = smem + Smem<D>::kQ + which * Smem<D>::kQTile;
   // chunk c of row r of the tile, where the 128-byte swizzle puts it
   auto chunk_of = [&](int r, int c) { return reinterpret_cast<uint4*>(tile + (c / 8) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
 
@@ -321,11 +331,11 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
         w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
 #pragma unroll
         for (int e = 4 * c; e < 4 * c + 4; ++e) w[e] = ((p.bf16 ? bf16_pair_to_half(w[e], mul) : w[e]) ^ flip) & keep;
-        if (!Smem<D>::kQInTmem) *at = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        if (!Smem<D>::kOne) *at = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
       }
-      if constexpr (Smem<D>::kQInTmem) tmem_st16(sh->tmem + ((uint32_t)(warp * 32) << 16) + kTok + c0 * 4, w);
+      if constexpr (Smem<D>::kOne) tmem_st16(sh->tmem + ((uint32_t)(warp * 32) << 16) + kQueryColumn + c0 * 4, w);
     }
-    if constexpr (Smem<D>::kQInTmem) {
+    if constexpr (Smem<D>::kOne) {
       tmem_wait_st();
       fence_before();
     } else {
@@ -339,7 +349,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   const int limit = job.rq.length - job.rq.queries + row_c / p.group + 1;
   const int low = p.window > 0 ? max(limit - p.window, 0) : 0;
   const uint32_t lane_base = sh->tmem + ((uint32_t)(warp * 32) << 16);
-  const uint32_t s_at = lane_base + which * kTok, o_at = lane_base + 2 * kTok + which * D;
+  const uint32_t o_at = lane_base + kSumColumn + which * D;
 
   // The loop reads a tile's logits twice, once for the maximum and once for the weights: that is little
   // against 128 exponentials a row, and the loops stay short enough for the instruction
@@ -347,19 +357,27 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   float m = -INFINITY, sum0 = 0.0f, sum1 = 0.0f;  // m in units of log 2
   uint32_t poison = 0;                             // value groups in which this row is NaN
   for (int i = 0; i < job.tiles; ++i) {
-    wait_warp(&sh->s_full[which], i & 1, sh);
+    const int buf = Smem<D>::kOne ? i & 1 : which;
+    const uint32_t s_at = lane_base + buf * kTok;
+    wait_warp(&sh->s_full[buf], (Smem<D>::kOne ? i >> 1 : i) & 1, sh);
     fence_after();
     const int pos0 = job.from + i * kTok;
-    const uint32_t* valid = sh->valid[i & 3];
-    const uint32_t* nan_rows = sh->nan_rows[i & 3];
-    const uint4 valid4 = *reinterpret_cast<const uint4*>(valid), nan4 = *reinterpret_cast<const uint4*>(nan_rows);
+    const uint32_t* valid = sh->valid + i % kRing * (kTok / 32);
+    const uint32_t* nan_rows = sh->nan_rows + i % kRing * (kTok / 32);
+    const uint2 valid2 = *reinterpret_cast<const uint2*>(valid), nan2 = *reinterpret_cast<const uint2*>(nan_rows);
+    uint32_t all_valid = valid2.x & valid2.y, any_nan = nan2.x | nan2.y;
+    if constexpr (kTok == 128) {
+      const uint2 v = *reinterpret_cast<const uint2*>(valid + 2), n = *reinterpret_cast<const uint2*>(nan_rows + 2);
+      all_valid &= v.x & v.y;
+      any_nan |= n.x | n.y;
+    }
     float top;
     bool hidden = false;
 #pragma unroll 1
     for (;;) {
       float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kTok / 64; ++h) {
         uint32_t x[64];
         tmem_read64(s_at + 64 * h, x);
         const float* s = reinterpret_cast<const float*>(x);
@@ -373,13 +391,12 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
       }
       top = fmaxf(max3(t0, t1, t2), t3) * factor;
       // (looked at only now: the words come from shared memory, which the products keep busy)
-      const bool plain = (valid4.x & valid4.y & valid4.z & valid4.w) == ~0u && pos0 + kTok <= limit && pos0 >= low &&
-                         (nan4.x | nan4.y | nan4.z | nan4.w) == 0;
+      const bool plain = all_valid == ~0u && pos0 + kTok <= limit && pos0 >= low && any_nan == 0;
       if (hidden || __all_sync(~0u, plain)) break;
       // hide what this row does not see, in tensor memory, and take the maximum again
       hidden = true;
 #pragma unroll 1
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < kTok / 32; ++w) {
         uint32_t y[32];
         tmem_read32(s_at + 32 * w, y);
         const int a = low - (pos0 + 32 * w), b = limit - (pos0 + 32 * w);  // (low >= 0: no overflow)
@@ -391,20 +408,25 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
           if (!((see >> c) & 1u)) y[c] = 0xFF800000u;
         tmem_st32(s_at + 32 * w, y);
         for (uint32_t left = nan_rows[w] & see; left != 0; left &= left - 1)
-          poison |= sh->nan_groups[i & 3][32 * w + __ffs(left) - 1];
+          poison |= sh->nan_groups[i % kRing * kTok + 32 * w + __ffs(left) - 1];
         __syncwarp();
       }
       tmem_wait_st();
     }
     const bool moves = top > m + kSlack || (m == -INFINITY && top > m);
     if (__any_sync(~0u, moves)) {
-      // S(i) is there, so the product O += P V of tile i - 1, issued before it, is done
+      // the product O += P V of tile i - 1 has to be done: with two row tiles S(i) was issued after it; with one
+      // S(i) came before it, but after that of tile i - 2, so that this is the phase to wait for
       const float now = moves ? top : m;
       const float a = moves ? exp2_fast(m - now) : 1.0f;
       m = now;
       sum0 *= a;
       sum1 *= a;
       if (i > 0) {
+        if constexpr (Smem<D>::kOne) {
+          wait_warp(&sh->o_tile, (i - 1) & 1, sh);
+          fence_after();
+        }
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           uint32_t o[16];
@@ -418,7 +440,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
     }
     const float ref = m == -INFINITY ? 0.0f : kShift - m;
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kTok / 64; ++h) {
       uint32_t x[64], pk[32];
       tmem_read64(s_at + 64 * h, x);
       float* s = reinterpret_cast<float*>(x);
@@ -433,7 +455,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
       tmem_st32(s_at + 32 * h, pk);  // (columns whose logits have been read)
       tmem_wait_st();
       fence_before();
-      named_arrive(weights_ready(which, h), kWeightsThreads);  // the second product starts on the first half
+      named_arrive(weights_ready(buf, h), kWeightsThreads);  // the second product starts on the first half
       __syncwarp();
     }
   }
@@ -502,11 +524,11 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
 template <int D>
 __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& job, Shared* sh, uint8_t* smem) {
   constexpr int kRow = row_bytes(D);
-  constexpr int kPart = Smem<D>::kPart, kParts = Smem<D>::kParts;
+  constexpr int kParts = Smem<D>::kParts, kRaw = Smem<D>::kRaw;
   constexpr int kMost = kPart / 32;  // runs of a lane, at pages of one position; words of a stage's valid bits
   const int lane = threadIdx.x & 31;
   const uint32_t packed_at = lt::smem_u32(smem + Smem<D>::kPacked);
-  const int run_shift = min(p.shift, kPart == 64 ? 6 : 5), runs = kPart >> run_shift;
+  const int run_shift = min(p.shift, 6), runs = kPart >> run_shift;
   const int32_t* table = p.table + (int64_t)job.request * p.width;
   const int stages = kParts * job.tiles;
   int page[kMost];
@@ -543,7 +565,7 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
     }
     if (lane == 0) {
 #pragma unroll
-      for (int w = 0; w < kMost; ++w) sh->valid[(n / kParts) & 3][n % kParts * kMost + w] = valid[w];
+      for (int w = 0; w < kMost; ++w) sh->valid[n % (16 / kMost) * kMost + w] = valid[w];
       lt::mbar_arrive_tx(&sh->packed_full[stage], there * kRow);
     }
     __syncwarp();
@@ -564,11 +586,12 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
 }
 
 // ---- unpacking: a packed stage's positions at a time, a thread the key or the value of a position (with
-// D = 256 a quarter of its channels); half of the threads have keys, half values
+// D = 256 half of its channels); half of the threads have keys, half values
 template <int D>
 __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t* smem) {
   constexpr int kRow = row_bytes(D);
-  constexpr int kPart = Smem<D>::kPart, kParts = Smem<D>::kParts, kSlots = Smem<D>::kSlots;
+  constexpr int kParts = Smem<D>::kParts, kRaw = Smem<D>::kRaw;
+  constexpr int kTok = Smem<D>::kTok, kRing = Smem<D>::kRing;
   constexpr int kBlocks = D / 64 * 2 * kPart / Smem<D>::kUnpackers;  // 64-channel blocks of a thread
   const int t = threadIdx.x - (384 - Smem<D>::kUnpackers), lane = t & 31, row = t % kPart, part = t / kPart & 1;
   const int block0 = t / (2 * kPart) * kBlocks;
@@ -582,12 +605,12 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
 #pragma unroll 1
   for (int i = 0; i < job.tiles; ++i) {
     wait_warp(&sh->kv_empty[slot], slot_parity, sh);
-    if (Smem<D>::kQInTmem && i == 1) wait_warp(&sh->q_full, 0, sh);  // until then the queries are in the last slot
+    if (Smem<D>::kOne && i == kSlots / 2 - 1) wait_warp(&sh->q_full, 0, sh);  // until then the queries are in the last slots
 #pragma unroll 1
     for (int half = 0; half < kParts; ++half) {
       fed = fed && wait_warp(&sh->packed_full[stage], stage_parity, sh);  // (once in vain is enough)
-      const int word = half * (kPart / 32) + row / 32;  // (the warp's rows are one word's)
-      const uint32_t valid = sh->valid[i & 3][word];
+      const int word = i % kRing * (kTok / 32) + half * (kPart / 32) + row / 32;  // (the warp's rows are one word's)
+      const uint32_t valid = sh->valid[word];
       const bool there = (valid >> lane) & 1u;
       const uint8_t* from = smem + Smem<D>::kPacked + (stage * kPart + row) * kRow;
       // scales, fp16 pairs; a position that is not there counts as zeros, and so does a NaN value
@@ -606,8 +629,8 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
           nan |= ((n & 1u) | ((n >> 15) & 2u)) << (2 * g);
         }
         const uint32_t nan_rows = __ballot_sync(~0u, nan != 0);
-        if (lane == 0) sh->nan_rows[i & 3][word] = nan_rows;
-        if (nan_rows) sh->nan_groups[i & 3][half * kPart + row] = (uint8_t)nan;
+        if (lane == 0) sh->nan_rows[word] = nan_rows;
+        if (nan_rows) sh->nan_groups[i % kRing * kTok + half * kPart + row] = (uint8_t)nan;
       }
       const uint32_t to = slot * Smem<D>::kOperand + half * (kPart * 128);
 #pragma unroll
@@ -647,54 +670,59 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
 // ---- the products, issued by one warp
 template <int D>
 __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t* smem) {
-  constexpr uint32_t kIdescS = instruction(kTok, false), kIdescO = instruction(D, true);
+  constexpr uint32_t kIdescS = instruction(Smem<D>::kTok, false), kIdescO = instruction(D, true);
   const uint32_t q_at = lt::smem_u32(smem + Smem<D>::kQ), kv_at = lt::smem_u32(smem + Smem<D>::kKv);
   const uint32_t tmem = __shfl_sync(~0u, sh->tmem, 0), lead = elect_one();
   wait_warp(&sh->q_full, 0, sh);
-  constexpr int kSlots = Smem<D>::kSlots;
+  constexpr int kTok = Smem<D>::kTok;
+  constexpr bool kOne = Smem<D>::kOne;
   const int tiles = job.tiles;
-  if (tiles > 0) named_sync(slot_ready(0), kSlotThreads<D>);
-  // One place for each product, in a rolled loop: even steps row tile A, odd ones row tile B; first the weights
-  // of tile i by its values, then the logits of tile i + 1. (Descriptors hold addresses in
-  // units of 16 bytes; the steps' offsets are added to them.)
+  if (!kOne && tiles > 0) named_sync(slot_ready(0), kSlotThreads<D>);
+  // One place for each product, in a rolled loop: first the weights of a tile by its values, then the logits
+  // of a later one, into the columns that the weights were in. With two row tiles even steps
+  // are row tile A's, odd ones B's, and the later tile is the next; with one row tile a step
+  // is a tile's, and the later tile is the next but one. (Descriptors hold addresses in units of 16 bytes; the steps'
+  // offsets are added to them.)
 #pragma unroll 1
-  for (int step = 0; step <= 2 * tiles + 1 && tiles > 0; ++step) {
-    const int which = step & 1, i = (step >> 1) - 1;
-    const bool weights = i >= 0, keys = i + 1 < tiles;
-    const int value_slot = (uint32_t)(2 * i + 1) % kSlots, key_slot = (uint32_t)(2 * i + 2) % kSlots;
+  for (int step = 0; step < (kOne ? tiles + 2 : 2 * tiles + 2) && tiles > 0; ++step) {
+    const int buf = step & 1, which = kOne ? 0 : buf;
+    const int i = kOne ? step - 2 : (step >> 1) - 1, next = kOne ? step : i + 1;
+    const bool weights = i >= 0 && i < tiles, keys = next < tiles;
+    const int value_slot = (uint32_t)(2 * i + 1) % kSlots, key_slot = (uint32_t)(2 * next) % kSlots;
     if (which == 1 && !job.two) continue;
     const bool last = which == 1 || !job.two;  // the product after which a slot is free
     if (weights) {
       if (which == 0) named_sync(slot_ready(value_slot), kSlotThreads<D>);
       const uint64_t value = desc_mn_major(kv_at + value_slot * Smem<D>::kOperand, Smem<D>::kHalf);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        named_sync(weights_ready(which, half), kWeightsThreads);
+      for (int half = 0; half < kTok / 64; ++half) {
+        named_sync(weights_ready(buf, half), kWeightsThreads);
         fence_after();
-        mma_ts4<128>(tmem + 2 * kTok + which * D, tmem + which * kTok + half * 32, value + half * ((kTok / 2 * 128) >> 4), kIdescO,
+        mma_ts4<128>(tmem + kSumColumn + which * D, tmem + buf * kTok + half * 32, value + half * ((64 * 128) >> 4), kIdescO,
                      i > 0 || half > 0, lead);
       }
       if (last) mma_commit(&sh->kv_empty[value_slot], lead);
+      if (kOne) mma_commit(&sh->o_tile, lead);
     }
     if (keys) {
-      if (which == 0 && weights) named_sync(slot_ready(key_slot), kSlotThreads<D>);
+      if (which == 0 && (kOne || weights)) named_sync(slot_ready(key_slot), kSlotThreads<D>);
       fence_after();
-      const uint64_t q = desc_k_major(q_at + which * Smem<D>::kOperand);
+      const uint64_t q = desc_k_major(q_at + which * Smem<D>::kQTile);
       const uint64_t key = desc_k_major(kv_at + key_slot * Smem<D>::kOperand);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         const uint64_t k = key + c * (Smem<D>::kHalf >> 4);
-        if constexpr (Smem<D>::kQInTmem)
-          mma_ts4<2>(tmem, tmem + kTok + c * 32, k, kIdescS, c > 0, lead);
+        if constexpr (kOne)
+          mma_ts4<2>(tmem + buf * kTok, tmem + kQueryColumn + c * 32, k, kIdescS, c > 0, lead);
         else
-          mma_ss4(tmem + which * kTok, q + c * (Smem<D>::kHalf >> 4), k, kIdescS, c > 0, lead);
+          mma_ss4(tmem + buf * kTok, q + c * (Smem<D>::kQHalf >> 4), k, kIdescS, c > 0, lead);
       }
-      mma_commit(&sh->s_full[which], lead);
+      mma_commit(&sh->s_full[buf], lead);
       if (last) mma_commit(&sh->kv_empty[key_slot], lead);
     }
   }
   mma_commit(&sh->o_full[0], lead);
-  mma_commit(&sh->o_full[1], lead);
+  if (job.two) mma_commit(&sh->o_full[1], lead);
 }
 
 template <int D>
@@ -704,11 +732,12 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   Shared* sh = reinterpret_cast<Shared*>(smem + Smem<D>::kBars);
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0);
   if (tid == 0) {
-    for (int s = 0; s < kRaw; ++s) {
+    for (int s = 0; s < Smem<D>::kRaw; ++s) {
       lt::mbar_init(&sh->packed_full[s], 1);
       lt::mbar_init(&sh->packed_empty[s], Smem<D>::kUnpackers / 32);
     }
-    for (int s = 0; s < kMaxSlots; ++s) lt::mbar_init(&sh->kv_empty[s], 1);
+    for (int s = 0; s < kSlots; ++s) lt::mbar_init(&sh->kv_empty[s], 1);
+    lt::mbar_init(&sh->o_tile, 1);
     lt::mbar_init(&sh->q_full, Smem<D>::kRowTiles * 128);
     for (int t = 0; t < 2; ++t) {
       lt::mbar_init(&sh->s_full[t], 1);
@@ -746,8 +775,8 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
     const int last = min(job.rows - 1, job.row0 + kRows - 1) / p.group;
     job.to = min(job.to, job.rq.length - job.rq.queries + last + 1);
     if (p.window > 0)
-      job.from = max(job.from, (job.rq.length - job.rq.queries + job.row0 / p.group + 1 - p.window) / kTok * kTok);
-    job.tiles = job.to > job.from ? (job.to - job.from + kTok - 1) / kTok : 0;
+      job.from = max(job.from, (job.rq.length - job.rq.queries + job.row0 / p.group + 1 - p.window) / p.align * p.align);
+    job.tiles = job.to > job.from ? (job.to - job.from + Smem<D>::kTok - 1) / Smem<D>::kTok : 0;
   }
 
   if (warp == 12) {
