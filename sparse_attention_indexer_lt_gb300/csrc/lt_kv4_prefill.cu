@@ -604,8 +604,6 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
   bool fed = true;
 #pragma unroll 1
   for (int i = 0; i < job.tiles; ++i) {
-    wait_warp(&sh->kv_empty[slot], slot_parity, sh);
-    if (Smem<D>::kOne && i == kSlots / 2 - 1) wait_warp(&sh->q_full, 0, sh);  // until then the queries are in the last slots
 #pragma unroll 1
     for (int half = 0; half < kParts; ++half) {
       fed = fed && wait_warp(&sh->packed_full[stage], stage_parity, sh);  // (once in vain is enough)
@@ -632,13 +630,22 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
         if (lane == 0) sh->nan_rows[word] = nan_rows;
         if (nan_rows) sh->nan_groups[i % kRing * kTok + half * kPart + row] = (uint8_t)nan;
       }
+      uint4 codes[2 * kBlocks];
+#pragma unroll
+      for (int c = 0; c < 2 * kBlocks; ++c) codes[c] = reinterpret_cast<const uint4*>(from + part * (D / 2))[2 * block0 + c];
+      __syncwarp();  // every lane has read the stage
+      if (lane == 0) arrive(&sh->packed_empty[stage]);
+      if (half == 0) {
+        wait_warp(&sh->kv_empty[slot], slot_parity, sh);
+        // (until then the queries are in the last slots)
+        if (Smem<D>::kOne && i == kSlots / 2 - 1) wait_warp(&sh->q_full, 0, sh);
+      }
       const uint32_t to = slot * Smem<D>::kOperand + half * (kPart * 128);
 #pragma unroll
       for (int c = 0; c < kBlocks; ++c) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const uint4 v = reinterpret_cast<const uint4*>(from + part * (D / 2))[2 * (block0 + c) + g];
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t w[4] = {codes[2 * c + g].x, codes[2 * c + g].y, codes[2 * c + g].z, codes[2 * c + g].w};
           const uint32_t scale = __byte_perm(sc[c], 0, g ? 0x3232 : 0x1010);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -650,8 +657,6 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
           }
         }
       }
-      __syncwarp();  // every lane has read the stage
-      if (lane == 0) arrive(&sh->packed_empty[stage]);
       if (++stage == kRaw) {
         stage = 0;
         stage_parity ^= 1u;
