@@ -756,8 +756,13 @@ constexpr int kPrefillMinChunk = 512;
 // Query rows a kv head from which the kernel for many rows is taken, each side's us with 8 kv heads of D:
 //   1 request of 8192 positions, D = 128: 26 there, 25 here with 16 rows, 28 and 37 with 32, 36 and 74 with 256
 //   16 requests of 4096, D = 128: 81 and 74 with 32 rows, 87 and 119 with 64; D = 64: 68 and 59, 73 and 57
-// so from two row tiles of this kernel on (D = 64: from three), and with few CTAs from 17 rows.
-int prefill_from(int d, bool few) { return few ? 17 : d == 64 ? 65 : 33; }
+//   D = 256, 4 kv heads: 1 request of 8192 positions 32 and 35 with 32 rows; 4 of them 48 and 39, with 64 rows 49 and
+//   70; 64 requests of 2048 94 and 66 with 20 rows, 101 and 117 with 40
+// so from two row tiles of this kernel on (D = 64: from three), and with few CTAs from 17 rows (D = 256, whose
+// tiles have fewer rows: with very few).
+int prefill_from(int d, int64_t units, int sms) {
+  return units * (d == 256 ? 16 : 4) <= sms ? 17 : d == 64 ? 65 : 33;
+}
 constexpr int kPartPositions = 2048;  // positions of a part up to which requests are cut into equal numbers of parts
 
 Plan finish_plan(Plan a, int heads, int d, int requests) {
@@ -776,7 +781,7 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
                int64_t positions, int window) {
   Plan a = {};
   const int64_t rows = (int64_t)(list_len > 0 ? 1 : max_new) * group;
-  a.prefill = list_len == 0 && rows >= prefill_from(d, (int64_t)requests * heads * 4 <= sms);
+  a.prefill = list_len == 0 && rows >= prefill_from(d, (int64_t)requests * heads, sms);
   if (a.prefill) {
     a.cta_rows = prefill_rows(d);
     a.row_tiles = (int)((rows + a.cta_rows - 1) / a.cta_rows);

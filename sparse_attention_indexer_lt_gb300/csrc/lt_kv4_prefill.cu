@@ -1,8 +1,8 @@
 // lt_kv4_prefill.cu -- attention over the 4-bit cache for many query rows a
 // request (prefill chunks): tcgen05 with the sums in tensor memory.
 //
-// A CTA takes 256 query rows of one kv head (two tiles of 128, a thread a row; one tile
-// with heads of 256) and a range of positions in tiles of 128, with one role a warpgroup:
+// A CTA takes 256 query rows of one kv head (two tiles of 128, a thread a row) and a
+// range of positions in tiles of 128, with one role a warpgroup:
 //   warpgroups 0 and 1  softmax of row tile A and B: logits from tensor memory,
 //                       weights back into it as fp16, where the second product reads them
 //   warpgroup 2         unpacks: a thread turns one position's key or value codes into fp16,
@@ -13,9 +13,14 @@
 //
 // Keys are laid out channels inner (K-major), values are the same bytes read as
 // the transposed operand (their channels are the product's N). Unpacked tiles live in a
-// ring of four; the packed rows' pitch is an odd multiple of 16 bytes, so eight threads
-// reading 16 bytes of eight rows touch all banks, and the swizzle does the same
-// for their stores.
+// ring of four; the packed rows' pitch is an odd multiple of 16 bytes (with heads of 256
+// twice one), so eight threads reading 16 bytes of eight rows touch all banks (half of them), and the
+// swizzle does the same for their stores.
+//
+// With heads of 256 tensor memory holds one row tile's sums, its queries and two tiles
+// of logits of 64 positions: the order is  S(0), S(1), O += P(0) V(0), S(2), O += P(1) V(1), S(3), ... ,
+// so that one position tile's softmax runs beside the next one's first product and the last
+// one's second, and warpgroup 1 unpacks too.
 //
 // The running maximum moves only when a row's logits pass it by 2^8 (the sums are
 // then rescaled in tensor memory, seldom); weights are held as 2^6 exp(s - max) at
@@ -33,6 +38,12 @@
 // allow. Measured and dropped: a quarter, a third or half of the exponentials on the FMA
 // pipes (541, 557, 621 us against 511), two threads a row (541), the first half's weights taken
 // before the tile's maximum is known (804 against 716).
+//
+// Heads of 256, the same chunk: 5063 us with the kernel for few rows; here 1586 with queries
+// in shared memory and a key and a value tile, 1238 with the queries in tensor memory and three tiles, 1100 with
+// eight warps unpacking, 854 with tiles of 64, logits a tile ahead and five packed stages in place of three
+// of 32 positions (1160 with those): 1.21 PFLOP/s, 63% of cuBLAS's burst, where four waves of 512 CTAs on 152
+// SMs allow 84%. The unpacked tile's way, read, write and fence, is what is left: 748 us without its writes.
 //
 // A value that is NaN is unpacked as zero, and the rows that see it note the group:
 // a row's output is NaN there whatever its weight, and rows that do not see it stay clean.
