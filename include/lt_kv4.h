@@ -23,6 +23,8 @@
  * nearest to x / scale (ties to the even code), so it is off by at most one
  * scale, and code * scale is an exact fp16 number. Finite values beyond
  * 6 * 10912 saturate. A group that holds a NaN or an infinity is stored as NaN.
+ * Other scales (an infinity, a magnitude above 10912) are outside the format;
+ * lt_kv4_store writes none.
  *
  * A slot is page * page_size + offset (int64): the place of one position. A
  * block table int32 [requests][table_width] names the pages of each request in
@@ -138,7 +140,9 @@ lt_status lt_kv4_load(const void* cache, int64_t pages, int32_t page_size, const
  * entries (-1 pads) are ignored, a repeated one counts as often as it stands
  * there -- and window must be 0. A query that sees nothing gets zeros and
  * lse = -inf; so does position data on a page outside [0, pages), which nothing
- * sees. What is not visible has no effect, whatever bytes it holds.
+ * sees. What is not visible has no effect, whatever bytes it holds. Where a query
+ * sees a group whose scale is outside the format, its results there (from a key, its
+ * whole row) are NaN, infinite or finite: not specified.
  *
  * Arithmetic: the products run on the tensor cores in fp16 with fp32 sums. A
  * stored value is an exact fp16 number; a bf16 query is scaled by a power of two

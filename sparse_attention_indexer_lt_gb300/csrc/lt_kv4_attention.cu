@@ -457,13 +457,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
       for (int i = 0; i < kWordsV; ++i) {
         uint32_t s01 = __byte_perm(sv[0][i], sv[1][i], pick), s23 = __byte_perm(sv[2][i], sv[3][i], pick);
         if (masked) {
-          // what no row sees counts as zero, whatever it holds; a NaN that only some rows see is put
-          // into those rows below
+          // what no row sees counts as zero, whatever it holds; a NaN (or a scale that is none) that only some
+          // rows see is put into those rows below
           const uint32_t b01 = valid >> (mt * 16 + 2 * c), b23 = b01 >> 8;
           s01 &= ((b01 & 1u) ? 0xFFFFu : 0u) | ((b01 & 2u) ? 0xFFFF0000u : 0u);
           s23 &= ((b23 & 1u) ? 0xFFFFu : 0u) | ((b23 & 2u) ? 0xFFFF0000u : 0u);
           if constexpr (!kList) {
-            const uint32_t n01 = nan_halves(s01), n23 = nan_halves(s23);
+            const uint32_t n01 = unfit_halves(s01), n23 = unfit_halves(s23);
             poisoned = poisoned || (n01 | n23) != 0;
             s01 &= ~n01;
             s23 &= ~n23;
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
           lds_words(base + at * kRow + D + D / 16, sv);
 #pragma unroll
           for (int i = 0; i < kWordsV; ++i) {
-            if (nan_halves((g >> 2) ? sv[i] >> 16 : sv[i] & 0xFFFFu) == 0) continue;
+            if (unfit_halves((g >> 2) ? sv[i] >> 16 : sv[i] & 0xFFFFu) == 0) continue;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -203,9 +203,11 @@ __device__ __forceinline__ void bulk_in(uint32_t dst, const void* src, uint32_t 
                :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
-// 0xFFFF in each half of the word that is an fp16 NaN.
-__device__ __forceinline__ uint32_t nan_halves(uint32_t h) {
-  return ((h & 0x7FFFu) > 0x7C00u ? 0xFFFFu : 0u) | ((h & 0x7FFF0000u) > 0x7C000000u ? 0xFFFF0000u : 0u);
+// 0xFFFF in each half of the word that is no scale of the format: an fp16 NaN, an infinity, or a magnitude above
+// 10912 (0x7154), whose product with a code overflows fp16. Weight 0 times such a value would be NaN, so they
+// are kept out of the products and put into the rows that see them. (Testing for NaN alone let the others through.)
+__device__ __forceinline__ uint32_t unfit_halves(uint32_t h) {
+  return ((h & 0x7FFFu) > 0x7154u ? 0xFFFFu : 0u) | ((h & 0x7FFF0000u) > 0x71540000u ? 0xFFFF0000u : 0u);
 }
 
 // bf16 rows become fp16 rows times a power of two: the one that brings the row's largest (magnitude's

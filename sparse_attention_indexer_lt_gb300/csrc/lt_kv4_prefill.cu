@@ -45,8 +45,8 @@
 // of 32 positions (1160 with those): 1.21 PFLOP/s, 63% of cuBLAS's burst, where four waves of 512 CTAs on 152
 // SMs allow 84%. The unpacked tile's way, read, write and fence, is what is left: 748 us without its writes.
 //
-// A value that is NaN is unpacked as zero, and the rows that see it note the group:
-// a row's output is NaN there whatever its weight, and rows that do not see it stay clean.
+// A value that is NaN, or whose scale is outside the format, is unpacked as zero, and the rows that see it note
+// the group: a row's output is NaN there whatever its weight, and rows that do not see it stay clean.
 
 #include <mutex>
 
@@ -102,7 +102,7 @@ struct Shared {
   // notes of the tiles in work, a ring of 512 positions (they are made at most three tiles of 128, or six of
   // 64, ahead of the softmax: slots that its products give back hold the rest up)
   alignas(16) uint32_t valid[16];     // positions on a page of the cache and in range, as bits
-  alignas(16) uint32_t nan_rows[16];  // positions with a NaN value scale
+  alignas(16) uint32_t nan_rows[16];  // positions with a value scale that is NaN or outside the format
   uint8_t nan_groups[512];
   int64_t sums[kCta / 32];
   Place found;
@@ -627,14 +627,14 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
 #pragma unroll
       for (int g = 0; g < kBlocks; ++g) {
         sc[g] = there ? reinterpret_cast<const uint32_t*>(from + D + part * (D / 16))[block0 + g] : 0u;
-        if (part == 1) sc[g] &= ~nan_halves(sc[g]);
+        if (part == 1) sc[g] &= ~unfit_halves(sc[g]);
       }
       if (part == 0 && block0 == 0) {
         // the NaN values are noted here, with the keys: the softmax starts when the keys are there
         uint32_t nan = 0;
 #pragma unroll
         for (int g = 0; g < D / 64; ++g) {
-          const uint32_t n = there ? nan_halves(reinterpret_cast<const uint32_t*>(from + D + D / 16)[g]) : 0u;
+          const uint32_t n = there ? unfit_halves(reinterpret_cast<const uint32_t*>(from + D + D / 16)[g]) : 0u;
           nan |= ((n & 1u) | ((n >> 15) & 2u)) << (2 * g);
         }
         const uint32_t nan_rows = __ballot_sync(~0u, nan != 0);

@@ -625,3 +625,42 @@ def test_the_example_runs_and_is_right():
         # outputs are averages of values of unit size, rounded to bf16 and with fp16 weights
         assert example.check(results, held) < 2.0 ** -8 * 4 + 2.0 ** -9 * 4
         assert free == pages and len(results) == kw["steps"]
+
+
+@pytest.mark.parametrize("bits", [0x7C00, 0xFC00, 0x7BFF, 0x7155])
+@pytest.mark.parametrize("dim,new,group,window", [(64, 6, 2, 0), (64, 6, 2, 20), (128, 6, 2, 0), (128, 6, 2, 20), (128, 3, 10, 20), (256, 6, 2, 20),
+                                                  (64, 80, 2, 0), (64, 80, 2, 90), (128, 80, 2, 0), (128, 80, 2, 90), (256, 80, 2, 0), (256, 80, 2, 90)])
+def test_scales_outside_the_format_where_nothing_looks(bits, dim, new, group, window):
+    """Infinite scales, and finite ones above 10912 (whose product with a code overflows fp16), at positions that a
+    row's mask hides leave the row as it is: later than the row's own, before its window, before every row's."""
+    p = Problem([200], [new], 1, group, dim, 16, "bf16", seed=dim + new + window)
+    clean, clean_lse = p.run(window=window)
+    scale = torch.tensor([bits - 0x10000 if bits > 0x7FFF else bits], dtype=torch.int16).view(torch.uint8)
+    codes = torch.tensor([0x00, 0x77, 0x70, 0xF7] * 4, dtype=torch.uint8)  # 0 * inf and 6 * 10920 both
+
+    def put(position, value_group=None, key_group=None):
+        row = p.cache[p.table[0, position // 16], 0, position % 16]
+        if value_group is not None:
+            row[dim + dim // 16 + 2 * value_group:][:2] = scale
+            row[dim // 2 + 16 * value_group:][:16] = codes
+        if key_group is not None:
+            row[dim + 2 * key_group:][:2] = scale
+            row[16 * key_group:][:16] = codes
+    first, late = 0, new // 2
+    put(200 - new + late, value_group=1)       # seen by the queries from `late` on
+    if window:
+        first = 1
+        lowest = 200 - new - window + 1        # the lowest position of query 0, which no later one sees
+        put(lowest, value_group=0)
+        put(lowest - 1, value_group=1, key_group=0)  # seen by none
+    out, lse = p.run(window=window)
+    assert torch.equal(lse, clean_lse)
+    assert torch.equal(out[first:late], clean[first:late])
+    keep = [c for c in range(dim) if not 32 <= c < 64]
+    assert torch.equal(out[late:, :, keep], clean[late:, :, keep])
+    put(199, key_group=1)                      # the last query's own position
+    out, lse = p.run(window=window)
+    # (one row's logits may move when the others' maximum is taken: two results within their bounds of the same)
+    vmax = 6 * 0.35 * 2.72
+    assert ((out[first:late] - clean[first:late]).float().abs() <= 2 * (2.0 ** -8 * clean[first:late].float().abs() + 2.0 ** -10 * vmax)).all()
+    assert (lse[:-1] - clean_lse[:-1]).abs().max() <= 1e-4
