@@ -59,8 +59,9 @@ int32_t lt_kv4_row_bytes(int32_t head_dim);
  *
  * The pages of every request r with finished[r] != 0, table[r][0 .. ceil(lengths[r] / page_size)), go
  * on top of the stack of free pages, in request and then table order:
- * free_pages[num_free ..]. out_num_free is the new height, out_lengths[r] is 0
- * for those requests and lengths[r] for the others.
+ * free_pages[num_free ..]. Cells below 0 hold no page and are passed over (a page
+ * dropped behind a window, say, whose cell was set to -1). out_num_free is the
+ * new height, out_lengths[r] is 0 for those requests and lengths[r] for the others.
  *
  *   lengths       int32 [requests]; clamped to [0, table_width * page_size]
  *   finished      uint8 [requests]

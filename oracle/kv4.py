@@ -93,7 +93,7 @@ def release(lengths, finished, table, free, num_free, page):
     for r, done in enumerate(finished):
         if done:
             for j in range(min(-(-max(int(lengths[r]), 0) // page), table.shape[1])):
-                if n < len(free):
+                if n < len(free) and table[r, j] >= 0:  # (a cell below 0 holds no page)
                     free[n] = table[r, j]
                     n += 1
             lengths[r] = 0

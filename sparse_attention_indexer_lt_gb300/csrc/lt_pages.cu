@@ -7,11 +7,13 @@
 // block-wide scan over all requests (8 bytes a request, from L2 after the first
 // CTA) in segments of kSegment, and then writes its share of the segment's
 // tokens and pages, finding an item's request by a binary search in the
-// scanned sums. No CTA waits for another one, and one launch does the step.
+// scanned sums. One launch does the step. No CTA of extend waits for another one; release runs as one
+// cluster, whose CTAs exchange how many pages they found.
 //
-// Bound by latency: release and extend take some 5 us each in a graph for 64 requests, and 6
-// for 1000 requests with 128000 token slots (1.6 MB, a quarter of a microsecond at
-// HBM's rate).
+// Bound by latency. In a graph of the same call 20 times, a call: for 64 requests, 4 of them ended, release
+// 4.1 us and extend 3.8; for 1000, 50 ended, up to 128 new tokens each (1.6 MB, a quarter of a microsecond at
+// HBM's rate), 5.9 and 5.5. Release took 2.7 and 2.9 when it passed on every cell, pages or not.
+// When everything ends at once it has eight SMs: 262144 pages of 64 requests 36 us, 512000 of 2000 requests 71.
 
 #include <cuda_runtime.h>
 
@@ -105,56 +107,148 @@ __device__ __forceinline__ int64_t first_item(int64_t from) {
   return (turn * gridDim.x + blockIdx.x) * kThreads;
 }
 
-__global__ void __launch_bounds__(kThreads) release_kernel(PageParams p) {
-  __shared__ Sums warp_sums[kThreads / 32];
-  __shared__ int64_t ends[kSegment];
-  __shared__ int32_t held_of[kSegment];
+// Which cells of the ended requests hold a page is known only by reading them (a page may have been dropped
+// behind a window), so a cell's place on the stack hangs on all the cells before it. The CTAs of one cluster
+// take equal runs of a segment's cells, count the pages in theirs, exchange the counts over distributed shared
+// memory and write; the first tile of a run, the usual run, stays in registers between the two.
+constexpr int kMaxRanks = 8;  // CTAs of a portable cluster
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive;\n barrier.cluster.wait;" ::: "memory");
+}
+__device__ __forceinline__ int64_t peer_i64(const int64_t* own, int rank) {
+  int64_t v;
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.s64 %0, [a];\n}"
+               : "=l"(v) : "r"((uint32_t)__cvta_generic_to_shared(own)), "r"(rank) : "memory");
+  return v;
+}
+
+constexpr int kReleaseThreads = 1024;                  // a request each
+constexpr int kReleaseTile = kReleaseThreads * kItems;  // cells
+
+// Inclusive scan of one number per thread over the block; *total gets the block's sum.
+template <class T>
+__device__ __forceinline__ T wide_scan(T v, T* total, T* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T u = __shfl_up_sync(~0u, v, d);
+    if (lane >= d) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  const T own = warp_sums[lane];  // (32 warps)
+  T run = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T u = __shfl_up_sync(~0u, run, d);
+    if (lane >= d) run += u;
+  }
+  *total = __shfl_sync(~0u, run, 31);
+  return v + __shfl_sync(~0u, run - own, warp);
+}
+
+__global__ void __launch_bounds__(kReleaseThreads) release_kernel(PageParams p) {
+  __shared__ int64_t request_sums[32];
+  __shared__ int page_sums[32];
+  __shared__ int64_t ends[kReleaseThreads];
+  __shared__ int32_t held_of[kReleaseThreads];
+  __shared__ int64_t counts[2];  // pages in this CTA's cells, by turns: a peer may still read the last segment's
+  const int rank = blockIdx.x, ranks = gridDim.x;
   lt::kv4::dependency_wait();
   const int64_t low = clamp_i32(*p.num_free, 0, p.capacity);
   int64_t taken = 0;
-  for (int base = 0; base < p.requests; base += kSegment) {
-    const int count = min(kSegment, p.requests - base);
-    int64_t held[kItems];
-    Sums mine = {0, 0};
+  int turn = 0;
+  bool met = false;
+  for (int base = 0; base < p.requests; base += kReleaseThreads) {
+    const int r = base + threadIdx.x;
+    int64_t held = 0;
+    if (r < p.requests) {
+      const int32_t len = p.lengths[r];
+      const bool ends_now = p.finished[r] != 0;
+      if (ends_now) {
+        held = ((int64_t)max(len, 0) + ((1 << p.shift) - 1)) >> p.shift;
+        if (held > p.width) held = p.width;
+      }
+      if (base / kReleaseThreads % ranks == rank) p.out_lengths[r] = ends_now ? 0 : len;
+    }
+    int64_t cells;
+    const int64_t end = wide_scan(held, &cells, request_sums);
+    if (cells == 0) continue;  // (the same for all CTAs)
+    ends[threadIdx.x] = end;
+    held_of[threadIdx.x] = (int32_t)held;
+    __syncthreads();
+    // a single tile in all is the first CTA's, without an exchange
+    const bool alone = cells <= kReleaseTile && p.requests <= kReleaseThreads;
+    const int64_t share = alone ? cells : (cells + ranks - 1) / ranks;
+    const int64_t from = rank * share < cells ? rank * share : cells, to = from + share < cells ? from + share : cells;
+    // kItems neighbouring cells a thread, -1 past the run; how many are pages
+    auto read = [&](int64_t at, int32_t (&id)[kItems]) {
+      const int64_t first = at + threadIdx.x * kItems;
+      // the request of a cell: how many ends are at or below it (side by side for the thread's cells)
+      int o[kItems] = {}, pages = 0;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int r = base + threadIdx.x * kItems + i;
-      held[i] = 0;
-      if (r < p.requests) {
-        const int32_t len = p.lengths[r];
-        const bool ends_now = p.finished[r] != 0;
-        if (ends_now) {
-          held[i] = ((int64_t)max(len, 0) + ((1 << p.shift) - 1)) >> p.shift;
-          if (held[i] > p.width) held[i] = p.width;
+      for (int step = kReleaseThreads / 2; step > 0; step /= 2)
+#pragma unroll
+        for (int i = 0; i < kItems; ++i)
+          if (ends[o[i] + step - 1] <= first + i) o[i] += step;
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        id[i] = -1;
+        if (first + i < to) id[i] = p.table[(int64_t)(base + o[i]) * p.width + (first + i - (ends[o[i]] - held_of[o[i]]))];
+      }
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) pages += id[i] >= 0;
+      return pages;
+    };
+    auto put = [&](int64_t at, const int32_t (&id)[kItems]) {
+#pragma unroll
+      for (int i = 0; i < kItems; ++i)
+        if (id[i] >= 0) {
+          if (at < p.capacity) p.free_pages[at] = id[i];
+          ++at;
         }
-        if ((r / kSegment) % gridDim.x == blockIdx.x) p.out_lengths[r] = ends_now ? 0 : len;
+    };
+    int32_t id[kItems];
+    int here;
+    const int pages = read(from, id);
+    const int upto = wide_scan(pages, &here, page_sums);
+    int64_t mine = here;
+    if (to - from > kReleaseTile) {
+      int64_t more = 0;
+      int32_t next[kItems];
+      for (int64_t at = from + kReleaseTile; at < to; at += kReleaseTile) more += read(at, next);
+      int64_t sum;
+      wide_scan(more, &sum, request_sums);
+      mine += sum;
+    }
+    int64_t place = low + taken;
+    if (alone) {
+      taken = mine;  // (of use to the first CTA)
+    } else {
+      if (threadIdx.x == 0) counts[turn] = mine;
+      cluster_sync();
+      for (int q = 0; q < ranks; ++q) {
+        const int64_t n = peer_i64(&counts[turn], q);
+        if (q < rank) place += n;
+        taken += n;
       }
-      mine.a += held[i];
+      turn ^= 1;
+      met = true;
     }
-    Sums total;
-    const Sums scan = block_scan(mine, &total, warp_sums);
-    int64_t run = taken + scan.a - mine.a;
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      run += held[i];
-      ends[threadIdx.x * kItems + i] = run;
-      held_of[threadIdx.x * kItems + i] = (int32_t)held[i];
+    put(place + upto - pages, id);
+    place += here;
+    for (int64_t at = from + kReleaseTile; at < to; at += kReleaseTile) {
+      const int n = read(at, id), s = wide_scan(n, &here, page_sums);
+      put(place + s - n, id);
+      place += here;
     }
-    __syncthreads();
-    const int64_t stop = taken + total.a;
-    for (int64_t b = first_item(taken); b < stop; b += (int64_t)gridDim.x * kThreads) {
-      const int64_t i = b + threadIdx.x;
-      if (i >= taken && i < stop && low + i < p.capacity) {
-        const int o = owner_of(ends, count, i);
-        const int64_t col = i - (ends[o] - held_of[o]);
-        p.free_pages[low + i] = p.table[(int64_t)(base + o) * p.width + col];
-      }
-    }
-    taken = stop;
-    __syncthreads();
+    __syncthreads();  // (the next segment's sums go where this one's were read)
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.out_num_free = clamp_i32(low + taken, 0, p.capacity);
+  if (rank == 0 && threadIdx.x == 0) *p.out_num_free = clamp_i32(low + taken, 0, p.capacity);
   lt::kv4::dependents_launch();
+  if (met) cluster_sync();  // (a CTA's counts stay until its peers have read them)
 }
 
 __global__ void __launch_bounds__(kThreads) extend_kernel(PageParams p) {
@@ -295,11 +389,11 @@ lt_status lt_page_release(const int32_t* lengths, const uint8_t* finished, int32
   p.width = table_width;
   p.capacity = free_capacity;
   p.shift = shift;
-  // pages come back a request at a time: a CTA for every four requests' pages
-  const int64_t most = ((int64_t)requests * table_width + 4 * kThreads - 1) / (4 * kThreads);
-  int64_t grid = most < requests / 4 + 1 ? most : requests / 4 + 1;
-  grid = grid < 1 ? 1 : grid > 152 ? 152 : grid;
-  return lt::kv4::launch(reinterpret_cast<const void*>(&release_kernel), dim3((unsigned)grid), kThreads, 0, &p, stream);
+  // one cluster: a CTA for every tile of the table, up to the portable size
+  const int64_t cells = (int64_t)requests * table_width;
+  unsigned ranks = 1;
+  while (ranks < kMaxRanks && (int64_t)ranks * kReleaseTile < cells) ranks *= 2;
+  return lt::kv4::launch(reinterpret_cast<const void*>(&release_kernel), dim3(ranks), kReleaseThreads, 0, &p, stream, ranks);
 }
 
 lt_status lt_page_extend(const int32_t* lengths, const int32_t* new_tokens, int32_t requests,

@@ -664,3 +664,41 @@ def test_scales_outside_the_format_where_nothing_looks(bits, dim, new, group, wi
     vmax = 6 * 0.35 * 2.72
     assert ((out[first:late] - clean[first:late]).float().abs() <= 2 * (2.0 ** -8 * clean[first:late].float().abs() + 2.0 ** -10 * vmax)).all()
     assert (lse[:-1] - clean_lse[:-1]).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("requests,width", [(1, 1), (1, 5000), (3, 40), (33, 300), (1500, 7), (2500, 40)])
+def test_release_takes_no_cell_that_holds_no_page(requests, width):
+    """Cells below 0 in an ended request's row (pages dropped behind a window, or never given) are not pages."""
+    import sparse_attention_indexer_lt_gb300 as lt
+    rng = np.random.default_rng(requests + width)
+    page = 8
+    lengths = rng.integers(-2, width * page + 20, requests).astype(np.int32)
+    done = rng.random(requests) < 0.5
+    done[0] = True
+    if requests == 2500:
+        done[1:1500] = False  # (few cells first, many later)
+    table = rng.permutation(requests * width).astype(np.int32).reshape(requests, width)
+    table[rng.random((requests, width)) < 0.3] = -1
+    table[rng.random((requests, width)) < 0.05] = -2 ** 31
+    if requests > 2:
+        table[1] = -1
+    for capacity, num_free in ((requests * width + 9, 3), (requests * width // 5 + 4, 1)):
+        free = np.full(capacity, -7, np.int32)
+        free[:num_free] = requests * width + np.arange(num_free)
+        held = [int(x) for r in range(requests) if done[r] for x in table[r, :-(-max(int(lengths[r]), 0) // page)] if x >= 0]
+        want = np.concatenate([free[:num_free], np.array(held, np.int32)])[:capacity]
+        d = [torch.as_tensor(x).cuda() for x in (lengths, done, table, free, np.array([num_free], np.int32))]
+        got_l, got_n = lt.page_release(*d[:4], d[4], page)
+        torch.cuda.synchronize()
+        assert np.array_equal(got_l.cpu().numpy(), np.where(done, 0, lengths))
+        assert int(got_n) == len(want)
+        got = d[3].cpu().numpy()
+        assert np.array_equal(got[:len(want)], want) and (got[len(want):] == -7).all()
+        oracle = ok.release(lengths, done, table, free, num_free, page)
+        assert oracle[2] == len(want) and np.array_equal(oracle[1], got)
+        # what is taken next are pages
+        few = min(len(want), 50)
+        rows = torch.full((1, 64), -1, dtype=torch.int32, device="cuda")
+        zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+        step = lt.page_extend(zero, zero + few * page, rows, d[3], got_n, page, few * page)
+        assert int(step.lengths) == few * page and (step.slots >= 0).all()

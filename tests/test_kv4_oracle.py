@@ -225,3 +225,13 @@ def test_binding_refuses_cpu_tensors_and_bad_sizes():
         lt.kv4_row_bytes(96)
     with pytest.raises(ValueError):
         lt.kv4_cache(2, 1, 24, 128, device="cpu")
+
+
+def test_release_passes_over_cells_without_a_page():
+    table = np.array([[7, -1, 3], [-1, -1, 4]], np.int32)
+    free = np.array([9, 5, -7, -7, -7], np.int32)
+    lengths, got, n = ok.release(np.array([12, 8]), [True, True], table, free, 2, 4)
+    assert lengths.tolist() == [0, 0] and got.tolist() == [9, 5, 7, 3, -7] and n == 4
+    # the next pages taken are pages
+    s = ok.extend(np.array([0]), np.array([8]), np.full((1, 2), -1, np.int32), got, n, 4, 8)
+    assert s["table"].tolist() == [[3, 7]] and (s["slots"] >= 0).all()
