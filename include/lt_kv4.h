@@ -19,10 +19,10 @@
  *
  * A code is an e2m1 number (sign bit, then 0, 0.5, 1, 1.5, 2, 3, 4, 6). The scale
  * of a group is the smallest number at least amax / 6 that has 9 significant
- * bits and is a multiple of 2^-23, at most 10912; a channel is stored as the code
- * nearest to x / scale (ties to the even code), so it is off by at most one
- * scale, and code * scale is an exact fp16 number. Finite values beyond
- * 6 * 10912 saturate. A group that holds a NaN or an infinity is stored as NaN.
+ * bits and is a multiple of 2^-23, at most 10912; a channel is stored as its sign
+ * (a zero's too) and the code nearest to |x| / scale (ties to the even code), so
+ * it is off by at most one scale, and code * scale is an exact fp16 number. Finite
+ * values beyond 6 * 10912 saturate. A group that holds a NaN or an infinity is stored as NaN.
  * Other scales (an infinity, a magnitude above 10912) are outside the format;
  * lt_kv4_store writes none.
  *

@@ -10,7 +10,7 @@
 // The rounding has to be that of the quotient as a real number, though y itself is
 // rounded. For 16-bit inputs that is so: the scale has 9 significant bits and x
 // at most 11, so x / scale is a level border exactly or at least 2^-13 of it away,
-// and q + r / scale with r = x - q * scale (one exact fused step) is the exact
+// and q - r / scale with r = q * scale - x (one exact fused step) is the exact
 // quotient where that has at most 24 bits, borders among them. fp32 inputs can lie nearer to
 // a border; they are compared with border * scale, which has at most 12 bits.
 //
@@ -83,8 +83,8 @@ struct Eight {  // 16-bit types: pairs in words
   // t: amax / 6 times 1 - 2^-18 or so. amax has at most 11 bits, so amax / 6 is a number of the grid or at
   // least 2^-13 of itself away from one: the next number above t is the next at or above amax / 6.
   static __device__ __forceinline__ float scale(float amax) { return scale_above(amax * 0x1.55550p-3f); }
-  // y = x / s as q + r / s with the exact remainder r = x - q s: exact where the quotient is a level border
-  // (inv within 2^-22 of 1 / s will do).
+  // y = x / s as q - r / s with the exact remainder r = q s - x: exact where the quotient is a level border
+  // (inv within 2^-22 of 1 / s will do). A zero keeps its sign, also with s = 0: r is +0 then, and -0 + q is q.
   __device__ __forceinline__ uint32_t codes(float s) const {
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
@@ -94,7 +94,7 @@ struct Eight {  // 16-bit types: pairs in words
     for (int i = 0; i < 8; ++i) {
       const float x = number(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
       const float q = x * inv;
-      y[i] = fmaf(fmaf(-q, s, x), inv, q);
+      y[i] = fmaf(-fmaf(q, s, -x), inv, q);
     }
     return lt::kv4::codes_of(y);
   }
@@ -130,14 +130,13 @@ struct Eight<float> {
   // (fp32 may lie nearer to a border than a rounded quotient tells; border * s has at most 12 bits)
   __device__ __forceinline__ uint32_t codes(float s) const {
     uint32_t w = 0;
-    if (s > 0.0f) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = fabsf(x[i]);
-        const uint32_t c = (a > 0.25f * s) + (a >= 0.75f * s) + (a > 1.25f * s) + (a >= 1.75f * s) + (a > 2.5f * s) +
-                           (a >= 3.5f * s) + (a > 5.0f * s);
-        w |= (c | (x[i] < 0.0f ? 8u : 0u)) << (4 * i);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(x[i]);
+      uint32_t c = (a > 0.25f * s) + (a >= 0.75f * s) + (a > 1.25f * s) + (a >= 1.75f * s) + (a > 2.5f * s) +
+                   (a >= 3.5f * s) + (a > 5.0f * s);
+      if (s == 0.0f) c = 0;  // (a group of zeros)
+      w |= (c | (__float_as_uint(x[i]) >> 31 << 3)) << (4 * i);  // (a zero has a sign, too)
     }
     return w;
   }

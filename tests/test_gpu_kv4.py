@@ -702,3 +702,28 @@ def test_release_takes_no_cell_that_holds_no_page(requests, width):
         zero = torch.zeros(1, dtype=torch.int32, device="cuda")
         step = lt.page_extend(zero, zero + few * page, rows, d[3], got_n, page, few * page)
         assert int(step.lengths) == few * page and (step.slots >= 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_stored_rows_are_the_oracles_byte_for_byte(dtype, dim):
+    """Codes with the sign of zeros, and the padding; scales of groups with NaN are some NaN."""
+    import sparse_attention_indexer_lt_gb300 as lt
+    torch.manual_seed(dim)
+    t = TYPES[dtype]
+    x = special(torch.randn(24, 2, dim) * 10.0 ** torch.randint(-6, 3, (24, 2, 1)))
+    x[5, :, :32] = torch.tensor([0.0, -0.0] * 16)                   # a group of zeros alone
+    x[6, :, :32] = torch.tensor([-0.0, 3.0, 0.0, -1e-6, 1e-6, -6.0, -0.0, 1.0] * 4)
+    x[7, :, 32:64] = torch.tensor([-0.0, -1e-9, 1e-9, 0.0] * 8)
+    x[8:16][x[8:16].abs() < 0.5] = -0.0
+    x = x.to(t)
+    for k, v in ((x, x.flip(0)), (x.flip(0), x)):
+        cache = torch.full((3, 2, 8, lt.kv4_row_bytes(dim)), 0xA5, dtype=torch.uint8, device="cuda")
+        lt.kv4_store(k.cuda(), v.cuda(), cache, torch.arange(24, device="cuda"))
+        got = cache.cpu().transpose(1, 2).reshape(24, 2, -1).numpy()
+        for i in range(24):
+            want = ok.rows_of(num(k[i]), num(v[i]))
+            scales = slice(dim, dim + dim // 8)
+            assert np.array_equal(got[i, :, :dim], want[:, :dim]), f"codes of token {i}"
+            assert np.array_equal(got[i, :, scales].copy().view(np.float16), want[:, scales].copy().view(np.float16), equal_nan=True)
+            assert np.array_equal(got[i, :, dim + dim // 8:], want[:, dim + dim // 8:]), f"padding of token {i}"
