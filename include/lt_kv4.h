@@ -174,8 +174,11 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
                            void* stream);
 
 /* Bytes of workspace that lt_kv4_attention needs for these sizes on the current
- * device: 0 where a request's parts are joined within the launch. list_len 0:
- * without positions (else window is 0); positions = table_width * page_size. */
+ * device: 0 where a request's parts are joined within the launch, else room for the
+ * parts of the requests that are cut, each with the fp32 outputs of up to max_new
+ * queries. How many parts there can be goes by the device's SMs and the query rows,
+ * and beyond that not by the requests. list_len 0: without positions (else window
+ * is 0); positions = table_width * page_size. */
 lt_status lt_kv4_workspace(int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                            int32_t requests, int32_t max_new, int32_t list_len, int64_t positions,
                            int32_t window, int64_t* bytes);

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
 
   // the request, its rows of this CTA and the range of positions (of list entries)
   Request rq;
-  int request, count, token0, rows, from, to;
+  int request, count, token0, rows, from, to, nth_part = 0;
   if constexpr (kList) {
     token0 = flat;  // one query token
     request = owner_of_token(p, token0);
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   } else if (p.parts > 0) {
     request = flat;
     rq = request_of(p, request);
-    rows = rq.queries * p.group;
+    rows = rq.computed * p.group;
     token0 = rq.first;
     from = rq.low;
     to = rq.length;
@@ -182,9 +182,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
     rq = request_of(p, request);
     count = pl.count;
     token0 = rq.first;
-    rows = rq.queries * p.group;
+    rows = rq.computed * p.group;
+    nth_part = pl.part + pl.split;
     if (flat == pl.base && head == 0 && row_tile == 0 && tid == 0 && p.plan != nullptr)
-      p.plan[request] = make_int2(pl.base, pl.count);
+      p.plan[request] = make_int2(pl.part, pl.count);
     // chunks start on tiles: rq.low is a multiple of kTile
     const int64_t at = rq.low + pl.split * chunk_of(p, rq, pl.count), end = at + chunk_of(p, rq, pl.count);
     from = (int)(at < rq.length ? at : rq.length);
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
     }
   __syncthreads();
   const int here = min(NT * 8, rows - row0) * (D / 4);  // groups of four channels
-  const int64_t part = (((int64_t)flat * p.heads + head) * p.row_tiles + row_tile) * (NT * 8);
+  const int64_t part = ((int64_t)nth_part * p.heads + head) * p.part_rows + row0;
   for (int u = tid; u < here; u += kThreads) {
     const int row = u / (D / 4), ch = u % (D / 4) * 4;
     float4 o = *reinterpret_cast<const float4*>(joined + row * kPitch + ch);
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
 constexpr int kJoinThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionParams p, int rows_per_cta) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionParams p) {
   constexpr int kVec = D / 32;
   __shared__ float o_of[kJoinThreads / 32][D];
   __shared__ float sum_of[kJoinThreads / 32], top_of[kJoinThreads / 32];
@@ -651,16 +652,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttentionParams p, i
   const int request = owner_of_token(p, (int)token);
   if (request < 0) return;
   const int2 pl = p.plan[request];
-  const int base = pl.x, n = pl.y;
+  const int n = pl.y;
   const Request rq = request_of(p, request);
   const int64_t nth = token - rq.first;
-  if (nth >= rq.queries) return;
-  const int row = (int)nth * p.group + qh % p.group;
+  if (nth >= rq.computed) return;
   if (n <= 1) return;  // written whole
-  const int row_tile = row / rows_per_cta, in_tile = row % rows_per_cta;
-  if (row_tile >= p.row_tiles) return;  // past max_new: not computed
-  const int64_t step = (int64_t)p.heads * p.row_tiles * rows_per_cta;
-  const int64_t first = (((int64_t)base * p.heads + head) * p.row_tiles + row_tile) * rows_per_cta + in_tile;
+  const int64_t step = (int64_t)p.heads * p.part_rows;
+  const int64_t first = pl.x * step + (int64_t)head * p.part_rows + nth * p.group + qh % p.group;
 
   float top = -INFINITY;
   bool bad = false;
@@ -741,7 +739,8 @@ RowsKernel rows_kernel_of(int d, int nt, bool list) {
 // The launch for these sizes: row tiles, parts and workspace.
 struct Plan {
   bool prefill;        // the kernel for many query rows
-  int nt, row_tiles, cta_rows;
+  int nt, row_tiles;
+  int64_t part_rows;   // query rows of a part
   int parts;           // > 0: every request (list) in that many parts, a cluster; 0: chunks of like work
   int target;          // chunks wanted over all requests
   int min_chunk;
@@ -765,14 +764,18 @@ int prefill_from(int d, int64_t units, int sms) {
 }
 constexpr int kPartPositions = 2048;  // positions of a part up to which requests are cut into equal numbers of parts
 
-Plan finish_plan(Plan a, int heads, int d, int requests) {
-  // (a chunk is at least total / target long, so the requests have at most target + requests)
+// rows: the most query rows of a request
+Plan finish_plan(Plan a, int heads, int d, int requests, int64_t rows) {
+  // A chunk is at least total / target long, so the requests have fewer than target + requests. Parts are kept for
+  // the requests that have several chunks alone: each of those is longer than a chunk, so they are fewer than
+  // target, and have fewer than 2 target chunks.
   if (a.flats == 0) a.flats = a.target == 1 ? requests : a.target + (int64_t)requests;
   a.join = a.parts == 0 && a.target > 1;
-  const int64_t part_rows = a.flats * heads * a.row_tiles * a.cta_rows;
+  const int64_t parts = (a.target < requests ? (int64_t)a.target : (int64_t)requests) + a.target - 1;
+  a.part_rows = rows;
   a.plan_bytes = ((int64_t)requests * 8 + 15) / 16 * 16;
-  a.lse_bytes = (part_rows * 4 + 15) / 16 * 16;
-  a.o_bytes = part_rows * d * 4;
+  a.lse_bytes = (parts * heads * rows * 4 + 15) / 16 * 16;
+  a.o_bytes = parts * heads * rows * d * 4;
   return a;
 }
 
@@ -781,21 +784,21 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
                int64_t positions, int window) {
   Plan a = {};
   const int64_t rows = (int64_t)(list_len > 0 ? 1 : max_new) * group;
+  const int64_t part_rows = (max_new < tokens ? (int64_t)max_new : tokens) * group;
   a.prefill = list_len == 0 && rows >= prefill_from(d, (int64_t)requests * heads, sms);
   if (a.prefill) {
-    a.cta_rows = prefill_rows(d);
-    a.row_tiles = (int)((rows + a.cta_rows - 1) / a.cta_rows);
+    a.row_tiles = (int)((rows + prefill_rows(d) - 1) / prefill_rows(d));
     a.min_chunk = kPrefillMinChunk;
-    // one CTA an SM: chunks only where the row tiles alone do not fill the SMs (their joins cost more than an
-    // uneven second wave: 256 row tiles of 16384 positions take 511 us whole, 690 us in halves)
+    // one CTA an SM: chunks only where one request's row tiles alone do not fill the SMs (their joins cost more
+    // than an uneven second wave: 256 row tiles of 16384 positions take 511 us whole, 690 us in halves). With
+    // several requests the chunks are cut from all their positions together, so the long ones alone are cut.
     const int64_t units = (int64_t)heads * a.row_tiles;
     a.target = (int)((sms + units - 1) / units);
-    return finish_plan(a, heads, d, requests);
+    return finish_plan(a, heads, d, requests, part_rows);
   }
   const int most = d == 256 ? 2 : 4;
   a.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : most;
   if (a.nt > most) a.nt = most;
-  a.cta_rows = a.nt * 8;
   a.row_tiles = (int)((rows + a.nt * 8 - 1) / (a.nt * 8));
   a.min_chunk = kMinChunk;
   const int slots = sms * rows_kernel_of(d, a.nt, list_len > 0).per_sm;
@@ -815,14 +818,14 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
   if (list_len > 0 || whole_ones || seen <= (int64_t)parts * kPartPositions) {
     a.parts = parts;
     a.flats = list_len > 0 ? tokens : requests;
-    return finish_plan(a, heads, d, requests);
+    return finish_plan(a, heads, d, requests, part_rows);
   }
   // Several chunks a slot where requests differ in length, so that the last ones to end are short (64 ragged
   // requests: 324, 279, 271, 269 us with 1, 2, 3, 4); one request's chunks are alike, and one
   // wave of them has the fewest starts and joins (262144 positions at D = 256: 82 us, 96 with 2).
   const int64_t target = ((int64_t)slots * (requests == 1 ? 1 : 4) + units - 1) / units;
   a.target = (int)(target < 1 ? 1 : target);
-  return finish_plan(a, heads, d, requests);
+  return finish_plan(a, heads, d, requests, part_rows);
 }
 
 lt_status device_of(int* dev, int* sms) {
@@ -938,6 +941,8 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
   p.target = plan.target;
   p.min_chunk = plan.min_chunk;
   p.row_tiles = plan.row_tiles;
+  p.max_new = max_new;
+  p.part_rows = (int32_t)plan.part_rows;
   p.align = plan.prefill ? 128 : kTile;
   p.bf16 = dtype == LT_DTYPE_BF16;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -964,7 +969,6 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
   const void* func = head_dim == 64    ? reinterpret_cast<const void*>(&join_kernel<64>)
                      : head_dim == 128 ? reinterpret_cast<const void*>(&join_kernel<128>)
                                        : reinterpret_cast<const void*>(&join_kernel<256>);
-  int rows_per_cta = plan.cta_rows;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)joins);
   cfg.blockDim = dim3(kJoinThreads);
@@ -974,7 +978,7 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  void* a[] = {&p, &rows_per_cta};
+  void* a[] = {&p};
   return cudaLaunchKernelExC(&cfg, func, a) == cudaSuccess ? LT_OK : LT_ERR_CUDA;
 }
 

@@ -23,12 +23,14 @@ struct AttentionParams {
   const int32_t* positions;
   void* out;
   float* lse;
-  int2* plan;       // [requests]: first chunk, chunks
-  float* part_lse;  // [chunk][kv head][row], in units of log 2
-  float* part_o;    // [chunk][kv head][row][D], divided by the part's own sum
+  int2* plan;       // [requests]: first part, chunks
+  float* part_lse;  // [part][kv head][row], in units of log 2; parts: the chunks of requests that have several
+  float* part_o;    // [part][kv head][row][D], divided by the part's own sum
   int64_t q_token, q_head;
   int32_t pages, tokens, requests, width, heads, group, shift, list_len, window;
   int32_t parts, target, min_chunk, row_tiles, bf16;
+  int32_t max_new;
+  int32_t part_rows;  // query rows of a part: max_new * group
   int32_t align;    // positions at which chunks and windows start: multiples of this (32 or 128)
   float scale_log2;
 };
@@ -37,6 +39,7 @@ struct Request {
   int length;   // positions in the cache
   int first;    // its first query's row
   int queries;
+  int computed;  // the first max_new of them
   int low;      // the first position that any of its queries sees, rounded down to p.align
   int span;     // length - low
 };
@@ -53,6 +56,7 @@ __device__ __forceinline__ Request request_of(const AttentionParams& p, int r) {
   }
   q.first = first;
   q.queries = max(end - first, 0);
+  q.computed = min(q.queries, p.max_new);
   q.low = 0;
   if (p.window > 0) q.low = (int)(max((int64_t)q.length - q.queries + 1 - p.window, (int64_t)0) / p.align * p.align);
   if (q.low > q.length) q.low = q.length / p.align * p.align;
@@ -63,7 +67,10 @@ __device__ __forceinline__ Request request_of(const AttentionParams& p, int r) {
 // Which request and chunk this CTA has: the requests' positions cut into chunks of one size, flat.
 struct Place {
   int request, split, base, count;  // count chunks, the first with flat number base
+  int part;                         // where they are several: the number of the first among such chunks
 };
+// Chunks and, above them, those of requests that have several: one number, so that one scan adds up both.
+__device__ __forceinline__ int64_t both_counts(int n) { return n > 1 ? ((int64_t)n << 32) + n : n; }
 
 // The positions of each of a request's chunks: alike, and multiples of p.align.
 __device__ __forceinline__ int64_t chunk_of(const AttentionParams& p, const Request& q, int count) {
@@ -87,17 +94,20 @@ __device__ __forceinline__ bool find_place_in_warp(const AttentionParams& p, int
   chunk = (chunk + p.align - 1) / p.align * p.align;
   if (chunk < p.min_chunk) chunk = p.min_chunk;
   const int n = q.queries > 0 ? max(1, (int)((q.span + chunk - 1) / chunk)) : 0;
-  int end = n;
+  const int64_t own = both_counts(n);
+  int64_t sum = own;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int u = __shfl_up_sync(~0u, end, d);
-    if (lane >= d) end += u;
+    const int64_t u = __shfl_up_sync(~0u, sum, d);
+    if (lane >= d) sum += u;
   }
-  const uint32_t here = __ballot_sync(~0u, flat >= end - n && flat < end);
+  const int begin = (int)(sum - own);
+  const uint32_t here = __ballot_sync(~0u, flat >= begin && flat < begin + n);
   if (here == 0) return false;
   const int r = __ffs(here) - 1;
   out->request = r;
-  out->base = __shfl_sync(~0u, end - n, r);
+  out->base = __shfl_sync(~0u, begin, r);
+  out->part = __shfl_sync(~0u, (int)((sum - own) >> 32), r);
   out->count = __shfl_sync(~0u, n, r);
   out->split = flat - out->base;
   return true;
@@ -124,7 +134,7 @@ __device__ __forceinline__ bool find_place(const AttentionParams& p, int flat, P
   int64_t chunk = (total + p.target - 1) / p.target;
   chunk = (chunk + p.align - 1) / p.align * p.align;
   if (chunk < p.min_chunk) chunk = p.min_chunk;
-  int base = 0;
+  int64_t base = 0;
   for (int first = 0; first < p.requests; first += kCta) {
     const int r = first + tid;
     int n = 0;
@@ -132,30 +142,32 @@ __device__ __forceinline__ bool find_place(const AttentionParams& p, int flat, P
       const Request q = request_of(p, r);
       n = q.queries > 0 ? max(1, (int)((q.span + chunk - 1) / chunk)) : 0;
     }
-    int end = n;
+    const int64_t own = both_counts(n);
+    int64_t end = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(~0u, end, d);
+      const int64_t u = __shfl_up_sync(~0u, end, d);
       if ((tid & 31) >= d) end += u;
     }
     __syncthreads();
     if ((tid & 31) == 31) sums[tid >> 5] = end;
     __syncthreads();
-    int all = 0;
+    int64_t all = 0;
 #pragma unroll 4
     for (int w = 0; w < kCta / 32; ++w) {
-      if (w < (tid >> 5)) end += (int)sums[w];
-      all += (int)sums[w];
+      if (w < (tid >> 5)) end += sums[w];
+      all += sums[w];
     }
-    const int begin = base + end - n;
+    const int begin = (int)(base + end - own);
     if (flat >= begin && flat < begin + n) {
       found->request = r;
       found->split = flat - begin;
       found->base = begin;
       found->count = n;
+      found->part = (int)((base + end - own) >> 32);
     }
     base += all;
-    if (base > flat) break;  // (the same for all threads)
+    if ((int)base > flat) break;  // (the same for all threads)
   }
   __syncthreads();
   *out = *found;

@@ -287,7 +287,7 @@ __device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
 // What a CTA works on: row0 .. of the request's query rows, positions [from, to).
 struct Job {
   Request rq;
-  int request, head, row_tile, flat, rows, row0, from, to, tiles;
+  int request, head, row_tile, flat, part, rows, row0, from, to, tiles;
   bool two, final_here;
 };
 
@@ -480,7 +480,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   float log2_sum = sum == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m - kShift) + __log2f(sum);
   if (!ok) log2_sum = NAN;
-  const int64_t part = (((int64_t)job.flat * p.heads + job.head) * p.row_tiles + job.row_tile) * (Smem<D>::kRowTiles * 128) + which * 128;
+  const int64_t part = ((int64_t)job.part * p.heads + job.head) * p.part_rows + job.row0 + which * 128;
   const int per_pass = job.final_here ? D : D / 2;  // columns that fit the tile's rows
 #pragma unroll 1
   for (int c0 = 0; c0 < D; c0 += per_pass) {
@@ -775,13 +775,14 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   if (!find_place<kCta>(p, job.flat, &pl, sh->sums, &sh->found)) return;
   job.request = pl.request;
   job.rq = request_of(p, pl.request);
-  job.rows = job.rq.queries * p.group;
+  job.rows = job.rq.computed * p.group;
+  job.part = pl.part + pl.split;
   constexpr int kRows = Smem<D>::kRowTiles * 128;
   job.row_tile = min((job.rows + kRows - 1) / kRows, p.row_tiles) - 1 - nth;
   if (job.row_tile < 0) return;
   job.final_here = pl.count == 1;
   if (job.flat == pl.base && job.head == 0 && job.row_tile == 0 && tid == 0 && p.plan != nullptr)
-    p.plan[pl.request] = make_int2(pl.base, pl.count);
+    p.plan[pl.request] = make_int2(pl.part, pl.count);
   job.row0 = job.row_tile * kRows;
   job.two = kRows > 128 && job.rows - job.row0 > 128;
   {

@@ -727,3 +727,72 @@ def test_stored_rows_are_the_oracles_byte_for_byte(dtype, dim):
             assert np.array_equal(got[i, :, :dim], want[:, :dim]), f"codes of token {i}"
             assert np.array_equal(got[i, :, scales].copy().view(np.float16), want[:, scales].copy().view(np.float16), equal_nan=True)
             assert np.array_equal(got[i, :, dim + dim // 8:], want[:, dim + dim // 8:]), f"padding of token {i}"
+
+
+def _workspace(tokens, q_heads, kv_heads, dim, requests, max_new, positions, window=0):
+    import ctypes
+
+    import sparse_attention_indexer_lt_gb300 as lt
+    need = ctypes.c_int64(-1)
+    assert lt.load().lt_kv4_workspace(tokens, q_heads, kv_heads, dim, requests, max_new, 0, positions, window, ctypes.byref(need)) == 0
+    return need.value
+
+
+@pytest.mark.parametrize("tokens,q_heads,kv_heads,dim,requests,max_new", [
+    (1215, 32, 8, 128, 64, 1152), (1407, 32, 8, 128, 256, 1152), (5000, 32, 8, 128, 1000, 500), (768, 128, 8, 256, 256, 3),
+    (320, 64, 8, 128, 64, 5), (4000, 16, 4, 64, 6, 1500)])
+def test_workspace_is_for_the_parts_that_can_be(tokens, q_heads, kv_heads, dim, requests, max_new):
+    """With c chunks wanted for all the requests a chunk has at least a cth of their positions, so the requests that
+    are longer than a chunk are cut into fewer than 2 c parts, each of the most query rows that a request has: the
+    scratch memory does not grow with the requests that stay whole."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = max_new * (q_heads // kv_heads)
+    tile = 128 if dim == 256 else 256
+    wanted = -(-sms // (kv_heads * -(-rows // tile)))
+    parts = 2 * wanted * kv_heads * rows
+    assert _workspace(tokens, q_heads, kv_heads, dim, requests, max_new, 65536) <= parts * (dim + 1) * 4 + 8 * requests + 64
+
+
+@pytest.mark.parametrize("lengths,new,dim,group", [
+    ([5, 2600, 40, 1700, 0, 1300, 7], [3, 20, 1, 33, 0, 17, 7], 64, 1),           # many rows, several requests in parts among whole ones
+    ([700, 1, 1300, 9], [19, 1, 40, 2], 128, 2), ([9, 900, 3, 700], [2, 17, 3, 30], 256, 1),
+    ([2100, 30, 1600], [150, 3, 90], 64, 3),                                      # (more than one row tile)
+    ([40] * 20 + [3000] + [50] * 60 + [2500, 1, 600] + [60] * 70, [1] * 154, 64, 2),  # few rows, more requests than a CTA has threads
+    ([17000] + [30] * 20 + [9000, 5], [2] + [1] * 20 + [2, 2], 64, 2)])
+def test_requests_in_parts_among_whole_ones(lengths, new, dim, group):
+    p = Problem(lengths, new, 1, group, dim, 64, "f16", seed=sum(new), extra_width=230)
+    out, lse = p.run()
+    p.check(out, lse)
+    again, lse2 = p.run(max_new=p.max_new + 3)
+    p.check(again, lse2)
+
+
+def test_a_long_chunk_beside_requests_of_one_token():
+    """A step that mixes a prefill chunk with decoding requests, scratch memory given at its stated size."""
+    new = [1] * 10 + [70] + [1] * 30
+    lengths = [(r * 53) % 300 + 1 for r in range(10)] + [1400] + [(r * 31) % 200 + 1 for r in range(30)]
+    for dim, heads, group in ((64, 2, 2), (256, 1, 2)):
+        p = Problem(lengths, new, heads, group, dim, 16, "bf16", seed=dim)
+        need = _workspace(sum(new), heads * group, heads, dim, len(new), 70, p.table.shape[1] * 16)
+        space = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        p.check(*p.run(workspace=space[:need]))
+        assert (space[need:] == 0x5A).all(), "written past the scratch memory"
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_queries_past_max_new_are_not_computed(dim):
+    """A max_new below a request's queries: its rows from there on are not touched, and nobody else's are harmed."""
+    lengths, new = [1500, 30, 1300], [40, 3, 33]
+    p = Problem(lengths, new, 1, 2, dim, 64, "f16", seed=dim)
+    want, want_lse = p.run(max_new=40)
+    out, lse = torch.full_like(want, 7.0), torch.full_like(want_lse, 7.0)
+    need = _workspace(sum(new), 2, 1, dim, 3, 25, p.table.shape[1] * 64)
+    space = torch.full((need + (1 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    p.run(max_new=25, out=out, out_lse=lse, workspace=space[:need])
+    for first, count in ((0, 40), (40, 3), (43, 33)):
+        got = min(count, 25)
+        a, b = out[first:first + got].float(), want[first:first + got].float()
+        assert ((a - b).abs() <= 2.0 ** -10 * b.abs() + 2.0 ** -10 * 6 * 0.35 * 2.72).all()
+        assert (lse[first:first + got] - want_lse[first:first + got]).abs().max() <= 1e-4
+        assert (out[first + got:first + count] == 7.0).all() and (lse[first + got:first + count] == 7.0).all()
+    assert (space[need:] == 0x5A).all()
