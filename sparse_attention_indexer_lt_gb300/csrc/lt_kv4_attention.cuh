@@ -222,6 +222,11 @@ __device__ __forceinline__ uint32_t unfit_halves(uint32_t h) {
   return ((h & 0x7FFFu) > 0x7154u ? 0xFFFFu : 0u) | ((h & 0x7FFF0000u) > 0x71540000u ? 0xFFFF0000u : 0u);
 }
 
+// 0 times each half of the word: zero, or NaN where it is an infinity or a NaN.
+__device__ __forceinline__ uint32_t zero_times_halves(uint32_t h) {
+  return ((h & 0x7C00u) == 0x7C00u ? 0x7FFFu : 0u) | ((h & 0x7C000000u) == 0x7C000000u ? 0x7FFF0000u : 0u);
+}
+
 // bf16 rows become fp16 rows times a power of two: the one that brings the row's largest (magnitude's
 // fp32 word `big`) into [2^14, 2^15), so nothing overflows and what lies within 2^-28 of the
 // largest stays exact. Rows of zeros, or with an infinity or NaN, are taken as they are.

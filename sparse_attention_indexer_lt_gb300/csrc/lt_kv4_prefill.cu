@@ -329,8 +329,10 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
       mul = bf16_row_power(big);
       factor /= mul;  // (exact: a power of two)
     }
-    // logits are compared before they are scaled: a negative scale turns the row round instead
-    const uint32_t flip = factor < 0.0f ? 0x80008000u : 0u, keep = factor == 0.0f ? 0u : ~0u;
+    // logits are compared before they are scaled: a negative scale turns the row round instead, and a scale of
+    // zero makes its channels zeros, or NaN where they are not finite
+    const uint32_t flip = factor < 0.0f ? 0x80008000u : 0u;
+    const bool zero = factor == 0.0f;
     factor = factor == 0.0f ? 1.0f : fabsf(factor);
 #pragma unroll 1
     for (int c0 = 0; c0 < kChunks; c0 += 4) {
@@ -341,10 +343,17 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
         const uint4 v = *at;
         w[4 * c] = v.x, w[4 * c + 1] = v.y, w[4 * c + 2] = v.z, w[4 * c + 3] = v.w;
 #pragma unroll
-        for (int e = 4 * c; e < 4 * c + 4; ++e) w[e] = ((p.bf16 ? bf16_pair_to_half(w[e], mul) : w[e]) ^ flip) & keep;
+        for (int e = 4 * c; e < 4 * c + 4; ++e) w[e] = (p.bf16 ? bf16_pair_to_half(w[e], mul) : w[e]) ^ flip;
+        if (zero) {
+#pragma unroll
+          for (int e = 4 * c; e < 4 * c + 4; ++e) w[e] = zero_times_halves(w[e]);
+        }
         if (!Smem<D>::kOne) *at = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
       }
-      if constexpr (Smem<D>::kOne) tmem_st16(sh->tmem + ((uint32_t)(warp * 32) << 16) + kQueryColumn + c0 * 4, w);
+      if constexpr (Smem<D>::kOne) {
+        __syncwarp();  // (`zero` may differ from row to row, and the store is the whole warp's)
+        tmem_st16(sh->tmem + ((uint32_t)(warp * 32) << 16) + kQueryColumn + c0 * 4, w);
+      }
     }
     if constexpr (Smem<D>::kOne) {
       tmem_wait_st();

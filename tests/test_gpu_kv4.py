@@ -796,3 +796,16 @@ def test_queries_past_max_new_are_not_computed(dim):
         assert (lse[first:first + got] - want_lse[first:first + got]).abs().max() <= 1e-4
         assert (out[first + got:first + count] == 7.0).all() and (lse[first + got:first + count] == 7.0).all()
     assert (space[need:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("dim,new", [(64, 2), (64, 70), (128, 70), (256, 70)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_scale_of_zero_keeps_what_is_not_finite(dim, new, dtype):
+    """0 * NaN and 0 * inf are NaN: the row of such a query, and no other."""
+    p = Problem([100], [new], 1, 1, dim, 16, dtype, seed=dim + new)
+    clean, clean_lse = p.run(scale=0.0)
+    p.check(clean, clean_lse, scale=0.0)
+    p.q[0, 0, 5], p.q[1, 0, dim - 1] = float("nan"), float("-inf")
+    out, lse = p.run(scale=0.0)
+    assert torch.isnan(out[:2]).all() and torch.isnan(lse[:2]).all()
+    assert torch.equal(out[2:], clean[2:]) and torch.equal(lse[2:], clean_lse[2:])
