@@ -25,13 +25,15 @@
 // after a shift by 2^6 that keeps small ones normal; the sums that divide them are
 // fp32 and of the unrounded weights.
 //
-// What bounds it: issue. A tile of 32 positions of D = 128 takes some 725 warp
-// instructions (858 before the maximum became lazy and a CTA's start and end were
-// shortened), of which unpacking and scaling are 450; more resident warps or deeper rings change
+// What bounds it: issue, and the waits between a warp's own instructions. A tile of 32 positions of D = 128
+// takes some 725 warp instructions (858 before the maximum became lazy and a CTA's start and end were
+// shortened), of which unpacking and scaling are 450; 2.50 are issued a clock and SM, 62% of what its schedulers
+// could (2.17, 54%, with heads of 256, whose 168 registers leave 12 warps). More resident warps or deeper rings change
 // nothing (5 CTAs an SM with 2 stages 272 us, 4 with 2 or 3 267 to 269, 3 with 4 281, on the 64 ragged
 // requests). Measured (4.5-bit rows read once): 64 requests of 2048 to 65536 positions,
-// 4 kv heads of 128, 256 us, 4.9 TB/s; one request of 262144 positions, 4 heads of 256,
-// 66 us, 4.6 TB/s; the copy rate is 6.8.
+// 4 kv heads of 128, 253 us, 4.9 TB/s; one request of 262144 positions, 4 heads of 256,
+// 65 us, 4.7 TB/s; the copy rate is 6.8. The widest instances (32 rows; 16 with heads of 256), which serve 17 to
+// 64 rows, do not fit the registers: they spill 468 bytes a thread with heads of 128, 252 with 64, 232 with 256.
 
 #include <mutex>
 

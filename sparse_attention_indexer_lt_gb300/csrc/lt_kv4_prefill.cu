@@ -81,6 +81,7 @@ struct Smem {
   static constexpr int kUnpackers = kOne ? 256 : 128;      // threads that unpack: row tile B's warpgroup is free to
   static constexpr int kParts = kTok / kPart;
   static constexpr int kRing = 512 / kTok;                 // tiles whose notes are kept
+  static_assert(kSlots / 2 * kParts + kRaw < kRing * kParts, "notes are read before they are written over");
   static constexpr int kQHalf = 128 * 128;                 // 128 rows by 64 channels, swizzled
   static constexpr int kQTile = kQHalf * (D / 64);
   static constexpr int kHalf = kTok * 128;                 // a tile's positions by 64 channels
@@ -99,8 +100,9 @@ struct Shared {
   uint64_t kv_empty[kSlots];
   uint64_t q_full, s_full[2], o_full[2];
   uint64_t o_tile;  // with one row tile: a position tile's second product is done
-  // notes of the tiles in work, a ring of 512 positions (they are made at most three tiles of 128, or six of
-  // 64, ahead of the softmax: slots that its products give back hold the rest up)
+  // notes of the tiles in work, a ring of 512 positions, eight packed stages. They are made up to seven stages
+  // ahead of the softmax (Smem's assertion): while it reads tile i's, tile i's values are not given back, so the
+  // unpackers have released at most the first stage of tile i + kSlots / 2, and the copies run kRaw stages on from there
   alignas(16) uint32_t valid[16];     // positions on a page of the cache and in range, as bits
   alignas(16) uint32_t nan_rows[16];  // positions with a value scale that is NaN or outside the format
   uint8_t nan_groups[512];

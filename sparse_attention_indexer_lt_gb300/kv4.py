@@ -128,8 +128,8 @@ def _check_table(block_table, index, n):
 def page_release(lengths: torch.Tensor, finished: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
                  num_free: torch.Tensor, page_size: int, *, out_lengths: torch.Tensor | None = None,
                  out_num_free: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
-    """Gives the pages of finished requests (bool or uint8 [requests]) back to free_pages (in place);
-    returns (lengths, num_free): 0 for the finished requests, and the new number of free pages."""
+    """Gives the pages of finished requests (bool or uint8 [requests]) back to free_pages (in place; cells of
+    block_table below 0 hold no page); returns (lengths, num_free): 0 for the finished requests, and the new number of free pages."""
     _want("lengths", lengths, torch.int32)
     index, n = lengths.get_device(), lengths.numel()
     if not isinstance(finished, torch.Tensor) or finished.dtype not in (torch.bool, torch.uint8):
