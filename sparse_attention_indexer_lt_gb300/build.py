@@ -31,10 +31,13 @@ def nvcc() -> str:
 
 
 def source_hash() -> str:
-    """Hash of the CUDA sources and the C header (ties a profile to the code it measured)."""
+    """Hash of the CUDA sources and C headers of the top-k and the compressor (ties a profile of their kernels to
+    the code it measured). The 4-bit cache's files are no part of those kernels: a change there leaves it."""
     import hashlib
     h = hashlib.sha256()
     for f in sorted(list(CSRC.glob("*")) + list(INCLUDE.glob("*.h"))):
+        if f.name.startswith(("lt_kv4", "lt_pages")):
+            continue
         h.update(f.name.encode())
         h.update(f.read_bytes())
     return h.hexdigest()[:16]
