@@ -760,7 +760,8 @@ constexpr int kPrefillMinChunk = 512;
 //   D = 256, 4 kv heads: 1 request of 8192 positions 32 and 35 with 32 rows; 4 of them 48 and 39, with 64 rows 49 and
 //   70; 64 requests of 2048 94 and 66 with 20 rows, 101 and 117 with 40
 // so from two row tiles of this kernel on (D = 64: from three), and with few CTAs from 17 rows (D = 256, whose
-// tiles have fewer rows: with very few).
+// tiles have fewer rows: with very few). The rows are those of max_new queries, for all requests of the call:
+// where one has many queries and others one, these are computed there, too (not measured).
 int prefill_from(int d, int64_t units, int sms) {
   return units * (d == 256 ? 16 : 4) <= sms ? 17 : d == 64 ? 65 : 33;
 }
@@ -805,7 +806,8 @@ Plan make_plan(int sms, int64_t tokens, int heads, int group, int d, int request
   a.min_chunk = kMinChunk;
   const int slots = sms * rows_kernel_of(d, a.nt, list_len > 0).per_sm;
   const int64_t units = (int64_t)heads * a.row_tiles;
-  // what one query (a request's queries) can see
+  // what one query (a request's queries) can see at most: lengths are known on the device alone, so a table wider
+  // than the requests counts as if they filled it
   int64_t seen = list_len > 0 ? list_len : positions;
   if (list_len == 0 && window > 0 && (int64_t)window + max_new + kTile < seen) seen = (int64_t)window + max_new + kTile;
   const int64_t whole = (list_len > 0 ? tokens : (int64_t)requests) * units;
