@@ -116,6 +116,43 @@ lt_status lt_kv4_store(const void* k, const void* v, int32_t dtype, int64_t toke
                        void* cache, int64_t pages, int32_t page_size, void* stream);
 
 /*
+ * lt_kv4_append -- turns queries and keys by their positions and stores keys and
+ * values: the way of a step's new tokens into the cache.
+ *
+ * Of the first rotary_dim channels of a head, pair i (channels i and i + rotary_dim / 2;
+ * 2 i and 2 i + 1 where `interleaved` is not 0) turns by the angle whose cosine and sine the
+ * tables hold for the token's position:
+ *
+ *   a' = a c - b s,   b' = b c + a s
+ *
+ * each product and each sum rounded to 32 bits. The other channels stay. Queries are
+ * rounded to their type; keys are quantised from the 32-bit numbers, values as
+ * lt_kv4_store does.
+ *
+ *   q           [tokens][q_heads][head_dim], or NULL with q_heads 0
+ *   k, v        [tokens][kv_heads][head_dim]; all of `dtype` (LT_DTYPE_F32, _BF16 or _F16),
+ *               channels contiguous, the strides of tokens and heads in elements
+ *   cos_table,  float [max_positions][rotary_dim / 2], 16-byte aligned; rotary_dim is a
+ *   sin_table   multiple of 16, at most head_dim
+ *   positions   int32 [tokens]: where each token lies in its request. A token whose position is
+ *               outside [0, max_positions) (-1, past a step's last token) is passed over:
+ *               nothing is stored and its row of out_q stays as it was
+ *   slots       int64 [tokens]; a slot outside [0, pages * page_size) stores nothing (its
+ *               query is turned all the same). No two tokens have the same slot: what it
+ *               holds then is not specified
+ *   out_q       like q, strides of its own; it may be q itself (with q's strides), else
+ *               it overlaps nothing
+ */
+lt_status lt_kv4_append(const void* q, const void* k, const void* v, int32_t dtype, int64_t tokens,
+                        int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t q_token_stride,
+                        int64_t q_head_stride, int64_t k_token_stride, int64_t k_head_stride,
+                        int64_t v_token_stride, int64_t v_head_stride, const float* cos_table,
+                        const float* sin_table, int32_t max_positions, int32_t rotary_dim,
+                        int32_t interleaved, const int32_t* positions, const int64_t* slots, void* cache,
+                        int64_t pages, int32_t page_size, void* out_q, int64_t out_token_stride,
+                        int64_t out_head_stride, void* stream);
+
+/*
  * lt_kv4_load -- the numbers that the slots stand for: k, v
  * [tokens][kv_heads][head_dim] of `dtype`, contiguous; exact in fp16 and fp32,
  * rounded to nearest even in bf16; zeros for a slot outside the cache.

@@ -52,6 +52,20 @@ def quantise(x):
     return scales.reshape(*x.shape[:-1], -1), codes.reshape(x.shape)
 
 
+def rotate(x, cos, sin, interleaved=False):
+    """x [tokens, heads, D] (numbers of 32 bits or fewer) turned by the tokens' angles cos, sin [tokens, pairs]: each product
+    (exact in 64 bits) and each sum rounded to 32 bits, in float32."""
+    x, cos, sin = (np.asarray(a, np.float64) for a in (x, cos, sin))
+    out, half = x.copy(), cos.shape[1]
+    with np.errstate(invalid="ignore", over="ignore"):
+        for i in range(half):
+            m, n = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+            c, s = cos[:, i, None], sin[:, i, None]
+            ac, bs, bc, as_ = ((y * z).astype(np.float32) for y, z in ((x[..., m], c), (x[..., n], s), (x[..., n], c), (x[..., m], s)))
+            out[..., m], out[..., n] = ac - bs, bc + as_  # float32 sums
+    return out.astype(np.float32)
+
+
 def values(scales, codes):
     with np.errstate(invalid="ignore"):  # NaN scales
         return _values(scales, codes)

@@ -5,7 +5,7 @@ cache's format and every argument. A serving step:
 
     kept, num_free = page_release(lengths, finished, table, free_pages, num_free, page_size)
     step = page_extend(kept, new_tokens, table, free_pages, num_free, page_size, max_tokens)
-    kv4_store(k, v, cache, step.slots)
+    q = kv4_append(q, k, v, cache, step.slots, step.positions, cos, sin)  # or kv4_store(k, v, cache, step.slots)
     out = kv4_attention(q, cache, table, step.lengths, starts=step.starts, max_new=max_new)
 
 and, over the positions that the indexer's top-k kept,
@@ -199,6 +199,64 @@ def kv4_store(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torc
     _check_slots(slots, index, tokens)
     _call("lt_kv4_store", index, k.data_ptr(), v.data_ptr(), dtype, tokens, heads, dim, ks[0], ks[1], vs[0], vs[1],
           slots.data_ptr(), cache.data_ptr(), pages, page_size, _raw_stream(stream, index))
+
+
+def _check_table_of_angles(name, t, index, half):
+    _want(name, t, torch.float32, index)
+    if t.dim() != 2 or (half is not None and t.shape != half):
+        raise ValueError(f"{name} must be float32 [positions, channel pairs], the same for cosines and sines")
+    return t.shape
+
+
+def kv4_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
+               positions: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, *, interleaved: bool = False,
+               out_q: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor | None:
+    """Turns q [tokens, q_heads, head_dim] and k [tokens, kv_heads, head_dim] by the tokens' positions (int32
+    [tokens]) and quantises k and v into the cache rows that slots (int64 [tokens]; -1 skips) name; returns
+    the turned queries.
+
+    cos, sin: float32 [max_positions, pairs], of the first 2 * pairs channels (a multiple of 16): channel i pairs
+    with i + pairs, or neighbours with each other where interleaved. q, k and v have one type (float32, bfloat16
+    or float16) and any strides of tokens and heads. Tokens whose position is outside the tables are passed
+    over, their rows of out_q stay as they were. out_q may be q; q may be None (keys and values alone).
+    """
+    pages, heads, page_size, dim, index = _check_cache(cache)
+    for name, t in (("k", k), ("v", v)) if q is None else (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.get_device() != index or t.dim() != 3 or t.shape[2] != dim or (name != "q" and t.shape[1] != heads):
+            raise ValueError(f"{name} must be [tokens, {'heads' if name == 'q' else heads}, {dim}] on cuda:{index}")
+    dtype, tokens = _ALL.get(k.dtype), k.shape[0]
+    if dtype is None or v.dtype != k.dtype or v.shape != k.shape or (q is not None and (q.dtype != k.dtype or q.shape[0] != tokens)):
+        raise ValueError("q, k and v must have one number of tokens and one type: float32, bfloat16 or float16")
+    ks, vs = k.stride(), v.stride()
+    if tokens > 0 and (ks[2] != 1 or vs[2] != 1 or (q is not None and q.stride(2) != 1)):
+        raise ValueError("the channels of q, k and v must be contiguous")
+    _check_slots(slots, index, tokens)
+    _want("positions", positions, torch.int32, index, (tokens,))
+    shape = _check_table_of_angles("cos", cos, index, None)
+    _check_table_of_angles("sin", sin, index, shape)
+    if shape[1] == 0 or shape[1] % 8 or 2 * shape[1] > dim:
+        raise ValueError(f"cos and sin must have a multiple of 8 channel pairs, at most {dim // 2}, got {shape[1]}")
+    max_positions = _int32("the tables' positions", shape[0], 0)
+    qs = os = (0, 0)
+    q_heads = 0
+    if q is None:
+        if out_q is not None:
+            raise ValueError("out_q needs q")
+    else:
+        q_heads, qs = q.shape[1], q.stride()
+        if out_q is None:
+            out_q = _result("out_q", None, q.shape, q.dtype, q, stream)
+        elif not isinstance(out_q, torch.Tensor) or not out_q.is_cuda or out_q.get_device() != index or out_q.dtype != q.dtype \
+                or out_q.shape != q.shape or (tokens > 0 and out_q.stride(2) != 1):
+            raise ValueError(f"out_q must be a {q.dtype} tensor of shape {tuple(q.shape)} on cuda:{index}, its channels contiguous")
+        os = out_q.stride()
+    _call("lt_kv4_append", index, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype, tokens, q_heads, heads,
+          dim, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], cos.data_ptr(), sin.data_ptr(), max_positions, 2 * shape[1],
+          int(bool(interleaved)), positions.data_ptr(), slots.data_ptr(), cache.data_ptr(), pages, page_size,
+          None if q is None else out_q.data_ptr(), os[0], os[1], _raw_stream(stream, index))
+    return out_q
 
 
 def kv4_load(cache: torch.Tensor, slots: torch.Tensor, *, dtype: torch.dtype = torch.float16,
