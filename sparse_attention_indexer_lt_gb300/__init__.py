@@ -22,7 +22,7 @@ import torch
 __all__ = ["topk", "topk_blocked", "topk_candidates", "compress", "compress_decode", "plan", "DTYPE_F32", "DTYPE_BF16", "load", "library_path", "LtError", "NUM_COUNTERS",
            "status_string", "version", "PlanInfo", "KERNEL_AUTO", "KERNEL_RESIDENT", "KERNEL_STREAM",
            "KERNEL_LISTED", "plan_candidates", "DTYPE_F16", "kv4_cache", "kv4_row_bytes", "kv4_store", "kv4_append", "kv4_load",
-           "kv4_attention", "page_extend", "page_release", "PageStep"]
+           "kv4_attention", "page_extend", "page_release", "PageStep", "w4_quantise", "w4_linear"]
 
 _LIB_PATH = Path(__file__).resolve().parent / "liblt_topk.so"
 _lib = None
@@ -102,8 +102,11 @@ def load() -> ctypes.CDLL:
     lib.lt_kv4_attention.argtypes = [vp, i32, i64, i32, i32, i32, i64, i64, vp, i64, i32, vp, i32, vp, i32, vp, i32,
                                      vp, i32, i32, ctypes.c_float, vp, vp, vp, i64, vp]
     lib.lt_kv4_workspace.argtypes = [i64, i32, i32, i32, i32, i32, i32, i64, i32, vp]
+    lib.lt_w4_quantise.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+    lib.lt_w4_linear.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, i64, vp]
+    lib.lt_w4_workspace.argtypes = [i64, i64, i64, vp]
     for name in ("lt_page_release", "lt_page_extend", "lt_kv4_store", "lt_kv4_append", "lt_kv4_load", "lt_kv4_attention",
-                 "lt_kv4_workspace"):
+                 "lt_kv4_workspace", "lt_w4_quantise", "lt_w4_linear", "lt_w4_workspace"):
         getattr(lib, name).restype = ctypes.c_int
     lib.lt_test_inject.argtypes = [i32, i32]
     lib.lt_test_inject.restype = ctypes.c_int
@@ -375,3 +378,4 @@ def plan_candidates(rows: int, row_stride: int, block: int, n_cand: int, k: int,
 
 from .kv4 import (DTYPE_F16, PageStep, kv4_append, kv4_attention, kv4_cache, kv4_load, kv4_row_bytes, kv4_store,  # noqa: E402
                   page_extend, page_release)
+from .w4 import w4_linear, w4_quantise  # noqa: E402

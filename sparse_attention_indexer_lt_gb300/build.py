@@ -18,7 +18,7 @@ BUILD = PKG / "_build"
 LIB = PKG / "liblt_topk.so"
 SOURCES = ["lt_api.cu", "lt_topk_kernels.cu", "lt_stream_kernels.cu", "lt_blocked_256_f32.cu",
            "lt_blocked_256_bf16.cu", "lt_blocked_512_f32.cu", "lt_blocked_512_bf16.cu", "lt_listed_kernels.cu", "lt_compress.cu",
-           "lt_pages.cu", "lt_kv4_cache.cu", "lt_kv4_append.cu", "lt_kv4_attention.cu", "lt_kv4_prefill.cu"]
+           "lt_pages.cu", "lt_kv4_cache.cu", "lt_kv4_append.cu", "lt_kv4_attention.cu", "lt_kv4_prefill.cu", "lt_w4_linear.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", f"-I{INCLUDE}"]
 
@@ -32,11 +32,12 @@ def nvcc() -> str:
 
 def source_hash() -> str:
     """Hash of the CUDA sources and C headers of the top-k and the compressor (ties a profile of their kernels to
-    the code it measured). The 4-bit cache's files are no part of those kernels: a change there leaves it."""
+    the code it measured). The files of the 4-bit cache and weights are no part of those kernels: a change there
+    leaves it."""
     import hashlib
     h = hashlib.sha256()
     for f in sorted(list(CSRC.glob("*")) + list(INCLUDE.glob("*.h"))):
-        if f.name.startswith(("lt_kv4", "lt_pages")):
+        if f.name.startswith(("lt_kv4", "lt_pages", "lt_w4")):
             continue
         h.update(f.name.encode())
         h.update(f.read_bytes())

@@ -1,0 +1,439 @@
+// lt_w4_linear.cu -- products with 4-bit weights (lt_w4_linear) for few tokens, and the
+// weights' quantisation (lt_w4_quantise).
+//
+// Few tokens: the weights are read once and that is the time, so what counts is the work per weight: unpacking,
+// scaling, feeding the tensor core. The weights are the 16-row operand straight from registers (m16n8k16,
+// fp32 sums), the tokens the eight columns. The order of the inputs within a product is free, so a lane
+// takes 16 bytes of codes, a whole group of 32 inputs, of rows g and g + 8: four lanes
+// read 64 bytes of a row, a lane has one scale a row, and the tokens' fragments are 16 bytes
+// of the same inputs from shared memory.
+//
+// A CTA's eight warps are WR row tiles of 16 by 8 / WR parts of the inputs; a cluster cuts the inputs
+// further where there are few rows. The parts join in shared memory and over
+// distributed shared memory, in one order whatever the timing.
+
+#include <mutex>
+
+#include "../../include/lt_w4.h"
+#include "lt_async.cuh"
+#include "lt_kv4_quantise.cuh"
+
+namespace {
+
+using namespace lt::kv4;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStep = 128;  // inputs of a warp's step
+constexpr int kMaxParts = 8;
+
+struct LinearParams {
+  const void* x;
+  const uint8_t* codes;
+  const __half* scales;
+  const void* bias;
+  void* out;
+  int64_t x_stride, out_stride;
+  int32_t n, k, tokens;
+  int32_t row_warps;   // row tiles of a CTA: 1, 2, 4 or 8
+  int32_t parts;       // CTAs of a cluster, along the inputs
+  int32_t chunk;       // steps whose inputs are in shared memory at a time
+  int32_t bf16;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 load_once(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive;\n barrier.cluster.wait;" ::: "memory");
+}
+__device__ __forceinline__ float peer_f32(uint32_t addr, int rank) {
+  float v;
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}"
+               : "=f"(v) : "r"(addr), "r"(rank) : "memory");
+  return v;
+}
+
+// bf16 tokens become fp16 ones times a power of two: the one that brings the largest finite magnitude (its fp32
+// word) into [2^14, 2^15).
+__device__ __forceinline__ float token_power(uint32_t big) {
+  const int e = (int)(big >> 23);
+  return __uint_as_float((uint32_t)(e == 0 ? 253 : min(268 - e, 253)) << 23);
+}
+__device__ __forceinline__ uint32_t finite_bf16_pair(uint32_t w) {  // the larger finite magnitude of two, as an fp32 word
+  const uint32_t lo = w << 16 & 0x7FFF0000u, hi = w & 0x7FFF0000u;
+  return max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u);
+}
+__device__ __forceinline__ uint32_t pair_to_half(uint32_t w, float mul) {
+  const float lo = __uint_as_float(w << 16) * mul, hi = __uint_as_float(w & 0xFFFF0000u) * mul;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
+}
+
+// Where 16-byte piece q of token t lies: pieces of a step (16) by lane group and word, the upper eight's turned
+// by one, tokens 32 bytes apart beyond whole 128-byte lines, so that the eight lanes (two tokens, four groups)
+// that read 16 bytes together have all banks.
+__device__ __forceinline__ int piece_at(int t, int q, int pitch) { return t * pitch + ((q ^ (q >> 3 & 1)) << 4); }
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) few_kernel(LinearParams p) {
+  constexpr int kTokens = NT * 8;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t largest[kTokens];
+  __shared__ float inverse[kTokens];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int k_warps = kWarps / p.row_warps, wr = warp % p.row_warps, wk = warp / p.row_warps;
+  const int rank = blockIdx.x % p.parts;
+  const int row0 = (int)(blockIdx.x / p.parts) * p.row_warps * 16;
+  const int token0 = blockIdx.y * kTokens, tokens = min(p.tokens - token0, kTokens);
+  const int steps = (p.k + kStep - 1) / kStep, groups = p.k / 32;
+  // the CTA's steps, then the warp's
+  const int s_begin = (int)((int64_t)steps * rank / p.parts), s_end = (int)((int64_t)steps * (rank + 1) / p.parts);
+  if (tid < kTokens) largest[tid] = 0u;
+  dependency_wait();
+  __syncthreads();
+
+  const int ra = min(row0 + wr * 16 + g, p.n - 1), rb = min(row0 + wr * 16 + g + 8, p.n - 1);
+  const uint8_t* codes_a = p.codes + (int64_t)ra * (p.k / 2) + c * 16;
+  const uint8_t* codes_b = p.codes + (int64_t)rb * (p.k / 2) + c * 16;
+  const uint16_t* scales_a = reinterpret_cast<const uint16_t*>(p.scales) + (int64_t)ra * groups + c;
+  const uint16_t* scales_b = reinterpret_cast<const uint16_t*>(p.scales) + (int64_t)rb * groups + c;
+
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+  float power[NT][2];  // of tokens 2c and 2c + 1, whose sums a lane has
+#pragma unroll
+  for (int t = 0; t < NT; ++t) power[t][0] = power[t][1] = 1.0f;
+
+  const int pitch = p.chunk * kStep * 2 + 32;
+  constexpr int U = 2;  // steps of a batch; one batch is on its way while another is worked on
+  struct Batch {
+    uint4 a[U], b[U];
+    uint32_t sa[U], sb[U];
+  };
+  auto fetch = [&](Batch& w, int from, int to) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = from + u;
+      w.a[u] = w.b[u] = make_uint4(0u, 0u, 0u, 0u);
+      w.sa[u] = w.sb[u] = 0u;
+      if (s < to && s * 4 + c < groups) {
+        w.a[u] = load_once(codes_a + (int64_t)s * 64);
+        w.b[u] = load_once(codes_b + (int64_t)s * 64);
+        w.sa[u] = __ldg(scales_a + s * 4);
+        w.sb[u] = __ldg(scales_b + s * 4);
+      }
+    }
+  };
+  const uint32_t x_at = lt::smem_u32(smem);
+
+  for (int c0 = s_begin; c0 < s_end; c0 += p.chunk) {
+    const int c1 = min(c0 + p.chunk, s_end), wide = c1 - c0;
+    // the warp's steps of the chunk
+    const int from = c0 + wide * wk / k_warps, to = c0 + wide * (wk + 1) / k_warps;
+    Batch w[2];
+    fetch(w[0], from, to);
+    fetch(w[1], from + U, to);
+    // the chunk's inputs into shared memory; past the last input, zeros
+    const int pieces = wide * 16;
+    for (int t = 0; t < tokens; ++t) {
+      const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)(token0 + t) * p.x_stride + (int64_t)c0 * kStep;
+      uint32_t big = 0;
+      for (int q = tid; q < pieces; q += kThreads) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (c0 * kStep + q * 8 < p.k) v = __ldg(reinterpret_cast<const uint4*>(x) + q);
+        *reinterpret_cast<uint4*>(smem + piece_at(t, q, pitch)) = v;
+        if (p.bf16) big = max(max(big, max(finite_bf16_pair(v.x), finite_bf16_pair(v.y))), max(finite_bf16_pair(v.z), finite_bf16_pair(v.w)));
+      }
+      if (p.bf16) {
+        big = __reduce_max_sync(~0u, big);
+        if (lane == 0) atomicMax(&largest[t], big);
+      }
+    }
+    if (p.bf16) {
+      __syncthreads();
+      for (int t = 0; t < tokens; ++t) {
+        const float mul = token_power(largest[t]);
+        for (int q = tid; q < pieces; q += kThreads) {
+          uint4* at = reinterpret_cast<uint4*>(smem + piece_at(t, q, pitch));
+          const uint4 v = *at;
+          *at = make_uint4(pair_to_half(v.x, mul), pair_to_half(v.y, mul), pair_to_half(v.z, mul), pair_to_half(v.w, mul));
+        }
+      }
+      // sums so far go over to the new power, which is the largest input's so far and never grows
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float now = token_power(largest[min(t * 8 + 2 * c + e, tokens - 1)]);
+          if (c0 > s_begin) {
+            const float f = fmaxf(now / power[t][e], 0x1p-126f);  // (not 0: an infinity stays one)
+            acc[t][e] *= f;
+            acc[t][e + 2] *= f;
+          }
+          power[t][e] = now;
+        }
+    }
+    __syncthreads();
+
+    for (int s0 = from; s0 < to; s0 += 2 * U) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int s = s0 + half * U + u;
+          if (s >= to) break;
+          const uint32_t ka = __byte_perm(w[half].sa[u], 0, 0x1010), kb = __byte_perm(w[half].sb[u], 0, 0x1010);
+          const uint32_t wa[4] = {w[half].a[u].x, w[half].a[u].y, w[half].a[u].z, w[half].a[u].w};
+          const uint32_t wb[4] = {w[half].b[u].x, w[half].b[u].y, w[half].b[u].z, w[half].b[u].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t ha[4], hb[4];
+            codes_to_half2(wa[j], ha);
+            codes_to_half2(wb[j], hb);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ha[i] = hmul2(ha[i], ka);
+              hb[i] = hmul2(hb[i], kb);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const int token = min(t * 8 + g, tokens - 1), q = (s - c0) * 16 + c * 4 + j;
+              uint32_t b0, b1, b2, b3;
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3) : "r"(x_at + piece_at(token, q, pitch)));
+              mma16816(acc[t], ha[0], hb[0], ha[1], hb[1], b0, b1);
+              mma16816(acc[t], ha[2], hb[2], ha[3], hb[3], b2, b3);
+            }
+          }
+        }
+        fetch(w[half], s0 + (half + 2) * U, to);
+      }
+    }
+    __syncthreads();  // the chunk's inputs have been read
+  }
+  dependents_launch();
+
+  // join the warps: [k warp][token][row]
+  if (p.bf16 && tid < kTokens) inverse[tid] = 1.0f / token_power(largest[min(tid, tokens - 1)]);
+  __syncthreads();
+  const int rows = p.row_warps * 16;
+  float* joined = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int token = t * 8 + 2 * c + (e & 1), row = wr * 16 + g + (e >> 1) * 8;
+      joined[(wk * kTokens + token) * rows + row] = p.bf16 ? acc[t][e] * inverse[token] : acc[t][e];
+    }
+  __syncthreads();
+  const int all = tokens * rows;
+  if (p.parts > 1) {
+    for (int u = tid; u < all; u += kThreads) {
+      float y = joined[u];
+      for (int w = 1; w < k_warps; ++w) y += joined[w * kTokens * rows + u];
+      joined[u] = y;
+    }
+    cluster_sync();
+  }
+  for (int u = rank * kThreads + tid; u < all; u += p.parts * kThreads) {
+    const int token = u / rows, row = row0 + u % rows;
+    float y = 0.0f;
+    if (p.parts > 1) {
+#pragma unroll
+      for (int r = 0; r < kMaxParts; ++r)
+        if (r < p.parts) y += peer_f32(x_at + u * 4, r);
+    } else {
+      for (int w = 0; w < k_warps; ++w) y += joined[w * kTokens * rows + u];
+    }
+    if (row < p.n) {
+      const int64_t at = (int64_t)(token0 + token) * p.out_stride + row;
+      if (p.bf16) {
+        if (p.bias != nullptr) y += __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[row]);
+        static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+      } else {
+        if (p.bias != nullptr) y += __half2float(static_cast<const __half*>(p.bias)[row]);
+        static_cast<__half*>(p.out)[at] = __float2half_rn(y);
+      }
+    }
+  }
+  if (p.parts > 1) cluster_sync();  // (a CTA's shared memory stays until its peers have read it)
+}
+
+// ---- quantisation: a thread eight inputs, four lanes a group
+
+struct QuantiseParams {
+  const void* w;
+  uint8_t* codes;
+  uint16_t* scales;
+  int64_t n, k, stride;
+};
+
+template <class S>
+__global__ void __launch_bounds__(kThreads) quantise_kernel(QuantiseParams p, bool wide) {
+  dependency_wait();
+  const int64_t pieces = p.k / 8, whole = (pieces + 31) / 32 * 32;
+  for (int64_t row = blockIdx.x; row < p.n; row += gridDim.x) {
+    const S* w = static_cast<const S*>(p.w) + row * p.stride;
+    for (int64_t q = threadIdx.x + (int64_t)blockIdx.y * kThreads; q < whole; q += (int64_t)gridDim.y * kThreads) {
+      Eight<S> x;
+      x.clear();
+      if (q < pieces) x.load(w + q * 8, wide);
+      uint32_t largest = x.largest();
+      largest = max(largest, __shfl_xor_sync(~0u, largest, 1));
+      largest = max(largest, __shfl_xor_sync(~0u, largest, 2));
+      if (q < pieces) {
+        const bool bad = !Eight<S>::finite(largest);
+        const float s = bad ? 0.0f : Eight<S>::scale(Eight<S>::number(largest));
+        reinterpret_cast<uint32_t*>(p.codes + row * (p.k / 2))[q] = bad ? 0u : x.codes(s);
+        if ((q & 3) == 0) p.scales[row * (p.k / 32) + q / 4] = bad ? (uint16_t)0x7FFF : __half_as_ushort(__float2half_rn(s));
+      }
+    }
+  }
+  dependents_launch();
+}
+
+// ---- host side
+
+bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+int g_sms[kMaxDevices];
+bool g_set[kMaxDevices][3];
+
+lt_status device_of(int* dev, int* sms) {
+  if (cudaGetDevice(dev) != cudaSuccess) return LT_ERR_CUDA;
+  if (*dev < 0 || *dev >= kMaxDevices) return LT_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (g_sms[*dev] == 0 && cudaDeviceGetAttribute(&g_sms[*dev], cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess)
+    return LT_ERR_CUDA;
+  *sms = g_sms[*dev];
+  return LT_OK;
+}
+
+const void* few_ptr(int nt) {
+  return nt == 1   ? reinterpret_cast<const void*>(&few_kernel<1>)
+         : nt == 2 ? reinterpret_cast<const void*>(&few_kernel<2>)
+                   : reinterpret_cast<const void*>(&few_kernel<4>);
+}
+
+constexpr int kFewSmem = 64 * 1024;
+
+lt_status check_sizes(int64_t tokens, int64_t n, int64_t k) {
+  if (tokens < 0 || n < 0 || k < 0) return LT_ERR_INVALID_ARG;
+  if (k == 0 || k % 32 != 0 || k > INT32_MAX - 1024 || n > INT32_MAX - 1024 || tokens > 65535 * 8) return LT_ERR_UNSUPPORTED;
+  return LT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lt_status lt_w4_quantise(const void* w, int32_t dtype, int64_t n, int64_t k, int64_t row_stride, void* codes, void* scales,
+                         void* stream) {
+  if (dtype != LT_DTYPE_F32 && dtype != LT_DTYPE_BF16 && dtype != LT_DTYPE_F16) return LT_ERR_INVALID_ARG;
+  if (n > 0 && k > 0 && (w == nullptr || codes == nullptr || scales == nullptr)) return LT_ERR_INVALID_ARG;
+  const uintptr_t size = dtype == LT_DTYPE_F32 ? 4 : 2;
+  if (!aligned(w, size) || !aligned(codes, 16) || !aligned(scales, 16)) return LT_ERR_INVALID_ARG;
+  const lt_status st = check_sizes(0, n, k);
+  if (st != LT_OK) return st;
+  if (n == 0) return LT_OK;
+  QuantiseParams p = {w, static_cast<uint8_t*>(codes), static_cast<uint16_t*>(scales), n, k, row_stride};
+  bool wide = aligned(w, 16) && (row_stride * (int64_t)size) % 16 == 0;
+  const void* func = dtype == LT_DTYPE_F32    ? reinterpret_cast<const void*>(&quantise_kernel<float>)
+                     : dtype == LT_DTYPE_BF16 ? reinterpret_cast<const void*>(&quantise_kernel<__nv_bfloat16>)
+                                              : reinterpret_cast<const void*>(&quantise_kernel<__half>);
+  if (lt::take_injected_failure()) return LT_ERR_CUDA;
+  const int64_t across = (k / 8 + kThreads - 1) / kThreads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(n < 1 << 20 ? n : 1 << 20), (unsigned)(across < 64 ? across : 64));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void* a[] = {&p, &wide};
+  return cudaLaunchKernelExC(&cfg, func, a) == cudaSuccess ? LT_OK : LT_ERR_CUDA;
+}
+
+lt_status lt_w4_workspace(int64_t tokens, int64_t n, int64_t k, int64_t* bytes) {
+  if (bytes == nullptr) return LT_ERR_INVALID_ARG;
+  const lt_status st = check_sizes(tokens, n, k);
+  if (st != LT_OK) return st;
+  *bytes = 0;
+  return LT_OK;
+}
+
+lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_stride, const void* codes, const void* scales,
+                       int64_t n, int64_t k, const void* bias, void* out, int64_t out_stride, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  if (dtype != LT_DTYPE_BF16 && dtype != LT_DTYPE_F16) return LT_ERR_INVALID_ARG;
+  lt_status st = check_sizes(tokens, n, k);
+  if (st == LT_ERR_INVALID_ARG) return st;
+  if (tokens > 0 && n > 0) {
+    if (x == nullptr || codes == nullptr || scales == nullptr || out == nullptr) return LT_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || x_stride % 8 || !aligned(codes, 16) || !aligned(scales, 16) || !aligned(out, 2) || !aligned(bias, 2))
+      return LT_ERR_INVALID_ARG;
+  }
+  if (st != LT_OK) return st;
+  if (tokens == 0 || n == 0) return LT_OK;
+  int dev = 0, sms = 0;
+  st = device_of(&dev, &sms);
+  if (st != LT_OK) return st;
+  LinearParams p = {};
+  p.x = x;
+  p.codes = static_cast<const uint8_t*>(codes);
+  p.scales = static_cast<const __half*>(scales);
+  p.bias = bias;
+  p.out = out;
+  p.x_stride = x_stride;
+  p.out_stride = out_stride;
+  p.n = (int32_t)n;
+  p.k = (int32_t)k;
+  p.tokens = (int32_t)tokens;
+  p.bf16 = dtype == LT_DTYPE_BF16;
+  const int nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
+  const int64_t token_tiles = (tokens + nt * 8 - 1) / (nt * 8);
+  const int here = tokens < nt * 8 ? (int)tokens : nt * 8;
+  p.row_warps = here <= 2 ? 1 : here <= 4 ? 2 : here <= 8 ? 4 : 8;
+  const int64_t row_blocks = (n + p.row_warps * 16 - 1) / (p.row_warps * 16);
+  const int steps = (int)((k + kStep - 1) / kStep), k_warps = kWarps / p.row_warps;
+  const int64_t slots = (int64_t)sms * (nt == 4 ? 2 : 3);
+  p.parts = 1;
+  while (p.parts < kMaxParts && row_blocks * token_tiles * p.parts * 2 <= slots * 2 && steps >= p.parts * 2 * k_warps * 2) p.parts *= 2;
+  // inputs in shared memory at a time: as many steps as fit
+  const int most = (kFewSmem / here - 32) / (kStep * 2);
+  const int mine = (steps + p.parts - 1) / p.parts;
+  p.chunk = mine < most ? mine : most / k_warps * k_warps;
+  const int x_bytes = here * (p.chunk * kStep * 2 + 32), join_bytes = k_warps * nt * 8 * p.row_warps * 16 * 4;
+  const int smem = x_bytes > join_bytes ? x_bytes : join_bytes;
+  if (row_blocks * p.parts > INT32_MAX || token_tiles > 65535) return LT_ERR_UNSUPPORTED;
+  const void* func = few_ptr(nt);
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    bool& set = g_set[dev][nt / 2];
+    if (!set) {
+      if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) != cudaSuccess) return LT_ERR_CUDA;
+      set = true;
+    }
+  }
+  return launch(func, dim3((unsigned)(row_blocks * p.parts), (unsigned)token_tiles), kThreads, (unsigned)smem, &p, stream, p.parts);
+}
+
+}  // extern "C"

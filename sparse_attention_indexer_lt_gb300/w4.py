@@ -1,0 +1,90 @@
+"""Products with 4-bit weights: argument marshalling for the calls of ``include/lt_w4.h``, which documents
+the format and every argument.
+
+    codes, scales = w4_quantise(weight)           # once
+    y = w4_linear(x, codes, scales, bias=bias)    # x @ weight.T + bias
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from .kv4 import _ALL, _call, _raw_stream, _result, _want
+
+_GROUP = 32
+
+
+def w4_quantise(weight: torch.Tensor, *, out_codes: torch.Tensor | None = None, out_scales: torch.Tensor | None = None,
+                stream: torch.cuda.Stream | None = None):
+    """Codes uint8 [n, k / 2] and scales float16 [n, k / 32] of weight [n, k] (float32, bfloat16 or float16; any
+    stride of rows), with the rounding of kv4_store."""
+    if not isinstance(weight, torch.Tensor) or not weight.is_cuda:
+        raise TypeError("weight must be a CUDA tensor")
+    dtype, index = _ALL.get(weight.dtype), weight.get_device()
+    if dtype is None or weight.dim() != 2 or weight.shape[1] < _GROUP or weight.shape[1] % _GROUP:
+        raise ValueError("weight must be [n, a multiple of 32] in float32, bfloat16 or float16")
+    n, k = weight.shape
+    if n > 0 and weight.stride(1) != 1:
+        raise ValueError("the rows of weight must be contiguous")
+    codes = _result("out_codes", out_codes, (n, k // 2), torch.uint8, weight, stream)
+    scales = _result("out_scales", out_scales, (n, k // _GROUP), torch.float16, weight, stream)
+    _call("lt_w4_quantise", index, weight.data_ptr(), dtype, n, k, weight.stride(0), codes.data_ptr(), scales.data_ptr(),
+          _raw_stream(stream, index))
+    return codes, scales
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(index, tokens, n, k):
+    """lt_w4_workspace's answer: it goes by these sizes and the device alone."""
+    need = ctypes.c_int64(0)
+    _call("lt_w4_workspace", index, tokens, n, k, ctypes.byref(need))
+    return need.value
+
+
+def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, bias: torch.Tensor | None = None,
+              out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+              stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """x [tokens, k] (bfloat16 or float16) times the weights that codes (uint8 [n, k / 2]) and scales (float16
+    [n, k / 32]) hold, transposed, plus bias [n] in x's type: [tokens, n] in x's type.
+
+    x may have any stride of rows that is a multiple of 8, out any stride of rows. workspace (uint8) replaces
+    the scratch memory that a call takes from torch's allocator for its stream; see lt_w4_workspace.
+    """
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    dtype, index = x.dtype, x.get_device()
+    if dtype != torch.bfloat16 and dtype != torch.float16:
+        raise TypeError("x must be bfloat16 or float16")
+    _want("codes", codes, torch.uint8, index)
+    _want("scales", scales, torch.float16, index)
+    if x.dim() != 2 or codes.dim() != 2 or x.shape[1] < _GROUP or x.shape[1] % _GROUP or codes.shape[1] * 2 != x.shape[1]:
+        raise ValueError("x must be [tokens, k] and codes [n, k / 2], k a multiple of 32")
+    tokens, k = x.shape
+    n = codes.shape[0]
+    if scales.shape != (n, k // _GROUP):
+        raise ValueError(f"scales must have shape {(n, k // _GROUP)}, has {tuple(scales.shape)}")
+    if tokens > 0 and (x.stride(1) != 1 or x.stride(0) % 8 or x.data_ptr() % 16):
+        raise ValueError("x must have contiguous rows, a row stride that is a multiple of 8 and a 16-byte aligned start")
+    if codes.data_ptr() % 16 or scales.data_ptr() % 16:
+        raise ValueError("codes and scales must start on 16 bytes")
+    if bias is not None:
+        _want("bias", bias, dtype, index, (n,))
+    if out is None:
+        out = _result("out", None, (tokens, n), dtype, x, stream)
+    elif not isinstance(out, torch.Tensor) or not out.is_cuda or out.get_device() != index or out.dtype != dtype \
+            or out.shape != (tokens, n) or (tokens > 0 and n > 0 and out.stride(1) != 1):
+        raise ValueError(f"out must be a {dtype} tensor of shape {(tokens, n)} on cuda:{index}, its rows contiguous")
+    need = _workspace_bytes(index, tokens, n, k)
+    if workspace is not None:
+        _want("workspace", workspace, torch.uint8, index)
+        if workspace.numel() < need or workspace.data_ptr() % 16:
+            raise ValueError(f"workspace must have at least {need} bytes and start on 16")
+    elif need > 0:
+        workspace = _result("workspace", None, (need,), torch.uint8, x, stream)
+    _call("lt_w4_linear", index, x.data_ptr(), _ALL[dtype], tokens, x.stride(0), codes.data_ptr(), scales.data_ptr(), n, k,
+          None if bias is None else bias.data_ptr(), out.data_ptr(), out.stride(0),
+          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
+          _raw_stream(stream, index))
+    return out
