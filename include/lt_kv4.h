@@ -210,6 +210,36 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
                            void* out, float* lse, void* workspace, int64_t workspace_bytes,
                            void* stream);
 
+/*
+ * lt_kv4_attention_ex -- lt_kv4_attention with logits that are capped, lowered with the
+ * distance, or seen through a prefix mask. With `own` a query's position and p a cached one,
+ *
+ *   s_p = scale * sum_c q[c] k_p[c]
+ *   s_p = softcap * tanh(s_p / softcap)       with softcap > 0
+ *   s_p = s_p - slopes[h] * |own - p|         with slopes
+ *
+ * and visible are the positions up to the query's own, and those below prefix[r], whichever query of
+ * request r looks (a query that lies before the first position sees the prefix alone).
+ *
+ *   softcap   0 (none), or LT_KV4_MIN_CAP to LT_KV4_MAX_CAP. A capped logit is off by at most
+ *             2^-22 of caps to 64, 2^-20 of itself with larger ones
+ *   slopes    float [q_heads], finite, or NULL; listed positions have distances, too
+ *   prefix    int32 [requests] or NULL; below 0 counts as 0, past the request's length as
+ *             that; NULL where window > 0 or positions are given
+ * All else, the workspace among it, is lt_kv4_attention's.
+ */
+#define LT_KV4_MIN_CAP 0.0009765625f /* 2^-10 */
+#define LT_KV4_MAX_CAP 1048576.0f    /* 2^20 */
+lt_status lt_kv4_attention_ex(const void* q, int32_t dtype, int64_t tokens, int32_t q_heads,
+                              int32_t kv_heads, int32_t head_dim, int64_t q_token_stride,
+                              int64_t q_head_stride, const void* cache, int64_t pages, int32_t page_size,
+                              const int32_t* block_table, int32_t table_width, const int32_t* lengths,
+                              int32_t requests, const int32_t* starts, int32_t max_new,
+                              const int32_t* positions, int32_t list_len, int32_t window, float scale,
+                              float softcap, const float* slopes, const int32_t* prefix,
+                              void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                              void* stream);
+
 /* Bytes of workspace that lt_kv4_attention needs for these sizes on the current
  * device: 0 where a request's parts are joined within the launch, else room for the
  * parts of the requests that are cut, each with the fp32 outputs of up to max_new

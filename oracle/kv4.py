@@ -137,7 +137,7 @@ def extend(lengths, new, table, free, num_free, page, max_tokens):
             "starts": np.array(starts, np.int32), "lengths": out_lengths, "num_free": n, "table": table}
 
 
-def attention(q, rows_at, lengths, starts, kv_heads, scale, window=0, positions=None):
+def attention(q, rows_at, lengths, starts, kv_heads, scale, window=0, positions=None, softcap=0.0, slopes=None, prefix=None):
     """out, lse, and for error bounds: the weighted |v| and the largest sum of |q k| over the visible positions.
 
     q [tokens, heads, D]; rows_at(request, head, p) gives (k, v) of one position in 64 bits, or None where
@@ -154,6 +154,8 @@ def attention(q, rows_at, lengths, starts, kv_heads, scale, window=0, positions=
                 t, at = starts[r] + i, length - count + i
                 if positions is None:
                     seen = [p for p in range(max(0, at - window + 1 if window else 0), at + 1)]
+                    if prefix is not None:
+                        seen += range(max(at + 1, 0), min(int(prefix[r]), length))
                 else:
                     seen = [int(p) for p in positions[t] if 0 <= p < length]
                 seen = [p for p in seen if known[p] is not None]
@@ -163,6 +165,10 @@ def attention(q, rows_at, lengths, starts, kv_heads, scale, window=0, positions=
                 v = np.stack([known[p][1] for p in seen])
                 for g in range(h * group, (h + 1) * group):
                     s = scale * (k @ q[t, g])
+                    if softcap:
+                        s = softcap * np.tanh(s / softcap)
+                    if slopes is not None:
+                        s = s - float(slopes[g]) * np.abs(at - np.asarray(seen))
                     top = s.max()
                     w = np.exp(s - top)
                     out[t, g] = w @ v / w.sum()

@@ -101,11 +101,13 @@ def load() -> ctypes.CDLL:
     lib.lt_kv4_load.argtypes = [vp, i64, i32, vp, i64, i32, i32, vp, vp, i32, vp]
     lib.lt_kv4_attention.argtypes = [vp, i32, i64, i32, i32, i32, i64, i64, vp, i64, i32, vp, i32, vp, i32, vp, i32,
                                      vp, i32, i32, ctypes.c_float, vp, vp, vp, i64, vp]
+    a = lib.lt_kv4_attention.argtypes
+    lib.lt_kv4_attention_ex.argtypes = a[:21] + [ctypes.c_float, vp, vp] + a[21:]
     lib.lt_kv4_workspace.argtypes = [i64, i32, i32, i32, i32, i32, i32, i64, i32, vp]
     lib.lt_w4_quantise.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
     lib.lt_w4_linear.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp, i64, vp]
     lib.lt_w4_workspace.argtypes = [i64, i64, i64, vp]
-    for name in ("lt_page_release", "lt_page_extend", "lt_kv4_store", "lt_kv4_append", "lt_kv4_load", "lt_kv4_attention",
+    for name in ("lt_page_release", "lt_page_extend", "lt_kv4_store", "lt_kv4_append", "lt_kv4_load", "lt_kv4_attention", "lt_kv4_attention_ex",
                  "lt_kv4_workspace", "lt_w4_quantise", "lt_w4_linear", "lt_w4_workspace"):
         getattr(lib, name).restype = ctypes.c_int
     lib.lt_test_inject.argtypes = [i32, i32]

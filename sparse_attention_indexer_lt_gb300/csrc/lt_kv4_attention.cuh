@@ -33,6 +33,12 @@ struct AttentionParams {
   int32_t part_rows;  // query rows of a part: max_new * group
   int32_t align;    // positions at which chunks and windows start: multiples of this (32 or 128)
   float scale_log2;
+  // shaped logits: cap tanh(s / cap) where cap > 0, less slope |own position - position|
+  const float* slopes;    // [query heads]
+  const int32_t* prefix;  // [requests]: positions below it are seen by all of the request's queries
+  float cap;              // in units of log 2
+  float two_over_cap;     // 2 / cap, of the cap itself
+  int32_t wide_cap;       // the cap is large against the logits that a hyperbolic tangent by one exponential keeps exact
 };
 
 struct Request {
@@ -260,6 +266,28 @@ __device__ __forceinline__ float bf16_row_to_half(uint32_t (&w)[N][4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[j][i] = bf16_pair_to_half(w[j][i], mul);
   return 1.0f / mul;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// cap tanh(s / cap) in units of log 2. tanh(x) = 1 - 2 / (1 + e^2x) is off by 2^-22, absolute, so the capped logit
+// by 2^-22 of the cap: for caps to 64 less than what 32-bit sums of the products are off by. With larger caps,
+// logits below a quarter of them go by the series x - x^3 / 3 + 2 x^5 / 15 - 17 x^7 / 315 + 62 x^9 / 2835 (2^-27).
+// An infinity gives the cap, NaN stays NaN.
+__device__ __forceinline__ float capped(const AttentionParams& p, float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_fast(s * p.two_over_cap)));
+  float y = fmaf(-2.0f * p.cap, r, p.cap);
+  if (p.wide_cap) {
+    const float x = s * (p.two_over_cap * 0.34657359028f), u = x * x;
+    const float t = fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0.0218694885f, -0.0539682540f), 0.1333333333f), -0.3333333333f), 1.0f);
+    if (fabsf(x) < 0.25f) y = s * t;
+  }
+  return y;
 }
 
 // Two outputs, rounded once.

@@ -1,5 +1,6 @@
-// lt_kv4_prefill.cu -- attention over the 4-bit cache for many query rows a
-// request (prefill chunks): tcgen05 with the sums in tensor memory.
+// lt_kv4_prefill.cuh -- attention over the 4-bit cache for many query rows a
+// request (prefill chunks): tcgen05 with the sums in tensor memory; one translation unit
+// without and one with shaped logits (caps, slopes, prefixes).
 //
 // A CTA takes 256 query rows of one kv head (two tiles of 128, a thread a row) and a
 // range of positions in tiles of 128, with one role a warpgroup:
@@ -48,7 +49,7 @@
 // A value that is NaN, or whose scale is outside the format, is unpacked as zero, and the rows that see it note
 // the group: a row's output is NaN there whatever its weight, and rows that do not see it stay clean.
 
-#include <mutex>
+#pragma once
 
 #include "lt_kv4.cuh"
 #include "lt_kv4_attention.cuh"
@@ -266,11 +267,6 @@ __device__ __forceinline__ int slot_ready(int slot) { return 5 + slot; }
 template <int D>
 constexpr int kSlotThreads = Smem<D>::kUnpackers / 2 + 32;
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -294,7 +290,7 @@ struct Job {
 };
 
 // ---- one row tile's softmax: a thread a row
-template <int D>
+template <int D, bool kShaped>
 __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job& job, Shared* sh, uint8_t* smem, int which) {
   constexpr int kHalf = Smem<D>::kQHalf, kTok = Smem<D>::kTok, kRing = Smem<D>::kRing;
   constexpr int kChunks = D / 8;                          // 16-byte chunks of a row of 16-bit values
@@ -368,8 +364,16 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   }
   if (which == 1 && !job.two) return;
 
-  const int limit = job.rq.length - job.rq.queries + row_c / p.group + 1;
-  const int low = p.window > 0 ? max(limit - p.window, 0) : 0;
+  const int own = job.rq.length - job.rq.queries + row_c / p.group;  // the row's position
+  const int low = p.window > 0 ? max(own + 1 - p.window, 0) : 0;
+  int limit = own + 1;
+  float slope = 0.0f, shaped_factor = 1.0f;
+  if constexpr (kShaped) {
+    if (p.prefix != nullptr) limit = max(limit, __ldg(p.prefix + job.request));
+    if (p.slopes != nullptr) slope = __ldg(p.slopes + job.head * p.group + row_c % p.group) * 1.4426950408889634f;
+    shaped_factor = factor;  // logits are shaped in units of log 2, and stay so
+    factor = 1.0f;
+  }
   const uint32_t lane_base = sh->tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t o_at = lane_base + kSumColumn + which * D;
 
@@ -395,8 +399,46 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
     }
     float top;
     bool hidden = false;
+    if constexpr (kShaped) {
+      // shaped and hidden in tensor memory, 32 columns at a time, and the maximum taken on the way
+      top = -INFINITY;
 #pragma unroll 1
-    for (;;) {
+      for (int w = 0; w < kTok / 32; ++w) {
+        uint32_t y[32];
+        tmem_read32(s_at + 32 * w, y);
+        float* s = reinterpret_cast<float*>(y);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[c] *= shaped_factor;
+        if (p.cap > 0.0f) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s[c] = capped(p, s[c]);
+        }
+        if (p.slopes != nullptr) {
+          const float from = (float)(own - pos0 - 32 * w);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, fabsf(from - (float)c), s[c]);
+        }
+        const int a = low - (pos0 + 32 * w), b = limit - (pos0 + 32 * w);  // (low >= 0: no overflow)
+        uint32_t see = valid[w];
+        see &= b >= 32 ? ~0u : b <= 0 ? 0u : (1u << b) - 1u;
+        see &= a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a;
+        if (!__all_sync(~0u, see == ~0u)) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!((see >> c) & 1u)) y[c] = 0xFF800000u;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) top = max3(top, s[c], s[c + 1]);
+        tmem_st32(s_at + 32 * w, y);
+        if (any_nan != 0)
+          for (uint32_t left = nan_rows[w] & see; left != 0; left &= left - 1)
+            poison |= sh->nan_groups[i % kRing * kTok + 32 * w + __ffs(left) - 1];
+        __syncwarp();
+      }
+      tmem_wait_st();
+    }
+#pragma unroll 1
+    for (; !kShaped;) {
       float t0 = -INFINITY, t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
 #pragma unroll 1
       for (int h = 0; h < kTok / 64; ++h) {
@@ -752,7 +794,7 @@ __device__ __forceinline__ void product_role(const Job& job, Shared* sh, uint8_t
   if (job.two) mma_commit(&sh->o_full[1], lead);
 }
 
-template <int D>
+template <int D, bool kShaped>
 __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (lt::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -801,7 +843,9 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
     job.from = (int)(at < job.rq.length ? at : job.rq.length);
     job.to = (int)(end < job.rq.length ? end : job.rq.length);
     const int last = min(job.rows - 1, job.row0 + kRows - 1) / p.group;
-    job.to = min(job.to, job.rq.length - job.rq.queries + last + 1);
+    int seen_to = job.rq.length - job.rq.queries + last + 1;
+    if (kShaped && p.prefix != nullptr) seen_to = max(seen_to, __ldg(p.prefix + job.request));
+    job.to = min(job.to, seen_to);
     if (p.window > 0)
       job.from = max(job.from, (job.rq.length - job.rq.queries + job.row0 / p.group + 1 - p.window) / p.align * p.align);
     job.tiles = job.to > job.from ? (job.to - job.from + Smem<D>::kTok - 1) / Smem<D>::kTok : 0;
@@ -816,7 +860,7 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   fence_after();
 
   if (warp < 4 * Smem<D>::kRowTiles)
-    softmax_role<D>(p, job, sh, smem, warp / 4);
+    softmax_role<D, kShaped>(p, job, sh, smem, warp / 4);
   else if (warp < 12)
     unpack_role<D>(job, sh, smem);
   else if (warp == 12)
@@ -836,17 +880,18 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
 namespace lt {
 namespace kv4 {
 
+template <bool kShaped>
 const void* prefill_kernel_ptr(int head_dim, int* smem) {
   if (head_dim == 64) {
     *smem = Smem<64>::kTotal;
-    return reinterpret_cast<const void*>(&prefill_kernel<64>);
+    return reinterpret_cast<const void*>(&prefill_kernel<64, kShaped>);
   }
   if (head_dim == 128) {
     *smem = Smem<128>::kTotal;
-    return reinterpret_cast<const void*>(&prefill_kernel<128>);
+    return reinterpret_cast<const void*>(&prefill_kernel<128, kShaped>);
   }
   *smem = Smem<256>::kTotal;
-  return reinterpret_cast<const void*>(&prefill_kernel<256>);
+  return reinterpret_cast<const void*>(&prefill_kernel<256, kShaped>);
 }
 
 }  // namespace kv4

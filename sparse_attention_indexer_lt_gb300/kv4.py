@@ -287,7 +287,8 @@ def _workspace_bytes(index, tokens, q_heads, kv_heads, head_dim, requests, max_n
 
 def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor, *,
                   starts: torch.Tensor | None = None, max_new: int = 1, positions: torch.Tensor | None = None,
-                  window: int = 0, scale: float | None = None, with_lse: bool = False,
+                  window: int = 0, scale: float | None = None, softcap: float = 0.0, slopes: torch.Tensor | None = None,
+                  prefix: torch.Tensor | None = None, with_lse: bool = False,
                   out: torch.Tensor | None = None, out_lse: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
     """Attention of the requests' new tokens over the cache.
@@ -296,7 +297,10 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     starts[r] .. starts[r + 1] (starts int32 [requests + 1], at most max_new rows a request; None: one
     a request), the last of its lengths[r] cached positions. Causal; the last `window` positions only if
     window > 0; or the listed `positions` (int32 [tokens, n], -1 pads) instead. scale is
-    1 / sqrt(head_dim) by default. Returns out, or (out, lse) with with_lse.
+    1 / sqrt(head_dim) by default. With softcap > 0 a logit s becomes softcap * tanh(s / softcap); with slopes
+    (float32 [q_heads]) it is lowered by the head's slope times the distance of the positions; with prefix (int32
+    [requests], without window and positions) a request's queries see its positions below that, whatever
+    their own. Returns out, or (out, lse) with with_lse.
 
     workspace (uint8) replaces the scratch memory that a call takes from torch's allocator for its
     stream; see lt_kv4_workspace for its size.
@@ -332,6 +336,17 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         if positions.dim() != 2 or positions.shape[0] != tokens or positions.shape[1] < 1:
             raise ValueError("positions must be int32 [tokens, at least one]")
         list_len = positions.shape[1]
+    shaped = softcap != 0.0 or slopes is not None or prefix is not None
+    if shaped:
+        if slopes is not None:
+            _want("slopes", slopes, torch.float32, index, (q_heads,))
+        if prefix is not None:
+            if window or positions is not None:
+                raise ValueError("prefix is not used with window or positions")
+            _want("prefix", prefix, torch.int32, index, (n,))
+        softcap = float(softcap)
+        if softcap != 0.0 and not 2.0 ** -10 <= softcap <= 2.0 ** 20:
+            raise ValueError(f"softcap must be 0 or from 2^-10 to 2^20, got {softcap}")
     out = _result("out", out, (tokens, q_heads, dim), dtype, q, stream)
     lse = _result("out_lse", out_lse, (tokens, q_heads), torch.float32, q, stream) if with_lse else None
     need = _workspace_bytes(index, tokens, q_heads, heads, dim, n, max_new, list_len, width * page_size, window)
@@ -341,10 +356,11 @@ def kv4_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
             raise ValueError(f"workspace must have at least {need} bytes")
     elif need > 0:
         workspace = _result("workspace", None, (need,), torch.uint8, q, stream)
-    _call("lt_kv4_attention", index, q_ptr, _ALL[dtype], tokens, q_heads, heads, dim, token_stride, head_stride,
+    extra = (softcap, None if slopes is None else slopes.data_ptr(), None if prefix is None else prefix.data_ptr()) if shaped else ()
+    _call("lt_kv4_attention_ex" if shaped else "lt_kv4_attention", index, q_ptr, _ALL[dtype], tokens, q_heads, heads, dim, token_stride, head_stride,
           cache.data_ptr(), pages, page_size, block_table.data_ptr(), width, lengths.data_ptr(), n,
           None if starts is None else starts.data_ptr(), max_new, None if positions is None else positions.data_ptr(),
-          list_len, window, dim ** -0.5 if scale is None else scale, out.data_ptr(),
+          list_len, window, dim ** -0.5 if scale is None else scale, *extra, out.data_ptr(),
           None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
           0 if workspace is None else workspace.numel(), _raw_stream(stream, index))
     return (out, lse) if with_lse else out
