@@ -14,18 +14,18 @@
 
 #include <mutex>
 
-#include "../../include/lt_w4.h"
 #include "lt_async.cuh"
 #include "lt_kv4_quantise.cuh"
+#include "lt_w4_linear.h"
 
 namespace {
 
 using namespace lt::kv4;
+using namespace lt::w4;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStep = 128;  // inputs of a warp's step
-constexpr int kMaxParts = 8;
 
 struct LinearParams {
   const void* x;
@@ -54,32 +54,6 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive;\n barrier.cluster.wait;" ::: "memory");
-}
-__device__ __forceinline__ float peer_f32(uint32_t addr, int rank) {
-  float v;
-  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}"
-               : "=f"(v) : "r"(addr), "r"(rank) : "memory");
-  return v;
-}
-
-// bf16 tokens become fp16 ones times a power of two: the one that brings the largest finite magnitude (its fp32
-// word) into [2^14, 2^15).
-__device__ __forceinline__ float token_power(uint32_t big) {
-  const int e = (int)(big >> 23);
-  return __uint_as_float((uint32_t)(e == 0 ? 253 : min(268 - e, 253)) << 23);
-}
-__device__ __forceinline__ uint32_t finite_bf16_pair(uint32_t w) {  // the larger finite magnitude of two, as an fp32 word
-  const uint32_t lo = w << 16 & 0x7FFF0000u, hi = w & 0x7FFF0000u;
-  return max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u);
-}
-__device__ __forceinline__ uint32_t pair_to_half(uint32_t w, float mul) {
-  const float lo = __uint_as_float(w << 16) * mul, hi = __uint_as_float(w & 0xFFFF0000u) * mul;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  return w;
-}
-
 // Where 16-byte piece q of token t lies: pieces of a step (16) by lane group and word, the upper eight's turned
 // by one, tokens 32 bytes apart beyond whole 128-byte lines, so that the eight lanes (two tokens, four groups)
 // that read 16 bytes together have all banks.
@@ -154,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) few_kernel(LinearPa
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (c0 * kStep + q * 8 < p.k) v = __ldg(reinterpret_cast<const uint4*>(x) + q);
         *reinterpret_cast<uint4*>(smem + piece_at(t, q, pitch)) = v;
-        if (p.bf16) big = max(max(big, max(finite_bf16_pair(v.x), finite_bf16_pair(v.y))), max(finite_bf16_pair(v.z), finite_bf16_pair(v.w)));
+        if (p.bf16) big = max(big, largest_of(v));
       }
       if (p.bf16) {
         big = __reduce_max_sync(~0u, big);
@@ -167,8 +141,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) few_kernel(LinearPa
         const float mul = token_power(largest[t]);
         for (int q = tid; q < pieces; q += kThreads) {
           uint4* at = reinterpret_cast<uint4*>(smem + piece_at(t, q, pitch));
-          const uint4 v = *at;
-          *at = make_uint4(pair_to_half(v.x, mul), pair_to_half(v.y, mul), pair_to_half(v.z, mul), pair_to_half(v.w, mul));
+          *at = to_half(*at, mul);
         }
       }
       // sums so far go over to the new power, which is the largest input's so far and never grows
@@ -257,16 +230,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) few_kernel(LinearPa
     } else {
       for (int w = 0; w < k_warps; ++w) y += joined[w * kTokens * rows + u];
     }
-    if (row < p.n) {
-      const int64_t at = (int64_t)(token0 + token) * p.out_stride + row;
-      if (p.bf16) {
-        if (p.bias != nullptr) y += __bfloat162float(static_cast<const __nv_bfloat16*>(p.bias)[row]);
-        static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
-      } else {
-        if (p.bias != nullptr) y += __half2float(static_cast<const __half*>(p.bias)[row]);
-        static_cast<__half*>(p.out)[at] = __float2half_rn(y);
-      }
-    }
+    if (row < p.n) put(p.out, (int64_t)(token0 + token) * p.out_stride + row, y, p.bias, row, p.bf16);
   }
   if (p.parts > 1) cluster_sync();  // (a CTA's shared memory stays until its peers have read it)
 }
@@ -330,6 +294,7 @@ const void* few_ptr(int nt) {
 }
 
 constexpr int kFewSmem = 64 * 1024;
+constexpr int kFew = 16;  // tokens up to which the weights go to the tensor core from registers
 
 lt_status check_sizes(int64_t tokens, int64_t n, int64_t k) {
   if (tokens < 0 || n < 0 || k < 0) return LT_ERR_INVALID_ARG;
@@ -375,14 +340,16 @@ lt_status lt_w4_workspace(int64_t tokens, int64_t n, int64_t k, int64_t* bytes) 
   const lt_status st = check_sizes(tokens, n, k);
   if (st != LT_OK) return st;
   *bytes = 0;
-  return LT_OK;
+  if (tokens <= kFew || n == 0) return LT_OK;
+  int dev = 0, sms = 0;
+  const lt_status found = device_of(&dev, &sms);
+  if (found == LT_OK) *bytes = many_plan(sms, tokens, n, k).bytes;
+  return found;
 }
 
 lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_stride, const void* codes, const void* scales,
                        int64_t n, int64_t k, const void* bias, void* out, int64_t out_stride, void* workspace,
                        int64_t workspace_bytes, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   if (dtype != LT_DTYPE_BF16 && dtype != LT_DTYPE_F16) return LT_ERR_INVALID_ARG;
   lt_status st = check_sizes(tokens, n, k);
   if (st == LT_ERR_INVALID_ARG) return st;
@@ -396,6 +363,25 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
   int dev = 0, sms = 0;
   st = device_of(&dev, &sms);
   if (st != LT_OK) return st;
+  if (tokens > kFew) {
+    const ManyPlan plan = many_plan(sms, tokens, n, k);
+    if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < plan.bytes) return LT_ERR_INVALID_ARG;
+    ManyParams m = {};
+    m.x = x;
+    m.codes = static_cast<const uint8_t*>(codes);
+    m.scales = static_cast<const uint16_t*>(scales);
+    m.bias = bias;
+    m.out = out;
+    m.tiles_at = static_cast<uint8_t*>(workspace);
+    m.inverse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.x_bytes);
+    m.x_stride = x_stride;
+    m.out_stride = out_stride;
+    m.n = (int32_t)n;
+    m.k = (int32_t)k;
+    m.tokens = (int32_t)tokens;
+    m.bf16 = dtype == LT_DTYPE_BF16;
+    return launch_many(dev, &m, plan, stream);
+  }
   LinearParams p = {};
   p.x = x;
   p.codes = static_cast<const uint8_t*>(codes);
