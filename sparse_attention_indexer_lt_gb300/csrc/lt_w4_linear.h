@@ -55,6 +55,7 @@ constexpr int kBlock = 64;  // inputs of a stage
 
 struct ManyPlan {
   int tile, tiles;    // tokens of a tile, a multiple of 16 up to 256; tiles
+  int row_tiles;      // tiles of 128 outputs of a CTA: 1 or 2
   int parts;          // CTAs of a cluster, along the inputs
   int stages;
   int smem;

@@ -20,12 +20,16 @@ namespace {
 using namespace lt::kv4;
 using namespace lt::w4;
 
-constexpr int kUnpackers = 256;
-constexpr int kCta = kUnpackers + 64;
-constexpr int kRows = 128;
-constexpr int kWeights = kRows * 128;  // bytes of a step's unpacked weights
+// A CTA has one or two tiles of 128 outputs, two threads an output that unpack.
+template <int kTiles>
+struct Many {
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kUnpackers = 2 * kRows;
+  static constexpr int kCta = kUnpackers + 64;
+  static constexpr int kWeights = kRows * 128;  // bytes of a step's unpacked weights
+};
 constexpr int kMaxStages = 8;
-constexpr int kAhead = 4;  // steps whose codes a thread has asked for
+constexpr int kAhead = 6;  // steps whose codes a thread has asked for
 
 struct Shared {
   uint64_t tokens_full[kMaxStages], weights_full[kMaxStages], empty[kMaxStages];
@@ -61,6 +65,8 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_kernel(ManyParams p) {
   __shared__ uint32_t big_of[kLayoutThreads / 32];
   const int tid = threadIdx.x, token = blockIdx.x;
   dependency_wait();
+  // (the product's CTAs may start: everything before this launch is done, so they ask for weights at once)
+  dependents_launch();
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + (int64_t)token * p.x_stride);
   const int pieces = p.blocks * 8, there = p.k / 8;
   uint4 held[kHeld];
@@ -93,7 +99,6 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_kernel(ManyParams p) {
     if (tid + i * kLayoutThreads < pieces) write(tid + i * kLayoutThreads, held[i]);
   for (int q = tid + kHeld * kLayoutThreads; q < pieces; q += kLayoutThreads)
     write(q, q < there ? __ldg(x + q) : make_uint4(0u, 0u, 0u, 0u));
-  dependents_launch();
 }
 
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
@@ -152,7 +157,10 @@ __device__ __forceinline__ void unpack_role(const ManyParams& p, Shared* sh, uin
   }
 }
 
-__global__ void __launch_bounds__(kCta) many_kernel(ManyParams p) {
+template <int kTiles>
+__global__ void __launch_bounds__(Many<kTiles>::kCta) many_kernel(ManyParams p) {
+  constexpr int kRows = Many<kTiles>::kRows, kCta = Many<kTiles>::kCta, kWeights = Many<kTiles>::kWeights;
+  constexpr int kUnpackWarps = Many<kTiles>::kUnpackers / 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (lt::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ Shared shared;
@@ -162,30 +170,29 @@ __global__ void __launch_bounds__(kCta) many_kernel(ManyParams p) {
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
       lt::mbar_init(&sh->tokens_full[s], 1);
-      lt::mbar_init(&sh->weights_full[s], kUnpackers / 32);
+      lt::mbar_init(&sh->weights_full[s], kUnpackWarps);
       lt::mbar_init(&sh->empty[s], 1);
     }
     lt::mbar_init(&sh->done, 1);
     sh->gave_up = 0;
     lt::mbar_fence_init();
   }
-  if (warp == 8) {
+  if (warp == kUnpackWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(lt::smem_u32(&sh->tmem)), "r"(p.columns) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
   __syncthreads();
   fence_after();
-  dependency_wait();
 
   const int rank = blockIdx.x % p.parts, row0 = (int)(blockIdx.x / p.parts) * kRows;
   const int token0 = blockIdx.y * p.tile, tokens = min(p.tokens - token0, p.tile);
   const int from = (int)((int64_t)p.blocks * rank / p.parts), to = (int)((int64_t)p.blocks * (rank + 1) / p.parts);
   const uint32_t tmem = sh->tmem;
 
-  if (warp < 8) {
+  if (warp < kUnpackWarps) {
     unpack_role(p, sh, ring, stage_bytes, row0, from, to);
-  } else if (warp == 8) {
+  } else if (warp == kUnpackWarps) {
     const uint32_t lead = elect_one(), idesc = instruction(p.tile, false), d = __shfl_sync(~0u, tmem, 0);
     int stage = 0;
     uint32_t parity = 0;
@@ -195,7 +202,9 @@ __global__ void __launch_bounds__(kCta) many_kernel(ManyParams p) {
       wait_warp(&sh->weights_full[stage], parity, sh);
       fence_after();
       const uint32_t at = ring + stage * stage_bytes;
-      mma_ss4(d, desc_k_major(at), desc_k_major(at + kWeights), idesc, b > from, lead);
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m)
+        mma_ss4(d + m * (p.columns / kTiles), desc_k_major(at + m * (128 * 128)), desc_k_major(at + kWeights), idesc, b > from, lead);
       mma_commit(&sh->empty[stage], lead);
       if (++stage == p.stages) {
         stage = 0;
@@ -204,6 +213,7 @@ __global__ void __launch_bounds__(kCta) many_kernel(ManyParams p) {
     }
     mma_commit(&sh->done, lead);
   } else {
+    dependency_wait();  // the launch that lays the tokens out
     const uint8_t* src = p.tiles_at + (int64_t)blockIdx.y * p.blocks * p.tile * 128;
     const uint32_t bytes = p.tile * 128;
     int stage = 0;
@@ -234,13 +244,14 @@ __global__ void __launch_bounds__(kCta) many_kernel(ManyParams p) {
   __syncthreads();
   const bool bad = *(volatile int*)&sh->gave_up != 0;
 
-  // a thread a row, 16 tokens at a time; the two sets of four warps take turns
+  // a thread a row, 16 tokens at a time; two sets of four warps take turns with a tile's
   float* joined = reinterpret_cast<float*>(smem);  // [token][row]
-  if (warp < 8) {
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  dependency_wait();
+  if (warp < kUnpackWarps) {
+    const int tile = warp >> 3, row = tile * 128 + (warp & 3) * 32 + lane;
+    const uint32_t at = tmem + tile * (p.columns / kTiles) + ((uint32_t)((warp & 3) * 32) << 16);
 #pragma unroll 1
-    for (int c = (warp >> 2) * 16; c < tokens; c += 32) {
+    for (int c = (warp >> 2 & 1) * 16; c < tokens; c += 32) {
       uint32_t y[16];
       tmem_read16(at + c, y);
 #pragma unroll
@@ -273,12 +284,12 @@ __global__ void __launch_bounds__(kCta) many_kernel(ManyParams p) {
   }
   fence_after();
   dependents_launch();
-  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(p.columns) : "memory");
+  if (warp == kUnpackWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(p.columns) : "memory");
 }
 
 std::mutex g_mu;
-bool g_set[64];
-constexpr int kSmemMost = 200 * 1024;
+bool g_set[64][2];
+constexpr int kSmemMost = 220 * 1024;
 
 }  // namespace
 
@@ -291,16 +302,16 @@ ManyPlan many_plan(int sms, int64_t tokens, int64_t n, int64_t k) {
   a.tile = (int)((tokens + a.tiles - 1) / a.tiles + 15) / 16 * 16;
   a.tiles = (int)((tokens + a.tile - 1) / a.tile);
   a.blocks = (k + kBlock - 1) / kBlock;
-  const int stage = kWeights + a.tile * 128;
-  // two CTAs an SM where four stages of each fit
-  a.stages = 4;
-  const int64_t slots = (int64_t)sms * (4 * stage <= 110 * 1024 ? 2 : 1);
-  const int64_t ctas = (n + kRows - 1) / kRows * a.tiles;
+  a.row_tiles = 2;
+  const int stage = a.row_tiles * 128 * 128 + a.tile * 128;
+  a.stages = (kSmemMost - 2048) / stage;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  const int64_t ctas = (n + a.row_tiles * 128 - 1) / (a.row_tiles * 128) * a.tiles;
   a.parts = 1;
-  while (a.parts < kMaxParts && ctas * a.parts * 2 <= slots && a.blocks >= a.parts * 8) a.parts *= 2;
+  while (a.parts < kMaxParts && ctas * (a.parts + 1) <= sms && a.blocks >= (a.parts + 1) * 4) ++a.parts;
   a.smem = a.stages * stage;
-  const int join = a.tile * kRows * 4;
-  if (a.parts > 1 && join > a.smem) a.smem = join;
+  const int join = a.tile * a.row_tiles * 128 * 4;
+  if (a.parts > 1 && join > a.smem) a.parts = 1;
   a.smem += 1024;
   a.x_bytes = (int64_t)a.tiles * a.tile * a.blocks * 128;
   a.bytes = a.x_bytes + (int64_t)a.tiles * a.tile * 4;
@@ -308,12 +319,13 @@ ManyPlan many_plan(int sms, int64_t tokens, int64_t n, int64_t k) {
 }
 
 lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream) {
+  const bool two = plan.row_tiles == 2;
+  const void* func = two ? reinterpret_cast<const void*>(&many_kernel<2>) : reinterpret_cast<const void*>(&many_kernel<1>);
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    if (!g_set[dev]) {
-      if (cudaFuncSetAttribute(reinterpret_cast<const void*>(&many_kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess)
-        return LT_ERR_CUDA;
-      g_set[dev] = true;
+    if (!g_set[dev][two]) {
+      if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess) return LT_ERR_CUDA;
+      g_set[dev][two] = true;
     }
   }
   p->tile = plan.tile;
@@ -322,10 +334,11 @@ lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream
   p->blocks = (int32_t)plan.blocks;
   p->columns = 32;
   while (p->columns < plan.tile) p->columns *= 2;
+  p->columns *= plan.row_tiles;
   const lt_status st = kv4::launch(reinterpret_cast<const void*>(&layout_kernel), dim3((unsigned)p->tokens), kLayoutThreads, 0, p, stream);
   if (st != LT_OK) return st;
-  const int64_t row_tiles = ((int64_t)p->n + kRows - 1) / kRows;
-  return kv4::launch(reinterpret_cast<const void*>(&many_kernel), dim3((unsigned)(row_tiles * plan.parts), (unsigned)plan.tiles), kCta,
+  const int64_t rows = ((int64_t)p->n + plan.row_tiles * 128 - 1) / (plan.row_tiles * 128);
+  return kv4::launch(func, dim3((unsigned)(rows * plan.parts), (unsigned)plan.tiles), two ? Many<2>::kCta : Many<1>::kCta,
                      (unsigned)plan.smem, p, stream, plan.parts);
 }
 
