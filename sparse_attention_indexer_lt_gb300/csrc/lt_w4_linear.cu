@@ -38,6 +38,7 @@ struct LinearParams {
   int32_t row_warps;   // row tiles of a CTA: 1, 2, 4 or 8
   int32_t parts;       // CTAs of a cluster, along the inputs
   int32_t chunk;       // steps whose inputs are in shared memory at a time
+  int32_t join_at;     // where the warps' sums are joined, behind the inputs
   int32_t bf16;
 };
 
@@ -59,74 +60,88 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
 // that read 16 bytes together have all banks.
 __device__ __forceinline__ int piece_at(int t, int q, int pitch) { return t * pitch + ((q ^ (q >> 3 & 1)) << 4); }
 
+constexpr int few_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+
 template <int NT>
-__global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) few_kernel(LinearParams p) {
+__global__ void __launch_bounds__(kThreads, few_per_sm(NT)) few_kernel(LinearParams p) {
   constexpr int kTokens = NT * 8;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t largest[kTokens];
-  __shared__ float inverse[kTokens];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int k_warps = kWarps / p.row_warps, wr = warp % p.row_warps, wk = warp / p.row_warps;
   const int rank = blockIdx.x % p.parts;
-  const int row0 = (int)(blockIdx.x / p.parts) * p.row_warps * 16;
-  const int token0 = blockIdx.y * kTokens, tokens = min(p.tokens - token0, kTokens);
+  const int rows = p.row_warps * 16;
+  const int tokens = p.tokens;
   const int steps = (p.k + kStep - 1) / kStep, groups = p.k / 32;
-  // the CTA's steps, then the warp's
+  // the CTA's steps, in chunks whose inputs fit into shared memory; its row blocks are every so many
   const int s_begin = (int)((int64_t)steps * rank / p.parts), s_end = (int)((int64_t)steps * (rank + 1) / p.parts);
+  const int chunks = (s_end - s_begin + p.chunk - 1) / p.chunk;
+  const int blocks = (p.n + rows - 1) / rows, first = blockIdx.x / p.parts, every = gridDim.x / p.parts;
   if (tid < kTokens) largest[tid] = 0u;
   dependency_wait();
   __syncthreads();
 
-  const int ra = min(row0 + wr * 16 + g, p.n - 1), rb = min(row0 + wr * 16 + g + 8, p.n - 1);
-  const uint8_t* codes_a = p.codes + (int64_t)ra * (p.k / 2) + c * 16;
-  const uint8_t* codes_b = p.codes + (int64_t)rb * (p.k / 2) + c * 16;
-  const uint16_t* scales_a = reinterpret_cast<const uint16_t*>(p.scales) + (int64_t)ra * groups + c;
-  const uint16_t* scales_b = reinterpret_cast<const uint16_t*>(p.scales) + (int64_t)rb * groups + c;
+  // the warp's steps of a chunk
+  auto range = [&](int chunk, int* from, int* to) {
+    const int c0 = s_begin + chunk * p.chunk, wide = min(p.chunk, s_end - c0);
+    *from = c0 + wide * wk / k_warps;
+    *to = c0 + wide * (wk + 1) / k_warps;
+  };
 
-  float acc[NT][4];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-  float power[NT][2];  // of tokens 2c and 2c + 1, whose sums a lane has
-#pragma unroll
-  for (int t = 0; t < NT; ++t) power[t][0] = power[t][1] = 1.0f;
-
-  const int pitch = p.chunk * kStep * 2 + 32;
-  constexpr int U = 2;  // steps of a batch; one batch is on its way while another is worked on
+  constexpr int U = 2;  // steps of a batch; two batches are on their way
   struct Batch {
     uint4 a[U], b[U];
     uint32_t sa[U], sb[U];
   };
-  auto fetch = [&](Batch& w, int from, int to) {
+  // where the next batch is fetched from: it runs ahead over chunks and row blocks
+  struct Next {
+    int block, chunk, s, to;
+    const uint8_t *a, *b;
+    const uint16_t *sa, *sb;
+  } next = {};
+  auto aim = [&]() {  // at the rows of next.block
+    const int ra = min(next.block * rows + wr * 16 + g, p.n - 1), rb = min(next.block * rows + wr * 16 + g + 8, p.n - 1);
+    next.a = p.codes + (int64_t)ra * (p.k / 2);
+    next.b = p.codes + (int64_t)rb * (p.k / 2);
+    next.sa = reinterpret_cast<const uint16_t*>(p.scales) + (int64_t)ra * groups;
+    next.sb = reinterpret_cast<const uint16_t*>(p.scales) + (int64_t)rb * groups;
+  };
+  auto fetch = [&](Batch& w) {
+    if (next.block >= blocks) return;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int s = from + u;
-      w.a[u] = w.b[u] = make_uint4(0u, 0u, 0u, 0u);
-      w.sa[u] = w.sb[u] = 0u;
-      if (s < to && s * 4 + c < groups) {
-        w.a[u] = load_once(codes_a + (int64_t)s * 64);
-        w.b[u] = load_once(codes_b + (int64_t)s * 64);
-        w.sa[u] = __ldg(scales_a + s * 4);
-        w.sb[u] = __ldg(scales_b + s * 4);
-      }
+      // (past the inputs' end, and for the odd step of a batch, the last group again: its inputs in shared memory are
+      // zeros there, or it is not used)
+      const int group = min((next.s + u) * 4 + c, groups - 1);
+      w.a[u] = load_once(next.a + (int64_t)group * 16);
+      w.b[u] = load_once(next.b + (int64_t)group * 16);
+      w.sa[u] = __ldg(next.sa + group);
+      w.sb[u] = __ldg(next.sb + group);
     }
+    next.s += U;
+    if (next.s < next.to) return;
+    do {
+      if (++next.chunk == chunks) {
+        next.chunk = 0;
+        next.block += every;
+        if (next.block >= blocks) return;
+        aim();
+      }
+      range(next.chunk, &next.s, &next.to);
+    } while (next.s >= next.to);  // (every warp has steps in the first chunk, or none at all)
   };
-  const uint32_t x_at = lt::smem_u32(smem);
 
-  for (int c0 = s_begin; c0 < s_end; c0 += p.chunk) {
-    const int c1 = min(c0 + p.chunk, s_end), wide = c1 - c0;
-    // the warp's steps of the chunk
-    const int from = c0 + wide * wk / k_warps, to = c0 + wide * (wk + 1) / k_warps;
-    Batch w[2];
-    fetch(w[0], from, to);
-    fetch(w[1], from + U, to);
-    // the chunk's inputs into shared memory; past the last input, zeros
-    const int pieces = wide * 16;
+  const int pitch = p.chunk * kStep * 2 + 32;
+  const uint32_t x_at = lt::smem_u32(smem);
+  // a chunk's inputs into shared memory; past the last input, zeros
+  auto stage = [&](int chunk) {
+    const int c0 = s_begin + chunk * p.chunk, pieces = min(p.chunk, s_end - c0) * 16;
     for (int t = 0; t < tokens; ++t) {
-      const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)(token0 + t) * p.x_stride + (int64_t)c0 * kStep;
+      const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)t * p.x_stride + (int64_t)c0 * kStep;
       uint32_t big = 0;
       for (int q = tid; q < pieces; q += kThreads) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (c0 * kStep + q * 8 < p.k) v = __ldg(reinterpret_cast<const uint4*>(x) + q);
+        if ((int64_t)c0 * kStep + q * 8 < p.k) v = __ldg(reinterpret_cast<const uint4*>(x) + q);
         *reinterpret_cast<uint4*>(smem + piece_at(t, q, pitch)) = v;
         if (p.bf16) big = max(big, largest_of(v));
       }
@@ -135,104 +150,141 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) few_kernel(LinearPa
         if (lane == 0) atomicMax(&largest[t], big);
       }
     }
-    if (p.bf16) {
-      __syncthreads();
-      for (int t = 0; t < tokens; ++t) {
-        const float mul = token_power(largest[t]);
-        for (int q = tid; q < pieces; q += kThreads) {
-          uint4* at = reinterpret_cast<uint4*>(smem + piece_at(t, q, pitch));
-          *at = to_half(*at, mul);
-        }
+    __syncthreads();
+    if (!p.bf16) return;
+    for (int t = 0; t < tokens; ++t) {
+      const float mul = token_power(largest[t]);
+      for (int q = tid; q < pieces; q += kThreads) {
+        uint4* at = reinterpret_cast<uint4*>(smem + piece_at(t, q, pitch));
+        *at = to_half(*at, mul);
       }
-      // sums so far go over to the new power, which is the largest input's so far and never grows
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float now = token_power(largest[min(t * 8 + 2 * c + e, tokens - 1)]);
-          if (c0 > s_begin) {
-            const float f = fmaxf(now / power[t][e], 0x1p-126f);  // (not 0: an infinity stays one)
-            acc[t][e] *= f;
-            acc[t][e + 2] *= f;
-          }
-          power[t][e] = now;
-        }
     }
     __syncthreads();
+  };
 
-    for (int s0 = from; s0 < to; s0 += 2 * U) {
+  Batch w0, w1;
+  next.block = first;
+  next.chunk = 0;
+  range(0, &next.s, &next.to);
+  const bool works = next.s < next.to && first < blocks;
+  if (works) {
+    aim();
+    fetch(w0);
+    fetch(w1);
+  }
+  if (chunks == 1) stage(0);
+
+  float acc[NT][4];
+  float power[NT][2];  // of tokens 2c and 2c + 1, whose sums a lane has
+  uint32_t xa[NT];     // the lane's token's inputs
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+  for (int t = 0; t < NT; ++t) xa[t] = x_at + min(t * 8 + g, tokens - 1) * pitch;
+  const int q0 = c * 4, turn = c >> 1;  // (see piece_at)
+  auto work = [&](const Batch& w, int at, int count) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int s = s0 + half * U + u;
-          if (s >= to) break;
-          const uint32_t ka = __byte_perm(w[half].sa[u], 0, 0x1010), kb = __byte_perm(w[half].sb[u], 0, 0x1010);
-          const uint32_t wa[4] = {w[half].a[u].x, w[half].a[u].y, w[half].a[u].z, w[half].a[u].w};
-          const uint32_t wb[4] = {w[half].b[u].x, w[half].b[u].y, w[half].b[u].z, w[half].b[u].w};
+    for (int u = 0; u < U; ++u) {
+      if (u >= count) break;
+      const uint32_t ka = __byte_perm(w.sa[u], 0, 0x1010), kb = __byte_perm(w.sb[u], 0, 0x1010);
+      const uint32_t wa[4] = {w.a[u].x, w.a[u].y, w.a[u].z, w.a[u].w};
+      const uint32_t wb[4] = {w.b[u].x, w.b[u].y, w.b[u].z, w.b[u].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t ha[4], hb[4];
-            codes_to_half2(wa[j], ha);
-            codes_to_half2(wb[j], hb);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t ha[4], hb[4];
+        codes_to_half2(wa[j], ha);
+        codes_to_half2(wb[j], hb);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              ha[i] = hmul2(ha[i], ka);
-              hb[i] = hmul2(hb[i], kb);
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const int token = min(t * 8 + g, tokens - 1), q = (s - c0) * 16 + c * 4 + j;
-              uint32_t b0, b1, b2, b3;
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3) : "r"(x_at + piece_at(token, q, pitch)));
-              mma16816(acc[t], ha[0], hb[0], ha[1], hb[1], b0, b1);
-              mma16816(acc[t], ha[2], hb[2], ha[3], hb[3], b2, b3);
-            }
-          }
+        for (int i = 0; i < 4; ++i) {
+          ha[i] = hmul2(ha[i], ka);
+          hb[i] = hmul2(hb[i], kb);
         }
-        fetch(w[half], s0 + (half + 2) * U, to);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          uint32_t b0, b1, b2, b3;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3) : "r"(xa[t] + (((at + u) * 16 + q0 + (j ^ turn)) << 4)));
+          mma16816(acc[t], ha[0], hb[0], ha[1], hb[1], b0, b1);
+          mma16816(acc[t], ha[2], hb[2], ha[3], hb[3], b2, b3);
+        }
       }
     }
-    __syncthreads();  // the chunk's inputs have been read
+  };
+
+  float* joined = reinterpret_cast<float*>(smem + p.join_at);  // two times [k warp][token][row], in turn
+  int phase = 0, turns = 0;
+  for (int block = first; block < blocks; block += every, turns ^= 1) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+      power[t][0] = power[t][1] = p.bf16 ? 0.0f : 1.0f;
+    }
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+      if (chunks > 1) {
+        __syncthreads();  // the last chunk's inputs have been read
+        stage(chunk);
+      }
+      if (p.bf16) {
+        // sums so far go over to the new power, which is the largest input's so far and never grows
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float now = token_power(largest[min(t * 8 + 2 * c + e, tokens - 1)]);
+            if (chunk > 0) {
+              const float f = fmaxf(now / power[t][e], 0x1p-126f);  // (not 0: an infinity stays one)
+              acc[t][e] *= f;
+              acc[t][e + 2] *= f;
+            }
+            power[t][e] = now;
+          }
+      }
+      int from, to;
+      range(chunk, &from, &to);
+      const int c0 = s_begin + chunk * p.chunk;
+      for (int s = from; s < to; s += U) {
+        if (phase == 0) {
+          work(w0, s - c0, to - s);
+          fetch(w0);
+        } else {
+          work(w1, s - c0, to - s);
+          fetch(w1);
+        }
+        phase ^= 1;
+      }
+    }
+    // join the warps, and with a cluster its CTAs
+    float* mine = joined + turns * (kWarps * 16 * kTokens);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int token = t * 8 + 2 * c + (e & 1), row = wr * 16 + g + (e >> 1) * 8;
+        if (token < tokens) mine[(wk * kTokens + token) * rows + row] = p.bf16 ? acc[t][e] * (1.0f / power[t][e & 1]) : acc[t][e];
+      }
+    __syncthreads();
+    const int all = tokens * rows;
+    if (p.parts > 1) {
+      for (int u = tid; u < all; u += kThreads) {
+        float y = mine[u];
+        for (int w = 1; w < k_warps; ++w) y += mine[w * kTokens * rows + u];
+        mine[u] = y;
+      }
+      cluster_sync();
+    }
+    for (int u = rank * kThreads + tid; u < all; u += p.parts * kThreads) {
+      const int token = u / rows, row = block * rows + u % rows;
+      float y = 0.0f;
+      if (p.parts > 1) {
+#pragma unroll
+        for (int r = 0; r < kMaxParts; ++r)
+          if (r < p.parts) y += peer_f32(lt::smem_u32(mine) + u * 4, r);
+      } else {
+        for (int w = 0; w < k_warps; ++w) y += mine[w * kTokens * rows + u];
+      }
+      if (row < p.n) put(p.out, (int64_t)token * p.out_stride + row, y, p.bias, row, p.bf16);
+    }
+    if (p.parts > 1) cluster_sync();  // (a CTA's shared memory stays until its peers have read it)
   }
   dependents_launch();
-
-  // join the warps: [k warp][token][row]
-  if (p.bf16 && tid < kTokens) inverse[tid] = 1.0f / token_power(largest[min(tid, tokens - 1)]);
-  __syncthreads();
-  const int rows = p.row_warps * 16;
-  float* joined = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int token = t * 8 + 2 * c + (e & 1), row = wr * 16 + g + (e >> 1) * 8;
-      joined[(wk * kTokens + token) * rows + row] = p.bf16 ? acc[t][e] * inverse[token] : acc[t][e];
-    }
-  __syncthreads();
-  const int all = tokens * rows;
-  if (p.parts > 1) {
-    for (int u = tid; u < all; u += kThreads) {
-      float y = joined[u];
-      for (int w = 1; w < k_warps; ++w) y += joined[w * kTokens * rows + u];
-      joined[u] = y;
-    }
-    cluster_sync();
-  }
-  for (int u = rank * kThreads + tid; u < all; u += p.parts * kThreads) {
-    const int token = u / rows, row = row0 + u % rows;
-    float y = 0.0f;
-    if (p.parts > 1) {
-#pragma unroll
-      for (int r = 0; r < kMaxParts; ++r)
-        if (r < p.parts) y += peer_f32(x_at + u * 4, r);
-    } else {
-      for (int w = 0; w < k_warps; ++w) y += joined[w * kTokens * rows + u];
-    }
-    if (row < p.n) put(p.out, (int64_t)(token0 + token) * p.out_stride + row, y, p.bias, row, p.bf16);
-  }
-  if (p.parts > 1) cluster_sync();  // (a CTA's shared memory stays until its peers have read it)
 }
 
 // ---- quantisation: a thread eight inputs, four lanes a group
@@ -275,7 +327,7 @@ bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
-bool g_set[kMaxDevices][3];
+bool g_set[kMaxDevices][2];
 
 lt_status device_of(int* dev, int* sms) {
   if (cudaGetDevice(dev) != cudaSuccess) return LT_ERR_CUDA;
@@ -288,12 +340,11 @@ lt_status device_of(int* dev, int* sms) {
 }
 
 const void* few_ptr(int nt) {
-  return nt == 1   ? reinterpret_cast<const void*>(&few_kernel<1>)
-         : nt == 2 ? reinterpret_cast<const void*>(&few_kernel<2>)
-                   : reinterpret_cast<const void*>(&few_kernel<4>);
+  return nt == 1 ? reinterpret_cast<const void*>(&few_kernel<1>) : reinterpret_cast<const void*>(&few_kernel<2>);
 }
 
-constexpr int kFewSmem = 64 * 1024;
+constexpr int kFewInputs = 56 * 1024;  // bytes of inputs in shared memory: three CTAs an SM
+constexpr int kFewSmem = kFewInputs + 16 * 1024;
 constexpr int kFew = 16;  // tokens up to which the weights go to the tensor core from registers
 
 lt_status check_sizes(int64_t tokens, int64_t n, int64_t k) {
@@ -394,32 +445,33 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
   p.k = (int32_t)k;
   p.tokens = (int32_t)tokens;
   p.bf16 = dtype == LT_DTYPE_BF16;
-  const int nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
-  const int64_t token_tiles = (tokens + nt * 8 - 1) / (nt * 8);
-  const int here = tokens < nt * 8 ? (int)tokens : nt * 8;
+  const int nt = tokens <= 8 ? 1 : 2, here = (int)tokens;
   p.row_warps = here <= 2 ? 1 : here <= 4 ? 2 : here <= 8 ? 4 : 8;
   const int64_t row_blocks = (n + p.row_warps * 16 - 1) / (p.row_warps * 16);
   const int steps = (int)((k + kStep - 1) / kStep), k_warps = kWarps / p.row_warps;
-  const int64_t slots = (int64_t)sms * (nt == 4 ? 2 : 3);
+  const int64_t slots = (int64_t)sms * few_per_sm(nt);
+  // as many steps' inputs in shared memory as fit; the inputs are cut over a cluster where the CTAs do not fill the SMs
+  const int most = (kFewInputs / here - 32) / (kStep * 2);
   p.parts = 1;
-  while (p.parts < kMaxParts && row_blocks * token_tiles * p.parts * 2 <= slots * 2 && steps >= p.parts * 2 * k_warps * 2) p.parts *= 2;
-  // inputs in shared memory at a time: as many steps as fit
-  const int most = (kFewSmem / here - 32) / (kStep * 2);
+  while (p.parts < kMaxParts && steps >= p.parts * 2 * k_warps &&
+         (row_blocks * p.parts * 2 <= slots || (steps + p.parts - 1) / p.parts > most))
+    p.parts *= 2;
   const int mine = (steps + p.parts - 1) / p.parts;
   p.chunk = mine < most ? mine : most / k_warps * k_warps;
-  const int x_bytes = here * (p.chunk * kStep * 2 + 32), join_bytes = k_warps * nt * 8 * p.row_warps * 16 * 4;
-  const int smem = x_bytes > join_bytes ? x_bytes : join_bytes;
-  if (row_blocks * p.parts > INT32_MAX || token_tiles > 65535) return LT_ERR_UNSUPPORTED;
+  p.join_at = here * (p.chunk * kStep * 2 + 32);
+  const int smem = p.join_at + 2 * kWarps * 16 * nt * 8 * 4;
+  const int64_t resident = slots / p.parts;
+  const int64_t ctas = row_blocks < resident ? row_blocks : resident;
   const void* func = few_ptr(nt);
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    bool& set = g_set[dev][nt / 2];
+    bool& set = g_set[dev][nt - 1];
     if (!set) {
       if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) != cudaSuccess) return LT_ERR_CUDA;
       set = true;
     }
   }
-  return launch(func, dim3((unsigned)(row_blocks * p.parts), (unsigned)token_tiles), kThreads, (unsigned)smem, &p, stream, p.parts);
+  return launch(func, dim3((unsigned)(ctas * p.parts)), kThreads, (unsigned)smem, &p, stream, p.parts);
 }
 
 }  // extern "C"
