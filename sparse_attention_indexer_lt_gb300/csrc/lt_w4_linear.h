@@ -57,7 +57,8 @@ struct ManyPlan {
   int tile, tiles;    // tokens of a tile, a multiple of 16 up to 256; tiles
   int row_tiles;      // tiles of 128 outputs of a CTA: 1 or 2
   int parts;          // CTAs of a cluster, along the inputs
-  int stages;
+  int code_ring, token_ring, row_ring;  // places for codes and tokens in shared memory, unpacked weights in tensor memory
+  int sum_columns;    // of tensor memory, for the sums of a tile of outputs
   int smem;
   int64_t blocks;     // of 64 inputs
   int64_t x_bytes, bytes;  // workspace: the tokens as the tensor core reads them; with their powers
@@ -73,8 +74,9 @@ struct ManyParams {
   uint8_t* tiles_at;  // [tile][block][token][64 inputs], each token's eight 16-byte pieces turned by the token
   float* inverse;     // [token]
   int64_t x_stride, out_stride;
-  int32_t n, k, tokens, tile, parts, stages, blocks, columns;
-  int32_t bf16;
+  int32_t n, k, tokens, tile, parts, blocks;
+  int32_t code_ring, token_ring, row_ring, sum_columns, rows_column;
+  int32_t bf16, wide_scales;
 };
 lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream);
 

@@ -1,16 +1,20 @@
 // lt_w4_many.cu -- products with 4-bit weights for many tokens: tcgen05, the sums in tensor memory.
 //
-// A CTA takes 128 outputs and a tile of up to 256 tokens; the weights are the product's 128 rows, the tokens its
-// columns, so a tile of few tokens wastes nothing. In steps of 64 inputs,
-//   warps 0 to 7  unpack the step's weights: a thread a group of 32 of one output, codes times scale in fp16, written with the
-//                 128-byte swizzle that the tensor core reads; its codes come straight from memory, four steps ahead
-//   warp 8        issues the products
-//   warp 9        brings the step's tokens, one bulk copy
+// A CTA takes one or two tiles of 128 outputs and a tile of up to 256 tokens; the weights are the product's
+// 128 rows, the tokens its columns, so a tile of few tokens wastes nothing. In steps of 64 inputs,
+//   eight warps a tile of outputs   unpack: a thread a group of 32 inputs of one output, codes times scale in fp16, into tensor
+//                 memory, where the product reads its rows: shared memory, which carries codes and tokens,
+//                 could not take the unpacked weights' way in and out as well
+//   one warp      issues the products
+//   two warps     bring the codes, 256 inputs at a time by a tensor map, and the tokens, a bulk copy a step
 // The tokens are laid out for that by a launch before: fp16, scaled by a power of two for each token (bf16's
 // range does not fit), swizzled, a step's tile contiguous. Where there are few outputs a cluster cuts the inputs, and its
 // parts join over distributed shared memory in one order.
 
+#include <cmath>
 #include <mutex>
+
+#include <cudaTypedefs.h>
 
 #include "lt_kv4_tcgen05.cuh"
 #include "lt_w4_linear.h"
@@ -20,19 +24,20 @@ namespace {
 using namespace lt::kv4;
 using namespace lt::w4;
 
-// A CTA has one or two tiles of 128 outputs, two threads an output that unpack.
 template <int kTiles>
 struct Many {
   static constexpr int kRows = 128 * kTiles;
-  static constexpr int kUnpackers = 2 * kRows;
-  static constexpr int kCta = kUnpackers + 64;
-  static constexpr int kWeights = kRows * 128;  // bytes of a step's unpacked weights
+  static constexpr int kUnpackWarps = 8 * kTiles;
+  static constexpr int kCta = kUnpackWarps * 32 + 96;
+  static constexpr int kPacked = kRows * 128;  // bytes of the codes of 256 inputs
 };
-constexpr int kMaxStages = 8;
-constexpr int kAhead = 6;  // steps whose codes a thread has asked for
+constexpr int kMaxRing = 8;
+constexpr int kColumns = 512;
 
 struct Shared {
-  uint64_t tokens_full[kMaxStages], weights_full[kMaxStages], empty[kMaxStages];
+  uint64_t codes_full[kMaxRing], codes_empty[kMaxRing];
+  uint64_t tokens_full[kMaxRing], tokens_empty[kMaxRing];
+  uint64_t rows_full[kMaxRing], rows_empty[kMaxRing];  // unpacked weights in tensor memory
   uint64_t done;
   uint32_t tmem;
   int gave_up;
@@ -101,84 +106,114 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_kernel(ManyParams p) {
     write(q, q < there ? __ldg(x + q) : make_uint4(0u, 0u, 0u, 0u));
 }
 
-__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+// A place in a ring: its index and the parity of its round.
+struct Turn {
+  int at = 0;
+  uint32_t parity;
+  __device__ __forceinline__ explicit Turn(uint32_t first) : parity(first) {}
+  __device__ __forceinline__ void next(int ring) {
+    if (++at == ring) {
+      at = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ void tensor_in(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+               :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(lt::smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ void unpack_role(const ManyParams& p, Shared* sh, uint32_t ring, uint32_t stage_bytes, int row0, int from, int to) {
-  const int tid = threadIdx.x, lane = tid & 31, row = tid / 2, half = tid & 1;
-  const int64_t of = min(row0 + row, p.n - 1);
+// Super-steps of 256 inputs, four steps each. A thread has an output, and one of the two groups of each step.
+template <int kTiles>
+__device__ __forceinline__ void unpack_role(const ManyParams& p, Shared* sh, uint32_t packed, int row0, int from, int to) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = warp >> 2 & 1, tile = warp >> 3;
+  const int row = tile * 128 + (warp & 3) * 32 + lane;  // (a warp reaches 32 lanes of tensor memory, by its number)
   const int groups = p.k / 32;
-  const uint8_t* codes = p.codes + of * (p.k / 2) + half * 16;
-  const uint16_t* scales = p.scales + of * groups + half;
-  uint32_t piece[4];  // where the group's four 16-byte pieces of fp16 lie
+  const uint16_t* scales = p.scales + (int64_t)min(row0 + row, p.n - 1) * groups;
+  // a row is 64 bytes of each of two boxes, its four 16-byte pieces turned by the row's second and third bit
+  const uint32_t row_at = packed + row * 64;
+  const uint32_t turn = (uint32_t)(row >> 1 & 3);
+  const uint32_t column = sh->tmem + ((uint32_t)((warp & 3) * 32) << 16) + p.rows_column + tile * 32 + half * 16;
+  auto scales_of = [&](uint32_t (&s)[4], int u) {
+    if (u >= to) return;
+    if (p.wide_scales) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(scales + u * 8));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) piece[j] = ring + row * 128 + (((half * 4 + j) ^ (row & 7)) << 4);
-  uint4 code[kAhead];
-  uint32_t scale[kAhead];
-  auto fetch = [&](int i, int b) {
-    code[i] = make_uint4(0u, 0u, 0u, 0u);
-    scale[i] = 0u;
-    if (b < to && b * 2 + half < groups) {
-      code[i] = load_codes(codes + (int64_t)b * 32);
-      scale[i] = __ldg(scales + b * 2);
+      for (int i = 0; i < 4; ++i) s[i] = half ? w[i] >> 16 : w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = __ldg(scales + min(u * 8 + i * 2 + half, groups - 1));  // (codes past the end are zeros)
     }
   };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch(i, from + i);
-  int stage = 0;
-  uint32_t parity = 1;  // (the first round's stages are free)
+  uint32_t s[4] = {}, later[4] = {};
+  scales_of(s, from);
+  Turn code(0), place(1);
 #pragma unroll 1
-  for (int b0 = from; b0 < to; b0 += kAhead) {
+  for (int u = from; u < to; ++u) {
+    scales_of(later, u + 1);
+    wait_warp(&sh->codes_full[code.at], code.parity, sh);
+    uint32_t w[4][4];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (b0 + i >= to) break;
-      const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w}, s = __byte_perm(scale[i], 0, 0x1010);
-      fetch(i, b0 + i + kAhead);
-      wait_warp(&sh->empty[stage], parity, sh);
+    for (int i = 0; i < 4; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                   : "r"(row_at + code.at * Many<kTiles>::kPacked + (i >> 1) * (Many<kTiles>::kRows * 64) + ((((i & 1) * 2 + half) ^ turn) << 4)));
+    __syncwarp();
+    if (lane == 0) arrive(&sh->codes_empty[code.at]);
+    code.next(p.code_ring);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (u * 4 + i >= p.blocks) break;
+      const uint32_t scale = __byte_perm(s[i], 0, 0x1010);
+      uint32_t h[16];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        uint32_t h[4];
-        codes_to_half2(w[j], h);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                     :: "r"(piece[j] + stage * stage_bytes), "r"(hmul2(h[0], s)), "r"(hmul2(h[1], s)), "r"(hmul2(h[2], s)),
-                        "r"(hmul2(h[3], s)) : "memory");
+        uint32_t x[4];
+        codes_to_half2(w[i][j], x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[4 * j + e] = hmul2(x[e], scale);
       }
-      fence_async();
+      wait_warp(&sh->rows_empty[place.at], place.parity, sh);
+      fence_after();
+      tmem_st16(column + place.at * (kTiles * 32), h);
+      tmem_wait_st();
+      fence_before();
       __syncwarp();
-      if (lane == 0) arrive(&sh->weights_full[stage]);
-      if (++stage == p.stages) {
-        stage = 0;
-        parity ^= 1u;
-      }
+      if (lane == 0) arrive(&sh->rows_full[place.at]);
+      place.next(p.row_ring);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = later[i];
   }
 }
 
 template <int kTiles>
-__global__ void __launch_bounds__(Many<kTiles>::kCta) many_kernel(ManyParams p) {
-  constexpr int kRows = Many<kTiles>::kRows, kCta = Many<kTiles>::kCta, kWeights = Many<kTiles>::kWeights;
-  constexpr int kUnpackWarps = Many<kTiles>::kUnpackers / 32;
+__global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams p, const __grid_constant__ CUtensorMap codes) {
+  constexpr int kRows = Many<kTiles>::kRows, kCta = Many<kTiles>::kCta, kUnpackWarps = Many<kTiles>::kUnpackWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (lt::smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ Shared shared;
   Shared* sh = &shared;
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
-  const uint32_t ring = lt::smem_u32(smem), stage_bytes = kWeights + p.tile * 128;
+  const uint32_t packed = lt::smem_u32(smem), token_bytes = p.tile * 128;
+  const uint32_t tokens_at = packed + p.code_ring * Many<kTiles>::kPacked;
   if (tid == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (int s = 0; s < kMaxRing; ++s) {
+      lt::mbar_init(&sh->codes_full[s], 1);
+      lt::mbar_init(&sh->codes_empty[s], kUnpackWarps);
       lt::mbar_init(&sh->tokens_full[s], 1);
-      lt::mbar_init(&sh->weights_full[s], kUnpackWarps);
-      lt::mbar_init(&sh->empty[s], 1);
+      lt::mbar_init(&sh->tokens_empty[s], 1);
+      lt::mbar_init(&sh->rows_full[s], kUnpackWarps);
+      lt::mbar_init(&sh->rows_empty[s], 1);
     }
     lt::mbar_init(&sh->done, 1);
     sh->gave_up = 0;
     lt::mbar_fence_init();
   }
   if (warp == kUnpackWarps) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(lt::smem_u32(&sh->tmem)), "r"(p.columns) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(lt::smem_u32(&sh->tmem)), "n"(kColumns) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
@@ -187,59 +222,69 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta) many_kernel(ManyParams p) 
 
   const int rank = blockIdx.x % p.parts, row0 = (int)(blockIdx.x / p.parts) * kRows;
   const int token0 = blockIdx.y * p.tile, tokens = min(p.tokens - token0, p.tile);
-  const int from = (int)((int64_t)p.blocks * rank / p.parts), to = (int)((int64_t)p.blocks * (rank + 1) / p.parts);
+  // super-steps of 256 inputs, and their steps
+  const int supers = (p.blocks + 3) / 4;
+  const int from = (int)((int64_t)supers * rank / p.parts), to = (int)((int64_t)supers * (rank + 1) / p.parts);
+  const int first = from * 4, last = min(to * 4, p.blocks);
   const uint32_t tmem = sh->tmem;
 
   if (warp < kUnpackWarps) {
-    unpack_role(p, sh, ring, stage_bytes, row0, from, to);
+    unpack_role<kTiles>(p, sh, packed, row0, from, to);
   } else if (warp == kUnpackWarps) {
     const uint32_t lead = elect_one(), idesc = instruction(p.tile, false), d = __shfl_sync(~0u, tmem, 0);
-    int stage = 0;
-    uint32_t parity = 0;
+    Turn token(0), place(0);
 #pragma unroll 1
-    for (int b = from; b < to; ++b) {
-      wait_warp(&sh->tokens_full[stage], parity, sh);
-      wait_warp(&sh->weights_full[stage], parity, sh);
+    for (int b = first; b < last; ++b) {
+      wait_warp(&sh->tokens_full[token.at], token.parity, sh);
+      wait_warp(&sh->rows_full[place.at], place.parity, sh);
       fence_after();
-      const uint32_t at = ring + stage * stage_bytes;
+      const uint64_t x = desc_k_major(tokens_at + token.at * token_bytes);
 #pragma unroll
       for (int m = 0; m < kTiles; ++m)
-        mma_ss4(d + m * (p.columns / kTiles), desc_k_major(at + m * (128 * 128)), desc_k_major(at + kWeights), idesc, b > from, lead);
-      mma_commit(&sh->empty[stage], lead);
-      if (++stage == p.stages) {
-        stage = 0;
-        parity ^= 1u;
-      }
+        mma_ts4<2>(d + m * p.sum_columns, d + p.rows_column + (place.at * kTiles + m) * 32, x, idesc, b > first, lead);
+      mma_commit(&sh->rows_empty[place.at], lead);
+      mma_commit(&sh->tokens_empty[token.at], lead);
+      token.next(p.token_ring);
+      place.next(p.row_ring);
     }
     mma_commit(&sh->done, lead);
-  } else {
-    dependency_wait();  // the launch that lays the tokens out
-    const uint8_t* src = p.tiles_at + (int64_t)blockIdx.y * p.blocks * p.tile * 128;
-    const uint32_t bytes = p.tile * 128;
-    int stage = 0;
-    uint32_t parity = 1;
+  } else if (warp == kUnpackWarps + 1) {
+    Turn code(1);
 #pragma unroll 1
-    for (int b = from; b < to; ++b) {
-      wait_warp(&sh->empty[stage], parity, sh);
+    for (int u = from; u < to; ++u) {
+      wait_warp(&sh->codes_empty[code.at], code.parity, sh);
       if (lane == 0) {
-        lt::mbar_arrive_tx(&sh->tokens_full[stage], bytes);
-        lt::bulk_g2s(smem + stage * stage_bytes + kWeights, src + (int64_t)b * bytes, bytes, &sh->tokens_full[stage]);
+        uint64_t* bar = &sh->codes_full[code.at];
+        const uint32_t at = packed + code.at * Many<kTiles>::kPacked;
+        lt::mbar_arrive_tx(bar, Many<kTiles>::kPacked);
+        tensor_in(at, &codes, u * 128, row0, bar);
+        tensor_in(at + kRows * 64, &codes, u * 128 + 64, row0, bar);
       }
       __syncwarp();
-      if (++stage == p.stages) {
-        stage = 0;
-        parity ^= 1u;
+      code.next(p.code_ring);
+    }
+    // nothing is on its way any more, also where somebody gave up
+    const int left = min(to - from, p.code_ring);
+    for (int i = to - from - left; i < to - from; ++i) wait_warp(&sh->codes_full[i % p.code_ring], i / p.code_ring & 1, sh);
+  } else {
+    dependency_wait();  // the launch that lays the tokens out
+    const uint8_t* src = p.tiles_at + (int64_t)blockIdx.y * p.blocks * token_bytes;
+    Turn token(1);
+#pragma unroll 1
+    for (int b = first; b < last; ++b) {
+      wait_warp(&sh->tokens_empty[token.at], token.parity, sh);
+      if (lane == 0) {
+        lt::mbar_arrive_tx(&sh->tokens_full[token.at], token_bytes);
+        lt::bulk_g2s(smem + (tokens_at - packed) + token.at * token_bytes, src + (int64_t)b * token_bytes, token_bytes, &sh->tokens_full[token.at]);
       }
+      __syncwarp();
+      token.next(p.token_ring);
     }
-    // nothing is on its way any more, also where the products' warp gave up
-    const int last = min(to - from, p.stages);
-    for (int i = 0; i < last; ++i) {
-      const int nth = to - from - last + i;
-      wait_warp(&sh->tokens_full[nth % p.stages], nth / p.stages & 1, sh);
-    }
+    const int left = min(last - first, p.token_ring);
+    for (int i = last - first - left; i < last - first; ++i) wait_warp(&sh->tokens_full[i % p.token_ring], i / p.token_ring & 1, sh);
   }
   __syncwarp();
-  wait_warp(&sh->done, 0, sh);  // every product is done: the sums are there, and the ring is free
+  wait_warp(&sh->done, 0, sh);  // every product is done: the sums are there, and the rings are free
   fence_after();
   __syncthreads();
   const bool bad = *(volatile int*)&sh->gave_up != 0;
@@ -249,7 +294,7 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta) many_kernel(ManyParams p) 
   dependency_wait();
   if (warp < kUnpackWarps) {
     const int tile = warp >> 3, row = tile * 128 + (warp & 3) * 32 + lane;
-    const uint32_t at = tmem + tile * (p.columns / kTiles) + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t at = tmem + tile * p.sum_columns + ((uint32_t)((warp & 3) * 32) << 16);
 #pragma unroll 1
     for (int c = (warp >> 2 & 1) * 16; c < tokens; c += 32) {
       uint32_t y[16];
@@ -284,38 +329,87 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta) many_kernel(ManyParams p) 
   }
   fence_after();
   dependents_launch();
-  if (warp == kUnpackWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(p.columns) : "memory");
+  if (warp == kUnpackWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(kColumns) : "memory");
 }
 
 std::mutex g_mu;
 bool g_set[64][2];
 constexpr int kSmemMost = 220 * 1024;
+constexpr int kSmemAlone = 118 * 1024;  // more than half of an SM's
+
+// The driver's call that makes a tensor map, by its name: the library is not linked against it.
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 found = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+        how != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return found;
+}
 
 }  // namespace
 
 namespace lt {
 namespace w4 {
 
+lt_status map_codes(CUtensorMap* map, const void* codes, int64_t n, int64_t k, int rows) {
+  const auto encode = encoder();
+  if (encode == nullptr) return LT_ERR_CUDA;
+  const cuuint64_t dims[2] = {(cuuint64_t)k / 2, (cuuint64_t)n}, strides[1] = {(cuuint64_t)k / 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)rows}, steps[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? LT_OK
+             : LT_ERR_CUDA;
+}
+
 ManyPlan many_plan(int sms, int64_t tokens, int64_t n, int64_t k) {
-  ManyPlan a = {};
-  a.tiles = (int)((tokens + 255) / 256);
-  a.tile = (int)((tokens + a.tiles - 1) / a.tiles + 15) / 16 * 16;
-  a.tiles = (int)((tokens + a.tile - 1) / a.tile);
-  a.blocks = (k + kBlock - 1) / kBlock;
-  a.row_tiles = 2;
-  const int stage = a.row_tiles * 128 * 128 + a.tile * 128;
-  a.stages = (kSmemMost - 2048) / stage;
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  const int64_t ctas = (n + a.row_tiles * 128 - 1) / (a.row_tiles * 128) * a.tiles;
-  a.parts = 1;
-  while (a.parts < kMaxParts && ctas * (a.parts + 1) <= sms && a.blocks >= (a.parts + 1) * 4) ++a.parts;
-  a.smem = a.stages * stage;
-  const int join = a.tile * a.row_tiles * 128 * 4;
-  if (a.parts > 1 && join > a.smem) a.parts = 1;
-  a.smem += 1024;
-  a.x_bytes = (int64_t)a.tiles * a.tile * a.blocks * 128;
-  a.bytes = a.x_bytes + (int64_t)a.tiles * a.tile * 4;
-  return a;
+  ManyPlan best = {};
+  double least = 0.0;
+  const int64_t blocks = (k + kBlock - 1) / kBlock, supers = (blocks + 3) / 4;
+  for (int row_tiles = 1; row_tiles <= 2; ++row_tiles) {
+    // sums and two steps' unpacked weights, at least, in 512 columns
+    const int most = row_tiles == 1 ? 256 : 192, rows = row_tiles * 128;
+    const int64_t row_ctas = (n + rows - 1) / rows;
+    const int64_t fewest = (tokens + most - 1) / most;
+    for (int64_t tiles = fewest; tiles < fewest + 6 && tiles <= (tokens + 15) / 16; ++tiles) {
+      ManyPlan a = {};
+      a.row_tiles = row_tiles;
+      a.tile = (int)((tokens + tiles - 1) / tiles + 15) / 16 * 16;
+      a.tiles = (int)((tokens + a.tile - 1) / a.tile);
+      a.code_ring = 3;
+      a.token_ring = (kSmemMost - 1024 - a.code_ring * rows * 128) / (a.tile * 128);
+      if (a.token_ring > kMaxRing) a.token_ring = kMaxRing;
+      a.sum_columns = (a.tile + 31) / 32 * 32;
+      a.row_ring = (kColumns - row_tiles * a.sum_columns) / (row_tiles * 32);
+      if (a.row_ring > kMaxRing) a.row_ring = kMaxRing;
+      a.smem = a.code_ring * rows * 128 + a.token_ring * a.tile * 128;
+      for (int parts = 1; parts <= kMaxParts && (parts == 1 || supers >= parts * 2); ++parts) {
+        if (parts > 1 && a.tile * rows * 4 > a.smem) break;
+        // clocks: the products, the unpacking and the bytes of a step, whichever is longest; a CTA's start and end
+        const double step = fmax(fmax(2.0 * a.tile * row_tiles, 140.0 * row_tiles), (a.tile * 128.0 + rows * 36.0) / 40.0);
+        const double waves = (double)((row_ctas * a.tiles * parts + sms - 1) / sms);
+        const double time = waves * ((double)((supers + parts - 1) / parts) * 4 * step + 4000.0 + a.tile * row_tiles * 8.0 * (parts > 1 ? 2.0 : 1.0));
+        if (best.tile == 0 || time < least) {
+          least = time;
+          best = a;
+          best.parts = parts;
+        }
+      }
+    }
+  }
+  // One CTA an SM, always: a CTA has all of tensor memory, and one that waits for it while its cluster waits for it
+  // could be waited for in turn by the cluster that holds it.
+  if (best.smem < kSmemAlone) best.smem = kSmemAlone;
+  best.smem += 1024;
+  best.blocks = blocks;
+  best.x_bytes = (int64_t)best.tiles * best.tile * blocks * 128;
+  best.bytes = best.x_bytes + (int64_t)best.tiles * best.tile * 4;
+  return best;
 }
 
 lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream) {
@@ -330,16 +424,34 @@ lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream
   }
   p->tile = plan.tile;
   p->parts = plan.parts;
-  p->stages = plan.stages;
   p->blocks = (int32_t)plan.blocks;
-  p->columns = 32;
-  while (p->columns < plan.tile) p->columns *= 2;
-  p->columns *= plan.row_tiles;
-  const lt_status st = kv4::launch(reinterpret_cast<const void*>(&layout_kernel), dim3((unsigned)p->tokens), kLayoutThreads, 0, p, stream);
+  p->code_ring = plan.code_ring;
+  p->token_ring = plan.token_ring;
+  p->row_ring = plan.row_ring;
+  p->sum_columns = plan.sum_columns;
+  p->rows_column = plan.row_tiles * plan.sum_columns;
+  p->wide_scales = p->k % 256 == 0;
+  CUtensorMap map;
+  lt_status st = map_codes(&map, p->codes, p->n, p->k, plan.row_tiles * 128);
   if (st != LT_OK) return st;
+  st = kv4::launch(reinterpret_cast<const void*>(&layout_kernel), dim3((unsigned)p->tokens), kLayoutThreads, 0, p, stream);
+  if (st != LT_OK) return st;
+  if (take_injected_failure()) return LT_ERR_CUDA;
   const int64_t rows = ((int64_t)p->n + plan.row_tiles * 128 - 1) / (plan.row_tiles * 128);
-  return kv4::launch(func, dim3((unsigned)(rows * plan.parts), (unsigned)plan.tiles), two ? Many<2>::kCta : Many<1>::kCta,
-                     (unsigned)plan.smem, p, stream, plan.parts);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * plan.parts), (unsigned)plan.tiles);
+  cfg.blockDim = dim3(two ? Many<2>::kCta : Many<1>::kCta);
+  cfg.dynamicSmemBytes = (unsigned)plan.smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim = {(unsigned)plan.parts, 1, 1};
+  cfg.attrs = attrs;
+  cfg.numAttrs = plan.parts > 1 ? 2 : 1;
+  void* args[] = {p, &map};
+  return cudaLaunchKernelExC(&cfg, func, args) == cudaSuccess ? LT_OK : LT_ERR_CUDA;
 }
 
 }  // namespace w4
