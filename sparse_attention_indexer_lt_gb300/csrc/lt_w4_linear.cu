@@ -25,7 +25,6 @@ using namespace lt::w4;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStep = 128;  // inputs of a warp's step
 
 struct LinearParams {
   const void* x;
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, few_per_sm(NT)) few_kernel(LinearPar
       } else {
         for (int w = 0; w < k_warps; ++w) y += mine[w * kTokens * rows + u];
       }
-      if (row < p.n) put(p.out, (int64_t)token * p.out_stride + row, y, p.bias, row, p.bf16);
+      if (row < p.n) put(p.out, (int64_t)token * p.out_stride + row, y + bias_of(p.bias, row, p.bf16), p.bf16);
     }
     if (p.parts > 1) cluster_sync();  // (a CTA's shared memory stays until its peers have read it)
   }

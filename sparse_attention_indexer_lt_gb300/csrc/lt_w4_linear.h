@@ -39,19 +39,28 @@ __device__ __forceinline__ float peer_f32(uint32_t addr, int rank) {
                : "=f"(v) : "r"(addr), "r"(rank) : "memory");
   return v;
 }
-// An output: the bias added, rounded once.
-__device__ __forceinline__ void put(void* out, int64_t at, float y, const void* bias, int row, int bf16) {
-  if (bf16) {
-    if (bias != nullptr) y += __bfloat162float(static_cast<const __nv_bfloat16*>(bias)[row]);
+__device__ __forceinline__ uint32_t peer_address(uint32_t addr, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void put_peer(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
+}
+// An output's bias, and the output, rounded once.
+__device__ __forceinline__ float bias_of(const void* bias, int row, int bf16) {
+  if (bias == nullptr) return 0.0f;
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(bias)[row]) : __half2float(static_cast<const __half*>(bias)[row]);
+}
+__device__ __forceinline__ void put(void* out, int64_t at, float y, int bf16) {
+  if (bf16)
     static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
-  } else {
-    if (bias != nullptr) y += __half2float(static_cast<const __half*>(bias)[row]);
+  else
     static_cast<__half*>(out)[at] = __float2half_rn(y);
-  }
 }
 
 // ---- many tokens (lt_w4_many.cu)
-constexpr int kBlock = 64;  // inputs of a stage
+constexpr int kStep = 128;  // inputs of a step
 
 struct ManyPlan {
   int tile, tiles;    // tokens of a tile, a multiple of 16 up to 256; tiles
@@ -60,7 +69,7 @@ struct ManyPlan {
   int code_ring, token_ring, row_ring;  // places for codes and tokens in shared memory, unpacked weights in tensor memory
   int sum_columns;    // of tensor memory, for the sums of a tile of outputs
   int smem;
-  int64_t blocks;     // of 64 inputs
+  int64_t steps;
   int64_t x_bytes, bytes;  // workspace: the tokens as the tensor core reads them; with their powers
 };
 ManyPlan many_plan(int sms, int64_t tokens, int64_t n, int64_t k);
@@ -71,10 +80,10 @@ struct ManyParams {
   const uint16_t* scales;
   const void* bias;
   void* out;
-  uint8_t* tiles_at;  // [tile][block][token][64 inputs], each token's eight 16-byte pieces turned by the token
+  uint8_t* tiles_at;  // [tile][64 inputs' block][token][64 inputs], each token's eight 16-byte pieces turned by the token
   float* inverse;     // [token]
   int64_t x_stride, out_stride;
-  int32_t n, k, tokens, tile, parts, blocks;
+  int32_t n, k, tokens, tile, parts, steps;
   int32_t code_ring, token_ring, row_ring, sum_columns, rows_column;
   int32_t bf16, wide_scales;
 };

@@ -1,10 +1,10 @@
 // lt_w4_many.cu -- products with 4-bit weights for many tokens: tcgen05, the sums in tensor memory.
 //
 // A CTA takes one or two tiles of 128 outputs and a tile of up to 256 tokens; the weights are the product's
-// 128 rows, the tokens its columns, so a tile of few tokens wastes nothing. In steps of 64 inputs,
-//   eight warps a tile of outputs   unpack: a thread a group of 32 inputs of one output, codes times scale in fp16, into tensor
-//                 memory, where the product reads its rows: shared memory, which carries codes and tokens,
-//                 could not take the unpacked weights' way in and out as well
+// 128 rows, the tokens its columns, so a tile of few tokens wastes nothing. In steps of 128 inputs,
+//   eight warps a tile of outputs   unpack, four of them every other step: a thread the step's inputs of one output, codes
+//                 times scale in fp16, into tensor memory, where the product reads its rows: shared memory, which carries
+//                 codes and tokens, could not take the unpacked weights' way in and out as well
 //   one warp      issues the products
 //   two warps     bring the codes, 256 inputs at a time by a tensor map, and the tokens, a bulk copy a step
 // The tokens are laid out for that by a launch before: fp16, scaled by a power of two for each token (bf16's
@@ -12,6 +12,8 @@
 // parts join over distributed shared memory in one order.
 
 #include <cmath>
+#include <cstdio>
+#include <cstdlib>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -39,6 +41,7 @@ struct Shared {
   uint64_t tokens_full[kMaxRing], tokens_empty[kMaxRing];
   uint64_t rows_full[kMaxRing], rows_empty[kMaxRing];  // unpacked weights in tensor memory
   uint64_t done;
+  float inverse[256];
   uint32_t tmem;
   int gave_up;
 };
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_kernel(ManyParams p) {
   // (the product's CTAs may start: everything before this launch is done, so they ask for weights at once)
   dependents_launch();
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + (int64_t)token * p.x_stride);
-  const int pieces = p.blocks * 8, there = p.k / 8;
+  const int pieces = p.steps * 16, there = p.k / 8;
   uint4 held[kHeld];
   uint32_t big = 0;
 #pragma unroll
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_kernel(ManyParams p) {
     mul = token_power(big);
   }
   if (tid == 0) p.inverse[token] = 1.0f / mul;
-  uint8_t* to = p.tiles_at + ((int64_t)(token / p.tile) * p.blocks * p.tile + token % p.tile) * 128;
+  uint8_t* to = p.tiles_at + ((int64_t)(token / p.tile) * p.steps * 2 * p.tile + token % p.tile) * 128;
   auto write = [&](int q, const uint4& v) {
     *reinterpret_cast<uint4*>(to + (int64_t)(q / 8) * p.tile * 128 + (((q & 7) ^ (token % p.tile & 7)) << 4)) = p.bf16 ? to_half(v, mul) : v;
   };
@@ -124,68 +127,79 @@ __device__ __forceinline__ void tensor_in(uint32_t dst, const CUtensorMap* map, 
                :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(lt::smem_u32(bar)) : "memory");
 }
 
-// Super-steps of 256 inputs, four steps each. A thread has an output, and one of the two groups of each step.
+// Codes come for two steps at once. A thread has an output, and every other step of it.
 template <int kTiles>
 __device__ __forceinline__ void unpack_role(const ManyParams& p, Shared* sh, uint32_t packed, int row0, int from, int to) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = warp >> 2 & 1, tile = warp >> 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, odd = warp >> 2 & 1, tile = warp >> 3;
   const int row = tile * 128 + (warp & 3) * 32 + lane;  // (a warp reaches 32 lanes of tensor memory, by its number)
   const int groups = p.k / 32;
   const uint16_t* scales = p.scales + (int64_t)min(row0 + row, p.n - 1) * groups;
-  // a row is 64 bytes of each of two boxes, its four 16-byte pieces turned by the row's second and third bit
-  const uint32_t row_at = packed + row * 64;
-  const uint32_t turn = (uint32_t)(row >> 1 & 3);
-  const uint32_t column = sh->tmem + ((uint32_t)((warp & 3) * 32) << 16) + p.rows_column + tile * 32 + half * 16;
-  auto scales_of = [&](uint32_t (&s)[4], int u) {
+  // a row is 64 bytes of the step's box, its four 16-byte pieces turned by the row's second and third bit
+  uint32_t piece[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) piece[g] = packed + odd * (Many<kTiles>::kRows * 64) + row * 64 + ((g ^ (row >> 1 & 3)) << 4);
+  const uint32_t column = sh->tmem + ((uint32_t)((warp & 3) * 32) << 16) + p.rows_column + tile * 64;
+  auto scales_of = [&](uint32_t (&s)[2], int u) {  // of the step's four groups, pairs
     if (u >= to) return;
     if (p.wide_scales) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(scales + u * 8));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = half ? w[i] >> 16 : w[i];
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(scales + u * 8 + odd * 4));
+      s[0] = v.x;
+      s[1] = v.y;
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = __ldg(scales + min(u * 8 + i * 2 + half, groups - 1));  // (codes past the end are zeros)
+      for (int i = 0; i < 2; ++i) {
+        const int group = u * 8 + odd * 4 + i * 2;  // (codes past the end are zeros)
+        s[i] = __ldg(scales + min(group, groups - 1)) | (uint32_t)__ldg(scales + min(group + 1, groups - 1)) << 16;
+      }
     }
   };
-  uint32_t s[4] = {}, later[4] = {};
+  uint32_t s[2] = {}, later[2] = {};
   scales_of(s, from);
   Turn code(0), place(1);
+  place.at = odd;
 #pragma unroll 1
   for (int u = from; u < to; ++u) {
+    if (u * 2 + odd >= p.steps) break;
     scales_of(later, u + 1);
+    const bool free = ready(&sh->rows_empty[place.at], place.parity);
     wait_warp(&sh->codes_full[code.at], code.parity, sh);
     uint32_t w[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int g = 0; g < 4; ++g)
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
-                   : "r"(row_at + code.at * Many<kTiles>::kPacked + (i >> 1) * (Many<kTiles>::kRows * 64) + ((((i & 1) * 2 + half) ^ turn) << 4)));
+                   : "=r"(w[g][0]), "=r"(w[g][1]), "=r"(w[g][2]), "=r"(w[g][3]) : "r"(piece[g] + code.at * Many<kTiles>::kPacked));
     __syncwarp();
     if (lane == 0) arrive(&sh->codes_empty[code.at]);
     code.next(p.code_ring);
+    if (!__all_sync(~0u, free)) wait_warp(&sh->rows_empty[place.at], place.parity, sh);
+    fence_after();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (u * 4 + i >= p.blocks) break;
-      const uint32_t scale = __byte_perm(s[i], 0, 0x1010);
-      uint32_t h[16];
+    for (int i = 0; i < 2; ++i) {
+      uint32_t h[32];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t x[4];
-        codes_to_half2(w[i][j], x);
+      for (int g = 0; g < 2; ++g) {
+        const uint32_t scale = __byte_perm(s[i], 0, g ? 0x3232 : 0x1010);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[4 * j + e] = hmul2(x[e], scale);
+        for (int j = 0; j < 4; ++j) {
+          uint32_t x[4];
+          codes_to_half2(w[2 * i + g][j], x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[16 * g + 4 * j + e] = hmul2(x[e], scale);
+        }
       }
-      wait_warp(&sh->rows_empty[place.at], place.parity, sh);
-      fence_after();
-      tmem_st16(column + place.at * (kTiles * 32), h);
-      tmem_wait_st();
-      fence_before();
-      __syncwarp();
-      if (lane == 0) arrive(&sh->rows_full[place.at]);
-      place.next(p.row_ring);
+      tmem_st32(column + place.at * (kTiles * 64) + i * 32, h);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = later[i];
+    tmem_wait_st();
+    fence_before();
+    __syncwarp();
+    if (lane == 0) arrive(&sh->rows_full[place.at]);
+    place.at += 2;  // (the ring is even)
+    if (place.at >= p.row_ring) {
+      place.at -= p.row_ring;
+      place.parity ^= 1u;
+    }
+    s[0] = later[0];
+    s[1] = later[1];
   }
 }
 
@@ -197,7 +211,7 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
   __shared__ Shared shared;
   Shared* sh = &shared;
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
-  const uint32_t packed = lt::smem_u32(smem), token_bytes = p.tile * 128;
+  const uint32_t packed = lt::smem_u32(smem), token_bytes = p.tile * 256;
   const uint32_t tokens_at = packed + p.code_ring * Many<kTiles>::kPacked;
   if (tid == 0) {
     for (int s = 0; s < kMaxRing; ++s) {
@@ -205,7 +219,7 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
       lt::mbar_init(&sh->codes_empty[s], kUnpackWarps);
       lt::mbar_init(&sh->tokens_full[s], 1);
       lt::mbar_init(&sh->tokens_empty[s], 1);
-      lt::mbar_init(&sh->rows_full[s], kUnpackWarps);
+      lt::mbar_init(&sh->rows_full[s], kUnpackWarps / 2);
       lt::mbar_init(&sh->rows_empty[s], 1);
     }
     lt::mbar_init(&sh->done, 1);
@@ -222,10 +236,9 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
 
   const int rank = blockIdx.x % p.parts, row0 = (int)(blockIdx.x / p.parts) * kRows;
   const int token0 = blockIdx.y * p.tile, tokens = min(p.tokens - token0, p.tile);
-  // super-steps of 256 inputs, and their steps
-  const int supers = (p.blocks + 3) / 4;
+  const int supers = (p.steps + 1) / 2;
   const int from = (int)((int64_t)supers * rank / p.parts), to = (int)((int64_t)supers * (rank + 1) / p.parts);
-  const int first = from * 4, last = min(to * 4, p.blocks);
+  const int first = from * 2, last = min(to * 2, p.steps);
   const uint32_t tmem = sh->tmem;
 
   if (warp < kUnpackWarps) {
@@ -241,7 +254,10 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
       const uint64_t x = desc_k_major(tokens_at + token.at * token_bytes);
 #pragma unroll
       for (int m = 0; m < kTiles; ++m)
-        mma_ts4<2>(d + m * p.sum_columns, d + p.rows_column + (place.at * kTiles + m) * 32, x, idesc, b > first, lead);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          mma_ts4<2>(d + m * p.sum_columns, d + p.rows_column + (place.at * kTiles + m) * 64 + i * 32, x + (uint32_t)(i * p.tile * 8), idesc,
+                     b > first || i > 0, lead);
       mma_commit(&sh->rows_empty[place.at], lead);
       mma_commit(&sh->tokens_empty[token.at], lead);
       token.next(p.token_ring);
@@ -268,7 +284,8 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
     for (int i = to - from - left; i < to - from; ++i) wait_warp(&sh->codes_full[i % p.code_ring], i / p.code_ring & 1, sh);
   } else {
     dependency_wait();  // the launch that lays the tokens out
-    const uint8_t* src = p.tiles_at + (int64_t)blockIdx.y * p.blocks * token_bytes;
+    for (int t = lane; t < tokens; t += 32) sh->inverse[t] = p.inverse[token0 + t];
+    const uint8_t* src = p.tiles_at + (int64_t)blockIdx.y * p.steps * token_bytes;
     Turn token(1);
 #pragma unroll 1
     for (int b = first; b < last; ++b) {
@@ -289,12 +306,17 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
   __syncthreads();
   const bool bad = *(volatile int*)&sh->gave_up != 0;
 
-  // a thread a row, 16 tokens at a time; two sets of four warps take turns with a tile's
-  float* joined = reinterpret_cast<float*>(smem);  // [token][row]
+  // A thread a row, 16 tokens at a time; two sets of four warps take turns with a tile's. A cluster's parts: 32 rows, a
+  // warp's, belong to one of its CTAs, which all of them write theirs to, [part][its 32 rows][token][row].
+  constexpr int kGroups = kRows / 32;
+  const int own_groups = (kGroups + p.parts - 1) / p.parts;
   dependency_wait();
+  if (p.parts > 1) cluster_sync();  // the peers' rings are free, too
   if (warp < kUnpackWarps) {
-    const int tile = warp >> 3, row = tile * 128 + (warp & 3) * 32 + lane;
-    const uint32_t at = tmem + tile * p.sum_columns + ((uint32_t)((warp & 3) * 32) << 16);
+    const int group = (warp >> 3) * 4 + (warp & 3), row = row0 + group * 32 + lane;
+    const uint32_t at = tmem + (warp >> 3) * p.sum_columns + ((uint32_t)((warp & 3) * 32) << 16);
+    const float bias = p.parts > 1 ? 0.0f : bias_of(p.bias, min(row, p.n - 1), p.bf16);
+    const uint32_t to = peer_address(packed + ((rank * own_groups + group / p.parts) * p.tile * 32 + lane) * 4, group % p.parts);
 #pragma unroll 1
     for (int c = (warp >> 2 & 1) * 16; c < tokens; c += 32) {
       uint32_t y[16];
@@ -302,11 +324,11 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         if (c + e >= tokens) break;
-        const float v = bad ? NAN : __uint_as_float(y[e]) * p.inverse[token0 + c + e];
+        const float v = bad ? NAN : __uint_as_float(y[e]) * sh->inverse[c + e];
         if (p.parts > 1)
-          joined[(c + e) * kRows + row] = v;
-        else if (row0 + row < p.n)
-          put(p.out, (int64_t)(token0 + c + e) * p.out_stride + row0 + row, v, p.bias, row0 + row, p.bf16);
+          put_peer(to + (c + e) * 128, v);
+        else if (row < p.n)
+          put(p.out, (int64_t)(token0 + c + e) * p.out_stride + row, v + bias, p.bf16);
       }
       __syncwarp();
     }
@@ -314,19 +336,27 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
   fence_before();
   if (p.parts > 1) {
     cluster_sync();
-    const uint32_t joined_at = lt::smem_u32(joined);
-    for (int u = rank * kCta + tid; u < tokens * kRows; u += p.parts * kCta) {
-      float v = 0.0f;
+    // the sums in the parts' order, a thread four rows of a token
+    const float4* parts = reinterpret_cast<const float4*>(smem);
+    for (int mine = 0; mine * p.parts + rank < kGroups; ++mine) {
+      const int row = row0 + (mine * p.parts + rank) * 32 + tid % 8 * 4;
+      float bias[4];
 #pragma unroll
-      for (int r = 0; r < kMaxParts; ++r)
-        if (r < p.parts) v += peer_f32(joined_at + u * 4, r);
-      const int row = row0 + u % kRows;
-      if (row < p.n) put(p.out, (int64_t)(token0 + u / kRows) * p.out_stride + row, v, p.bias, row, p.bf16);
+      for (int e = 0; e < 4; ++e) bias[e] = bias_of(p.bias, min(row + e, p.n - 1), p.bf16);
+      for (int t = tid / 8; t < tokens; t += kCta / 8) {
+        float4 v = parts[(mine * p.tile + t) * 8 + tid % 8];
+        for (int r = 1; r < p.parts; ++r) {
+          const float4 x = parts[((r * own_groups + mine) * p.tile + t) * 8 + tid % 8];
+          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row + e < p.n) put(p.out, (int64_t)(token0 + t) * p.out_stride + row + e, y[e] + bias[e], p.bf16);
+      }
     }
-    cluster_sync();  // (a CTA's shared memory stays until its peers have read it)
-  } else {
-    __syncthreads();
   }
+  __syncthreads();
   fence_after();
   dependents_launch();
   if (warp == kUnpackWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(kColumns) : "memory");
@@ -368,30 +398,33 @@ lt_status map_codes(CUtensorMap* map, const void* codes, int64_t n, int64_t k, i
 }
 
 ManyPlan many_plan(int sms, int64_t tokens, int64_t n, int64_t k) {
+  int f_rt = 0, f_tile = 0, f_parts = 0;
+  if (getenv("LT_FORCE")) sscanf(getenv("LT_FORCE"), "%d,%d,%d", &f_rt, &f_tile, &f_parts);
   ManyPlan best = {};
   double least = 0.0;
-  const int64_t blocks = (k + kBlock - 1) / kBlock, supers = (blocks + 3) / 4;
+  const int64_t steps = (k + kStep - 1) / kStep, supers = (steps + 1) / 2;
   for (int row_tiles = 1; row_tiles <= 2; ++row_tiles) {
     // sums and two steps' unpacked weights, at least, in 512 columns
-    const int most = row_tiles == 1 ? 256 : 192, rows = row_tiles * 128;
+    const int most = row_tiles == 1 ? 256 : 128, rows = row_tiles * 128;
     const int64_t row_ctas = (n + rows - 1) / rows;
     const int64_t fewest = (tokens + most - 1) / most;
-    for (int64_t tiles = fewest; tiles < fewest + 6 && tiles <= (tokens + 15) / 16; ++tiles) {
+    for (int64_t tiles = fewest; tiles < fewest + (f_rt ? 64 : 6) && tiles <= (tokens + 15) / 16; ++tiles) {
       ManyPlan a = {};
       a.row_tiles = row_tiles;
       a.tile = (int)((tokens + tiles - 1) / tiles + 15) / 16 * 16;
       a.tiles = (int)((tokens + a.tile - 1) / a.tile);
       a.code_ring = 3;
-      a.token_ring = (kSmemMost - 1024 - a.code_ring * rows * 128) / (a.tile * 128);
+      a.token_ring = (kSmemMost - 1024 - a.code_ring * rows * 128) / (a.tile * 256);
       if (a.token_ring > kMaxRing) a.token_ring = kMaxRing;
       a.sum_columns = (a.tile + 31) / 32 * 32;
-      a.row_ring = (kColumns - row_tiles * a.sum_columns) / (row_tiles * 32);
-      if (a.row_ring > kMaxRing) a.row_ring = kMaxRing;
-      a.smem = a.code_ring * rows * 128 + a.token_ring * a.tile * 128;
+      a.row_ring = (kColumns - row_tiles * a.sum_columns) / (row_tiles * 64);
+      a.row_ring = a.row_ring > kMaxRing ? kMaxRing : a.row_ring / 2 * 2;
+      a.smem = a.code_ring * rows * 128 + a.token_ring * a.tile * 256;
       for (int parts = 1; parts <= kMaxParts && (parts == 1 || supers >= parts * 2); ++parts) {
-        if (parts > 1 && a.tile * rows * 4 > a.smem) break;
+        if (parts > 1 && (rows / 32 + parts - 1) / parts * parts * a.tile * 128 > (a.smem > kSmemAlone ? a.smem : kSmemAlone)) continue;
         // clocks: the products, the unpacking and the bytes of a step, whichever is longest; a CTA's start and end
         const double step = fmax(fmax(2.0 * a.tile * row_tiles, 140.0 * row_tiles), (a.tile * 128.0 + rows * 36.0) / 40.0);
+        if (f_rt && (row_tiles != f_rt || a.tile != f_tile || parts != f_parts)) continue;
         const double waves = (double)((row_ctas * a.tiles * parts + sms - 1) / sms);
         const double time = waves * ((double)((supers + parts - 1) / parts) * 4 * step + 4000.0 + a.tile * row_tiles * 8.0 * (parts > 1 ? 2.0 : 1.0));
         if (best.tile == 0 || time < least) {
@@ -406,8 +439,8 @@ ManyPlan many_plan(int sms, int64_t tokens, int64_t n, int64_t k) {
   // could be waited for in turn by the cluster that holds it.
   if (best.smem < kSmemAlone) best.smem = kSmemAlone;
   best.smem += 1024;
-  best.blocks = blocks;
-  best.x_bytes = (int64_t)best.tiles * best.tile * blocks * 128;
+  best.steps = steps;
+  best.x_bytes = (int64_t)best.tiles * best.tile * steps * 256;
   best.bytes = best.x_bytes + (int64_t)best.tiles * best.tile * 4;
   return best;
 }
@@ -424,7 +457,7 @@ lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream
   }
   p->tile = plan.tile;
   p->parts = plan.parts;
-  p->blocks = (int32_t)plan.blocks;
+  p->steps = (int32_t)plan.steps;
   p->code_ring = plan.code_ring;
   p->token_ring = plan.token_ring;
   p->row_ring = plan.row_ring;

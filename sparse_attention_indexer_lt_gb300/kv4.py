@@ -26,6 +26,7 @@ from . import DTYPE_BF16, DTYPE_F32, LtError, load
 DTYPE_F16 = 2
 _ALL = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 _DIM_OF_ROW = {80: 64, 144: 128, 288: 256}
+_PAGE_SIZES = {1 << i for i in range(11)}
 
 
 class PageStep(NamedTuple):
@@ -45,10 +46,15 @@ def _raw_stream(stream, index):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+_FUNCTIONS = {}  # the library's functions, by name
+
+
 def _call(name, index, *args):
     """Calls the library with the tensors' device current; raises on an error status."""
-    fn = getattr(load(), name)
-    if torch.cuda.current_device() == index:
+    fn = _FUNCTIONS.get(name)
+    if fn is None:
+        fn = _FUNCTIONS[name] = getattr(load(), name)
+    if torch._C._cuda_getDevice() == index:
         st = fn(*args)
     else:
         with torch.cuda.device(index):
@@ -70,12 +76,15 @@ def _want(name, t, dtype, index=None, shape=None):
     return t
 
 
+_EMPTY = torch.empty
+
+
 def _result(name, t, shape, dtype, like, stream):
     """The caller's output tensor, or a new one whose memory belongs to the stream that writes it."""
     if t is not None:
         return _want(name, t, dtype, like.get_device(), shape)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _EMPTY(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
@@ -112,10 +121,13 @@ def kv4_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, device=N
 def _check_cache(cache):
     """(pages, kv_heads, page_size, head_dim, device index) of a cache."""
     _want("cache", cache, torch.uint8)
-    if cache.dim() != 4 or cache.shape[3] not in _DIM_OF_ROW:
+    shape = cache.shape
+    if len(shape) != 4 or shape[3] not in _DIM_OF_ROW:
         raise ValueError("cache must be [pages, kv_heads, page_size, row bytes], as kv4_cache makes it")
-    pages, heads, page_size, row = cache.shape
-    return pages, heads, _check_page_size(page_size), _DIM_OF_ROW[row], cache.get_device()
+    pages, heads, page_size, row = shape
+    if page_size not in _PAGE_SIZES:
+        _check_page_size(page_size)
+    return pages, heads, page_size, _DIM_OF_ROW[row], cache.get_device()
 
 
 def _check_table(block_table, index, n):
@@ -201,13 +213,6 @@ def kv4_store(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torc
           slots.data_ptr(), cache.data_ptr(), pages, page_size, _raw_stream(stream, index))
 
 
-def _check_table_of_angles(name, t, index, half):
-    _want(name, t, torch.float32, index)
-    if t.dim() != 2 or (half is not None and t.shape != half):
-        raise ValueError(f"{name} must be float32 [positions, channel pairs], the same for cosines and sines")
-    return t.shape
-
-
 def kv4_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
                positions: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, *, interleaved: bool = False,
                out_q: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None) -> torch.Tensor | None:
@@ -221,41 +226,65 @@ def kv4_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: 
     over, their rows of out_q stay as they were. out_q may be q; q may be None (keys and values alone).
     """
     pages, heads, page_size, dim, index = _check_cache(cache)
-    for name, t in (("k", k), ("v", v)) if q is None else (("q", q), ("k", k), ("v", v)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if t.get_device() != index or t.dim() != 3 or t.shape[2] != dim or (name != "q" and t.shape[1] != heads):
-            raise ValueError(f"{name} must be [tokens, {'heads' if name == 'q' else heads}, {dim}] on cuda:{index}")
-    dtype, tokens = _ALL.get(k.dtype), k.shape[0]
-    if dtype is None or v.dtype != k.dtype or v.shape != k.shape or (q is not None and (q.dtype != k.dtype or q.shape[0] != tokens)):
-        raise ValueError("q, k and v must have one number of tokens and one type: float32, bfloat16 or float16")
-    ks, vs = k.stride(), v.stride()
-    if tokens > 0 and (ks[2] != 1 or vs[2] != 1 or (q is not None and q.stride(2) != 1)):
-        raise ValueError("the channels of q, k and v must be contiguous")
-    _check_slots(slots, index, tokens)
-    _want("positions", positions, torch.int32, index, (tokens,))
-    shape = _check_table_of_angles("cos", cos, index, None)
-    _check_table_of_angles("sin", sin, index, shape)
-    if shape[1] == 0 or shape[1] % 8 or 2 * shape[1] > dim:
-        raise ValueError(f"cos and sin must have a multiple of 8 channel pairs, at most {dim // 2}, got {shape[1]}")
-    max_positions = _int32("the tables' positions", shape[0], 0)
-    qs = os = (0, 0)
-    q_heads = 0
+    if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor) or not k.is_cuda or not v.is_cuda:
+        raise TypeError("k and v must be CUDA tensors")
+    kind = k.dtype
+    dtype, shape = _ALL.get(kind), k.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or v.shape != shape or k.get_device() != index or v.get_device() != index:
+        raise ValueError(f"k and v must be [tokens, {heads}, {dim}] on cuda:{index}")
+    tokens = shape[0]
+    if dtype is None or v.dtype is not kind:
+        raise ValueError("q, k and v must have one type: float32, bfloat16 or float16")
+    k_token, k_head, k_one = k.stride()
+    v_token, v_head, v_one = v.stride()
+    if not (isinstance(slots, torch.Tensor) and slots.dtype is torch.int64 and slots.get_device() == index and slots.is_contiguous()
+            and slots.shape == (tokens,)):
+        _check_slots(slots, index, tokens)
+    if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32 and positions.get_device() == index
+            and positions.is_contiguous() and positions.shape == (tokens,)):
+        _want("positions", positions, torch.int32, index, (tokens,))
+    for name, t in (("cos", cos), ("sin", sin)):
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.get_device() == index and t.is_contiguous()):
+            _want(name, t, torch.float32, index)
+    table = cos.shape
+    if len(table) != 2 or sin.shape != table:
+        raise ValueError("cos and sin must be [positions, channel pairs], the same for both")
+    max_positions, pairs = table
+    if pairs == 0 or pairs % 8 or 2 * pairs > dim:
+        raise ValueError(f"cos and sin must have a multiple of 8 channel pairs, at most {dim // 2}, got {pairs}")
+    if max_positions > 2 ** 31 - 1:
+        raise ValueError("cos and sin must have at most 2^31 - 1 positions")
+    cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
+    if cos_ptr % 16 or sin_ptr % 16:
+        raise ValueError("cos and sin must start on 16 bytes")
+    q_heads = q_token = q_head = out_token = out_head = 0
+    q_ptr = out_ptr = None
+    q_one = 1
     if q is None:
         if out_q is not None:
             raise ValueError("out_q needs q")
     else:
-        q_heads, qs = q.shape[1], q.stride()
+        if not isinstance(q, torch.Tensor) or not q.is_cuda:
+            raise TypeError("q must be a CUDA tensor")
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or q.get_device() != index or q.dtype is not kind:
+            raise ValueError(f"q must be [{tokens}, heads, {dim}] on cuda:{index}, of the type of k and v")
+        q_heads = shape[1]
+        q_token, q_head, q_one = q.stride()
         if out_q is None:
-            out_q = _result("out_q", None, q.shape, q.dtype, q, stream)
-        elif not isinstance(out_q, torch.Tensor) or not out_q.is_cuda or out_q.get_device() != index or out_q.dtype != q.dtype \
-                or out_q.shape != q.shape or (tokens > 0 and out_q.stride(2) != 1):
-            raise ValueError(f"out_q must be a {q.dtype} tensor of shape {tuple(q.shape)} on cuda:{index}, its channels contiguous")
-        os = out_q.stride()
-    _call("lt_kv4_append", index, None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype, tokens, q_heads, heads,
-          dim, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], cos.data_ptr(), sin.data_ptr(), max_positions, 2 * shape[1],
-          int(bool(interleaved)), positions.data_ptr(), slots.data_ptr(), cache.data_ptr(), pages, page_size,
-          None if q is None else out_q.data_ptr(), os[0], os[1], _raw_stream(stream, index))
+            out_q = _result("out_q", None, shape, kind, q, stream)
+            out_token, out_head = q_heads * dim, dim
+        else:
+            if not isinstance(out_q, torch.Tensor) or not out_q.is_cuda or out_q.get_device() != index or out_q.dtype is not kind \
+                    or out_q.shape != shape or (tokens > 0 and out_q.stride(2) != 1):
+                raise ValueError(f"out_q must be a {kind} tensor of shape {tuple(shape)} on cuda:{index}, its channels contiguous")
+            out_token, out_head, _ = out_q.stride()
+        q_ptr, out_ptr = q.data_ptr(), out_q.data_ptr()
+    if tokens > 0 and (k_one != 1 or v_one != 1 or q_one != 1):
+        raise ValueError("the channels of q, k and v must be contiguous")
+    _call("lt_kv4_append", index, q_ptr, k.data_ptr(), v.data_ptr(), dtype, tokens, q_heads, heads, dim, q_token, q_head, k_token,
+          k_head, v_token, v_head, cos_ptr, sin_ptr, max_positions, 2 * pairs, 1 if interleaved else 0, positions.data_ptr(),
+          slots.data_ptr(), cache.data_ptr(), pages, page_size, out_ptr, out_token, out_head, _raw_stream(stream, index))
     return out_q
 
 
@@ -267,7 +296,9 @@ def kv4_load(cache: torch.Tensor, slots: torch.Tensor, *, dtype: torch.dtype = t
     pages, heads, page_size, dim, index = _check_cache(cache)
     if dtype not in _ALL:
         raise ValueError("dtype must be float32, bfloat16 or float16")
-    _check_slots(slots, index, None)
+    if not (isinstance(slots, torch.Tensor) and slots.dtype is torch.int64 and slots.get_device() == index and slots.is_contiguous()
+            and slots.dim() == 1):
+        _check_slots(slots, index, None)
     tokens = slots.shape[0]
     out_k = _result("out_k", out_k, (tokens, heads, dim), dtype, cache, stream)
     out_v = _result("out_v", out_v, (tokens, heads, dim), dtype, cache, stream)

@@ -11,9 +11,11 @@ import functools
 
 import torch
 
-from .kv4 import _ALL, _call, _raw_stream, _result, _want
+from . import DTYPE_BF16
+from .kv4 import _ALL, DTYPE_F16, _call, _raw_stream, _result, _want
 
 _GROUP = 32
+_KIND = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 
 
 def w4_quantise(weight: torch.Tensor, *, out_codes: torch.Tensor | None = None, out_scales: torch.Tensor | None = None,
@@ -55,27 +57,37 @@ def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, bia
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError("x must be a CUDA tensor")
     dtype, index = x.dtype, x.get_device()
-    if dtype != torch.bfloat16 and dtype != torch.float16:
+    kind = _KIND.get(dtype)
+    if kind is None:
         raise TypeError("x must be bfloat16 or float16")
-    _want("codes", codes, torch.uint8, index)
-    _want("scales", scales, torch.float16, index)
-    if x.dim() != 2 or codes.dim() != 2 or x.shape[1] < _GROUP or x.shape[1] % _GROUP or codes.shape[1] * 2 != x.shape[1]:
+    # (one look at each where all is as it should be; the reasons are found only where something is not)
+    if not (isinstance(codes, torch.Tensor) and codes.dtype is torch.uint8 and codes.get_device() == index and codes.is_contiguous()):
+        _want("codes", codes, torch.uint8, index)
+    if not (isinstance(scales, torch.Tensor) and scales.dtype is torch.float16 and scales.get_device() == index and scales.is_contiguous()):
+        _want("scales", scales, torch.float16, index)
+    x_shape, shape = x.shape, codes.shape
+    if len(x_shape) != 2 or len(shape) != 2 or x_shape[1] < _GROUP or x_shape[1] % _GROUP or shape[1] * 2 != x_shape[1]:
         raise ValueError("x must be [tokens, k] and codes [n, k / 2], k a multiple of 32")
-    tokens, k = x.shape
-    n = codes.shape[0]
+    tokens, k = x_shape
+    n = shape[0]
     if scales.shape != (n, k // _GROUP):
         raise ValueError(f"scales must have shape {(n, k // _GROUP)}, has {tuple(scales.shape)}")
-    if tokens > 0 and (x.stride(1) != 1 or x.stride(0) % 8 or x.data_ptr() % 16):
+    x_stride, one = x.stride()
+    x_ptr, codes_ptr, scales_ptr = x.data_ptr(), codes.data_ptr(), scales.data_ptr()
+    if tokens > 0 and (one != 1 or x_stride % 8 or x_ptr % 16):
         raise ValueError("x must have contiguous rows, a row stride that is a multiple of 8 and a 16-byte aligned start")
-    if codes.data_ptr() % 16 or scales.data_ptr() % 16:
+    if codes_ptr % 16 or scales_ptr % 16:
         raise ValueError("codes and scales must start on 16 bytes")
     if bias is not None:
         _want("bias", bias, dtype, index, (n,))
+    out_stride = n
     if out is None:
         out = _result("out", None, (tokens, n), dtype, x, stream)
-    elif not isinstance(out, torch.Tensor) or not out.is_cuda or out.get_device() != index or out.dtype != dtype \
-            or out.shape != (tokens, n) or (tokens > 0 and n > 0 and out.stride(1) != 1):
-        raise ValueError(f"out must be a {dtype} tensor of shape {(tokens, n)} on cuda:{index}, its rows contiguous")
+    else:
+        if not isinstance(out, torch.Tensor) or not out.is_cuda or out.get_device() != index or out.dtype != dtype \
+                or out.shape != (tokens, n) or (tokens > 0 and n > 0 and out.stride(1) != 1):
+            raise ValueError(f"out must be a {dtype} tensor of shape {(tokens, n)} on cuda:{index}, its rows contiguous")
+        out_stride = out.stride(0)
     need = _workspace_bytes(index, tokens, n, k)
     if workspace is not None:
         _want("workspace", workspace, torch.uint8, index)
@@ -83,8 +95,7 @@ def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, bia
             raise ValueError(f"workspace must have at least {need} bytes and start on 16")
     elif need > 0:
         workspace = _result("workspace", None, (need,), torch.uint8, x, stream)
-    _call("lt_w4_linear", index, x.data_ptr(), _ALL[dtype], tokens, x.stride(0), codes.data_ptr(), scales.data_ptr(), n, k,
-          None if bias is None else bias.data_ptr(), out.data_ptr(), out.stride(0),
-          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(),
-          _raw_stream(stream, index))
+    _call("lt_w4_linear", index, x_ptr, kind, tokens, x_stride, codes_ptr, scales_ptr, n, k,
+          None if bias is None else bias.data_ptr(), out.data_ptr(), out_stride,
+          None if workspace is None else workspace.data_ptr(), need, _raw_stream(stream, index))
     return out
