@@ -393,7 +393,7 @@ lt_status lt_w4_workspace(int64_t tokens, int64_t n, int64_t k, int64_t* bytes) 
   if (tokens <= kFew || n == 0) return LT_OK;
   int dev = 0, sms = 0;
   const lt_status found = device_of(&dev, &sms);
-  if (found == LT_OK) *bytes = many_plan(sms, tokens, n, k).bytes;
+  if (found == LT_OK) *bytes = many_plan(dev, tokens, n, k).bytes;
   return found;
 }
 
@@ -414,7 +414,7 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
   st = device_of(&dev, &sms);
   if (st != LT_OK) return st;
   if (tokens > kFew) {
-    const ManyPlan plan = many_plan(sms, tokens, n, k);
+    const ManyPlan plan = many_plan(dev, tokens, n, k);
     if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < plan.bytes) return LT_ERR_INVALID_ARG;
     ManyParams m = {};
     m.x = x;

@@ -44,19 +44,19 @@ __device__ __forceinline__ uint32_t peer_address(uint32_t addr, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
   return a;
 }
-__device__ __forceinline__ void put_peer(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void put_peer(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 // An output's bias, and the output, rounded once.
 __device__ __forceinline__ float bias_of(const void* bias, int row, int bf16) {
   if (bias == nullptr) return 0.0f;
   return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(bias)[row]) : __half2float(static_cast<const __half*>(bias)[row]);
 }
+__device__ __forceinline__ uint16_t bits_of(float y, int bf16) {
+  return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
+}
 __device__ __forceinline__ void put(void* out, int64_t at, float y, int bf16) {
-  if (bf16)
-    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
-  else
-    static_cast<__half*>(out)[at] = __float2half_rn(y);
+  static_cast<uint16_t*>(out)[at] = bits_of(y, bf16);
 }
 
 // ---- many tokens (lt_w4_many.cu)
@@ -72,7 +72,7 @@ struct ManyPlan {
   int64_t steps;
   int64_t x_bytes, bytes;  // workspace: the tokens as the tensor core reads them; with their powers
 };
-ManyPlan many_plan(int sms, int64_t tokens, int64_t n, int64_t k);
+ManyPlan many_plan(int dev, int64_t tokens, int64_t n, int64_t k);
 
 struct ManyParams {
   const void* x;
@@ -85,7 +85,7 @@ struct ManyParams {
   int64_t x_stride, out_stride;
   int32_t n, k, tokens, tile, parts, steps;
   int32_t code_ring, token_ring, row_ring, sum_columns, rows_column;
-  int32_t bf16, wide_scales;
+  int32_t bf16, wide_scales, wide_out;
 };
 lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream);
 

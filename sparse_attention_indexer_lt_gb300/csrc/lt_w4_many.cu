@@ -12,8 +12,6 @@
 // parts join over distributed shared memory in one order.
 
 #include <cmath>
-#include <cstdio>
-#include <cstdlib>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -41,7 +39,7 @@ struct Shared {
   uint64_t tokens_full[kMaxRing], tokens_empty[kMaxRing];
   uint64_t rows_full[kMaxRing], rows_empty[kMaxRing];  // unpacked weights in tensor memory
   uint64_t done;
-  float inverse[256];
+  alignas(16) float inverse[256];
   uint32_t tmem;
   int gave_up;
 };
@@ -171,8 +169,6 @@ __device__ __forceinline__ void unpack_role(const ManyParams& p, Shared* sh, uin
     __syncwarp();
     if (lane == 0) arrive(&sh->codes_empty[code.at]);
     code.next(p.code_ring);
-    if (!__all_sync(~0u, free)) wait_warp(&sh->rows_empty[place.at], place.parity, sh);
-    fence_after();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t h[32];
@@ -187,13 +183,17 @@ __device__ __forceinline__ void unpack_role(const ManyParams& p, Shared* sh, uin
           for (int e = 0; e < 4; ++e) h[16 * g + 4 * j + e] = hmul2(x[e], scale);
         }
       }
+      if (i == 0) {  // (the first half is converted before there has to be a place)
+        if (!__all_sync(~0u, free)) wait_warp(&sh->rows_empty[place.at], place.parity, sh);
+        fence_after();
+      }
       tmem_st32(column + place.at * (kTiles * 64) + i * 32, h);
     }
     tmem_wait_st();
     fence_before();
     __syncwarp();
     if (lane == 0) arrive(&sh->rows_full[place.at]);
-    place.at += 2;  // (the ring is even)
+    place.at += 2;
     if (place.at >= p.row_ring) {
       place.at -= p.row_ring;
       place.parity ^= 1u;
@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
   const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;
   const uint32_t packed = lt::smem_u32(smem), token_bytes = p.tile * 256;
   const uint32_t tokens_at = packed + p.code_ring * Many<kTiles>::kPacked;
+  if (tid == 32) asm volatile("prefetch.tensormap [%0];" :: "l"(&codes) : "memory");
   if (tid == 0) {
     for (int s = 0; s < kMaxRing; ++s) {
       lt::mbar_init(&sh->codes_full[s], 1);
@@ -307,52 +308,84 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
   const bool bad = *(volatile int*)&sh->gave_up != 0;
 
   // A thread a row, 16 tokens at a time; two sets of four warps take turns with a tile's. A cluster's parts: 32 rows, a
-  // warp's, belong to one of its CTAs, which all of them write theirs to, [part][its 32 rows][token][row].
+  // warp's, belong to one of its CTAs, which all of them write theirs to, [part][its 32 rows][four tokens][row][token].
   constexpr int kGroups = kRows / 32;
+  constexpr int kPitch = kRows + 8;  // of a token's outputs in shared memory, 16 bits each
   const int own_groups = (kGroups + p.parts - 1) / p.parts;
   dependency_wait();
+  if (bad) {
+    // (a wait gave up: everything becomes NaN by the tokens' factors)
+    for (int t = tid; t < p.tile; t += kCta) sh->inverse[t] = NAN;
+    __syncthreads();
+  }
   if (p.parts > 1) cluster_sync();  // the peers' rings are free, too
   if (warp < kUnpackWarps) {
     const int group = (warp >> 3) * 4 + (warp & 3), row = row0 + group * 32 + lane;
     const uint32_t at = tmem + (warp >> 3) * p.sum_columns + ((uint32_t)((warp & 3) * 32) << 16);
     const float bias = p.parts > 1 ? 0.0f : bias_of(p.bias, min(row, p.n - 1), p.bf16);
-    const uint32_t to = peer_address(packed + ((rank * own_groups + group / p.parts) * p.tile * 32 + lane) * 4, group % p.parts);
+    const uint32_t to = peer_address(packed + ((rank * own_groups + group / p.parts) * p.tile * 32 + lane * 4) * 4, group % p.parts);
+    uint16_t* line = reinterpret_cast<uint16_t*>(smem) + group * 32 + lane;
 #pragma unroll 1
-    for (int c = (warp >> 2 & 1) * 16; c < tokens; c += 32) {
+    for (int c = (warp >> 2 & 1) * 16; c < tokens; c += 32) {  // (a tile is whole 16s, so there is room past the last token)
       uint32_t y[16];
       tmem_read16(at + c, y);
+      float v[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        if (c + e >= tokens) break;
-        const float v = bad ? NAN : __uint_as_float(y[e]) * sh->inverse[c + e];
-        if (p.parts > 1)
-          put_peer(to + (c + e) * 128, v);
-        else if (row < p.n)
-          put(p.out, (int64_t)(token0 + c + e) * p.out_stride + row, v + bias, p.bf16);
+      for (int e = 0; e < 16; e += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&sh->inverse[c + e]);
+        v[e] = fmaf(__uint_as_float(y[e]), f.x, bias);
+        v[e + 1] = fmaf(__uint_as_float(y[e + 1]), f.y, bias);
+        v[e + 2] = fmaf(__uint_as_float(y[e + 2]), f.z, bias);
+        v[e + 3] = fmaf(__uint_as_float(y[e + 3]), f.w, bias);
       }
-      __syncwarp();
+      if (p.parts > 1) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) put_peer(to + (c + e) * 128, make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+      } else if (p.bf16) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) line[(c + e) * kPitch] = bits_of(v[e], 1);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) line[(c + e) * kPitch] = bits_of(v[e], 0);
+      }
     }
   }
   fence_before();
-  if (p.parts > 1) {
+  if (p.parts == 1) {
+    // whole lines out of shared memory: a token's outputs, 16 bytes a thread where they start on that
+    __syncthreads();
+    const uint16_t* lines = reinterpret_cast<const uint16_t*>(smem);
+    for (int u = tid; u < tokens * (kRows / 8); u += kCta) {
+      const int t = u / (kRows / 8), at = u % (kRows / 8) * 8;
+      const uint4 v = *reinterpret_cast<const uint4*>(lines + t * kPitch + at);
+      uint16_t* to = static_cast<uint16_t*>(p.out) + (int64_t)(token0 + t) * p.out_stride + row0 + at;
+      if (p.wide_out && row0 + at + 8 <= p.n) {
+        *reinterpret_cast<uint4*>(to) = v;
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (row0 + at + e < p.n) to[e] = (uint16_t)(e & 1 ? w[e / 2] >> 16 : w[e / 2]);
+      }
+    }
+  } else {
     cluster_sync();
-    // the sums in the parts' order, a thread four rows of a token
+    // the sums in the parts' order, a thread four tokens of a row
     const float4* parts = reinterpret_cast<const float4*>(smem);
     for (int mine = 0; mine * p.parts + rank < kGroups; ++mine) {
-      const int row = row0 + (mine * p.parts + rank) * 32 + tid % 8 * 4;
-      float bias[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) bias[e] = bias_of(p.bias, min(row + e, p.n - 1), p.bf16);
-      for (int t = tid / 8; t < tokens; t += kCta / 8) {
-        float4 v = parts[(mine * p.tile + t) * 8 + tid % 8];
+      const int row = row0 + (mine * p.parts + rank) * 32 + lane;
+      const float bias = bias_of(p.bias, min(row, p.n - 1), p.bf16);
+      for (int four = warp; four * 4 < tokens; four += kCta / 32) {
+        float4 v = parts[(mine * (p.tile / 4) + four) * 32 + lane];
         for (int r = 1; r < p.parts; ++r) {
-          const float4 x = parts[((r * own_groups + mine) * p.tile + t) * 8 + tid % 8];
+          const float4 x = parts[((r * own_groups + mine) * (p.tile / 4) + four) * 32 + lane];
           v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
         const float y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (row + e < p.n) put(p.out, (int64_t)(token0 + t) * p.out_stride + row + e, y[e] + bias[e], p.bf16);
+          if (row < p.n && four * 4 + e < tokens)
+            put(p.out, (int64_t)(token0 + four * 4 + e) * p.out_stride + row, y[e] + bias, p.bf16);
       }
     }
   }
@@ -380,6 +413,34 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return found;
 }
 
+// How many clusters of each size the device runs at once, with a CTA on each of their SMs; asked once.
+int g_fit[64][kMaxParts + 1];
+const int* clusters_that_fit(int dev) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  int* fit = g_fit[dev];
+  if (fit[0] != 0) return fit;
+  const void* func = reinterpret_cast<const void*>(&many_kernel<2>);
+  int sms = 0;
+  if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return fit;  // (no cluster fits: the launch will say why)
+  fit[1] = sms;
+  for (int parts = 2; parts <= kMaxParts; ++parts) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(parts * sms));
+    cfg.blockDim = dim3(Many<2>::kCta);
+    cfg.dynamicSmemBytes = kSmemMost;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)parts, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&fit[parts], func, &cfg) != cudaSuccess) fit[parts] = 0;
+  }
+  fit[0] = 1;
+  return fit;
+}
+
 }  // namespace
 
 namespace lt {
@@ -397,9 +458,8 @@ lt_status map_codes(CUtensorMap* map, const void* codes, int64_t n, int64_t k, i
              : LT_ERR_CUDA;
 }
 
-ManyPlan many_plan(int sms, int64_t tokens, int64_t n, int64_t k) {
-  int f_rt = 0, f_tile = 0, f_parts = 0;
-  if (getenv("LT_FORCE")) sscanf(getenv("LT_FORCE"), "%d,%d,%d", &f_rt, &f_tile, &f_parts);
+ManyPlan many_plan(int dev, int64_t tokens, int64_t n, int64_t k) {
+  const int* fit = clusters_that_fit(dev);
   ManyPlan best = {};
   double least = 0.0;
   const int64_t steps = (k + kStep - 1) / kStep, supers = (steps + 1) / 2;
@@ -408,25 +468,31 @@ ManyPlan many_plan(int sms, int64_t tokens, int64_t n, int64_t k) {
     const int most = row_tiles == 1 ? 256 : 128, rows = row_tiles * 128;
     const int64_t row_ctas = (n + rows - 1) / rows;
     const int64_t fewest = (tokens + most - 1) / most;
-    for (int64_t tiles = fewest; tiles < fewest + (f_rt ? 64 : 6) && tiles <= (tokens + 15) / 16; ++tiles) {
+    for (int64_t tiles = fewest; tiles < fewest + 6 && tiles <= (tokens + 15) / 16; ++tiles) {
       ManyPlan a = {};
       a.row_tiles = row_tiles;
       a.tile = (int)((tokens + tiles - 1) / tiles + 15) / 16 * 16;
       a.tiles = (int)((tokens + a.tile - 1) / a.tile);
-      a.code_ring = 3;
-      a.token_ring = (kSmemMost - 1024 - a.code_ring * rows * 128) / (a.tile * 256);
+      // four places for tokens, then as many for codes as there is room (they are asked for while the tokens are still laid
+      // out), the rest for tokens
+      const int room = kSmemMost - 1024;
+      a.code_ring = (room - 4 * a.tile * 256) / (rows * 128);
+      a.code_ring = a.code_ring > 6 ? 6 : a.code_ring < 2 ? 2 : a.code_ring;
+      a.token_ring = (room - a.code_ring * rows * 128) / (a.tile * 256);
       if (a.token_ring > kMaxRing) a.token_ring = kMaxRing;
       a.sum_columns = (a.tile + 31) / 32 * 32;
       a.row_ring = (kColumns - row_tiles * a.sum_columns) / (row_tiles * 64);
-      a.row_ring = a.row_ring > kMaxRing ? kMaxRing : a.row_ring / 2 * 2;
+      if (a.row_ring > kMaxRing) a.row_ring = kMaxRing;
       a.smem = a.code_ring * rows * 128 + a.token_ring * a.tile * 256;
       for (int parts = 1; parts <= kMaxParts && (parts == 1 || supers >= parts * 2); ++parts) {
+        if (fit[parts] < 1) break;
         if (parts > 1 && (rows / 32 + parts - 1) / parts * parts * a.tile * 128 > (a.smem > kSmemAlone ? a.smem : kSmemAlone)) continue;
-        // clocks: the products, the unpacking and the bytes of a step, whichever is longest; a CTA's start and end
-        const double step = fmax(fmax(2.0 * a.tile * row_tiles, 140.0 * row_tiles), (a.tile * 128.0 + rows * 36.0) / 40.0);
-        if (f_rt && (row_tiles != f_rt || a.tile != f_tile || parts != f_parts)) continue;
-        const double waves = (double)((row_ctas * a.tiles * parts + sms - 1) / sms);
-        const double time = waves * ((double)((supers + parts - 1) / parts) * 4 * step + 4000.0 + a.tile * row_tiles * 8.0 * (parts > 1 ? 2.0 : 1.0));
+        // Clocks, as measured: a step's products, unpacking, bytes from memory (all CTAs') and from the L2 cache, whichever is
+        // longest; a CTA's start, and its end, longer with a join.
+        const int64_t clusters = row_ctas * a.tiles, waves = (clusters + fit[parts] - 1) / fit[parts];
+        const double from_memory = (double)(clusters < fit[parts] ? clusters : fit[parts]) * parts * rows * 72.0 / a.tiles / 2800.0;
+        const double step = fmax(fmax((row_tiles == 1 ? 4.6 : 10.7) * a.tile, row_tiles == 1 ? 560.0 : 700.0), fmax(from_memory, (a.tile * 256.0 + rows * 72.0) / 64.0));
+        const double time = (double)waves * ((double)((supers + parts - 1) / parts) * 2 * step + 3000.0 + 18.0 * a.tile * row_tiles + (parts > 1 ? 4000.0 + 400.0 * parts : 500.0));
         if (best.tile == 0 || time < least) {
           least = time;
           best = a;
@@ -464,6 +530,7 @@ lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream
   p->sum_columns = plan.sum_columns;
   p->rows_column = plan.row_tiles * plan.sum_columns;
   p->wide_scales = p->k % 256 == 0;
+  p->wide_out = reinterpret_cast<uintptr_t>(p->out) % 16 == 0 && p->out_stride % 8 == 0;
   CUtensorMap map;
   lt_status st = map_codes(&map, p->codes, p->n, p->k, plan.row_tiles * 128);
   if (st != LT_OK) return st;
