@@ -331,6 +331,7 @@ lt_status lt_kv4_attention_ex(const void* q, int32_t dtype, int64_t tokens, int3
   p.prefix = prefix;
   p.cap = softcap * 1.4426950408889634f;
   p.two_over_cap = softcap > 0.0f ? 2.0f / softcap : 0.0f;
+  p.one_over_cap = softcap > 0.0f ? 1.0f / p.cap : 0.0f;
   p.wide_cap = softcap > 64.0f;
   const bool shaped = softcap > 0.0f || slopes != nullptr || prefix != nullptr;
 

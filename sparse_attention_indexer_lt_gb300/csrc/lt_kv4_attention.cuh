@@ -38,6 +38,7 @@ struct AttentionParams {
   const int32_t* prefix;  // [requests]: positions below it are seen by all of the request's queries
   float cap;              // in units of log 2
   float two_over_cap;     // 2 / cap, of the cap itself
+  float one_over_cap;     // 1 / cap, of the cap in units of log 2
   int32_t wide_cap;       // the cap is large against the logits that a hyperbolic tangent by one exponential keeps exact
 };
 
@@ -274,18 +275,36 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// tanh(x) / x for u = x^2 up to 1: the polynomial of degree 6 in u whose largest relative error is least (2^-24, found
+// by the exchange method); with its 32-bit steps 3 2^-24.
+__host__ __device__ constexpr float tanh_term(int i) {
+  return i == 0   ? 0.9999999404f
+         : i == 1 ? -0.3333283961f
+         : i == 2 ? 0.1332520396f
+         : i == 3 ? -0.0534570292f
+         : i == 4 ? 0.0202899799f
+         : i == 5 ? -0.0062033790f
+                  : 0.0010410226f;
+}
+__device__ __forceinline__ float tanh_over_x(float u) {
+  float t = tanh_term(6);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) t = fmaf(t, u, tanh_term(i));
+  return t;
+}
 // cap tanh(s / cap) in units of log 2. tanh(x) = 1 - 2 / (1 + e^2x) is off by 2^-22, absolute, so the capped logit
 // by 2^-22 of the cap: for caps to 64 less than what 32-bit sums of the products are off by. With larger caps,
-// logits below a quarter of them go by the series x - x^3 / 3 + 2 x^5 / 15 - 17 x^7 / 315 + 62 x^9 / 2835 (2^-27).
-// An infinity gives the cap, NaN stays NaN.
-__device__ __forceinline__ float capped(const AttentionParams& p, float s) {
+// logits up to the cap go by the polynomial. An infinity gives the cap, NaN stays NaN.
+__device__ __forceinline__ float capped_by_exp(const AttentionParams& p, float s) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_fast(s * p.two_over_cap)));
-  float y = fmaf(-2.0f * p.cap, r, p.cap);
+  return fmaf(-2.0f * p.cap, r, p.cap);
+}
+__device__ __forceinline__ float capped(const AttentionParams& p, float s) {
+  float y = capped_by_exp(p, s);
   if (p.wide_cap) {
-    const float x = s * (p.two_over_cap * 0.34657359028f), u = x * x;
-    const float t = fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0.0218694885f, -0.0539682540f), 0.1333333333f), -0.3333333333f), 1.0f);
-    if (fabsf(x) < 0.25f) y = s * t;
+    const float x = s * p.one_over_cap, u = x * x;
+    if (u <= 1.0f) y = s * tanh_over_x(u);
   }
   return y;
 }

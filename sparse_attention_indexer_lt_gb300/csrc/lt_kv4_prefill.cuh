@@ -162,6 +162,16 @@ __device__ __forceinline__ void add2(float& s0, float& s1, float x0, float x1) {
   asm("{\n .reg .b64 x, s;\n mov.b64 s, {%0, %1};\n mov.b64 x, {%2, %3};\n add.rn.f32x2 s, s, x;\n mov.b64 {%0, %1}, s;\n}"
       : "+f"(s0), "+f"(s1) : "f"(x0), "f"(x1));
 }
+__device__ __forceinline__ void mul2(float& x0, float& x1, float f) {
+  asm("{\n .reg .b64 x, f;\n mov.b64 x, {%0, %1};\n mov.b64 f, {%2, %2};\n mul.rn.f32x2 x, x, f;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(x0), "+f"(x1) : "f"(f));
+}
+// (d0, d1) = (a0 b0 + c, a1 b1 + c)
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c) {
+  asm("{\n .reg .b64 d, a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %6};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c));
+}
 // What a CTA works on: row0 .. of the request's query rows, positions [from, to).
 struct Job {
   Request rq;
@@ -288,15 +298,52 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
         tmem_read32(s_at + 32 * w, y);
         float* s = reinterpret_cast<float*>(y);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] *= shaped_factor;
+        for (int c = 0; c < 32; c += 2) mul2(s[c], s[c + 1], shaped_factor);
+        // A slope's term falls by the slope from column to column. Where rows see what lies before them alone, its sign
+        // is known, and its first column's part comes with the cap's last step.
+        const float from = (float)(own - pos0 - 32 * w);
+        const bool ahead = p.prefix != nullptr;
+        const float start = ahead ? 0.0f : -slope * from;
         if (p.cap > 0.0f) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) s[c] = capped(p, s[c]);
+          for (int c0 = 0; c0 < 32; c0 += 16) {
+            float u[16], most = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              u[c] = s[c0 + c], u[c + 1] = s[c0 + c + 1];
+              mul2(u[c], u[c + 1], p.one_over_cap);
+              fma2(u[c], u[c + 1], u[c], u[c + 1], u[c], u[c + 1], 0.0f);
+              most = max3(most, u[c], u[c + 1]);
+            }
+            if (__all_sync(~0u, most <= 1.0f)) {
+              // all logits are below the cap: no exponential and no reciprocal, of which the softmax needs one already
+#pragma unroll
+              for (int c = 0; c < 16; c += 2) {
+                float t0 = tanh_term(6), t1 = tanh_term(6);
+#pragma unroll
+                for (int i = 5; i >= 0; --i) fma2(t0, t1, t0, t1, u[c], u[c + 1], tanh_term(i));
+                fma2(s[c0 + c], s[c0 + c + 1], s[c0 + c], s[c0 + c + 1], t0, t1, start);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) {
+                const float t = s[c0 + c] * tanh_over_x(u[c]);
+                s[c0 + c] = (u[c] <= 1.0f ? t : capped_by_exp(p, s[c0 + c])) + start;
+              }
+            }
+          }
+        } else if (p.slopes != nullptr) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s[c] += start;
         }
         if (p.slopes != nullptr) {
-          const float from = (float)(own - pos0 - 32 * w);
+          if (ahead) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, fabsf(from - (float)c), s[c]);
+            for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, fabsf(from - (float)c), s[c]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] = fmaf(slope, (float)c, s[c]);
+          }
         }
         const int a = low - (pos0 + 32 * w), b = limit - (pos0 + 32 * w);  // (low >= 0: no overflow)
         uint32_t see = valid[w];

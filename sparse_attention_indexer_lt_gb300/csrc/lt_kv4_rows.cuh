@@ -399,7 +399,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
     // most tiles need neither the maximum over the lanes nor a new scale of the sums
     bool raised = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float away[2];  // how far the tile's first position of this lane is from the queries'
+      if constexpr (kShaped && !kList) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) away[e] = (float)(own[nt][e] - pos0 - g);
+      }
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -408,8 +413,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
           if constexpr (kShaped) {
             if (p.cap > 0.0f) s[mt][nt][e] = capped(p, s[mt][nt][e]);
             if (p.slopes != nullptr) {
-              const int cell = mt * 16 + g + (e >> 1) * 8, pos = kList ? pos_of[warp][stage][cell] : pos0 + cell;
-              s[mt][nt][e] = fmaf(-slope[nt][e & 1], (float)abs(own[nt][e & 1] - pos), s[mt][nt][e]);
+              const int cell = mt * 16 + (e >> 1) * 8;
+              float distance;
+              if constexpr (kList)
+                distance = (float)(own[nt][e & 1] - pos_of[warp][stage][cell + g]);
+              else
+                distance = away[e & 1] - (float)cell;
+              s[mt][nt][e] = fmaf(-slope[nt][e & 1], fabsf(distance), s[mt][nt][e]);
             }
           }
           if (masked) {
@@ -419,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
             if (!sees) s[mt][nt][e] = -INFINITY;
           }
         }
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

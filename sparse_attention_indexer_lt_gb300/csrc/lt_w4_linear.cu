@@ -34,7 +34,7 @@ struct LinearParams {
   void* out;
   int64_t x_stride, out_stride;
   int32_t n, k, tokens;
-  int32_t row_warps;   // row tiles of a CTA: 1, 2, 4 or 8
+  int32_t row_warps;   // row tiles of a CTA: 1 or 2
   int32_t parts;       // CTAs of a cluster, along the inputs
   int32_t chunk;       // steps whose inputs are in shared memory at a time
   int32_t join_at;     // where the warps' sums are joined, behind the inputs
@@ -59,11 +59,10 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
 // that read 16 bytes together have all banks.
 __device__ __forceinline__ int piece_at(int t, int q, int pitch) { return t * pitch + ((q ^ (q >> 3 & 1)) << 4); }
 
-constexpr int few_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+constexpr int kPerSm = 3;   // CTAs
+constexpr int kTokens = 8;  // columns of the product; a call has at most four tokens
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, few_per_sm(NT)) few_kernel(LinearParams p) {
-  constexpr int kTokens = NT * 8;
+__global__ void __launch_bounds__(kThreads, kPerSm) few_kernel(LinearParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t largest[kTokens];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -173,11 +172,9 @@ __global__ void __launch_bounds__(kThreads, few_per_sm(NT)) few_kernel(LinearPar
   }
   if (chunks == 1) stage(0);
 
-  float acc[NT][4];
-  float power[NT][2];  // of tokens 2c and 2c + 1, whose sums a lane has
-  uint32_t xa[NT];     // the lane's token's inputs
-#pragma unroll
-  for (int t = 0; t < NT; ++t) xa[t] = x_at + min(t * 8 + g, tokens - 1) * pitch;
+  float acc[4];
+  float power[2];  // of tokens 2c and 2c + 1, whose sums a lane has
+  const uint32_t xa = x_at + min(g, tokens - 1) * pitch;  // the lane's token's inputs
   const int q0 = c * 4, turn = c >> 1;  // (see piece_at)
   auto work = [&](const Batch& w, int at, int count) {
 #pragma unroll
@@ -196,14 +193,11 @@ __global__ void __launch_bounds__(kThreads, few_per_sm(NT)) few_kernel(LinearPar
           ha[i] = hmul2(ha[i], ka);
           hb[i] = hmul2(hb[i], kb);
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          uint32_t b0, b1, b2, b3;
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3) : "r"(xa[t] + (((at + u) * 16 + q0 + (j ^ turn)) << 4)));
-          mma16816(acc[t], ha[0], hb[0], ha[1], hb[1], b0, b1);
-          mma16816(acc[t], ha[2], hb[2], ha[3], hb[3], b2, b3);
-        }
+        uint32_t b0, b1, b2, b3;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3) : "r"(xa + (((at + u) * 16 + q0 + (j ^ turn)) << 4)));
+        mma16816(acc, ha[0], hb[0], ha[1], hb[1], b0, b1);
+        mma16816(acc, ha[2], hb[2], ha[3], hb[3], b2, b3);
       }
     }
   };
@@ -211,11 +205,8 @@ __global__ void __launch_bounds__(kThreads, few_per_sm(NT)) few_kernel(LinearPar
   float* joined = reinterpret_cast<float*>(smem + p.join_at);  // two times [k warp][token][row], in turn
   int phase = 0, turns = 0;
   for (int block = first; block < blocks; block += every, turns ^= 1) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
-      power[t][0] = power[t][1] = p.bf16 ? 0.0f : 1.0f;
-    }
+    acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+    power[0] = power[1] = 1.0f;
     for (int chunk = 0; chunk < chunks; ++chunk) {
       if (chunks > 1) {
         __syncthreads();  // the last chunk's inputs have been read
@@ -224,17 +215,15 @@ __global__ void __launch_bounds__(kThreads, few_per_sm(NT)) few_kernel(LinearPar
       if (p.bf16) {
         // sums so far go over to the new power, which is the largest input's so far and never grows
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float now = token_power(largest[min(t * 8 + 2 * c + e, tokens - 1)]);
-            if (chunk > 0) {
-              const float f = fmaxf(now / power[t][e], 0x1p-126f);  // (not 0: an infinity stays one)
-              acc[t][e] *= f;
-              acc[t][e + 2] *= f;
-            }
-            power[t][e] = now;
+        for (int e = 0; e < 2; ++e) {
+          const float now = token_power(largest[min(2 * c + e, tokens - 1)]);
+          if (chunk > 0) {
+            const float f = fmaxf(now / power[e], 0x1p-126f);  // (not 0: an infinity stays one)
+            acc[e] *= f;
+            acc[e + 2] *= f;
           }
+          power[e] = now;
+        }
       }
       int from, to;
       range(chunk, &from, &to);
@@ -253,12 +242,10 @@ __global__ void __launch_bounds__(kThreads, few_per_sm(NT)) few_kernel(LinearPar
     // join the warps, and with a cluster its CTAs
     float* mine = joined + turns * (kWarps * 16 * kTokens);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int token = t * 8 + 2 * c + (e & 1), row = wr * 16 + g + (e >> 1) * 8;
-        if (token < tokens) mine[(wk * kTokens + token) * rows + row] = p.bf16 ? acc[t][e] * (1.0f / power[t][e & 1]) : acc[t][e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      const int token = 2 * c + (e & 1), row = wr * 16 + g + (e >> 1) * 8;
+      if (token < tokens) mine[(wk * kTokens + token) * rows + row] = p.bf16 ? acc[e] * (1.0f / power[e & 1]) : acc[e];
+    }
     __syncthreads();
     const int all = tokens * rows;
     if (p.parts > 1) {
@@ -326,7 +313,7 @@ bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
-bool g_set[kMaxDevices][2];
+bool g_set[kMaxDevices];
 
 lt_status device_of(int* dev, int* sms) {
   if (cudaGetDevice(dev) != cudaSuccess) return LT_ERR_CUDA;
@@ -338,13 +325,16 @@ lt_status device_of(int* dev, int* sms) {
   return LT_OK;
 }
 
-const void* few_ptr(int nt) {
-  return nt == 1 ? reinterpret_cast<const void*>(&few_kernel<1>) : reinterpret_cast<const void*>(&few_kernel<2>);
-}
-
 constexpr int kFewInputs = 56 * 1024;  // bytes of inputs in shared memory: three CTAs an SM
-constexpr int kFewSmem = kFewInputs + 16 * 1024;
-constexpr int kFew = 16;  // tokens up to which the weights go to the tensor core from registers
+constexpr int kFewSmem = kFewInputs + 2 * kWarps * 16 * kTokens * 4;
+// Whether a call takes the kernel for few tokens. us there and in the one for many (in a graph; eagerly its second
+// launch costs the host 6 more):
+//   n x k            1 token      2            3            4            6            8
+//   1000 x 2048      4.9, 6.0     5.7, 6.1     6.3, 6.1     6.8, 6.1     8.8, 6.2
+//   4096 x 4096      6.4, 8.5     7.5, 8.6     8.8, 8.6     9.4, 8.6     10.6, 8.7    11.8, 8.7
+//   10240 x 8192     17.6, 19.4   19.7, 19.6   23.2, 19.7   23.2, 19.7   25.8, 19.9   30.4, 19.7
+//   28672 x 8192     35.3, 38.1   38.5, 37.8   39.0, 38.0   45.3, 37.8   44.0, 37.9   66.6, 38.1
+bool few(int64_t tokens, int64_t n, int64_t k) { return tokens <= 2 || (tokens <= 4 && n * k <= (int64_t)1 << 25); }
 
 lt_status check_sizes(int64_t tokens, int64_t n, int64_t k) {
   if (tokens < 0 || n < 0 || k < 0) return LT_ERR_INVALID_ARG;
@@ -390,7 +380,7 @@ lt_status lt_w4_workspace(int64_t tokens, int64_t n, int64_t k, int64_t* bytes) 
   const lt_status st = check_sizes(tokens, n, k);
   if (st != LT_OK) return st;
   *bytes = 0;
-  if (tokens <= kFew || n == 0) return LT_OK;
+  if (few(tokens, n, k) || n == 0) return LT_OK;
   int dev = 0, sms = 0;
   const lt_status found = device_of(&dev, &sms);
   if (found == LT_OK) *bytes = many_plan(dev, tokens, n, k).bytes;
@@ -413,7 +403,7 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
   int dev = 0, sms = 0;
   st = device_of(&dev, &sms);
   if (st != LT_OK) return st;
-  if (tokens > kFew) {
+  if (!few(tokens, n, k)) {
     const ManyPlan plan = many_plan(dev, tokens, n, k);
     if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < plan.bytes) return LT_ERR_INVALID_ARG;
     ManyParams m = {};
@@ -444,11 +434,11 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
   p.k = (int32_t)k;
   p.tokens = (int32_t)tokens;
   p.bf16 = dtype == LT_DTYPE_BF16;
-  const int nt = tokens <= 8 ? 1 : 2, here = (int)tokens;
-  p.row_warps = here <= 2 ? 1 : here <= 4 ? 2 : here <= 8 ? 4 : 8;
+  const int here = (int)tokens;
+  p.row_warps = here <= 2 ? 1 : 2;
   const int64_t row_blocks = (n + p.row_warps * 16 - 1) / (p.row_warps * 16);
   const int steps = (int)((k + kStep - 1) / kStep), k_warps = kWarps / p.row_warps;
-  const int64_t slots = (int64_t)sms * few_per_sm(nt);
+  const int64_t slots = (int64_t)sms * kPerSm;
   // as many steps' inputs in shared memory as fit; the inputs are cut over a cluster where the CTAs do not fill the SMs
   const int most = (kFewInputs / here - 32) / (kStep * 2);
   p.parts = 1;
@@ -458,16 +448,15 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
   const int mine = (steps + p.parts - 1) / p.parts;
   p.chunk = mine < most ? mine : most / k_warps * k_warps;
   p.join_at = here * (p.chunk * kStep * 2 + 32);
-  const int smem = p.join_at + 2 * kWarps * 16 * nt * 8 * 4;
+  const int smem = p.join_at + 2 * kWarps * 16 * kTokens * 4;
   const int64_t resident = slots / p.parts;
   const int64_t ctas = row_blocks < resident ? row_blocks : resident;
-  const void* func = few_ptr(nt);
+  const void* func = reinterpret_cast<const void*>(&few_kernel);
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    bool& set = g_set[dev][nt - 1];
-    if (!set) {
+    if (!g_set[dev]) {
       if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) != cudaSuccess) return LT_ERR_CUDA;
-      set = true;
+      g_set[dev] = true;
     }
   }
   return launch(func, dim3((unsigned)(ctas * p.parts)), kThreads, (unsigned)smem, &p, stream, p.parts);
