@@ -292,17 +292,16 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
     if constexpr (kShaped) {
       // shaped and hidden in tensor memory, 32 columns at a time, and the maximum taken on the way
       top = -INFINITY;
+      const bool plain = __all_sync(~0u, all_valid == ~0u && pos0 + kTok <= limit && pos0 >= low && any_nan == 0);
+      const bool ahead = p.prefix != nullptr;
+      float from = (float)(own - pos0);
 #pragma unroll 1
-      for (int w = 0; w < kTok / 32; ++w) {
+      for (int w = 0; w < kTok / 32; ++w, from -= 32.0f) {
         uint32_t y[32];
         tmem_read32(s_at + 32 * w, y);
         float* s = reinterpret_cast<float*>(y);
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) mul2(s[c], s[c + 1], shaped_factor);
         // A slope's term falls by the slope from column to column. Where rows see what lies before them alone, its sign
-        // is known, and its first column's part comes with the cap's last step.
-        const float from = (float)(own - pos0 - 32 * w);
-        const bool ahead = p.prefix != nullptr;
+        // is known, and its first column's part comes with the last step before.
         const float start = ahead ? 0.0f : -slope * from;
         if (p.cap > 0.0f) {
 #pragma unroll
@@ -310,6 +309,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
             float u[16], most = 0.0f;
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
+              mul2(s[c0 + c], s[c0 + c + 1], shaped_factor);
               u[c] = s[c0 + c], u[c + 1] = s[c0 + c + 1];
               mul2(u[c], u[c + 1], p.one_over_cap);
               fma2(u[c], u[c + 1], u[c], u[c + 1], u[c], u[c + 1], 0.0f);
@@ -317,24 +317,27 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
             }
             if (__all_sync(~0u, most <= 1.0f)) {
               // all logits are below the cap: no exponential and no reciprocal, of which the softmax needs one already
+              float t[16];
 #pragma unroll
-              for (int c = 0; c < 16; c += 2) {
-                float t0 = tanh_term(6), t1 = tanh_term(6);
+              for (int c = 0; c < 16; ++c) t[c] = tanh_term(6);
 #pragma unroll
-                for (int i = 5; i >= 0; --i) fma2(t0, t1, t0, t1, u[c], u[c + 1], tanh_term(i));
-                fma2(s[c0 + c], s[c0 + c + 1], s[c0 + c], s[c0 + c + 1], t0, t1, start);
-              }
+              for (int i = 5; i >= 0; --i)
+#pragma unroll
+                for (int c = 0; c < 16; c += 2) fma2(t[c], t[c + 1], t[c], t[c + 1], u[c], u[c + 1], tanh_term(i));
+#pragma unroll
+              for (int c = 0; c < 16; c += 2) fma2(s[c0 + c], s[c0 + c + 1], s[c0 + c], s[c0 + c + 1], t[c], t[c + 1], start);
             } else {
+              // (the same steps for those below it: a row's results do not go by its neighbours)
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
-                const float t = s[c0 + c] * tanh_over_x(u[c]);
-                s[c0 + c] = (u[c] <= 1.0f ? t : capped_by_exp(p, s[c0 + c])) + start;
+                const float t = fmaf(s[c0 + c], tanh_over_x(u[c]), start);
+                s[c0 + c] = u[c] <= 1.0f ? t : capped_by_exp(p, s[c0 + c]) + start;
               }
             }
           }
-        } else if (p.slopes != nullptr) {
+        } else {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) s[c] += start;
+          for (int c = 0; c < 32; c += 2) fma2(s[c], s[c + 1], shaped_factor, start);
         }
         if (p.slopes != nullptr) {
           if (ahead) {
@@ -345,22 +348,26 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
             for (int c = 0; c < 32; ++c) s[c] = fmaf(slope, (float)c, s[c]);
           }
         }
-        const int a = low - (pos0 + 32 * w), b = limit - (pos0 + 32 * w);  // (low >= 0: no overflow)
-        uint32_t see = valid[w];
-        see &= b >= 32 ? ~0u : b <= 0 ? 0u : (1u << b) - 1u;
-        see &= a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a;
-        if (!__all_sync(~0u, see == ~0u)) {
+        if (!plain) {
+          const int a = low - (pos0 + 32 * w), b = limit - (pos0 + 32 * w);  // (low >= 0: no overflow)
+          uint32_t see = valid[w];
+          see &= b >= 32 ? ~0u : b <= 0 ? 0u : (1u << b) - 1u;
+          see &= a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a;
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (!((see >> c) & 1u)) y[c] = 0xFF800000u;
-        }
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) top = max3(top, s[c], s[c + 1]);
-        tmem_st32(s_at + 32 * w, y);
-        if (any_nan != 0)
           for (uint32_t left = nan_rows[w] & see; left != 0; left &= left - 1)
             poison |= sh->nan_groups[i % kRing * kTok + 32 * w + __ffs(left) - 1];
-        __syncwarp();
+          __syncwarp();
+        }
+        float t0 = top, t1 = s[0];
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          t0 = max3(t0, s[c], s[c + 1]);
+          t1 = max3(t1, s[c + 2], s[c + 3]);
+        }
+        top = fmaxf(t0, t1);
+        tmem_st32(s_at + 32 * w, y);
       }
       tmem_wait_st();
     }
