@@ -21,7 +21,7 @@ using lt::kv4::Eight;
 using lt::kv4::row_bytes;
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // heads whose channels a thread asks for before it turns the first
+constexpr int kAheadMost = 4;  // heads whose channels a thread asks for before it turns the first; half of it with 32-bit ones
 
 struct AppendParams {
   const void* q;
@@ -37,25 +37,27 @@ struct AppendParams {
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
   int32_t q_heads, kv_heads, shift, max_pos, half;  // half: channel pairs that turn
   int32_t per;                                      // heads of a CTA
+  float minus_zero;
   int32_t q_parts, kv_parts;                        // CTAs that share a token's query heads, its keys
 };
 
-// Eight channels as fp32.
+// Eight channels: as they came (16-bit types: pairs), and as fp32.
 template <class S>
 struct Wide {
+  uint32_t w[sizeof(S) == 4 ? 8 : 4];
   float x[8];
   // (plain loads: the queries may be turned in place)
   __device__ __forceinline__ void load(const S* p, bool wide) {
     if constexpr (sizeof(S) == 4) {
+      const uint32_t* u = reinterpret_cast<const uint32_t*>(p);
       if (wide) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        const uint4 a = *reinterpret_cast<const uint4*>(u), b = *(reinterpret_cast<const uint4*>(u) + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = p[i];
+        for (int i = 0; i < 8; ++i) w[i] = u[i];
       }
     } else {
-      uint32_t w[4];
       if (wide) {
         const uint4 a = *reinterpret_cast<const uint4*>(p);
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
@@ -64,9 +66,17 @@ struct Wide {
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = u[2 * i] | ((uint32_t)u[2 * i + 1] << 16);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = Eight<S>::number(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
     }
+  }
+  static __device__ __forceinline__ float number(const uint32_t* w, int i) {
+    if constexpr (sizeof(S) == 4)
+      return __uint_as_float(w[i]);
+    else
+      return Eight<S>::number(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+  }
+  __device__ __forceinline__ void widen() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = number(w, i);
   }
   __device__ __forceinline__ void store(S* p, bool wide) const {
     if constexpr (sizeof(S) == 4) {
@@ -78,24 +88,33 @@ struct Wide {
         for (int i = 0; i < 8; ++i) p[i] = x[i];
       }
     } else {
-      uint32_t w[4];
+      uint32_t o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (std::is_same<S, __half>::value)
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
         else
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
       }
       if (wide) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
       } else {
         uint16_t* u = reinterpret_cast<uint16_t*>(p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+        for (int i = 0; i < 8; ++i) u[i] = (uint16_t)(i & 1 ? o[i / 2] >> 16 : o[i / 2]);
       }
     }
   }
 };
+
+// (x0, x1) = (x0 c0 + y0 s0, x1 c1 + y1 s1), every product and sum rounded by itself. Products and sums of pairs come
+// out of the compiler fused, also where each says how it rounds; so a product adds `zero`, -0.0f, of which only the
+// host knows that it leaves it as it is.
+__device__ __forceinline__ void turn2(float& x0, float& x1, float c0, float c1, float y0, float y1, float s0, float s1, float zero) {
+  asm("{\n .reg .b64 x, c, y, s, z;\n mov.b64 x, {%0, %1};\n mov.b64 c, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 s, {%6, %7};\n mov.b64 z, {%8, %8};\n"
+      " fma.rn.f32x2 x, x, c, z;\n fma.rn.f32x2 y, y, s, z;\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(x0), "+f"(x1) : "f"(c0), "f"(c1), "f"(y0), "f"(y1), "f"(s0), "f"(s1), "f"(zero));
+}
 
 // A thread's cosines and sines, and its channels' turn.
 template <bool kPairs>
@@ -126,22 +145,27 @@ struct Turn {
       s[i] = sign * b.x, s[i + 1] = sign * b.y, s[i + 2] = sign * b.z, s[i + 3] = sign * b.w;
     }
   }
-  // All lanes of the warp call this. a c - b s is a c + b (-s), rounded alike.
-  __device__ __forceinline__ void apply(float (&x)[8]) const {
+  // All lanes of the warp call this. a c - b s is a c + b (-s), rounded alike; two at a time.
+  template <class S>
+  __device__ __forceinline__ void apply(Wide<S>& v, float zero) const {
+    float(&x)[8] = v.x;
+    v.widen();
     if constexpr (kPairs) {
       if (turns) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-          x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
-        }
+        for (int i = 0; i < 4; ++i) turn2(x[2 * i], x[2 * i + 1], c[i], c[i], x[2 * i + 1], x[2 * i], -s[i], s[i], zero);
       }
     } else {
+      constexpr int kWords = sizeof(S) == 4 ? 8 : 4;
+      uint32_t w[kWords];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float y = __shfl_sync(~0u, x[i], other);
-        if (turns) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y, s[i]));
+      for (int i = 0; i < kWords; ++i) w[i] = __shfl_sync(~0u, v.w[i], other);
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = Wide<S>::number(w, i);
+      if (turns) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) turn2(x[i], x[i + 1], c[i], c[i + 1], y[i], y[i + 1], s[i], s[i + 1], zero);
       }
     }
   }
@@ -162,13 +186,25 @@ __device__ __forceinline__ void put_group(const E& x, uint8_t* row, int d, int a
 }
 
 template <class S, int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int wide) {
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(AppendParams p, int wide) {
   constexpr int kLanes = D / 8;
   constexpr int kRow = row_bytes(D);
+  constexpr int kAhead = sizeof(S) == 4 ? kAheadMost / 2 : kAheadMost;
   const int lane = threadIdx.x % kLanes, first = lane * 8;
   const int64_t t = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   const int part = blockIdx.y;
+  const int64_t tc = t < p.tokens ? t : 0;  // (a thread without a token reads the first one's channels in vain)
+  const bool is_q = part < p.q_parts, is_v = part >= p.q_parts + p.kv_parts;
+  const int from = (part - (is_q ? 0 : p.q_parts) - (is_v ? p.kv_parts : 0)) * p.per, to = min(from + p.per, is_q ? p.q_heads : p.kv_heads);
+  const S* src = static_cast<const S*>(is_q ? p.q : is_v ? p.v : p.k) + tc * (is_q ? p.q_token : is_v ? p.v_token : p.k_token) + first;
+  const int64_t step = is_q ? p.q_head : is_v ? p.v_head : p.k_head;
+  const bool whole = wide >> (is_q ? 0 : is_v ? 3 : 2) & 1;
   lt::kv4::dependency_wait();
+  // The channels go by no position: the first heads' are asked for before it, and the next ones' before these are worked on.
+  Wide<S> x[kAhead], later[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j)
+    if (from + j < to) x[j].load(src + (from + j) * step, whole);
   int pos = -1;
   int64_t slot = -1;
   if (t < p.tokens) {
@@ -176,62 +212,41 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p, int wi
     slot = __ldg(p.slots + t);
   }
   const bool there = pos >= 0 && pos < p.max_pos, kept = there && slot >= 0 && slot < p.slot_end;
-  const int64_t tc = t < p.tokens ? t : 0;  // (a thread without a token reads the first one's channels in vain)
   Turn<kPairs> turn;
-  if (part < p.q_parts) {
-    turn.load(p, pos, first, there);
-    const int from = part * p.per, to = min(from + p.per, p.q_heads);
-    for (int h0 = from; h0 < to; h0 += kAhead) {
-      Wide<S> x[kAhead];
+  if (!is_v) turn.load(p, pos, first, there);
+  uint8_t* page = p.cache + ((((kept ? slot : 0) >> p.shift) * p.kv_heads << p.shift) + ((kept ? slot : 0) & ((1 << p.shift) - 1))) * (int64_t)kRow;
+  const int64_t head_bytes = (int64_t)kRow << p.shift;
+#pragma unroll 1
+  for (int h0 = from; h0 < to; h0 += kAhead) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        if (h0 + j < to) x[j].load(static_cast<const S*>(p.q) + tc * p.q_token + (h0 + j) * p.q_head + first, wide & 1);
+    for (int j = 0; j < kAhead; ++j)
+      if (h0 + kAhead + j < to) later[j].load(src + (h0 + kAhead + j) * step, whole);
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (h0 + j >= to) break;  // (the same for the whole CTA)
-        turn.apply(x[j].x);
+    for (int j = 0; j < kAhead; ++j) {
+      if (h0 + j >= to) break;  // (the same for the whole CTA)
+      uint8_t* row = page + (h0 + j) * head_bytes;
+      if (is_q) {
+        turn.apply(x[j], p.minus_zero);
         if (there) x[j].store(static_cast<S*>(p.out_q) + t * p.out_token + (h0 + j) * p.out_head + first, wide & 2);
-      }
-    }
-  } else {
-    const bool is_v = part >= p.q_parts + p.kv_parts;
-    const int from = (part - p.q_parts - (is_v ? p.kv_parts : 0)) * p.per, to = min(from + p.per, p.kv_heads);
-    uint8_t* page = p.cache + ((((kept ? slot : 0) >> p.shift) * p.kv_heads << p.shift) + ((kept ? slot : 0) & ((1 << p.shift) - 1))) * (int64_t)kRow;
-    const int64_t step = (int64_t)kRow << p.shift;  // from one head to the next
-    if (!is_v) {
-      turn.load(p, pos, first, there);
-      for (int h0 = from; h0 < to; h0 += kAhead) {
-        Wide<S> x[kAhead];
+      } else if (is_v) {
+        Eight<S> e;
+        e.take(x[j].w);
+        put_group(e, row, D, D / 2 + lane * 4, D / 32 + lane / 4, kept);
+      } else {
+        turn.apply(x[j], p.minus_zero);
+        Eight<float> e;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          if (h0 + j < to) x[j].load(static_cast<const S*>(p.k) + tc * p.k_token + (h0 + j) * p.k_head + first, wide & 4);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          if (h0 + j >= to) break;
-          turn.apply(x[j].x);
-          Eight<float> e;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) e.x[i] = x[j].x[i];
-          uint8_t* row = page + (h0 + j) * step;
-          put_group(e, row, D, lane * 4, lane / 4, kept);
-          if constexpr (kRow > D + D / 8) {
-            if (lane == 0 && kept) *reinterpret_cast<uint2*>(row + D + D / 8) = make_uint2(0u, 0u);
-          }
-        }
-      }
-    } else {
-      for (int h0 = from; h0 < to; h0 += kAhead) {
-        Eight<S> x[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-          if (h0 + j < to) x[j].load(static_cast<const S*>(p.v) + tc * p.v_token + (h0 + j) * p.v_head + first, wide & 8);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          if (h0 + j >= to) break;
-          put_group(x[j], page + (h0 + j) * step, D, D / 2 + lane * 4, D / 32 + lane / 4, kept);
+        for (int i = 0; i < 8; ++i) e.x[i] = x[j].x[i];
+        put_group(e, row, D, lane * 4, lane / 4, kept);
+        if constexpr (kRow > D + D / 8) {
+          if (lane == 0 && kept) *reinterpret_cast<uint2*>(row + D + D / 8) = make_uint2(0u, 0u);
         }
       }
     }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof(x[j].w) / 4); ++i) x[j].w[i] = later[j].w[i];
   }
   lt::kv4::dependents_launch();
 }
@@ -302,11 +317,12 @@ extern "C" lt_status lt_kv4_append(const void* q, const void* k, const void* v, 
   p.shift = lt::kv4::page_shift(page_size);
   p.max_pos = max_positions;
   p.half = rotary_dim / 2;
+  p.minus_zero = -0.0f;
   const int per_cta = kThreads / (head_dim / 8);
   const int64_t blocks = (tokens + per_cta - 1) / per_cta;
   if (blocks > INT32_MAX) return LT_ERR_UNSUPPORTED;
-  // a head a thread while the CTAs are few, kAhead beside each other from where they fill the SMs
-  p.per = blocks * (q_heads + 2 * kv_heads) <= 152 * 8 && q_heads + 2 * kv_heads <= 65535 ? 1 : kAhead;
+  // a head a thread while the CTAs are few, two rounds of kAheadMost from where they fill the SMs
+  p.per = blocks * (q_heads + 2 * kv_heads) <= 152 * 8 && q_heads + 2 * kv_heads <= 65535 ? 1 : 2 * kAheadMost;
   p.q_parts = (q_heads + p.per - 1) / p.per;
   p.kv_parts = (kv_heads + p.per - 1) / p.per;
   // 16-byte accesses where every group of eight channels starts on 16 bytes: queries, their outputs, keys, values

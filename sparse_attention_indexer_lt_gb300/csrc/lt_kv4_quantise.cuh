@@ -10,7 +10,9 @@
 // at most 11, so x / scale is a level border exactly or at least 2^-13 of it away,
 // and q - r / scale with r = q * scale - x (one exact fused step) is the exact
 // quotient where that has at most 24 bits, borders among them. fp32 inputs can lie nearer to
-// a border; they are compared with border * scale, which has at most 12 bits.
+// a border, but not nearer than 2^-24 of it, and q - r / scale is off by 2^-45 before its own
+// rounding: it is on the right side, or on the border itself. Where it is on a number of three
+// bits, the inputs are compared with border * scale, which has at most 12 bits.
 #pragma once
 
 #include <cfloat>
@@ -46,6 +48,7 @@ struct Eight {  // 16-bit types: pairs in words
       for (int i = 0; i < 4; ++i) w[i] = __ldg(u + 2 * i) | ((uint32_t)__ldg(u + 2 * i + 1) << 16);
     }
   }
+  __device__ __forceinline__ void take(const uint32_t* words) { w[0] = words[0], w[1] = words[1], w[2] = words[2], w[3] = words[3]; }
   // The largest magnitude's bits; an infinity's bits or more where one is not finite (they order as integers).
   __device__ __forceinline__ uint32_t largest() const {
     const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
@@ -94,6 +97,10 @@ struct Eight<float> {
       for (int i = 0; i < 8; ++i) x[i] = __ldg(p + i);
     }
   }
+  __device__ __forceinline__ void take(const uint32_t* words) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(words[i]);
+  }
   __device__ __forceinline__ uint32_t largest() const {
     uint32_t m = 0;
 #pragma unroll
@@ -102,19 +109,39 @@ struct Eight<float> {
   }
   static __device__ __forceinline__ bool finite(uint32_t bits) { return bits < 0x7F800000u; }
   static __device__ __forceinline__ float number(uint32_t bits) { return __uint_as_float(bits); }
-  // The quotient rounded up to fp32 has the same next number of the grid as the exact one, since the grid's
-  // numbers are fp32 numbers.
-  static __device__ __forceinline__ float scale(float amax) { return scale_above(__fdiv_ru(amax, 6.0f)); }
-  // (fp32 may lie nearer to a border than a rounded quotient tells; border * s has at most 12 bits)
+  // As for 16 bits, but amax / 6 may lie nearer to a number of the grid than t is to it: where 6 s (12 bits, exact) does
+  // not reach amax, it is the next one.
+  static __device__ __forceinline__ float scale(float amax) {
+    const float s = scale_above(amax * 0x1.55550p-3f);
+    const float next = s >= 0x1p-15f ? __uint_as_float(__float_as_uint(s) + 0x8000u) : s + 0x1p-23f;
+    return fminf(6.0f * s < amax ? next : s, kScaleMax);
+  }
   __device__ __forceinline__ uint32_t codes(float s) const {
-    uint32_t w = 0;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    inv = s > 0.0f ? inv : 0.0f;
+    float y[8];
+    bool near = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float a = fabsf(x[i]);
+      const float q = x[i] * inv;
+      y[i] = fmaf(-fmaf(q, s, -x[i]), inv, q);  // (a zero keeps its sign)
+      near = near || (__float_as_uint(y[i]) & 0x1FFFFFu) == 0;
+    }
+    return near ? codes_by_borders(s) : codes_of(y);
+  }
+  __device__ __forceinline__ uint32_t codes_by_borders(float s) const {
+    uint32_t w = 0;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {  // (seldom: a short loop, its input picked out of the registers)
+      float v = x[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) v = i == j ? x[j] : v;
+      const float a = fabsf(v);
       uint32_t c = (a > 0.25f * s) + (a >= 0.75f * s) + (a > 1.25f * s) + (a >= 1.75f * s) + (a > 2.5f * s) +
                    (a >= 3.5f * s) + (a > 5.0f * s);
       if (s == 0.0f) c = 0;  // (a group of zeros)
-      w |= (c | (__float_as_uint(x[i]) >> 31 << 3)) << (4 * i);  // (a zero has a sign, too)
+      w |= (c | (__float_as_uint(v) >> 31 << 3)) << (4 * i);  // (a zero has a sign, too)
     }
     return w;
   }
