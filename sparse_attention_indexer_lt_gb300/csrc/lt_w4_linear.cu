@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) few_kernel(LinearParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t largest[kTokens];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int k_warps = kWarps / p.row_warps, wr = warp % p.row_warps, wk = warp / p.row_warps;
+  const int row_shift = p.row_warps >> 1, k_shift = 3 - row_shift;  // (one or two row tiles)
+  const int k_warps = kWarps >> row_shift, wr = warp & row_shift, wk = warp >> row_shift;
   const int rank = blockIdx.x % p.parts;
   const int rows = p.row_warps * 16;
   const int tokens = p.tokens;
@@ -82,14 +83,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) few_kernel(LinearParams p) {
   // the warp's steps of a chunk
   auto range = [&](int chunk, int* from, int* to) {
     const int c0 = s_begin + chunk * p.chunk, wide = min(p.chunk, s_end - c0);
-    *from = c0 + wide * wk / k_warps;
-    *to = c0 + wide * (wk + 1) / k_warps;
+    *from = c0 + (wide * wk >> k_shift);
+    *to = c0 + (wide * (wk + 1) >> k_shift);
   };
 
   constexpr int U = 2;  // steps of a batch; two batches are on their way
   struct Batch {
     uint4 a[U], b[U];
-    uint32_t sa[U], sb[U];
+    uint32_t sa, sb;  // scales of groups 2c and 2c + 1 of the batch's eight
   };
   // where the next batch is fetched from: it runs ahead over chunks and row blocks
   struct Next {
@@ -106,15 +107,26 @@ __global__ void __launch_bounds__(kThreads, kPerSm) few_kernel(LinearParams p) {
   };
   auto fetch = [&](Batch& w) {
     if (next.block >= blocks) return;
+    const int group = next.s * 4;
+    if (group + 4 * U <= groups && groups % 2 == 0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // (past the inputs' end, and for the odd step of a batch, the last group again: its inputs in shared memory are
-      // zeros there, or it is not used)
-      const int group = min((next.s + u) * 4 + c, groups - 1);
-      w.a[u] = load_once(next.a + (int64_t)group * 16);
-      w.b[u] = load_once(next.b + (int64_t)group * 16);
-      w.sa[u] = __ldg(next.sa + group);
-      w.sb[u] = __ldg(next.sb + group);
+      for (int u = 0; u < U; ++u) {
+        w.a[u] = load_once(next.a + (group + c) * 16 + u * 64);
+        w.b[u] = load_once(next.b + (group + c) * 16 + u * 64);
+      }
+      w.sa = __ldg(reinterpret_cast<const uint32_t*>(next.sa + group + 2 * c));
+      w.sb = __ldg(reinterpret_cast<const uint32_t*>(next.sb + group + 2 * c));
+    } else {
+      // past the inputs' end the last group again: its inputs in shared memory are zeros there
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = min(group + 4 * u + c, groups - 1);
+        w.a[u] = load_once(next.a + (int64_t)at * 16);
+        w.b[u] = load_once(next.b + (int64_t)at * 16);
+      }
+      const int lower = min(group + 2 * c, groups - 1), upper = min(group + 2 * c + 1, groups - 1);
+      w.sa = __ldg(next.sa + lower) | (uint32_t)__ldg(next.sa + upper) << 16;
+      w.sb = __ldg(next.sb + lower) | (uint32_t)__ldg(next.sb + upper) << 16;
     }
     next.s += U;
     if (next.s < next.to) return;
@@ -176,11 +188,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) few_kernel(LinearParams p) {
   float power[2];  // of tokens 2c and 2c + 1, whose sums a lane has
   const uint32_t xa = x_at + min(g, tokens - 1) * pitch;  // the lane's token's inputs
   const int q0 = c * 4, turn = c >> 1;  // (see piece_at)
+  const int scale_lane = (lane & ~3) | (c >> 1);
+  const uint32_t scale_half = c & 1 ? 0x3232u : 0x1010u;
   auto work = [&](const Batch& w, int at, int count) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u >= count) break;
-      const uint32_t ka = __byte_perm(w.sa[u], 0, 0x1010), kb = __byte_perm(w.sb[u], 0, 0x1010);
+      // the scale of group 4 u + c is with lane 2 u + c / 2 of the four
+      const uint32_t ka = __byte_perm(__shfl_sync(~0u, w.sa, scale_lane + 2 * u), 0, scale_half);
+      const uint32_t kb = __byte_perm(__shfl_sync(~0u, w.sb, scale_lane + 2 * u), 0, scale_half);
       const uint32_t wa[4] = {w.a[u].x, w.a[u].y, w.a[u].z, w.a[u].w};
       const uint32_t wb[4] = {w.b[u].x, w.b[u].y, w.b[u].z, w.b[u].w};
 #pragma unroll
