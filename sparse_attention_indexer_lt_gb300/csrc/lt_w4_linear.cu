@@ -4,13 +4,14 @@
 // Few tokens: the weights are read once and that is the time, so what counts is the work per weight: unpacking,
 // scaling, feeding the tensor core. The weights are the 16-row operand straight from registers (m16n8k16,
 // fp32 sums), the tokens the eight columns. The order of the inputs within a product is free, so a lane
-// takes 16 bytes of codes, a whole group of 32 inputs, of rows g and g + 8: four lanes
-// read 64 bytes of a row, a lane has one scale a row, and the tokens' fragments are 16 bytes
-// of the same inputs from shared memory.
+// takes 16 bytes of codes, a whole group of 32 inputs, of rows g and g + 8: one scale a row, and the
+// tokens' fragments are 16 bytes of the same inputs from shared memory.
 //
-// A CTA's eight warps are WR row tiles of 16 by 8 / WR parts of the inputs; a cluster cuts the inputs
-// further where there are few rows. The parts join in shared memory and over
-// distributed shared memory, in one order whatever the timing.
+// Each warp has a ring of its own, of 256 inputs of 16 rows (their codes by a tensor map, their scales by
+// another), and asks for the next ones itself. A CTA's eight warps are one or two row tiles by eight or four
+// parts of the inputs; it stays and walks over row blocks with the tokens in shared memory. A cluster cuts the inputs
+// further where there are few rows. The parts join in shared memory and over distributed shared memory, in one order
+// whatever the timing.
 
 #include <mutex>
 
@@ -23,13 +24,14 @@ namespace {
 using namespace lt::kv4;
 using namespace lt::w4;
 
+constexpr int kStep = 256;  // inputs of a stage
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 struct LinearParams {
   const void* x;
   const uint8_t* codes;
-  const __half* scales;
+  const uint16_t* scales;
   const void* bias;
   void* out;
   int64_t x_stride, out_stride;
@@ -38,7 +40,8 @@ struct LinearParams {
   int32_t parts;       // CTAs of a cluster, along the inputs
   int32_t chunk;       // steps whose inputs are in shared memory at a time
   int32_t join_at;     // where the warps' sums are joined, behind the inputs
-  int32_t bf16;
+  int32_t bf16, wide_scales;
+  uint32_t stage_bytes;
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -48,35 +51,62 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint4 load_once(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
+__device__ __forceinline__ void tensor_in(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+               :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(lt::smem_u32(bar)) : "memory");
 }
+// A warp waits for a phase, a bounded number of polls; false if it gave up. Every poll ends in a vote, so the warp goes
+// on converged.
+__device__ __forceinline__ bool wait_polls(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok) : "r"(lt::smem_u32(bar)), "r"(parity) : "memory");
+  bool done = ok != 0;
+  if (__all_sync(~0u, done)) return true;
+#pragma unroll 1
+  for (uint32_t i = 0; i < lt::kWaitPolls; ++i) {
+    done = done | lt::mbar_try_wait(bar, parity);
+    if (__all_sync(~0u, done)) return true;
+  }
+  return false;
+}
+
 // Where 16-byte piece q of token t lies: pieces of a step (16) by lane group and word, the upper eight's turned
 // by one, tokens 32 bytes apart beyond whole 128-byte lines, so that the eight lanes (two tokens, four groups)
 // that read 16 bytes together have all banks.
 __device__ __forceinline__ int piece_at(int t, int q, int pitch) { return t * pitch + ((q ^ (q >> 3 & 1)) << 4); }
 
 constexpr int kPerSm = 3;   // CTAs
-constexpr int kTokens = 8;  // columns of the product; a call has at most four tokens
+constexpr int kTokens = 4;  // at most, of the product's eight columns
+constexpr int kStages = 2;
+constexpr int kStageCodes = 16 * 128, kStageBytes = kStageCodes + 1024;  // 256 inputs of 16 rows; scales behind them
+constexpr int kRing = kWarps * kStages * kStageBytes;
 
-__global__ void __launch_bounds__(kThreads, kPerSm) few_kernel(LinearParams p) {
-  extern __shared__ __align__(128) uint8_t smem[];
+__global__ void __launch_bounds__(kThreads, kPerSm)
+few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __grid_constant__ CUtensorMap scales) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (lt::smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ uint32_t largest[kTokens];
+  __shared__ int gave_up;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int row_shift = p.row_warps >> 1, k_shift = 3 - row_shift;  // (one or two row tiles)
-  const int k_warps = kWarps >> row_shift, wr = warp & row_shift, wk = warp >> row_shift;
+  const int k_warps = kWarps >> row_shift, wr = warp & (p.row_warps - 1), wk = warp >> row_shift;
   const int rank = blockIdx.x % p.parts;
   const int rows = p.row_warps * 16;
   const int tokens = p.tokens;
   const int steps = (p.k + kStep - 1) / kStep, groups = p.k / 32;
-  // the CTA's steps, in chunks whose inputs fit into shared memory; its row blocks are every so many
+  // the CTA's steps of 256 inputs, in chunks whose inputs fit into shared memory; its row blocks are every so many
   const int s_begin = (int)((int64_t)steps * rank / p.parts), s_end = (int)((int64_t)steps * (rank + 1) / p.parts);
   const int chunks = (s_end - s_begin + p.chunk - 1) / p.chunk;
   const int blocks = (p.n + rows - 1) / rows, first = blockIdx.x / p.parts, every = gridDim.x / p.parts;
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) lt::mbar_init(&bars[warp][s], 1);
+    lt::mbar_fence_init();
+  }
   if (tid < kTokens) largest[tid] = 0u;
+  if (tid == 0) gave_up = 0;
   dependency_wait();
   __syncthreads();
 
@@ -87,72 +117,50 @@ __global__ void __launch_bounds__(kThreads, kPerSm) few_kernel(LinearParams p) {
     *to = c0 + (wide * (wk + 1) >> k_shift);
   };
 
-  constexpr int U = 2;  // steps of a batch; two batches are on their way
-  struct Batch {
-    uint4 a[U], b[U];
-    uint32_t sa, sb;  // scales of groups 2c and 2c + 1 of the batch's eight
-  };
-  // where the next batch is fetched from: it runs ahead over chunks and row blocks
-  struct Next {
-    int block, chunk, s, to;
-    const uint8_t *a, *b;
-    const uint16_t *sa, *sb;
-  } next = {};
-  auto aim = [&]() {  // at the rows of next.block
-    const int ra = min(next.block * rows + wr * 16 + g, p.n - 1), rb = min(next.block * rows + wr * 16 + g + 8, p.n - 1);
-    next.a = p.codes + (int64_t)ra * (p.k / 2);
-    next.b = p.codes + (int64_t)rb * (p.k / 2);
-    next.sa = reinterpret_cast<const uint16_t*>(p.scales) + (int64_t)ra * groups;
-    next.sb = reinterpret_cast<const uint16_t*>(p.scales) + (int64_t)rb * groups;
-  };
-  auto fetch = [&](Batch& w) {
-    if (next.block >= blocks) return;
-    const int group = next.s * 4;
-    if (group + 4 * U <= groups && groups % 2 == 0) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        w.a[u] = load_once(next.a + (group + c) * 16 + u * 64);
-        w.b[u] = load_once(next.b + (group + c) * 16 + u * 64);
-      }
-      w.sa = __ldg(reinterpret_cast<const uint32_t*>(next.sa + group + 2 * c));
-      w.sb = __ldg(reinterpret_cast<const uint32_t*>(next.sb + group + 2 * c));
-    } else {
-      // past the inputs' end the last group again: its inputs in shared memory are zeros there
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int at = min(group + 4 * u + c, groups - 1);
-        w.a[u] = load_once(next.a + (int64_t)at * 16);
-        w.b[u] = load_once(next.b + (int64_t)at * 16);
-      }
-      const int lower = min(group + 2 * c, groups - 1), upper = min(group + 2 * c + 1, groups - 1);
-      w.sa = __ldg(next.sa + lower) | (uint32_t)__ldg(next.sa + upper) << 16;
-      w.sb = __ldg(next.sb + lower) | (uint32_t)__ldg(next.sb + upper) << 16;
+  uint8_t* ring = smem + warp * kStages * kStageBytes;
+  // What is brought next runs ahead over chunks and row blocks. (Every warp has steps in the first chunk, or none at all.)
+  int from0, to0;
+  range(0, &from0, &to0);
+  int next_chunk = 0, next_s = from0, next_to = to0, next_row = first * rows + wr * 16;
+  const int end_row = from0 < to0 ? blocks * rows : 0;
+  auto bring = [&](int stage) {  // (the whole warp's numbers; lane 0 asks)
+    if (next_row >= end_row) return;
+    if (lane == 0) {
+      uint64_t* bar = &bars[warp][stage];
+      const uint32_t at = lt::smem_u32(ring) + stage * kStageBytes;
+      lt::mbar_arrive_tx(bar, p.stage_bytes);
+      tensor_in(at, &codes, next_s * 128, next_row, bar);
+      if (p.wide_scales) tensor_in(at + kStageCodes, &scales, next_s * 16, next_row, bar);
     }
-    next.s += U;
-    if (next.s < next.to) return;
+    if (++next_s < next_to) return;
+    if (chunks == 1) {
+      next_s = from0;
+      next_row += every * rows;
+      return;
+    }
     do {
-      if (++next.chunk == chunks) {
-        next.chunk = 0;
-        next.block += every;
-        if (next.block >= blocks) return;
-        aim();
+      if (++next_chunk == chunks) {
+        next_chunk = 0;
+        next_row += every * rows;
       }
-      range(next.chunk, &next.s, &next.to);
-    } while (next.s >= next.to);  // (every warp has steps in the first chunk, or none at all)
+      range(next_chunk, &next_s, &next_to);
+    } while (next_s >= next_to);
   };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) bring(s);
 
+  uint8_t* inputs = smem + kRing;
   const int pitch = p.chunk * kStep * 2 + 32;
-  const uint32_t x_at = lt::smem_u32(smem);
   // a chunk's inputs into shared memory; past the last input, zeros
-  auto stage = [&](int chunk) {
-    const int c0 = s_begin + chunk * p.chunk, pieces = min(p.chunk, s_end - c0) * 16;
+  auto stage_inputs = [&](int chunk) {
+    const int c0 = s_begin + chunk * p.chunk, pieces = min(p.chunk, s_end - c0) * (kStep / 8);
     for (int t = 0; t < tokens; ++t) {
       const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)t * p.x_stride + (int64_t)c0 * kStep;
       uint32_t big = 0;
       for (int q = tid; q < pieces; q += kThreads) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if ((int64_t)c0 * kStep + q * 8 < p.k) v = __ldg(reinterpret_cast<const uint4*>(x) + q);
-        *reinterpret_cast<uint4*>(smem + piece_at(t, q, pitch)) = v;
+        *reinterpret_cast<uint4*>(inputs + piece_at(t, q, pitch)) = v;
         if (p.bf16) big = max(big, largest_of(v));
       }
       if (p.bf16) {
@@ -165,102 +173,111 @@ __global__ void __launch_bounds__(kThreads, kPerSm) few_kernel(LinearParams p) {
     for (int t = 0; t < tokens; ++t) {
       const float mul = token_power(largest[t]);
       for (int q = tid; q < pieces; q += kThreads) {
-        uint4* at = reinterpret_cast<uint4*>(smem + piece_at(t, q, pitch));
+        uint4* at = reinterpret_cast<uint4*>(inputs + piece_at(t, q, pitch));
         *at = to_half(*at, mul);
       }
     }
     __syncthreads();
   };
-
-  Batch w0, w1;
-  next.block = first;
-  next.chunk = 0;
-  range(0, &next.s, &next.to);
-  const bool works = next.s < next.to && first < blocks;
-  if (works) {
-    aim();
-    fetch(w0);
-    fetch(w1);
-  }
-  if (chunks == 1) stage(0);
-
   float acc[4];
-  float power[2];  // of tokens 2c and 2c + 1, whose sums a lane has
-  const uint32_t xa = x_at + min(g, tokens - 1) * pitch;  // the lane's token's inputs
-  const int q0 = c * 4, turn = c >> 1;  // (see piece_at)
-  const int scale_lane = (lane & ~3) | (c >> 1);
-  const uint32_t scale_half = c & 1 ? 0x3232u : 0x1010u;
-  auto work = [&](const Batch& w, int at, int count) {
+  float power[2] = {1.0f, 1.0f}, inverse[2] = {1.0f, 1.0f};  // of tokens 2c and 2c + 1, whose sums a lane has
+  auto powers = [&](bool more) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u >= count) break;
-      // the scale of group 4 u + c is with lane 2 u + c / 2 of the four
-      const uint32_t ka = __byte_perm(__shfl_sync(~0u, w.sa, scale_lane + 2 * u), 0, scale_half);
-      const uint32_t kb = __byte_perm(__shfl_sync(~0u, w.sb, scale_lane + 2 * u), 0, scale_half);
-      const uint32_t wa[4] = {w.a[u].x, w.a[u].y, w.a[u].z, w.a[u].w};
-      const uint32_t wb[4] = {w.b[u].x, w.b[u].y, w.b[u].z, w.b[u].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t ha[4], hb[4];
-        codes_to_half2(wa[j], ha);
-        codes_to_half2(wb[j], hb);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ha[i] = hmul2(ha[i], ka);
-          hb[i] = hmul2(hb[i], kb);
-        }
-        uint32_t b0, b1, b2, b3;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3) : "r"(xa + (((at + u) * 16 + q0 + (j ^ turn)) << 4)));
-        mma16816(acc, ha[0], hb[0], ha[1], hb[1], b0, b1);
-        mma16816(acc, ha[2], hb[2], ha[3], hb[3], b2, b3);
+    for (int e = 0; e < 2; ++e) {
+      const float now = token_power(largest[min(2 * c + e, tokens - 1)]);
+      if (more) {
+        // sums so far go over to the new power, which is the largest input's so far and never grows
+        const float f = fmaxf(now / power[e], 0x1p-126f);  // (not 0: an infinity stays one)
+        acc[e] *= f;
+        acc[e + 2] *= f;
       }
+      power[e] = now;
+      inverse[e] = 1.0f / now;
     }
   };
-
-  float* joined = reinterpret_cast<float*>(smem + p.join_at);  // two times [k warp][token][row], in turn
-  int phase = 0, turns = 0;
+  if (chunks == 1) {
+    stage_inputs(0);
+    if (p.bf16) powers(false);
+  }
+  const uint8_t* xa = inputs + min(g, tokens - 1) * pitch + c * 64;  // the lane's token's inputs
+  const int turned = 16 - (c >> 1) * 32;                            // from an even piece to its odd neighbour (see piece_at)
+  xa += (c >> 1) * 16;
+  // a row's 128 bytes of codes, its 16-byte pieces turned by the row; row g + 8 turns alike
+  const uint8_t* lower = ring + g * 128 + ((c ^ g) << 4);
+  const int upper = (((4 + c) ^ g) << 4) - ((c ^ g) << 4);
+  const uint8_t* scale_at = ring + kStageCodes + g * 16 + c * 2;
+  float* joined = reinterpret_cast<float*>(inputs + p.join_at);  // two times [k warp][token][row], in turn
+  int place = 0, turns = 0;
+  uint32_t parity = 0;
+  bool ok = true;
   for (int block = first; block < blocks; block += every, turns ^= 1) {
     acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
-    power[0] = power[1] = 1.0f;
     for (int chunk = 0; chunk < chunks; ++chunk) {
       if (chunks > 1) {
         __syncthreads();  // the last chunk's inputs have been read
-        stage(chunk);
+        stage_inputs(chunk);
       }
-      if (p.bf16) {
-        // sums so far go over to the new power, which is the largest input's so far and never grows
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float now = token_power(largest[min(2 * c + e, tokens - 1)]);
-          if (chunk > 0) {
-            const float f = fmaxf(now / power[e], 0x1p-126f);  // (not 0: an infinity stays one)
-            acc[e] *= f;
-            acc[e + 2] *= f;
-          }
-          power[e] = now;
-        }
-      }
+      if (chunks > 1 && p.bf16) powers(chunk > 0);
       int from, to;
       range(chunk, &from, &to);
-      const int c0 = s_begin + chunk * p.chunk;
-      for (int s = from; s < to; s += U) {
-        if (phase == 0) {
-          work(w0, s - c0, to - s);
-          fetch(w0);
-        } else {
-          work(w1, s - c0, to - s);
-          fetch(w1);
+      const uint8_t* x = xa + (from - s_begin - chunk * p.chunk) * (kStep * 2);
+#pragma unroll 1
+      for (int s = from; s < to; ++s, x += kStep * 2) {
+        ok = wait_polls(&bars[warp][place], parity) && ok;
+        const uint8_t* code = lower + place * kStageBytes;
+        const uint8_t* scale = scale_at + place * kStageBytes;
+        uint4 wa[2], wb[2];
+        uint32_t ka[2], kb[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          wa[u] = *reinterpret_cast<const uint4*>(code);
+          wb[u] = *reinterpret_cast<const uint4*>(code + 1024);
+          code += upper;
+          if (p.wide_scales) {
+            ka[u] = *reinterpret_cast<const uint16_t*>(scale + u * 8);
+            kb[u] = *reinterpret_cast<const uint16_t*>(scale + u * 8 + 128);
+          } else {
+            // (codes past the last input are zeros)
+            const int group = min(s * 8 + u * 4 + c, groups - 1), ra = block * rows + wr * 16 + g;
+            ka[u] = __ldg(p.scales + (int64_t)min(ra, p.n - 1) * groups + group);
+            kb[u] = __ldg(p.scales + (int64_t)min(ra + 8, p.n - 1) * groups + group);
+          }
         }
-        phase ^= 1;
+        __syncwarp();  // every lane has read the stage
+        bring(place);
+        if (++place == kStages) {
+          place = 0;
+          parity ^= 1u;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t sa = __byte_perm(ka[u], 0, 0x1010), sb = __byte_perm(kb[u], 0, 0x1010);
+          const uint32_t ca[4] = {wa[u].x, wa[u].y, wa[u].z, wa[u].w}, cb[4] = {wb[u].x, wb[u].y, wb[u].z, wb[u].w};
+          const uint8_t* odd = x + turned;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t ha[4], hb[4];
+            codes_to_half2(ca[j], ha);
+            codes_to_half2(cb[j], hb);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ha[i] = hmul2(ha[i], sa);
+              hb[i] = hmul2(hb[i], sb);
+            }
+            const uint4 b = *reinterpret_cast<const uint4*>((j & 1 ? odd : x) + u * 256 + (j >> 1) * 32);
+            mma16816(acc, ha[0], hb[0], ha[1], hb[1], b.x, b.y);
+            mma16816(acc, ha[2], hb[2], ha[3], hb[3], b.z, b.w);
+          }
+        }
       }
     }
+    if (!ok && lane == 0) atomicExch(&gave_up, 1);
     // join the warps, and with a cluster its CTAs
     float* mine = joined + turns * (kWarps * 16 * kTokens);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int token = 2 * c + (e & 1), row = wr * 16 + g + (e >> 1) * 8;
-      if (token < tokens) mine[(wk * kTokens + token) * rows + row] = p.bf16 ? acc[e] * (1.0f / power[e & 1]) : acc[e];
+      if (token < tokens) mine[(wk * kTokens + token) * rows + row] = acc[e] * inverse[e & 1];
     }
     __syncthreads();
     const int all = tokens * rows;
@@ -268,19 +285,24 @@ __global__ void __launch_bounds__(kThreads, kPerSm) few_kernel(LinearParams p) {
       for (int u = tid; u < all; u += kThreads) {
         float y = mine[u];
         for (int w = 1; w < k_warps; ++w) y += mine[w * kTokens * rows + u];
-        mine[u] = y;
+        mine[u] = gave_up ? NAN : y;
       }
       cluster_sync();
     }
     for (int u = rank * kThreads + tid; u < all; u += p.parts * kThreads) {
-      const int token = u / rows, row = block * rows + u % rows;
+      const int token = u >> (4 + row_shift), row = block * rows + (u & (rows - 1));
       float y = 0.0f;
       if (p.parts > 1) {
 #pragma unroll
         for (int r = 0; r < kMaxParts; ++r)
           if (r < p.parts) y += peer_f32(lt::smem_u32(mine) + u * 4, r);
       } else {
-        for (int w = 0; w < k_warps; ++w) y += mine[w * kTokens * rows + u];
+        float part[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) part[w] = w < k_warps ? mine[w * kTokens * rows + u] : 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) y += part[w];
+        if (gave_up) y = NAN;  // (a wait ran out)
       }
       if (row < p.n) put(p.out, (int64_t)token * p.out_stride + row, y + bias_of(p.bias, row, p.bf16), p.bf16);
     }
@@ -341,8 +363,10 @@ lt_status device_of(int* dev, int* sms) {
   return LT_OK;
 }
 
-constexpr int kFewInputs = 56 * 1024;  // bytes of inputs in shared memory: three CTAs an SM
-constexpr int kFewSmem = kFewInputs + 2 * kWarps * 16 * kTokens * 4;
+constexpr int kFewInputs = 96 * 1024;  // bytes of inputs in shared memory at most
+constexpr int kFewJoin = 2 * kWarps * 16 * kTokens * 4;
+constexpr int kFewSmem = 1024 + kRing + kFewInputs + kFewJoin;
+
 // Whether a call takes the kernel for few tokens. us there and in the one for many (in a graph; eagerly its second
 // launch costs the host 6 more):
 //   n x k            1 token      2            3            4            6            8
@@ -441,7 +465,7 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
   LinearParams p = {};
   p.x = x;
   p.codes = static_cast<const uint8_t*>(codes);
-  p.scales = static_cast<const __half*>(scales);
+  p.scales = static_cast<const uint16_t*>(scales);
   p.bias = bias;
   p.out = out;
   p.x_stride = x_stride;
@@ -451,22 +475,31 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
   p.tokens = (int32_t)tokens;
   p.bf16 = dtype == LT_DTYPE_BF16;
   const int here = (int)tokens;
+  const int steps = (int)((k + kStep - 1) / kStep);
+  const auto smem_of = [&](int chunk) { return 1024 + kRing + here * (chunk * kStep * 2 + 32) + kFewJoin; };
   p.row_warps = here <= 2 ? 1 : 2;
   const int64_t row_blocks = (n + p.row_warps * 16 - 1) / (p.row_warps * 16);
-  const int steps = (int)((k + kStep - 1) / kStep), k_warps = kWarps / p.row_warps;
-  const int64_t slots = (int64_t)sms * kPerSm;
   // as many steps' inputs in shared memory as fit; the inputs are cut over a cluster where the CTAs do not fill the SMs
-  const int most = (kFewInputs / here - 32) / (kStep * 2);
-  p.parts = 1;
-  while (p.parts < kMaxParts && steps >= p.parts * 2 * k_warps &&
-         (row_blocks * p.parts * 2 <= slots || (steps + p.parts - 1) / p.parts > most))
-    p.parts *= 2;
-  const int mine = (steps + p.parts - 1) / p.parts;
-  p.chunk = mine < most ? mine : most / k_warps * k_warps;
+  const int k_warps = kWarps / p.row_warps, most = (kFewInputs / here - 32) / (kStep * 2);
+  int64_t per_sm = 0;
+  for (p.parts = 1;; p.parts *= 2) {
+    const int mine = (steps + p.parts - 1) / p.parts;
+    p.chunk = mine < most ? mine : most / k_warps * k_warps;
+    per_sm = (225 * 1024) / (smem_of(p.chunk) + 1024);
+    if (per_sm > kPerSm) per_sm = kPerSm;
+    if (p.parts == kMaxParts || steps < p.parts * 2 * k_warps) break;
+    if (row_blocks * p.parts * 2 > per_sm * sms && mine <= most) break;
+  }
   p.join_at = here * (p.chunk * kStep * 2 + 32);
-  const int smem = p.join_at + 2 * kWarps * 16 * kTokens * 4;
-  const int64_t resident = slots / p.parts;
+  const int64_t resident = per_sm * sms / p.parts;
   const int64_t ctas = row_blocks < resident ? row_blocks : resident;
+  p.wide_scales = k % 256 == 0;
+  p.stage_bytes = kStageCodes + (p.wide_scales ? 256 : 0);
+  CUtensorMap code_map, scale_map;
+  st = map_rows(&code_map, codes, n, k / 2, 128, 16);
+  if (st == LT_OK) st = p.wide_scales ? map_rows(&scale_map, scales, n, k / 16, 16, 16) : st;
+  if (st != LT_OK) return st;
+  if (!p.wide_scales) scale_map = code_map;  // (not used)
   const void* func = reinterpret_cast<const void*>(&few_kernel);
   {
     std::lock_guard<std::mutex> lk(g_mu);
@@ -475,7 +508,21 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
       g_set[dev] = true;
     }
   }
-  return launch(func, dim3((unsigned)(ctas * p.parts)), kThreads, (unsigned)smem, &p, stream, p.parts);
+  if (lt::take_injected_failure()) return LT_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ctas * p.parts));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (unsigned)smem_of(p.chunk);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim = {(unsigned)p.parts, 1, 1};
+  cfg.attrs = attrs;
+  cfg.numAttrs = p.parts > 1 ? 2 : 1;
+  void* args[] = {&p, &code_map, &scale_map};
+  return cudaLaunchKernelExC(&cfg, func, args) == cudaSuccess ? LT_OK : LT_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,6 +1,8 @@
 // lt_w4_linear.h -- internal: what the products with 4-bit weights share.
 #pragma once
 
+#include <cudaTypedefs.h>
+
 #include "../../include/lt_w4.h"
 #include "lt_kv4.cuh"
 
@@ -60,7 +62,7 @@ __device__ __forceinline__ void put(void* out, int64_t at, float y, int bf16) {
 }
 
 // ---- many tokens (lt_w4_many.cu)
-constexpr int kStep = 128;  // inputs of a step
+constexpr int kManyStep = 128;  // inputs of a step
 
 struct ManyPlan {
   int tile, tiles;    // tokens of a tile, a multiple of 16 up to 256; tiles
@@ -72,6 +74,10 @@ struct ManyPlan {
   int64_t steps;
   int64_t x_bytes, bytes;  // workspace: the tokens as the tensor core reads them; with their powers
 };
+// A tensor map of n rows of `bytes` bytes, in boxes of `wide` bytes of `rows` rows. Boxes of 64 and 128 bytes a row have its
+// 16-byte pieces turned by the row, so that eight lanes that read a piece of eight rows (of two, four pieces) have all
+// banks, or half of them.
+lt_status map_rows(CUtensorMap* map, const void* at, int64_t n, int64_t bytes, int wide, int rows);
 ManyPlan many_plan(int dev, int64_t tokens, int64_t n, int64_t k);
 
 struct ManyParams {

@@ -14,8 +14,6 @@
 #include <cmath>
 #include <mutex>
 
-#include <cudaTypedefs.h>
-
 #include "lt_kv4_tcgen05.cuh"
 #include "lt_w4_linear.h"
 
@@ -446,14 +444,17 @@ const int* clusters_that_fit(int dev) {
 namespace lt {
 namespace w4 {
 
-lt_status map_codes(CUtensorMap* map, const void* codes, int64_t n, int64_t k, int rows) {
+lt_status map_rows(CUtensorMap* map, const void* at, int64_t n, int64_t bytes, int wide, int rows) {
   const auto encode = encoder();
   if (encode == nullptr) return LT_ERR_CUDA;
-  const cuuint64_t dims[2] = {(cuuint64_t)k / 2, (cuuint64_t)n}, strides[1] = {(cuuint64_t)k / 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)rows}, steps[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, steps,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+  const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)n}, strides[1] = {(cuuint64_t)bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)wide, (cuuint32_t)rows}, steps[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(at), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE,
+                wide == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                : wide == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                             : CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? LT_OK
              : LT_ERR_CUDA;
 }
@@ -462,7 +463,7 @@ ManyPlan many_plan(int dev, int64_t tokens, int64_t n, int64_t k) {
   const int* fit = clusters_that_fit(dev);
   ManyPlan best = {};
   double least = 0.0;
-  const int64_t steps = (k + kStep - 1) / kStep, supers = (steps + 1) / 2;
+  const int64_t steps = (k + kManyStep - 1) / kManyStep, supers = (steps + 1) / 2;
   for (int row_tiles = 1; row_tiles <= 2; ++row_tiles) {
     // sums and two steps' unpacked weights, at least, in 512 columns
     const int most = row_tiles == 1 ? 256 : 128, rows = row_tiles * 128;
@@ -532,7 +533,7 @@ lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream
   p->wide_scales = p->k % 256 == 0;
   p->wide_out = reinterpret_cast<uintptr_t>(p->out) % 16 == 0 && p->out_stride % 8 == 0;
   CUtensorMap map;
-  lt_status st = map_codes(&map, p->codes, p->n, p->k, plan.row_tiles * 128);
+  lt_status st = map_rows(&map, p->codes, p->n, p->k / 2, 64, plan.row_tiles * 128);
   if (st != LT_OK) return st;
   st = kv4::launch(reinterpret_cast<const void*>(&layout_kernel), dim3((unsigned)p->tokens), kLayoutThreads, 0, p, stream);
   if (st != LT_OK) return st;
