@@ -264,6 +264,9 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
     shaped_factor = factor;  // logits are shaped in units of log 2, and stay so
     factor = 1.0f;
   }
+  // Whether slopes go by each column's distance: where rows see what lies after them, too, and where a slope is so steep that
+  // the rounding of its part at a tile's first column (2^-24 of up to 64 slopes beside the row's own position) would show.
+  const bool by_distance = kShaped && (p.prefix != nullptr || __any_sync(~0u, fabsf(slope) > 4.0f));
   const uint32_t lane_base = sh->tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t o_at = lane_base + kSumColumn + which * D;
 
@@ -293,16 +296,15 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
       // shaped and hidden in tensor memory, 32 columns at a time, and the maximum taken on the way
       top = -INFINITY;
       const bool plain = __all_sync(~0u, all_valid == ~0u && pos0 + kTok <= limit && pos0 >= low && any_nan == 0);
-      const bool ahead = p.prefix != nullptr;
       float from = (float)(own - pos0);
 #pragma unroll 1
       for (int w = 0; w < kTok / 32; ++w, from -= 32.0f) {
         uint32_t y[32];
         tmem_read32(s_at + 32 * w, y);
         float* s = reinterpret_cast<float*>(y);
-        // A slope's term falls by the slope from column to column. Where rows see what lies before them alone, its sign
-        // is known, and its first column's part comes with the last step before.
-        const float start = ahead ? 0.0f : -slope * from;
+        // A slope's term rises by the slope from column to column, up to the row's own position; its first column's
+        // part comes with the last step before.
+        const float start = by_distance ? 0.0f : -slope * from;
         if (p.cap > 0.0f) {
 #pragma unroll
           for (int c0 = 0; c0 < 32; c0 += 16) {
@@ -340,7 +342,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
           for (int c = 0; c < 32; c += 2) fma2(s[c], s[c + 1], shaped_factor, start);
         }
         if (p.slopes != nullptr) {
-          if (ahead) {
+          if (by_distance) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, fabsf(from - (float)c), s[c]);
           } else {

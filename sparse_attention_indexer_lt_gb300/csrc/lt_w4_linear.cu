@@ -445,6 +445,7 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
   if (st != LT_OK) return st;
   if (!few(tokens, n, k)) {
     const ManyPlan plan = many_plan(dev, tokens, n, k);
+    if (plan.tile == 0) return LT_ERR_CUDA;  // (the device told nothing about itself)
     if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < plan.bytes) return LT_ERR_INVALID_ARG;
     ManyParams m = {};
     m.x = x;

@@ -169,6 +169,27 @@ def test_nan_where_nothing_looks(dim, new):
     assert torch.isnan(out[-1]).all()
 
 
+@pytest.mark.parametrize("new", [3, 70])
+@pytest.mark.parametrize("slope", [4.0, 30.0, 1e5, -2.0])
+def test_steep_slopes(new, slope):
+    """The nearest positions keep their logits whatever the far ones' terms are: with a steep slope a query sees itself (with
+    a steep one of the other sign, the first position), and `lse` is that logit."""
+    p = Problem([260], [new], 1, 2, 64, 16, "f16", seed=3)
+    out, lse = p.run(slopes=torch.full((2,), slope, device="cuda"))
+    for i in (0, new - 1):
+        own = 260 - new + i
+        for h in range(2):
+            q = num(p.q)[i, h]
+            k, v = (np.stack([p.rows_at(0, 0, x)[j] for x in range(own + 1)]) for j in (0, 1))
+            s = k @ q / 8.0 - slope * np.abs(own - np.arange(own + 1))
+            want = s.max() + np.log(np.exp(s - s.max()).sum())
+            w = np.exp(s - want)
+            # 64-term sums and a few roundings of the logit, of the slope's term at the largest term's distance, and of the result
+            far = abs(slope) * (0 if slope > 0 else own)
+            assert abs(num(lse)[i, h] - want) <= 80 * EPS * np.abs(k * q).sum(1).max() / 8 + 8 * EPS * far + 70 * EPS * min(abs(slope), 4.0) + 2.0 ** -20 + 4 * EPS * abs(want)
+            assert np.abs(num(out)[i, h] - w @ v).max() <= 2.0 ** -9 * (w @ np.abs(v)).max() + 2.0 ** -9 * np.abs(v).max() * 2.0 ** -6
+
+
 def test_nan_queries():
     """A NaN query gives NaN, in its own row, whatever the cap makes of its logits."""
     p = Problem([70], [40], 1, 1, 64, 16, "bf16", seed=5)

@@ -145,6 +145,31 @@ def test_extremes(tokens):
         assert torch.equal(y[others], clean[others])
 
 
+@pytest.mark.parametrize("tokens", [1, 2, 4, 5])
+def test_inputs_beyond_shared_memory(tokens):
+    """More inputs than a CTA holds at a time, a cluster's share of them among it: in chunks, whose powers of two go
+    down as larger inputs come."""
+    import sparse_attention_indexer_lt_gb300 as lt
+    n, k = 37, 524288 + 96
+    codes, scales = make(n, k, seed=tokens, size=0.01)
+    torch.manual_seed(tokens)
+    x = (torch.randn(tokens, k) * 2.0 ** torch.linspace(-12, 6, k)).bfloat16()
+    y = lt.w4_linear(x.cuda(), codes.cuda(), scales.cuda())
+    check(y, x, codes, scales)
+    assert torch.equal(y, lt.w4_linear(x.cuda(), codes.cuda(), scales.cuda()))
+
+
+@pytest.mark.parametrize("tokens,n,k", [(3, 4096, 8192), (4, 5000, 8192), (2, 9000, 64), (1, 30000, 256)])
+def test_many_row_blocks(tokens, n, k):
+    """More row blocks than CTAs that stay, on both sides of the choice of kernel."""
+    import sparse_attention_indexer_lt_gb300 as lt
+    codes, scales = make(n, k, seed=n)
+    torch.manual_seed(n)
+    x = torch.randn(tokens, k).half()
+    y = lt.w4_linear(x.cuda(), codes.cuda(), scales.cuda())
+    check(y, x, codes, scales)
+
+
 @pytest.mark.parametrize("tokens", [1, 6, 40, 200])
 def test_strides_and_what_lies_around_the_output(tokens):
     import sparse_attention_indexer_lt_gb300 as lt
