@@ -264,6 +264,11 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
     shaped_factor = factor;  // logits are shaped in units of log 2, and stay so
     factor = 1.0f;
   }
+  // the polynomial of tanh(x) / x times the logits' factor, and what makes a logit x
+  float term[7];
+#pragma unroll
+  for (int i = 0; i < 7; ++i) term[i] = tanh_term(i) * shaped_factor;
+  const float to_cap = shaped_factor * p.one_over_cap;
   // Whether slopes go by each column's distance: where rows see what lies after them, too, and where a slope is so steep that
   // the rounding of its part at a tile's first column (2^-24 of up to 64 slopes beside the row's own position) would show.
   const bool by_distance = kShaped && (p.prefix != nullptr || __any_sync(~0u, fabsf(slope) > 4.0f));
@@ -311,9 +316,8 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
             float u[16], most = 0.0f;
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
-              mul2(s[c0 + c], s[c0 + c + 1], shaped_factor);
               u[c] = s[c0 + c], u[c + 1] = s[c0 + c + 1];
-              mul2(u[c], u[c + 1], p.one_over_cap);
+              mul2(u[c], u[c + 1], to_cap);
               fma2(u[c], u[c + 1], u[c], u[c + 1], u[c], u[c + 1], 0.0f);
               most = max3(most, u[c], u[c + 1]);
             }
@@ -321,19 +325,22 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
               // all logits are below the cap: no exponential and no reciprocal, of which the softmax needs one already
               float t[16];
 #pragma unroll
-              for (int c = 0; c < 16; ++c) t[c] = tanh_term(6);
+              for (int c = 0; c < 16; ++c) t[c] = term[6];
 #pragma unroll
               for (int i = 5; i >= 0; --i)
 #pragma unroll
-                for (int c = 0; c < 16; c += 2) fma2(t[c], t[c + 1], t[c], t[c + 1], u[c], u[c + 1], tanh_term(i));
+                for (int c = 0; c < 16; c += 2) fma2(t[c], t[c + 1], t[c], t[c + 1], u[c], u[c + 1], term[i]);
 #pragma unroll
               for (int c = 0; c < 16; c += 2) fma2(s[c0 + c], s[c0 + c + 1], s[c0 + c], s[c0 + c + 1], t[c], t[c + 1], start);
             } else {
               // (the same steps for those below it: a row's results do not go by its neighbours)
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
-                const float t = fmaf(s[c0 + c], tanh_over_x(u[c]), start);
-                s[c0 + c] = u[c] <= 1.0f ? t : capped_by_exp(p, s[c0 + c]) + start;
+                float t = term[6];
+#pragma unroll
+                for (int i = 5; i >= 0; --i) t = fmaf(t, u[c], term[i]);
+                t = fmaf(s[c0 + c], t, start);
+                s[c0 + c] = u[c] <= 1.0f ? t : capped_by_exp(p, s[c0 + c] * shaped_factor) + start;
               }
             }
           }

@@ -412,15 +412,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
           s[mt][nt][e] *= factor[nt][e & 1];
           if constexpr (kShaped) {
             if (p.cap > 0.0f) s[mt][nt][e] = capped(p, s[mt][nt][e]);
-            if (p.slopes != nullptr) {
-              const int cell = mt * 16 + (e >> 1) * 8;
-              float distance;
-              if constexpr (kList)
-                distance = (float)(own[nt][e & 1] - pos_of[warp][stage][cell + g]);
-              else
-                distance = away[e & 1] - (float)cell;
-              s[mt][nt][e] = fmaf(-slope[nt][e & 1], fabsf(distance), s[mt][nt][e]);
-            }
+            // (without slopes they are zeros: a branch around so little costs more)
+            const int cell = mt * 16 + (e >> 1) * 8;
+            float distance;
+            if constexpr (kList)
+              distance = (float)(own[nt][e & 1] - pos_of[warp][stage][cell + g]);
+            else
+              distance = away[e & 1] - (float)cell;
+            s[mt][nt][e] = fmaf(-slope[nt][e & 1], fabsf(distance), s[mt][nt][e]);
           }
           if (masked) {
             const int at = mt * 16 + g + (e >> 1) * 8;
