@@ -36,7 +36,7 @@ struct LinearParams {
   void* out;
   int64_t x_stride, out_stride;
   int32_t n, k, tokens;
-  int32_t row_warps;   // row tiles of a CTA: 1 or 2
+  int32_t row_warps;   // row tiles of a CTA: 1, 2 or 4
   int32_t parts;       // CTAs of a cluster, along the inputs
   int32_t chunk;       // steps whose inputs are in shared memory at a time
   int32_t join_at;     // where the warps' sums are joined, behind the inputs
@@ -77,7 +77,7 @@ __device__ __forceinline__ bool wait_polls(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ int piece_at(int t, int q, int pitch) { return t * pitch + ((q ^ (q >> 3 & 1)) << 4); }
 
 constexpr int kPerSm = 3;   // CTAs
-constexpr int kTokens = 4;  // at most, of the product's eight columns
+constexpr int kTokens = 8;  // at most: the product's columns
 constexpr int kStages = 2;
 constexpr int kStageCodes = 16 * 128, kStageBytes = kStageCodes + 1024;  // 256 inputs of 16 rows; scales behind them
 constexpr int kRing = kWarps * kStages * kStageBytes;
@@ -90,7 +90,7 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
   __shared__ uint32_t largest[kTokens];
   __shared__ int gave_up;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int row_shift = p.row_warps >> 1, k_shift = 3 - row_shift;  // (one or two row tiles)
+  const int row_shift = p.row_warps >> 1, k_shift = 3 - row_shift;  // (1, 2 or 4 row tiles)
   const int k_warps = kWarps >> row_shift, wr = warp & (p.row_warps - 1), wk = warp >> row_shift;
   const int rank = blockIdx.x % p.parts;
   const int rows = p.row_warps * 16;
@@ -151,27 +151,49 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
 
   uint8_t* inputs = smem + kRing;
   const int pitch = p.chunk * kStep * 2 + 32;
-  // a chunk's inputs into shared memory; past the last input, zeros
+  // A chunk's inputs into shared memory; past the last input, zeros. A thread asks for four pieces at a time, of up to four
+  // tokens.
+  const int side = tokens == 1 ? 0 : tokens == 2 ? 1 : 2;  // log 2 of the tokens beside each other
   auto stage_inputs = [&](int chunk) {
     const int c0 = s_begin + chunk * p.chunk, pieces = min(p.chunk, s_end - c0) * (kStep / 8);
-    for (int t = 0; t < tokens; ++t) {
-      const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)t * p.x_stride + (int64_t)c0 * kStep;
-      uint32_t big = 0;
-      for (int q = tid; q < pieces; q += kThreads) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if ((int64_t)c0 * kStep + q * 8 < p.k) v = __ldg(reinterpret_cast<const uint4*>(x) + q);
-        *reinterpret_cast<uint4*>(inputs + piece_at(t, q, pitch)) = v;
-        if (p.bf16) big = max(big, largest_of(v));
+    const int there = min((int64_t)pieces, (int64_t)(p.k / 8) - (int64_t)c0 * (kStep / 8));
+#pragma unroll 1
+    for (int t0 = 0; t0 < tokens; t0 += 4) {
+      const uint16_t* x = static_cast<const uint16_t*>(p.x) + (int64_t)t0 * p.x_stride + (int64_t)c0 * kStep;
+      uint32_t big[4] = {};
+#pragma unroll 1
+      for (int q = tid; q < pieces; q += kThreads * 4 >> side) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = i & ((1 << side) - 1), at = q + (i >> side) * kThreads;
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (at < there && t0 + t < tokens) v[i] = __ldg(reinterpret_cast<const uint4*>(x + t * p.x_stride) + at);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = i & ((1 << side) - 1), at = q + (i >> side) * kThreads;
+          if (at < pieces && t0 + t < tokens) {
+            *reinterpret_cast<uint4*>(inputs + piece_at(t0 + t, at, pitch)) = v[i];
+            big[i] = max(big[i], largest_of(v[i]));
+          }
+        }
       }
       if (p.bf16) {
-        big = __reduce_max_sync(~0u, big);
-        if (lane == 0) atomicMax(&largest[t], big);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = t0 + (i & ((1 << side) - 1));
+          big[i] = __reduce_max_sync(~0u, big[i]);
+          if (lane == 0 && t < tokens) atomicMax(&largest[t], big[i]);
+        }
       }
     }
     __syncthreads();
     if (!p.bf16) return;
+#pragma unroll 1
     for (int t = 0; t < tokens; ++t) {
       const float mul = token_power(largest[t]);
+#pragma unroll 4
       for (int q = tid; q < pieces; q += kThreads) {
         uint4* at = reinterpret_cast<uint4*>(inputs + piece_at(t, q, pitch));
         *at = to_half(*at, mul);
@@ -273,18 +295,18 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
     }
     if (!ok && lane == 0) atomicExch(&gave_up, 1);
     // join the warps, and with a cluster its CTAs
-    float* mine = joined + turns * (kWarps * 16 * kTokens);
+    float* mine = joined + turns * (kWarps * 16 * tokens);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int token = 2 * c + (e & 1), row = wr * 16 + g + (e >> 1) * 8;
-      if (token < tokens) mine[(wk * kTokens + token) * rows + row] = acc[e] * inverse[e & 1];
+      if (token < tokens) mine[(wk * tokens + token) * rows + row] = acc[e] * inverse[e & 1];
     }
     __syncthreads();
     const int all = tokens * rows;
     if (p.parts > 1) {
       for (int u = tid; u < all; u += kThreads) {
         float y = mine[u];
-        for (int w = 1; w < k_warps; ++w) y += mine[w * kTokens * rows + u];
+        for (int w = 1; w < k_warps; ++w) y += mine[w * all + u];
         mine[u] = gave_up ? NAN : y;
       }
       cluster_sync();
@@ -299,7 +321,7 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
       } else {
         float part[kWarps];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) part[w] = w < k_warps ? mine[w * kTokens * rows + u] : 0.0f;
+        for (int w = 0; w < kWarps; ++w) part[w] = w < k_warps ? mine[w * all + u] : 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) y += part[w];
         if (gave_up) y = NAN;  // (a wait ran out)
@@ -364,17 +386,19 @@ lt_status device_of(int* dev, int* sms) {
 }
 
 constexpr int kFewInputs = 96 * 1024;  // bytes of inputs in shared memory at most
-constexpr int kFewJoin = 2 * kWarps * 16 * kTokens * 4;
+constexpr int kFewJoin = 2 * kWarps * 16 * kTokens * 4;  // at most
 constexpr int kFewSmem = 1024 + kRing + kFewInputs + kFewJoin;
 
-// Whether a call takes the kernel for few tokens. us there and in the one for many (in a graph; eagerly its second
-// launch costs the host 6 more):
-//   n x k            1 token      2            3            4            6            8
-//   1000 x 2048      4.9, 6.0     5.7, 6.1     6.3, 6.1     6.8, 6.1     8.8, 6.2
-//   4096 x 4096      6.4, 8.5     7.5, 8.6     8.8, 8.6     9.4, 8.6     10.6, 8.7    11.8, 8.7
-//   10240 x 8192     17.6, 19.4   19.7, 19.6   23.2, 19.7   23.2, 19.7   25.8, 19.9   30.4, 19.7
-//   28672 x 8192     35.3, 38.1   38.5, 37.8   39.0, 38.0   45.3, 37.8   44.0, 37.9   66.6, 38.1
-bool few(int64_t tokens, int64_t n, int64_t k) { return tokens <= 2 || (tokens <= 4 && n * k <= (int64_t)1 << 25); }
+// Whether a call takes the kernel for few tokens. us there and in the one for many, in a graph; eagerly the second launch
+// of the latter costs the host 6 more, so that it is taken where it is faster by more than a tenth or so.
+//   n x k          1 token      2            3            4            6            8
+//   64 x 512       3.1, 4.6     3.2, 4.5     3.2, 4.5     3.3, 4.5     3.7, 4.5     3.9, 4.5
+//   4096 x 4096    6.4, 8.5     7.5, 8.6     8.4, 8.6     8.6, 8.6     8.3, 8.6     8.7, 8.6
+//   4099 x 5152    7.6, 11.4    9.5, 11.5    10.2, 11.5   10.6, 11.7   10.2, 11.7   10.8, 11.7
+//   14336 x 4096   11.3, 16.3   12.9, 16.4   14.8, 16.4   15.4, 16.6   16.7, 16.6   19.8, 16.7
+//   10240 x 8192   15.4, 19.4   17.3, 19.4   21.5, 19.7   24.7, 19.7   24.1, 19.8   29.1, 19.7
+//   28672 x 8192   29.1, 37.9   33.7, 37.9   33.8, 37.7   41.3, 38.0   39.1, 37.8   50.7, 38.0
+bool few(int64_t tokens, int64_t n, int64_t k) { return tokens <= 2 || (tokens <= 4 && n * k <= (int64_t)1 << 26) || (tokens <= 8 && n * k <= (int64_t)1 << 25); }
 
 lt_status check_sizes(int64_t tokens, int64_t n, int64_t k) {
   if (tokens < 0 || n < 0 || k < 0) return LT_ERR_INVALID_ARG;
@@ -477,8 +501,8 @@ lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_s
   p.bf16 = dtype == LT_DTYPE_BF16;
   const int here = (int)tokens;
   const int steps = (int)((k + kStep - 1) / kStep);
-  const auto smem_of = [&](int chunk) { return 1024 + kRing + here * (chunk * kStep * 2 + 32) + kFewJoin; };
-  p.row_warps = here <= 2 ? 1 : 2;
+  const auto smem_of = [&](int chunk) { return 1024 + kRing + here * (chunk * kStep * 2 + 32 + 2 * kWarps * 16 * 4); };
+  p.row_warps = here <= 2 ? 1 : here <= 4 ? 2 : 4;
   const int64_t row_blocks = (n + p.row_warps * 16 - 1) / (p.row_warps * 16);
   // as many steps' inputs in shared memory as fit; the inputs are cut over a cluster where the CTAs do not fill the SMs
   const int k_warps = kWarps / p.row_warps, most = (kFewInputs / here - 32) / (kStep * 2);
