@@ -67,6 +67,7 @@ constexpr int kManyStep = 128;  // inputs of a step
 struct ManyPlan {
   int tile, tiles;    // tokens of a tile, a multiple of 16 up to 256; tiles
   int row_tiles;      // tiles of 128 outputs of a CTA: 1 or 2
+  int columns;        // of tensor memory that a CTA has: 512 alone on its SM, 256 beside another
   int parts;          // CTAs of a cluster, along the inputs
   int code_ring, token_ring, row_ring;  // places for codes and tokens in shared memory, unpacked weights in tensor memory
   int sum_columns;    // of tensor memory, for the sums of a tile of outputs
@@ -90,7 +91,7 @@ struct ManyParams {
   float* inverse;     // [token]
   int64_t x_stride, out_stride;
   int32_t n, k, tokens, tile, parts, steps;
-  int32_t code_ring, token_ring, row_ring, sum_columns, rows_column;
+  int32_t code_ring, token_ring, row_ring, sum_columns, rows_column, columns;
   int32_t bf16, wide_scales, wide_out;
 };
 lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream);

@@ -30,7 +30,6 @@ struct Many {
   static constexpr int kPacked = kRows * 128;  // bytes of the codes of 256 inputs
 };
 constexpr int kMaxRing = 8;
-constexpr int kColumns = 512;
 
 struct Shared {
   uint64_t codes_full[kMaxRing], codes_empty[kMaxRing];
@@ -202,7 +201,7 @@ __device__ __forceinline__ void unpack_role(const ManyParams& p, Shared* sh, uin
 }
 
 template <int kTiles>
-__global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams p, const __grid_constant__ CUtensorMap codes) {
+__global__ void __launch_bounds__(Many<kTiles>::kCta, 3 - kTiles) many_kernel(ManyParams p, const __grid_constant__ CUtensorMap codes) {
   constexpr int kRows = Many<kTiles>::kRows, kCta = Many<kTiles>::kCta, kUnpackWarps = Many<kTiles>::kUnpackWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (lt::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
     lt::mbar_fence_init();
   }
   if (warp == kUnpackWarps) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(lt::smem_u32(&sh->tmem)), "n"(kColumns) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(lt::smem_u32(&sh->tmem)), "r"(p.columns) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
@@ -390,13 +389,15 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 1) many_kernel(ManyParams 
   __syncthreads();
   fence_after();
   dependents_launch();
-  if (warp == kUnpackWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "n"(kColumns) : "memory");
+  if (warp == kUnpackWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(p.columns) : "memory");
 }
 
 std::mutex g_mu;
 bool g_set[64][2];
 constexpr int kSmemMost = 220 * 1024;
-constexpr int kSmemAlone = 118 * 1024;  // more than half of an SM's
+constexpr int kSmemAlone = 118 * 1024;        // more than half of an SM's
+constexpr int kSmemBeside = 111 * 1024;       // less than half of it
+constexpr int kSmemBesideLeast = 78 * 1024;  // more than a third of it
 
 // The driver's call that makes a tensor map, by its name: the library is not linked against it.
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -464,36 +465,60 @@ ManyPlan many_plan(int dev, int64_t tokens, int64_t n, int64_t k) {
   ManyPlan best = {};
   double least = 0.0;
   const int64_t steps = (k + kManyStep - 1) / kManyStep, supers = (steps + 1) / 2;
-  for (int row_tiles = 1; row_tiles <= 2; ++row_tiles) {
-    // sums and two steps' unpacked weights, at least, in 512 columns
-    const int most = row_tiles == 1 ? 256 : 128, rows = row_tiles * 128;
+  // One or two tiles of outputs a CTA alone on its SM, with all of tensor memory, or (last) one with half of it and another
+  // CTA beside it.
+  for (int kind = 0; kind < 3; ++kind) {
+    const bool half = kind == 2;
+    const int row_tiles = kind == 1 ? 2 : 1, columns = half ? 256 : 512, rows = row_tiles * 128;
+    // sums and two steps' unpacked weights, at least, in the columns
+    const int most = kind == 0 ? 256 : 128, room = (half ? kSmemBeside : kSmemMost) - 1024;
     const int64_t row_ctas = (n + rows - 1) / rows;
     const int64_t fewest = (tokens + most - 1) / most;
     for (int64_t tiles = fewest; tiles < fewest + 6 && tiles <= (tokens + 15) / 16; ++tiles) {
       ManyPlan a = {};
       a.row_tiles = row_tiles;
+      a.columns = columns;
       a.tile = (int)((tokens + tiles - 1) / tiles + 15) / 16 * 16;
       a.tiles = (int)((tokens + a.tile - 1) / a.tile);
-      // four places for tokens, then as many for codes as there is room (they are asked for while the tokens are still laid
-      // out), the rest for tokens
-      const int room = kSmemMost - 1024;
-      a.code_ring = (room - 4 * a.tile * 256) / (rows * 128);
+      // four places for tokens (two, with half the room), then as many for codes as there is room (they are asked for while the
+      // tokens are still laid out), the rest for tokens
+      a.code_ring = (room - (half ? 2 : 4) * a.tile * 256) / (rows * 128);
       a.code_ring = a.code_ring > 6 ? 6 : a.code_ring < 2 ? 2 : a.code_ring;
+      if (half && a.code_ring > 3) a.code_ring = 3;
       a.token_ring = (room - a.code_ring * rows * 128) / (a.tile * 256);
       if (a.token_ring > kMaxRing) a.token_ring = kMaxRing;
       a.sum_columns = (a.tile + 31) / 32 * 32;
-      a.row_ring = (kColumns - row_tiles * a.sum_columns) / (row_tiles * 64);
+      a.row_ring = (columns - row_tiles * a.sum_columns) / (row_tiles * 64);
       if (a.row_ring > kMaxRing) a.row_ring = kMaxRing;
       a.smem = a.code_ring * rows * 128 + a.token_ring * a.tile * 256;
+      // Neither more CTAs an SM than that, ever, whatever the sizes: each finds its columns of tensor memory free. One that waited
+      // for them while its cluster waits for it could be waited for in turn by the cluster that holds them.
+      const int least_smem = half ? kSmemBesideLeast : kSmemAlone;
+      if (a.smem < least_smem) a.smem = least_smem;
       for (int parts = 1; parts <= kMaxParts && (parts == 1 || supers >= parts * 2); ++parts) {
         if (fit[parts] < 1) break;
-        if (parts > 1 && (rows / 32 + parts - 1) / parts * parts * a.tile * 128 > (a.smem > kSmemAlone ? a.smem : kSmemAlone)) continue;
+        if (parts > 1 && (rows / 32 + parts - 1) / parts * parts * a.tile * 128 > a.smem) continue;
         // Clocks, as measured: a step's products, unpacking, bytes from memory (all CTAs') and from the L2 cache, whichever is
-        // longest; a CTA's start, and its end, longer with a join.
-        const int64_t clusters = row_ctas * a.tiles, waves = (clusters + fit[parts] - 1) / fit[parts];
-        const double from_memory = (double)(clusters < fit[parts] ? clusters : fit[parts]) * parts * rows * 72.0 / a.tiles / 2800.0;
-        const double step = fmax(fmax((row_tiles == 1 ? 4.6 : 10.7) * a.tile, row_tiles == 1 ? 560.0 : 700.0), fmax(from_memory, (a.tile * 256.0 + rows * 72.0) / 64.0));
-        const double time = (double)waves * ((double)((supers + parts - 1) / parts) * 2 * step + 3000.0 + 18.0 * a.tile * row_tiles + (parts > 1 ? 4000.0 + 400.0 * parts : 500.0));
+        // longest; a CTA's start, and its end, longer with a join. Two CTAs beside each other have a step each in the
+        // time that their SM takes for both, and hide each other's start and end.
+        const int64_t clusters = row_ctas * a.tiles;
+        const auto round = [&](int64_t at_once, int beside) {
+          const double from_memory = (double)at_once * parts * rows * 72.0 / a.tiles / 2800.0;
+          const double products = (row_tiles == 1 ? 4.6 : 10.7) * a.tile;
+          const double unpacking = row_tiles == 1 ? 560.0 : 700.0, from_cache = (a.tile * 256.0 + rows * 72.0) / 64.0;
+          const double step = beside == 2 ? fmax(fmax(8.6 * a.tile, 800.0), fmax(from_memory, 2.0 * from_cache))
+                                          : fmax(fmax(products, unpacking), fmax(from_memory, from_cache));
+          return (double)((supers + parts - 1) / parts) * 2 * step + 3000.0 + 18.0 * a.tile * row_tiles +
+                 (parts > 1 ? 4000.0 + 400.0 * parts : 500.0);
+        };
+        double time;
+        if (half) {
+          const int64_t pairs = clusters / (2 * fit[parts]), left = clusters % (2 * fit[parts]);
+          time = (double)pairs * round(2 * fit[parts], 2) + (left == 0 ? 0.0 : round(left, pairs == 0 && left <= fit[parts] ? 1 : 2));
+        } else {
+          const int64_t waves = (clusters + fit[parts] - 1) / fit[parts];
+          time = (double)waves * round(clusters < fit[parts] ? clusters : fit[parts], 1);
+        }
         if (best.tile == 0 || time < least) {
           least = time;
           best = a;
@@ -502,9 +527,6 @@ ManyPlan many_plan(int dev, int64_t tokens, int64_t n, int64_t k) {
       }
     }
   }
-  // One CTA an SM, always: a CTA has all of tensor memory, and one that waits for it while its cluster waits for it
-  // could be waited for in turn by the cluster that holds it.
-  if (best.smem < kSmemAlone) best.smem = kSmemAlone;
   best.smem += 1024;
   best.steps = steps;
   best.x_bytes = (int64_t)best.tiles * best.tile * steps * 256;
@@ -530,6 +552,7 @@ lt_status launch_many(int dev, ManyParams* p, const ManyPlan& plan, void* stream
   p->row_ring = plan.row_ring;
   p->sum_columns = plan.sum_columns;
   p->rows_column = plan.row_tiles * plan.sum_columns;
+  p->columns = plan.columns;
   p->wide_scales = p->k % 256 == 0;
   p->wide_out = reinterpret_cast<uintptr_t>(p->out) % 16 == 0 && p->out_stride % 8 == 0;
   CUtensorMap map;
