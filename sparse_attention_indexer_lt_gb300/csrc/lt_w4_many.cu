@@ -506,7 +506,7 @@ ManyPlan many_plan(int dev, int64_t tokens, int64_t n, int64_t k) {
           const double from_memory = (double)at_once * parts * rows * 72.0 / a.tiles / 2800.0;
           const double products = (row_tiles == 1 ? 4.6 : 10.7) * a.tile;
           const double unpacking = row_tiles == 1 ? 560.0 : 700.0, from_cache = (a.tile * 256.0 + rows * 72.0) / 64.0;
-          const double step = beside == 2 ? fmax(fmax(8.6 * a.tile, 800.0), fmax(from_memory, 2.0 * from_cache))
+          const double step = beside == 2 ? fmax(fmax(8.6 * a.tile, 720.0), fmax(from_memory, 2.0 * from_cache))
                                           : fmax(fmax(products, unpacking), fmax(from_memory, from_cache));
           return (double)((supers + parts - 1) / parts) * 2 * step + 3000.0 + 18.0 * a.tile * row_tiles +
                  (parts > 1 ? 4000.0 + 400.0 * parts : 500.0);
