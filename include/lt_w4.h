@@ -41,7 +41,7 @@ lt_status lt_w4_quantise(const void* w, int32_t dtype, int64_t n, int64_t k, int
 /*
  * lt_w4_linear -- out[t][i] = sum_j x[t][j] code[i][j] scale[i][j / 32] (+ bias[i]).
  *
- *   x         [tokens][k] of `dtype` (LT_DTYPE_BF16 or _F16), inputs contiguous, the start
+ *   x         [tokens][k] of `dtype` (LT_DTYPE_BF16 or _F16), at most 524280 tokens, inputs contiguous, the start
  *             16-byte aligned, x_stride (elements, a multiple of 8) from token to token
  *   bias      [n] of `dtype`, or NULL
  *   out       [tokens][n] of `dtype`, outputs contiguous, out_stride elements from token to token

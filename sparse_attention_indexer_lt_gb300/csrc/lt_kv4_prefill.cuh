@@ -46,6 +46,14 @@
 // of 32 positions (1160 with those): 1.21 PFLOP/s, 63% of cuBLAS's burst, where four waves of 512 CTAs on 152
 // SMs allow 84%. The unpacked tile's way, read, write and fence, is what is left: 748 us without its writes.
 //
+// Shaped logits (caps, slopes, prefixes) pass once more through tensor memory: shaped, hidden and their maximum taken
+// 32 columns at a time. A cap is a polynomial while the logits are below it (12 instructions a logit in all; by
+// exponential and reciprocal, which the special function unit has to do for the softmax already, 1066 us against 1031 on the
+// chunk below); the chain from a tile's logits to its weights is what bounds it, twice the plain one's: 2048
+// tokens behind 14336, 32 query heads on 8 kv heads of 128, cap and slopes, 975 us (410 plain). Dropped: no shaping before the
+// weights where a bound shows that the maximum stays (1148: with slopes it moves, with a cap alone the two readings cost as
+// much), 16 columns at a time (1135).
+//
 // A value that is NaN, or whose scale is outside the format, is unpacked as zero, and the rows that see it note
 // the group: a row's output is NaN there whatever its weight, and rows that do not see it stay clean.
 

@@ -5,13 +5,21 @@
 // scaling, feeding the tensor core. The weights are the 16-row operand straight from registers (m16n8k16,
 // fp32 sums), the tokens the eight columns. The order of the inputs within a product is free, so a lane
 // takes 16 bytes of codes, a whole group of 32 inputs, of rows g and g + 8: one scale a row, and the
-// tokens' fragments are 16 bytes of the same inputs from shared memory.
+// tokens' fragments are 16 bytes of the same inputs from shared memory. (tcgen05 would want the unpacked
+// weights in tensor memory: that is the kernel for many tokens, slower up to two of them.)
 //
 // Each warp has a ring of its own, of 256 inputs of 16 rows (their codes by a tensor map, their scales by
-// another), and asks for the next ones itself. A CTA's eight warps are one or two row tiles by eight or four
-// parts of the inputs; it stays and walks over row blocks with the tokens in shared memory. A cluster cuts the inputs
+// another), and asks for the next ones itself. A CTA's eight warps are 1, 2 or 4 row tiles by 8, 4 or 2 parts of the
+// inputs; it stays and walks over row blocks with the tokens in shared memory. A cluster cuts the inputs
 // further where there are few rows. The parts join in shared memory and over distributed shared memory, in one order
 // whatever the timing.
+//
+// What bounds it: issue and the ALU pipe (66% and 52% of their rates): 16 rows by 128 inputs take some 180 warp
+// instructions, 64 of them conversions and scalings. One token through 8192 x 28672 (132 MB): 29 us, 4.5 TB/s, where
+// the copy rate allows 19.5. On the way: a CTA for each row block 40 us; CTAs that stay 34; scales of two groups a load
+// 33; tensor maps and rings of two stages 30 (with three stages, and a CTA less an SM, 33); fewer steps a join 28 to
+// 29. Through 4096 x 4096: 10.0, 6.4, 6.1, 6.0, 6.4 us, most of it the way from launch to
+// first weights and the join.
 
 #include <mutex>
 
@@ -392,12 +400,12 @@ constexpr int kFewSmem = 1024 + kRing + kFewInputs + kFewJoin;
 // Whether a call takes the kernel for few tokens. us there and in the one for many, in a graph; eagerly the second launch
 // of the latter costs the host 6 more, so that it is taken where it is faster by more than a tenth or so.
 //   n x k          1 token      2            3            4            6            8
-//   64 x 512       3.1, 4.6     3.2, 4.5     3.2, 4.5     3.3, 4.5     3.7, 4.5     3.9, 4.5
-//   4096 x 4096    6.4, 8.5     7.5, 8.6     8.4, 8.6     8.6, 8.6     8.3, 8.6     8.7, 8.6
-//   4099 x 5152    7.6, 11.4    9.5, 11.5    10.2, 11.5   10.6, 11.7   10.2, 11.7   10.8, 11.7
-//   14336 x 4096   11.3, 16.3   12.9, 16.4   14.8, 16.4   15.4, 16.6   16.7, 16.6   19.8, 16.7
-//   10240 x 8192   15.4, 19.4   17.3, 19.4   21.5, 19.7   24.7, 19.7   24.1, 19.8   29.1, 19.7
-//   28672 x 8192   29.1, 37.9   33.7, 37.9   33.8, 37.7   41.3, 38.0   39.1, 37.8   50.7, 38.0
+//   64 x 512       3.2, 4.7     3.6, 4.7     3.8, 4.7     3.9, 4.7     5.2, 4.7     5.6, 4.7
+//   4096 x 4096    6.4, 8.5     7.6, 8.6     8.3, 8.6     8.9, 8.6     9.7, 8.6     10.1, 8.6
+//   4099 x 5152    8.1, 10.0    9.1, 10.1    10.3, 10.2   10.7, 10.2   11.2, 10.3   11.6, 10.4
+//   14336 x 4096   11.9, 14.1   12.9, 14.3   14.6, 14.3   15.1, 14.5   16.5, 14.4   19.1, 14.5
+//   10240 x 8192   15.6, 16.7   17.5, 17.0   21.0, 17.1   23.3, 17.1   24.3, 17.1   28.5, 17.1
+//   28672 x 8192   29.3, 34.4   33.6, 34.6   33.1, 34.8   39.9, 34.6   39.2, 35.0   49.8, 35.0
 bool few(int64_t tokens, int64_t n, int64_t k) { return tokens <= 2 || (tokens <= 4 && n * k <= (int64_t)1 << 26) || (tokens <= 8 && n * k <= (int64_t)1 << 25); }
 
 lt_status check_sizes(int64_t tokens, int64_t n, int64_t k) {
