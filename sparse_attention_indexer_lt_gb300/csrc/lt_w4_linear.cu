@@ -49,7 +49,7 @@ struct LinearParams {
   int32_t chunk;       // steps whose inputs are in shared memory at a time
   int32_t join_at;     // where the warps' sums are joined, behind the inputs
   int32_t bf16, wide_scales;
-  uint32_t stage_bytes;
+  uint32_t stage_bytes, zero;
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -131,11 +131,11 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
   range(0, &from0, &to0);
   int next_chunk = 0, next_s = from0, next_to = to0, next_row = first * rows + wr * 16;
   const int end_row = from0 < to0 ? blocks * rows : 0;
-  auto bring = [&](int stage) {  // (the whole warp's numbers; lane 0 asks)
+  auto bring = [&](int stage, uint32_t zero) {  // (the whole warp's numbers; lane 0 asks)
     if (next_row >= end_row) return;
     if (lane == 0) {
       uint64_t* bar = &bars[warp][stage];
-      const uint32_t at = lt::smem_u32(ring) + stage * kStageBytes;
+      const uint32_t at = lt::smem_u32(ring) + stage * kStageBytes + zero;
       lt::mbar_arrive_tx(bar, p.stage_bytes);
       tensor_in(at, &codes, next_s * 128, next_row, bar);
       if (p.wide_scales) tensor_in(at + kStageCodes, &scales, next_s * 16, next_row, bar);
@@ -155,7 +155,7 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
     } while (next_s >= next_to);
   };
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) bring(s);
+  for (int s = 0; s < kStages; ++s) bring(s, 0);
 
   uint8_t* inputs = smem + kRing;
   const int pitch = p.chunk * kStep * 2 + 32;
@@ -273,8 +273,7 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
             kb[u] = __ldg(p.scales + (int64_t)min(ra + 8, p.n - 1) * groups + group);
           }
         }
-        __syncwarp();  // every lane has read the stage
-        bring(place);
+        bring(place, zero_of(wa[0].x ^ wa[1].x ^ wb[0].x ^ wb[1].x ^ ka[0] ^ ka[1] ^ kb[0] ^ kb[1], p.zero));
         if (++place == kStages) {
           place = 0;
           parity ^= 1u;

@@ -172,9 +172,9 @@ __device__ __forceinline__ void unpack_role(const ManyParams& p, Shared* sh, uin
 #pragma unroll
     for (int g = 0; g < 4; ++g)
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(w[g][0]), "=r"(w[g][1]), "=r"(w[g][2]), "=r"(w[g][3]) : "r"(piece[g] + code.at * Many<kTiles>::kPacked));
-    __syncwarp();
-    if (lane == 0) arrive(&sh->codes_empty[code.at]);
+                   : "=r"(w[g][0]), "=r"(w[g][1]), "=r"(w[g][2]), "=r"(w[g][3]) : "r"(piece[g] + code.at * Many<kTiles>::kPacked) : "memory");
+    const uint32_t here = zero_of(w[0][0] ^ w[1][0] ^ w[2][0] ^ w[3][0], p.zero);
+    if (lane == 0) arrive(&sh->codes_empty[code.at] + here);
     code.next(p.code_ring);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

@@ -220,6 +220,23 @@ def test_streams_graphs_and_workspaces(tokens):
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
 
 
+@pytest.mark.parametrize("tokens,n,k", [(64, 8192, 10240), (509, 4096, 4096), (200, 2048, 8192), (16, 6144, 8192), (1, 8192, 10240),
+                                        (8, 4096, 8192), (3, 4099, 5152)])
+def test_weights_from_memory_and_from_the_cache(tokens, n, k):
+    """A result does not go by how fast its weights come: as they are, and after a write of more than the L2 cache."""
+    import sparse_attention_indexer_lt_gb300 as lt
+    codes, scales = (t.cuda() for t in make(n, k, seed=n + k))
+    x = torch.randn(tokens, k, generator=torch.Generator().manual_seed(tokens)).half().cuda()
+    want = lt.w4_linear(x, codes, scales)
+    check(want[:, :300], x, codes[:300].contiguous(), scales[:300].contiguous())
+    flush, got = torch.empty(200 << 20, dtype=torch.uint8, device="cuda"), []
+    for i in range(40):
+        flush.fill_(i)
+        got.append(lt.w4_linear(x, codes, scales))
+    off = [i for i, y in enumerate(got) if not torch.equal(y, want)]
+    assert not off, f"calls {off}"
+
+
 def test_weights_beyond_32_bit_offsets():
     """More than 2^32 bytes of codes, and a last row that is right."""
     import sparse_attention_indexer_lt_gb300 as lt
