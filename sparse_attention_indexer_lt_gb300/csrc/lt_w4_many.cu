@@ -405,9 +405,10 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 3 - kTiles) many_kernel(Ma
 std::mutex g_mu;
 bool g_set[64][2];
 constexpr int kSmemMost = 220 * 1024;
-constexpr int kSmemAlone = 118 * 1024;        // more than half of an SM's
-constexpr int kSmemBeside = 111 * 1024;       // less than half of it
+constexpr int kSmemBeside = 111 * 1024;       // less than half of an SM's
 constexpr int kSmemBesideLeast = 78 * 1024;  // more than a third of it
+constexpr int kSmemAlone = 150 * 1024;        // more than what is left beside one of those
+static_assert(3 * kSmemBesideLeast >= 228 * 1024 && kSmemAlone + kSmemBesideLeast >= 228 * 1024, "columns for all CTAs of an SM");
 
 // The driver's call that makes a tensor map, by its name: the library is not linked against it.
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -501,8 +502,9 @@ ManyPlan many_plan(int dev, int64_t tokens, int64_t n, int64_t k) {
       a.row_ring = (columns - row_tiles * a.sum_columns) / (row_tiles * 64);
       if (a.row_ring > kMaxRing) a.row_ring = kMaxRing;
       a.smem = a.code_ring * rows * 128 + a.token_ring * a.tile * 256;
-      // Neither more CTAs an SM than that, ever, whatever the sizes: each finds its columns of tensor memory free. One that waited
-      // for them while its cluster waits for it could be waited for in turn by the cluster that holds them.
+      // Neither more CTAs an SM than that, ever, whatever the sizes, and also where calls of both kinds run at once: each
+      // finds its columns of tensor memory free. One that waited for them while its cluster waits for it could be waited
+      // for in turn by the cluster that holds them. (A CTA without a cluster may wait, or be waited for: it ends.)
       const int least_smem = half ? kSmemBesideLeast : kSmemAlone;
       if (a.smem < least_smem) a.smem = least_smem;
       for (int parts = 1; parts <= kMaxParts && (parts == 1 || supers >= parts * 2); ++parts) {

@@ -237,6 +237,28 @@ def test_weights_from_memory_and_from_the_cache(tokens, n, k):
     assert not off, f"calls {off}"
 
 
+def test_calls_of_all_kinds_at_once():
+    # CTAs alone on their SMs and beside each other, in clusters and not, on four streams: each call has its own answer
+    import sparse_attention_indexer_lt_gb300 as lt
+    sizes = [(64, 8192, 4096), (16, 2048, 8192), (509, 1024, 4096), (128, 512, 8192), (5, 4096, 1024), (64, 8192, 10240)]
+    calls = []
+    for i, (tokens, n, k) in enumerate(sizes):
+        codes, scales = lt.w4_quantise(torch.randn(n, k, device="cuda", generator=torch.Generator("cuda").manual_seed(i)) * 0.1)
+        x = torch.randn(tokens, k, device="cuda", generator=torch.Generator("cuda").manual_seed(50 + i)).to(torch.float16)
+        calls.append((x, codes, scales, lt.w4_linear(x, codes, scales)))
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(60):
+        for i, s in enumerate(streams):
+            which = (turn + i * (1 + turn // 6)) % len(calls)
+            x, codes, scales, _ = calls[which]
+            got.append((which, lt.w4_linear(x, codes, scales, stream=s)))
+    torch.cuda.synchronize()
+    for which, y in got:
+        assert torch.equal(y, calls[which][3]), which
+
+
 def test_weights_beyond_32_bit_offsets():
     """More than 2^32 bytes of codes, and a last row that is right."""
     import sparse_attention_indexer_lt_gb300 as lt
