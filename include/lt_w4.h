@@ -8,7 +8,7 @@
  *   codes   uint8 [n][k / 2], two a byte, the lower input in the low nibble
  *   scales  fp16 [n][k / 32]
  *
- * k is a multiple of 32, both start on 16 bytes. lt_w4_quantise makes them; codes and
+ * k is a multiple of 32, n and k are below 2^30, both start on 16 bytes. lt_w4_quantise makes them; codes and
  * scales from elsewhere serve as well, the scales finite, at least 0 and at most 10912 (then
  * code * scale does not overflow; lt_w4_quantise's have 9 significant bits, which makes
  * code * scale an exact fp16 number. Products of longer scales are rounded to fp16,

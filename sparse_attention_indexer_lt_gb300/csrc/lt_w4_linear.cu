@@ -15,11 +15,11 @@
 // whatever the timing.
 //
 // What bounds it: issue and the ALU pipe (66% and 52% of their rates): 16 rows by 128 inputs take some 180 warp
-// instructions, 64 of them conversions and scalings. One token through 8192 x 28672 (132 MB): 29 us, 4.5 TB/s, where
+// instructions, 64 of them conversions and scalings. One token through 8192 x 28672 (132 MB): 30 us, 4.4 TB/s, where
 // the copy rate allows 19.5. On the way: a CTA for each row block 40 us; CTAs that stay 34; scales of two groups a load
 // 33; tensor maps and rings of two stages 30 (with three stages, and a CTA less an SM, 33); fewer steps a join 28 to
-// 29. Through 4096 x 4096: 10.0, 6.4, 6.1, 6.0, 6.4 us, most of it the way from launch to
-// first weights and the join.
+// 29; places handed back by what was loaded from them 30. Through 4096 x 4096: 10.0, 6.4, 6.1, 6.0, 6.4, 6.5 us, most of
+// it the way from launch to first weights and the join.
 
 #include <mutex>
 
@@ -397,7 +397,8 @@ constexpr int kFewJoin = 2 * kWarps * 16 * kTokens * 4;  // at most
 constexpr int kFewSmem = 1024 + kRing + kFewInputs + kFewJoin;
 
 // Whether a call takes the kernel for few tokens. us there and in the one for many, in a graph; eagerly the second launch
-// of the latter costs the host 6 more, so that it is taken where it is faster by more than a tenth or so.
+// of the latter costs the host 6 more, so that it is taken where it is faster by more than a tenth or so. (Handing places back by what was loaded from them has since
+// added 1 to 3% to the former, 1% to the latter.)
 //   n x k          1 token      2            3            4            6            8
 //   64 x 512       3.2, 4.7     3.6, 4.7     3.8, 4.7     3.9, 4.7     5.2, 4.7     5.6, 4.7
 //   4096 x 4096    6.4, 8.5     7.6, 8.6     8.3, 8.6     8.9, 8.6     9.7, 8.6     10.1, 8.6
@@ -407,9 +408,12 @@ constexpr int kFewSmem = 1024 + kRing + kFewInputs + kFewJoin;
 //   28672 x 8192   29.3, 34.4   33.6, 34.6   33.1, 34.8   39.9, 34.6   39.2, 35.0   49.8, 35.0
 bool few(int64_t tokens, int64_t n, int64_t k) { return tokens <= 2 || (tokens <= 4 && n * k <= (int64_t)1 << 26) || (tokens <= 8 && n * k <= (int64_t)1 << 25); }
 
+constexpr int64_t kMostSize = (int64_t)1 << 30;
+
 lt_status check_sizes(int64_t tokens, int64_t n, int64_t k) {
   if (tokens < 0 || n < 0 || k < 0) return LT_ERR_INVALID_ARG;
-  if (k == 0 || k % 32 != 0 || k > INT32_MAX - 1024 || n > INT32_MAX - 1024 || tokens > 65535 * 8) return LT_ERR_UNSUPPORTED;
+  // (rows and inputs are 32-bit numbers, also those that a CTA would take next)
+  if (k == 0 || k % 32 != 0 || k >= kMostSize || n >= kMostSize || tokens > 65535 * 8) return LT_ERR_UNSUPPORTED;
   return LT_OK;
 }
 

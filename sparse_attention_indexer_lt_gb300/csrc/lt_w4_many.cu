@@ -12,9 +12,9 @@
 // parts join over distributed shared memory in one order.
 //
 // What bounds it. Tokens by the hundred: the tokens' way from the L2 cache, which each 128 outputs take again (some 10
-// TB/s), and the starts and ends of three waves: 509 tokens through 4096 x 14336 take 48 us, 1.25 PFLOP/s, 65% of
+// TB/s), and the starts and ends of three waves: 509 tokens through 4096 x 14336 take 49 us, 1.23 PFLOP/s, 63% of
 // cuBLAS's burst. Some ten tokens: the start (layout, 4 us to the first product), memory (4.7 TB/s of codes
-// while products run) and the cluster's join (4 us): 64 tokens through 8192 x 10240 take 20.4 us, the bytes 7.3.
+// while products run) and the cluster's join (4 us): 64 tokens through 8192 x 10240 take 20.6 us, the bytes 7.3.
 // On the way, us for those two: the kernel for few tokens, tokens in tiles of 32, 717 and 217; unpacked weights through shared memory,
 // 128 outputs, 76 and 67; 256 outputs and the weights asked for before the tokens' layout 62 and 46; codes by a tensor map,
 // unpacked weights in tensor memory, 80 and 23.5 (poor tiles); steps of 128 inputs in place of 64 57 and 22; whole lines

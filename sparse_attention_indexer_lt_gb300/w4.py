@@ -73,6 +73,8 @@ def w4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, bia
     if scales.shape != (n, k // _GROUP):
         raise ValueError(f"scales must have shape {(n, k // _GROUP)}, has {tuple(scales.shape)}")
     x_stride, one = x.stride()
+    if tokens == 1:
+        x_stride = k  # (of one token it says nothing)
     x_ptr, codes_ptr, scales_ptr = x.data_ptr(), codes.data_ptr(), scales.data_ptr()
     if tokens > 0 and (one != 1 or x_stride % 8 or x_ptr % 16):
         raise ValueError("x must have contiguous rows, a row stride that is a multiple of 8 and a 16-byte aligned start")

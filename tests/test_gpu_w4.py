@@ -259,6 +259,14 @@ def test_calls_of_all_kinds_at_once():
         assert torch.equal(y, calls[which][3]), which
 
 
+def test_one_token_has_any_stride():
+    import sparse_attention_indexer_lt_gb300 as lt
+    codes, scales = (t.cuda() for t in make(40, 64))
+    x = torch.randn(64, 1, generator=torch.Generator().manual_seed(0)).half().cuda().t()
+    assert x.shape == (1, 64) and x.stride(0) == 1
+    check(lt.w4_linear(x, codes, scales), x, codes, scales)
+
+
 def test_weights_beyond_32_bit_offsets():
     """More than 2^32 bytes of codes, and a last row that is right."""
     import sparse_attention_indexer_lt_gb300 as lt

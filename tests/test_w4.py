@@ -57,7 +57,8 @@ def _quantise(lib, **kw):
     (dict(x=None), 1), (dict(codes=None), 1), (dict(scales=None), 1), (dict(out=None), 1), (dict(dtype=0), 1), (dict(dtype=3), 1),
     (dict(tokens=-1), 1), (dict(n=-1), 1), (dict(k=-32), 1), (dict(xs=100), 1), (dict(x=P(0x1008)), 1), (dict(codes=P(0x1008)), 1),
     (dict(scales=P(0x1002)), 1), (dict(out=P(0x1001)), 1), (dict(bias=P(0x1001)), 1), (dict(k=48), 2), (dict(k=0), 2),
-    (dict(n=1 << 31), 2), (dict(k=1 << 31), 2), (dict(tokens=1 << 31), 2)])
+    (dict(n=1 << 31), 2), (dict(k=1 << 31), 2), (dict(tokens=1 << 31), 2), (dict(n=1 << 30), 2), (dict(k=1 << 30), 2),
+    (dict(tokens=524281), 2)])
 def test_linear_refuses(lib, bad, status):
     assert _linear(lib, **bad) == status
 
