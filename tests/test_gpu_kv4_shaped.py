@@ -215,6 +215,35 @@ def test_plain_calls_and_shapes_that_change_nothing():
             assert (got - out).abs().max() <= 2.0 ** -10 * out.abs().max() and (got_lse - lse).abs().max() <= 1e-5
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("page_size", [1, 16, 128])
+@pytest.mark.parametrize("new", [1, 4, 8, 300])
+def test_rows_from_memory_and_from_the_cache(dim, page_size, new):
+    """A result does not go by how fast the rows come: as they are, and after a write of more than the L2 cache."""
+    import sparse_attention_indexer_lt_gb300 as lt
+    requests, width, heads, group = 20, 2048 // page_size, 4, 4
+    gen = torch.Generator("cuda").manual_seed(dim + new)
+    cache = lt.kv4_cache(requests * width, heads, page_size, dim)
+    k, v = (torch.randn(requests * 2048, heads, dim, device="cuda", generator=gen).half() for _ in range(2))
+    lt.kv4_store(k, v, cache, torch.arange(requests * 2048, device="cuda"))
+    table = torch.randperm(requests * width, device="cuda", generator=gen).int().view(requests, width)
+    lengths = torch.randint(new, 2048, (requests,), device="cuda", generator=gen).int()
+    starts = torch.arange(requests + 1, device="cuda").int() * new
+    q = torch.randn(requests * new, heads * group, dim, device="cuda", generator=gen).bfloat16()
+    slopes = torch.tensor(slopes_of(heads * group), device="cuda")
+    flush = torch.empty(200 << 20, dtype=torch.uint8, device="cuda")
+    ways = [{}, dict(softcap=20.0, prefix=lengths // 3), dict(slopes=slopes, window=900)]
+    if new < 300:
+        ways.append(dict(slopes=slopes, positions=torch.randint(0, new, (requests * new, 500), device="cuda", generator=gen).int()))
+    for kw in ways:
+        call = lambda: lt.kv4_attention(q, cache, table, lengths, starts=starts, max_new=new, **kw)  # noqa: E731
+        want, got = call(), []
+        for i in range(15):
+            flush.fill_(i)
+            got.append(call())
+        assert all(torch.equal(y, want) for y in got), kw
+
+
 def test_graphs_and_streams():
     p = Problem([300, 80], [2, 1], 2, 2, 128, 16, "bf16", seed=9)
     import sparse_attention_indexer_lt_gb300 as lt
