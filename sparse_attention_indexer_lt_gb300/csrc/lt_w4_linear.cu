@@ -15,11 +15,11 @@
 // whatever the timing.
 //
 // What bounds it: issue and the ALU pipe (66% and 52% of their rates): 16 rows by 128 inputs take some 180 warp
-// instructions, 64 of them conversions and scalings. One token through 8192 x 28672 (132 MB): 30 us, 4.4 TB/s, where
+// instructions, 64 of them conversions and scalings. One token through 8192 x 28672 (132 MB): 29 us, 4.5 TB/s, where
 // the copy rate allows 19.5. On the way: a CTA for each row block 40 us; CTAs that stay 34; scales of two groups a load
 // 33; tensor maps and rings of two stages 30 (with three stages, and a CTA less an SM, 33); fewer steps a join 28 to
-// 29; places handed back by what was loaded from them 30. Through 4096 x 4096: 10.0, 6.4, 6.1, 6.0, 6.4, 6.5 us, most of
-// it the way from launch to first weights and the join.
+// 29. Through 4096 x 4096: 10.0, 6.4, 6.1, 6.0, 6.4 us, most of it the way from launch to
+// first weights and the join.
 
 #include <mutex>
 
@@ -273,11 +273,6 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
             kb[u] = __ldg(p.scales + (int64_t)min(ra + 8, p.n - 1) * groups + group);
           }
         }
-        bring(place, zero_of(wa[0].x ^ wa[1].x ^ wb[0].x ^ wb[1].x ^ ka[0] ^ ka[1] ^ kb[0] ^ kb[1], p.zero));
-        if (++place == kStages) {
-          place = 0;
-          parity ^= 1u;
-        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint32_t sa = __byte_perm(ka[u], 0, 0x1010), sb = __byte_perm(kb[u], 0, 0x1010);
@@ -296,6 +291,13 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
             const uint4 b = *reinterpret_cast<const uint4*>((j & 1 ? odd : x) + u * 256 + (j >> 1) * 32);
             mma16816(acc, ha[0], hb[0], ha[1], hb[1], b.x, b.y);
             mma16816(acc, ha[2], hb[2], ha[3], hb[3], b.z, b.w);
+          }
+          if (u == 0) {  // (at the start of the step the wait for all loads costs 3%)
+            bring(place, zero_of(wa[0].x ^ wa[1].x ^ wb[0].x ^ wb[1].x ^ ka[0] ^ ka[1] ^ kb[0] ^ kb[1], p.zero));
+            if (++place == kStages) {
+              place = 0;
+              parity ^= 1u;
+            }
           }
         }
       }
@@ -397,8 +399,7 @@ constexpr int kFewJoin = 2 * kWarps * 16 * kTokens * 4;  // at most
 constexpr int kFewSmem = 1024 + kRing + kFewInputs + kFewJoin;
 
 // Whether a call takes the kernel for few tokens. us there and in the one for many, in a graph; eagerly the second launch
-// of the latter costs the host 6 more, so that it is taken where it is faster by more than a tenth or so. (Handing places back by what was loaded from them has since
-// added 1 to 3% to the former, 1% to the latter.)
+// of the latter costs the host 6 more, so that it is taken where it is faster by more than a tenth or so.
 //   n x k          1 token      2            3            4            6            8
 //   64 x 512       3.2, 4.7     3.6, 4.7     3.8, 4.7     3.9, 4.7     5.2, 4.7     5.6, 4.7
 //   4096 x 4096    6.4, 8.5     7.6, 8.6     8.3, 8.6     8.9, 8.6     9.7, 8.6     10.1, 8.6

@@ -173,9 +173,6 @@ __device__ __forceinline__ void unpack_role(const ManyParams& p, Shared* sh, uin
     for (int g = 0; g < 4; ++g)
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(w[g][0]), "=r"(w[g][1]), "=r"(w[g][2]), "=r"(w[g][3]) : "r"(piece[g] + code.at * Many<kTiles>::kPacked) : "memory");
-    const uint32_t here = zero_of(w[0][0] ^ w[1][0] ^ w[2][0] ^ w[3][0], p.zero);
-    if (lane == 0) arrive(&sh->codes_empty[code.at] + here);
-    code.next(p.code_ring);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint32_t h[32];
@@ -191,6 +188,9 @@ __device__ __forceinline__ void unpack_role(const ManyParams& p, Shared* sh, uin
         }
       }
       if (i == 0) {  // (the first half is converted before there has to be a place)
+        const uint32_t here = zero_of(w[0][0] ^ w[1][0] ^ w[2][0] ^ w[3][0], p.zero);
+        if (lane == 0) arrive(&sh->codes_empty[code.at] + here);
+        code.next(p.code_ring);
         if (!__all_sync(~0u, free)) wait_warp(&sh->rows_empty[place.at], place.parity, sh);
         fence_after();
       }
