@@ -71,6 +71,11 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[8]) {
   return w;
 }
 
+// 0, `zero`, which only the host knows; to the compiler a number made of all lanes' x. What was loaded to x has arrived in
+// every lane before anything that goes by it: a place in a ring is handed back so. (After a __syncwarp alone a load that was
+// needed last has come behind the hand-back, and saw what came next into its place.)
+__device__ __forceinline__ uint32_t zero_of(uint32_t x, uint32_t zero) { return __ballot_sync(~0u, x != 0) & zero; }
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));

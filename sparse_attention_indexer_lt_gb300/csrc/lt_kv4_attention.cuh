@@ -33,6 +33,7 @@ struct AttentionParams {
   int32_t part_rows;  // query rows of a part: max_new * group
   int32_t align;    // positions at which chunks and windows start: multiples of this (32 or 128)
   float scale_log2;
+  uint32_t zero;  // 0, which only the host knows (see zero_of)
   // shaped logits: cap tanh(s / cap) where cap > 0, less slope |own position - position|
   const float* slopes;    // [query heads]
   const int32_t* prefix;  // [requests]: positions below it are seen by all of the request's queries

@@ -603,7 +603,7 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
 // ---- unpacking: a packed stage's positions at a time, a thread the key or the value of a position (with
 // D = 256 half of its channels); half of the threads have keys, half values
 template <int D>
-__device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t* smem) {
+__device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job& job, Shared* sh, uint8_t* smem) {
   constexpr int kRow = row_bytes(D);
   constexpr int kParts = Smem<D>::kParts, kRaw = Smem<D>::kRaw;
   constexpr int kTok = Smem<D>::kTok, kRing = Smem<D>::kRing;
@@ -627,10 +627,11 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
       const bool there = (valid >> lane) & 1u;
       const uint8_t* from = smem + Smem<D>::kPacked + (stage * kPart + row) * kRow;
       // scales, fp16 pairs; a position that is not there counts as zeros, and so does a NaN value
-      uint32_t sc[kBlocks];
+      uint32_t sc[kBlocks], seen = 0;  // seen: a word of every load
 #pragma unroll
       for (int g = 0; g < kBlocks; ++g) {
         sc[g] = there ? reinterpret_cast<const uint32_t*>(from + D + part * (D / 16))[block0 + g] : 0u;
+        seen ^= sc[g];
         if (part == 1) sc[g] &= ~unfit_halves(sc[g]);
       }
       if (part == 0 && block0 == 0) {
@@ -644,12 +645,18 @@ __device__ __forceinline__ void unpack_role(const Job& job, Shared* sh, uint8_t*
         const uint32_t nan_rows = __ballot_sync(~0u, nan != 0);
         if (lane == 0) sh->nan_rows[word] = nan_rows;
         if (nan_rows) sh->nan_groups[i % kRing * kTok + half * kPart + row] = (uint8_t)nan;
+        seen ^= nan;
       }
       uint4 codes[2 * kBlocks];
 #pragma unroll
-      for (int c = 0; c < 2 * kBlocks; ++c) codes[c] = reinterpret_cast<const uint4*>(from + part * (D / 2))[2 * block0 + c];
-      __syncwarp();  // every lane has read the stage
-      if (lane == 0) arrive(&sh->packed_empty[stage]);
+      for (int c = 0; c < 2 * kBlocks; ++c) {
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(codes[c].x), "=r"(codes[c].y), "=r"(codes[c].z), "=r"(codes[c].w)
+                     : "r"(lt::smem_u32(from + part * (D / 2) + (2 * block0 + c) * 16)) : "memory");
+        seen ^= codes[c].x;
+      }
+      const uint32_t here = zero_of(seen, p.zero);  // every lane has read the stage
+      if (lane == 0) arrive(&sh->packed_empty[stage] + here);
       if (half == 0) {
         wait_warp(&sh->kv_empty[slot], slot_parity, sh);
         // (until then the queries are in the last slots)
@@ -813,7 +820,7 @@ __global__ void __launch_bounds__(kCta, 1) prefill_kernel(AttentionParams p) {
   if (warp < 4 * Smem<D>::kRowTiles)
     softmax_role<D, kShaped>(p, job, sh, smem, warp / 4);
   else if (warp < 12)
-    unpack_role<D>(job, sh, smem);
+    unpack_role<D>(p, job, sh, smem);
   else if (warp == 12)
     product_role<D>(job, sh, smem);
   else if (warp == 13)

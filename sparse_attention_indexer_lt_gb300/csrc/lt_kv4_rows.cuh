@@ -76,7 +76,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
 template <int N>
@@ -84,10 +84,10 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[N]) {
   if constexpr (N == 1) {
     w[0] = lds32(a);
   } else if constexpr (N == 2) {
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
   } else {
     static_assert(N == 4, "1, 2 or 4 words");
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
   }
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -227,9 +227,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   };
   auto page_of = [&](int pos) { return pos >= 0 ? __ldg(table + (pos >> p.shift)) : -1; };
   auto row_at = [&](int page, int pos) { return (((int64_t)page * p.heads + head) << p.shift) + (pos & ((1 << p.shift) - 1)); };
-  auto bring = [&](int stage, int pos, int page) {
+  auto bring = [&](int stage, int pos, int page, uint32_t zero) {
     const bool there = pos >= 0 && page >= 0 && page < p.pages;
-    const uint32_t tile_at = ring + stage * Sh::kTileBytes;
+    const uint32_t tile_at = ring + stage * Sh::kTileBytes + zero;
     if constexpr (kList) {
       // one row a position: 16-byte copies, the lanes along the rows (a bulk copy a row is no faster: 51 us either
       // way on 1021 lists of 512, then bound by the chain of loads at a CTA's start)
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
     next_page = page_of(next_pos);
 #pragma unroll
     for (int s = 0; s < Sh::kStages; ++s)
-      if (warp + s * kWarps < tiles) bring(s, pos[s], page[s]);
+      if (warp + s * kWarps < tiles) bring(s, pos[s], page[s], 0);
   }
   float factor[NT][2];  // of columns 2c, 2c + 1: logits in units of log 2
   int limit[NT][2], low[NT][2];
@@ -540,9 +540,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
         }
       }
     }
-    __syncwarp();  // every lane has read the stage
+    __syncwarp();
     if (tile + Sh::kStages * kWarps < tiles) {
-      bring(stage, next_pos, next_page);
+      // Every lane has read the stage: the vote on the maximum went by all keys, and these sums by all values, a word of
+      // them each.
+      uint32_t seen = 0;
+#pragma unroll
+      for (int i = 0; i < kWordsV; ++i) seen ^= __float_as_uint(acc[0][i * 4 + 3][0]);
+      bring(stage, next_pos, next_page, zero_of(seen, p.zero));
       next_pos = later_pos;
       next_page = page_of(next_pos);
       later_pos = position_of(tile + (Sh::kStages + 2) * kWarps);

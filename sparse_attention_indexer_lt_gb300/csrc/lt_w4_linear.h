@@ -49,10 +49,6 @@ __device__ __forceinline__ uint32_t peer_address(uint32_t addr, int rank) {
 __device__ __forceinline__ void put_peer(uint32_t addr, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
-// 0, `zero`, which only the host knows; to the compiler a number made of all lanes' x. What was loaded to x has arrived in
-// every lane before anything that goes by it: a place in a ring is handed back so. (After a __syncwarp alone a load that was
-// needed last has come behind the hand-back, and saw what came next into its place.)
-__device__ __forceinline__ uint32_t zero_of(uint32_t x, uint32_t zero) { return __ballot_sync(~0u, x != 0) & zero; }
 // An output's bias, and the output, rounded once.
 __device__ __forceinline__ float bias_of(const void* bias, int row, int bf16) {
   if (bias == nullptr) return 0.0f;
