@@ -33,7 +33,7 @@
 // requests). Measured (4.5-bit rows read once): 64 requests of 2048 to 65536 positions,
 // 4 kv heads of 128, 253 us, 4.9 TB/s; one request of 262144 positions, 4 heads of 256,
 // 65 us, 4.7 TB/s; the copy rate is 6.8. The widest instances (32 rows; 16 with heads of 256), which serve 17 to
-// 64 rows, do not fit the registers: they spill 468 bytes a thread with heads of 128, 252 with 64, 232 with 256.
+// 64 rows, do not fit the registers: they spill 404 bytes a thread with heads of 128, 308 with 64, 224 with 256.
 //
 // Shaped logits cost a lane some 5 instructions a logit with a cap and 2 with a slope, of 8 a tile and row tile: 64 ragged requests
 // with slopes take 280 us (253 plain), with 127 registers a thread as without.
@@ -348,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   int stage = 0;
   uint32_t parity = 0;
   for (int tile = warp; tile < tiles; tile += kWarps) {
-    ok = wait_bounded(&bars[warp][stage], parity) && ok;  // (the warp votes: it stays converged)
+    ok = wait_bounded(&bars[warp][stage], parity);  // (the warp votes: it stays converged)
+    if (!ok) break;
     const uint32_t valid = valid_of[warp][stage];
     const uint32_t base = ring + stage * Sh::kTileBytes;
     const int pos0 = from + tile * kTile;
@@ -560,7 +561,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
   dependents_launch();
 
   // ---- join the warps
-  if (!ok && lane == 0) atomicExch(&gave_up, 1);
+  if (!ok) {
+    if (lane == 0) atomicExch(&gave_up, 1);
+    // the copies that are still on their way: the one that was waited for and those behind it, if they were asked for
+#pragma unroll 1
+    for (int s = 0; s < Sh::kStages; ++s) {
+      wait_bounded(&bars[warp][stage], parity);
+      if (++stage == Sh::kStages) {
+        stage = 0;
+        parity ^= 1u;
+      }
+    }
+  }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
