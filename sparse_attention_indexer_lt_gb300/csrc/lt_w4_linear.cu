@@ -240,8 +240,6 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
   int place = 0, turns = 0;
   uint32_t parity = 0;
   bool ok = true;
-  int lost_place = 0;  // of the wait that ran out, and its parity
-  uint32_t lost_parity = 0;
   for (int block = first; block < blocks; block += every, turns ^= 1) {
     acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
     for (int chunk = 0; chunk < chunks; ++chunk) {
@@ -252,16 +250,12 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
       if (chunks > 1 && p.bf16) powers(chunk > 0);
       int from, to;
       range(chunk, &from, &to);
+      if (!ok) to = from;
       const uint8_t* x = xa + (from - s_begin - chunk * p.chunk) * (kStep * 2);
 #pragma unroll 1
       for (int s = from; s < to; ++s, x += kStep * 2) {
-        if (ok && !wait_polls(&bars[warp][place], parity)) {
-          // nothing more is asked for, and nothing waited for before the end
-          ok = false;
-          next_row = end_row;
-          lost_place = place;
-          lost_parity = parity;
-        }
+        ok = wait_polls(&bars[warp][place], parity);
+        if (!ok) break;  // nothing more is asked for, and nothing waited for before the end
         const uint8_t* code = lower + place * kStageBytes;
         const uint8_t* scale = scale_at + place * kStageBytes;
         uint4 wa[2], wb[2];
@@ -351,10 +345,10 @@ few_kernel(LinearParams p, const __grid_constant__ CUtensorMap codes, const __gr
     // the copies that are still on their way: the one that was waited for and the next, if it was asked for
 #pragma unroll 1
     for (int s = 0; s < kStages; ++s) {
-      wait_polls(&bars[warp][lost_place], lost_parity);
-      if (++lost_place == kStages) {
-        lost_place = 0;
-        lost_parity ^= 1u;
+      wait_polls(&bars[warp][place], parity);
+      if (++place == kStages) {
+        place = 0;
+        parity ^= 1u;
       }
     }
   }
