@@ -557,9 +557,11 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
   look_up(0);
   int stage = 0;
   uint32_t parity = 1;  // (the first round's stages are free)
+  int n = 0;
 #pragma unroll 1
-  for (int n = 0; n < stages; ++n) {
-    wait_warp(&sh->packed_empty[stage], parity, sh);
+  for (; n < stages; ++n) {
+    // Where a wait has run out, here or with the unpackers, no place is written any more. (They wait for it in vain once.)
+    if (!wait_warp(&sh->packed_empty[stage], parity, sh) || __any_sync(~0u, *(volatile int*)&sh->gave_up)) break;
     uint32_t valid[kMost] = {};
     int count[kMost];
 #pragma unroll
@@ -598,6 +600,8 @@ __device__ __forceinline__ void copy_role(const AttentionParams& p, const Job& j
       parity ^= 1u;
     }
   }
+  // nothing is on its way any more when the CTA ends, also where somebody gave up
+  for (int i = max(n - kRaw, 0); i < n; ++i) wait_warp(&sh->packed_full[i % kRaw], i / kRaw & 1, sh);
 }
 
 // ---- unpacking: a packed stage's positions at a time, a thread the key or the value of a position (with
