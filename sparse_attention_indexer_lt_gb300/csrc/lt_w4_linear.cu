@@ -472,8 +472,11 @@ lt_status lt_w4_workspace(int64_t tokens, int64_t n, int64_t k, int64_t* bytes) 
   if (few(tokens, n, k) || n == 0) return LT_OK;
   int dev = 0, sms = 0;
   const lt_status found = device_of(&dev, &sms);
-  if (found == LT_OK) *bytes = many_plan(dev, tokens, n, k).bytes;
-  return found;
+  if (found != LT_OK) return found;
+  const ManyPlan plan = many_plan(dev, tokens, n, k);
+  if (plan.tile == 0) return LT_ERR_CUDA;  // (the device told nothing about itself)
+  *bytes = plan.bytes;
+  return LT_OK;
 }
 
 lt_status lt_w4_linear(const void* x, int32_t dtype, int64_t tokens, int64_t x_stride, const void* codes, const void* scales,
