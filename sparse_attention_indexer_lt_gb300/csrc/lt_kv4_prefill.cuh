@@ -277,9 +277,13 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
 #pragma unroll
   for (int i = 0; i < 7; ++i) term[i] = tanh_term(i) * shaped_factor;
   const float to_cap = shaped_factor * p.one_over_cap;
-  // Whether slopes go by each column's distance: where rows see what lies after them, too, and where a slope is so steep that
+  // Whether the row's slope goes by each column's distance: where rows see what lies after them, too, and where a slope is so steep that
   // the rounding of its part at a tile's first column (2^-24 of up to 64 slopes beside the row's own position) would show.
-  const bool by_distance = kShaped && (p.prefix != nullptr || __any_sync(~0u, fabsf(slope) > 4.0f));
+  // (then its start_slope is 0, which for a slope of 0 is all the same)
+  const bool steep = kShaped && (p.prefix != nullptr || fabsf(slope) > 4.0f);
+  const bool by_distance = __any_sync(~0u, steep);  // some row of the warp
+  const float start_slope = steep ? 0.0f : -slope;
+  slope = steep ? -slope : slope;
   const uint32_t lane_base = sh->tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t o_at = lane_base + kSumColumn + which * D;
 
@@ -317,7 +321,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
         float* s = reinterpret_cast<float*>(y);
         // A slope's term rises by the slope from column to column, up to the row's own position; its first column's
         // part comes with the last step before.
-        const float start = by_distance ? 0.0f : -slope * from;
+        const float start = start_slope * from;
         if (p.cap > 0.0f) {
 #pragma unroll
           for (int c0 = 0; c0 < 32; c0 += 16) {
@@ -358,8 +362,10 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
         }
         if (p.slopes != nullptr) {
           if (by_distance) {
+            // (rows that do not go by it take the same steps as below: their first column's distance is 0)
+            const float first = start_slope == 0.0f ? from : 0.0f;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) s[c] = fmaf(-slope, fabsf(from - (float)c), s[c]);
+            for (int c = 0; c < 32; ++c) s[c] = fmaf(slope, fabsf(first - (float)c), s[c]);
           } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) s[c] = fmaf(slope, (float)c, s[c]);
