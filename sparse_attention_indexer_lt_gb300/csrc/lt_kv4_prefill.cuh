@@ -268,7 +268,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   float slope = 0.0f, shaped_factor = 1.0f;
   if constexpr (kShaped) {
     if (p.prefix != nullptr) limit = max(limit, __ldg(p.prefix + job.request));
-    if (p.slopes != nullptr) slope = __ldg(p.slopes + job.head * p.group + row_c % p.group) * 1.4426950408889634f;
+    slope = slope_of(p, job.head * p.group + row_c % p.group);
     shaped_factor = factor;  // logits are shaped in units of log 2, and stay so
     factor = 1.0f;
   }
