@@ -270,11 +270,11 @@ __device__ __forceinline__ float bf16_row_to_half(uint32_t (&w)[N][4]) {
   return 1.0f / mul;
 }
 
-// A query head's slope in units of log 2, magnitudes above 2^95 as that: its product with a distance, which is below 2^31, stays
-// finite, and with a distance of 0 a zero.
-__device__ __forceinline__ float slope_of(const AttentionParams& p, int q_head) {
-  if (p.slopes == nullptr) return 0.0f;
-  return fminf(fmaxf(__ldg(p.slopes + q_head), -0x1p95f), 0x1p95f) * 1.4426950408889634f;
+// A slope in units of log 2, magnitudes above 2^95 (before the units) as that: its product with a distance, which is below 2^31,
+// stays finite, and with a distance of 0 a zero.
+__device__ __forceinline__ float bounded_slope(float x) {
+  constexpr float kMost = 0x1p95f * 1.4426950408889634f;
+  return fminf(fmaxf(x, -kMost), kMost);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

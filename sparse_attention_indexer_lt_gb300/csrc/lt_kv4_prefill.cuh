@@ -268,7 +268,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   float slope = 0.0f, shaped_factor = 1.0f;
   if constexpr (kShaped) {
     if (p.prefix != nullptr) limit = max(limit, __ldg(p.prefix + job.request));
-    slope = slope_of(p, job.head * p.group + row_c % p.group);
+    if (p.slopes != nullptr) slope = __ldg(p.slopes + job.head * p.group + row_c % p.group) * 1.4426950408889634f;
     shaped_factor = factor;  // logits are shaped in units of log 2, and stay so
     factor = 1.0f;
   }
@@ -283,7 +283,7 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
   const bool steep = kShaped && (p.prefix != nullptr || fabsf(slope) > 4.0f);
   const bool by_distance = __any_sync(~0u, steep);  // some row of the warp
   const float start_slope = steep ? 0.0f : -slope;
-  slope = steep ? -slope : slope;
+  slope = steep ? -bounded_slope(slope) : slope;
   const uint32_t lane_base = sh->tmem + ((uint32_t)(warp * 32) << 16);
   const uint32_t o_at = lane_base + kSumColumn + which * D;
 

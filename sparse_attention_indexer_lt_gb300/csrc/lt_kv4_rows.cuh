@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::kPerSm)) rows_kernel(
       if constexpr (kShaped) {
         const int row = min(row0 + nt * 8 + 2 * c + e, rows - 1);
         own[nt][e] = rq.length - rq.queries + (kList ? token0 - rq.first : token_of);
-        slope[nt][e] = slope_of(p, head * p.group + row % p.group);
+        slope[nt][e] = p.slopes != nullptr ? bounded_slope(__ldg(p.slopes + head * p.group + row % p.group) * 1.4426950408889634f) : 0.0f;
         if (!kList) limit[nt][e] = max(limit[nt][e], prefix);
       }
     }
