@@ -221,8 +221,8 @@ lt_status lt_kv4_attention(const void* q, int32_t dtype, int64_t tokens, int32_t
  * and visible are the positions up to the query's own, and those below prefix[r], whichever query of
  * request r looks (a query that lies before the first position sees the prefix alone).
  *
- *   softcap   0 (none), or LT_KV4_MIN_CAP to LT_KV4_MAX_CAP. A capped logit is off by at most
- *             2^-22 of caps to 64, 2^-20 of itself with larger ones
+ *   softcap   0 (none), or LT_KV4_MIN_CAP to LT_KV4_MAX_CAP. Beside what the logit before it is off
+ *             by, a capped logit is off by at most 2^-21 of caps to 64, 2^-20 of itself with larger ones
  *   slopes    float [q_heads], finite, or NULL; magnitudes above 2^95 count as that (a logit then is finite
  *             whatever the distance); listed positions have distances, too
  *   prefix    int32 [requests] or NULL; below 0 counts as 0, past the request's length as

@@ -300,8 +300,10 @@ __device__ __forceinline__ float tanh_over_x(float u) {
   for (int i = 5; i >= 0; --i) t = fmaf(t, u, tanh_term(i));
   return t;
 }
-// cap tanh(s / cap) in units of log 2. tanh(x) = 1 - 2 / (1 + e^2x) is off by 2^-22, absolute, so the capped logit
-// by 2^-22 of the cap: for caps to 64 less than what 32-bit sums of the products are off by. With larger caps,
+// cap tanh(s / cap) in units of log 2, as cap - 2 cap r with r = 1 / (1 + e^2x). In units of 2^-24, absolute: the
+// reciprocal is off by 2 of itself and so counts for 4 r, the sum before it for 2 r, the exponential (4 of itself) for 8 r (1 - r),
+// its argument's two roundings for 2 x / cosh(x)^2, the last step for |1 - 2 r|: less than 8 together, the most near
+// r = 7 / 8. So the capped logit is off by 2^-21 of the cap: for caps to 64 about what 32-bit sums of the products are off by. With larger caps,
 // logits up to the cap go by the polynomial. An infinity gives the cap, NaN stays NaN.
 __device__ __forceinline__ float capped_by_exp(const AttentionParams& p, float s) {
   float r;

@@ -1,4 +1,11 @@
-"""Single shaped logits: slopes of any finite size, and rows that do not go by their neighbours."""
+"""Single shaped logits: how far off a cap is, slopes of any finite size, and rows that do not go by their neighbours.
+
+A query that sees one position has that position's logit as its lse, so that caps are seen through nothing else. In units of
+eps = 2^-24: the claim, 8 of caps to 64 and 16 of the capped logit above, is what the steps of the hyperbolic tangent
+may add. Besides, a logit s in units of log 2 carries 3 roundings (the scale's factor 2, their product), of which a cap
+lets |s| / cosh(s / cap)^2 through, at most 0.45 caps; the cap in units of log 2 carries 2, the way back from them 2
+and the sum's logarithm, 6 after and before the shift by it, some 4 of (|lse| + 12).
+"""
 import numpy as np
 import pytest
 import torch
@@ -13,6 +20,28 @@ def _built():
     from sparse_attention_indexer_lt_gb300 import build
     build.build()
     assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dim,group,listed", [(64, 8, False), (128, 32, False), (64, 80, False), (128, 80, False), (256, 80, False), (128, 16, True)])
+@pytest.mark.parametrize("cap", [2.0 ** -10, 1.0, 30.0, 64.0, 65.0, 1000.0, 2.0 ** 20])
+def test_capped_logits(cap, dim, group, listed, dtype):
+    requests = 24
+    p = Problem([1] * requests, [1] * requests, 1, group, dim, 16, dtype, seed=dim + group, positions=np.zeros((requests, 1)) if listed else None)
+    p.cache[..., 0] = p.cache[..., 0] & 0xF0 | 2  # the first channel's code is 1
+    p.q[:] = 0
+    p.q[:, :, 0] = torch.linspace(-1.0, 1.0, requests * group).view(requests, group).to(p.q.dtype)
+    k = np.array([p.rows_at(r, 0, 0)[0][0] for r in range(requests)])
+    for reach in (0.6, 4.0, 40.0):  # caps: below them, around them, far past them
+        scale = float(np.float32(reach * cap / k.max()))
+        _, lse = p.run(scale=scale, softcap=cap)
+        s = scale * num(p.q)[:, :, 0] * k[:, None]
+        want = cap * np.tanh(s / cap)
+        through = np.abs(s) / np.cosh(np.minimum(np.abs(s) / cap, 300.0)) ** 2
+        claim = 8 * cap if cap <= 64 else 16 * np.abs(want)
+        tol = EPS * (claim + 3 * through + 4 * (np.abs(want) + 12.0))
+        err = np.abs(num(lse) - want)
+        assert (err <= tol).all(), f"reach {reach}: worst {float((err / tol).max()):.3g} of its bound"
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
