@@ -10,9 +10,10 @@
  *
  * k is a multiple of 32, n and k are below 2^30, both start on 16 bytes. lt_w4_quantise makes them; codes and
  * scales from elsewhere serve as well, the scales finite, at least 0 and at most 10912 (then
- * code * scale does not overflow; lt_w4_quantise's have 9 significant bits, which makes
- * code * scale an exact fp16 number. Products of longer scales are rounded to fp16,
- * 2^-11 relative). What other scales give is not specified, for their own outputs alone.
+ * code * scale does not overflow). lt_w4_quantise's have 9 significant bits and are multiples of 2^-23, which makes
+ * code * scale an exact fp16 number. Products of other scales are rounded to fp16, to the nearest, ties to even: 2^-11
+ * of a weight of 2^-14 or more, 2^-25 of smaller ones (half of the scale 2^-24 is 0).
+ * What scales outside that range give is not specified, for their own outputs alone.
  *
  * Memory, streams and errors are as in lt_topk.h: DEVICE memory owned by the
  * caller, nothing allocated, nothing kept, the stream never synchronised,
