@@ -326,7 +326,7 @@ extern "C" lt_status lt_kv4_append(const void* q, const void* k, const void* v, 
   const int per_cta = kThreads / (head_dim / 8);
   const int64_t blocks = (tokens + per_cta - 1) / per_cta;
   if (blocks > INT32_MAX) return LT_ERR_UNSUPPORTED;
-  // a head a thread while the CTAs are few, two rounds of kAheadMost from where they fill the SMs
+  // a head a thread while the CTAs are few, two rounds of kAheadMost from where they fill the GPU's 152 SMs, eight each
   p.per = blocks * (q_heads + 2 * kv_heads) <= 152 * 8 && q_heads + 2 * kv_heads <= 65535 ? 1 : 2 * kAheadMost;
   p.q_parts = (q_heads + p.per - 1) / p.per;
   p.kv_parts = (kv_heads + p.per - 1) / p.per;

@@ -34,8 +34,8 @@
 // behind 14336 positions (32 query heads on 8 kv heads): 941 us with one lane issuing, 716
 // with the warp issuing and copies in a warp of their own, 650 with short loops and whole-line
 // queries and outputs, 511 without cutting requests that fill the SMs, 494 with four
-// products a statement, 424 with named barriers, 410 with the longest row tiles first: 1.26
-// PFLOP/s, 65% of cuBLAS's burst; 84% is the most that two waves of 256 CTAs on 152 SMs
+// products a statement, 424 with named barriers, 410 with the longest row tiles first, 411 since packed stages are handed back by
+// what was loaded from them: 1.25 PFLOP/s, 65% of cuBLAS's burst; 84% is the most that two waves of 256 CTAs on 152 SMs
 // allow. Measured and dropped: a quarter, a third or half of the exponentials on the FMA
 // pipes (541, 557, 621 us against 511), two threads a row (541), the first half's weights taken
 // before the tile's maximum is known (804 against 716).
@@ -50,7 +50,8 @@
 // 32 columns at a time. A cap is a polynomial while the logits are below it (12 instructions a logit in all; by
 // exponential and reciprocal, which the special function unit has to do for the softmax already, 1066 us against 1031 on the
 // chunk below); the chain from a tile's logits to its weights is what bounds it, twice the plain one's: 2048
-// tokens behind 14336, 32 query heads on 8 kv heads of 128, cap and slopes, 975 us (410 plain). Dropped: no shaping before the
+// tokens behind 14336, 32 query heads on 8 kv heads of 128, cap and slopes, 985 us (411 plain; 975 before stages were handed
+// back so, and slopes of each row's own kind). Dropped: no shaping before the
 // weights where a bound shows that the maximum stays (1148: with slopes it moves, with a cap alone the two readings cost as
 // much), 16 columns at a time (1135).
 //

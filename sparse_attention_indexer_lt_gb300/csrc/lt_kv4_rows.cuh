@@ -31,12 +31,15 @@
 // could (2.17, 54%, with heads of 256, whose 168 registers leave 12 warps). More resident warps or deeper rings change
 // nothing (5 CTAs an SM with 2 stages 272 us, 4 with 2 or 3 267 to 269, 3 with 4 281, on the 64 ragged
 // requests). Measured (4.5-bit rows read once): 64 requests of 2048 to 65536 positions,
-// 4 kv heads of 128, 253 us, 4.9 TB/s; one request of 262144 positions, 4 heads of 256,
+// 4 kv heads of 128, 252 us, 4.9 TB/s; one request of 262144 positions, 4 heads of 256,
 // 65 us, 4.7 TB/s; the copy rate is 6.8. The widest instances (32 rows; 16 with heads of 256), which serve 17 to
 // 64 rows, do not fit the registers: they spill 404 bytes a thread with heads of 128, 308 with 64, 224 with 256.
 //
 // Shaped logits cost a lane some 5 instructions a logit with a cap and 2 with a slope, of 8 a tile and row tile: 64 ragged requests
-// with slopes take 280 us (253 plain), with 127 registers a thread as without.
+// with slopes take 281 us (252 plain), with 128 registers a thread (124 without). A stage is handed back by the second product's sums: a word of
+// each load of values takes 12 instructions more (288 and 254).
+//
+// The running maximum moves for all rows of a tile at once, so a row's roundings go by when its neighbours' logits rise.
 
 #pragma once
 
