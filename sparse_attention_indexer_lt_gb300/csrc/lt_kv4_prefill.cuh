@@ -34,8 +34,8 @@
 // behind 14336 positions (32 query heads on 8 kv heads): 941 us with one lane issuing, 716
 // with the warp issuing and copies in a warp of their own, 650 with short loops and whole-line
 // queries and outputs, 511 without cutting requests that fill the SMs, 494 with four
-// products a statement, 424 with named barriers, 410 with the longest row tiles first, 411 since packed stages are handed back by
-// what was loaded from them: 1.25 PFLOP/s, 65% of cuBLAS's burst; 84% is the most that two waves of 256 CTAs on 152 SMs
+// products a statement, 424 with named barriers, 410 with the longest row tiles first (405 to 416 since packed stages are handed back by
+// what was loaded from them): 1.25 PFLOP/s, 65% of cuBLAS's burst; 84% is the most that two waves of 256 CTAs on 152 SMs
 // allow. Measured and dropped: a quarter, a third or half of the exponentials on the FMA
 // pipes (541, 557, 621 us against 511), two threads a row (541), the first half's weights taken
 // before the tile's maximum is known (804 against 716).
@@ -43,14 +43,14 @@
 // Heads of 256, the same chunk: 5063 us with the kernel for few rows; here 1586 with queries
 // in shared memory and a key and a value tile, 1238 with the queries in tensor memory and three tiles, 1100 with
 // eight warps unpacking, 854 with tiles of 64, logits a tile ahead and five packed stages in place of three
-// of 32 positions (1160 with those): 1.21 PFLOP/s, 63% of cuBLAS's burst, where four waves of 512 CTAs on 152
-// SMs allow 84%. The unpacked tile's way, read, write and fence, is what is left: 748 us without its writes.
+// of 32 positions (1160 with those), 877 since packed stages are handed back by what was loaded from them: 1.18 PFLOP/s, 61% of
+// cuBLAS's burst, where four waves of 512 CTAs on 152 SMs allow 84%. The unpacked tile's way, read, write and fence, is what is left: 748 us without its writes.
 //
 // Shaped logits (caps, slopes, prefixes) pass once more through tensor memory: shaped, hidden and their maximum taken
 // 32 columns at a time. A cap is a polynomial while the logits are below it (12 instructions a logit in all; by
 // exponential and reciprocal, which the special function unit has to do for the softmax already, 1066 us against 1031 on the
 // chunk below); the chain from a tile's logits to its weights is what bounds it, twice the plain one's: 2048
-// tokens behind 14336, 32 query heads on 8 kv heads of 128, cap and slopes, 985 us (411 plain; 975 before stages were handed
+// tokens behind 14336, 32 query heads on 8 kv heads of 128, cap and slopes, 987 us (411 plain; 975 before stages were handed
 // back so, and slopes of each row's own kind). Dropped: no shaping before the
 // weights where a bound shows that the maximum stays (1148: with slopes it moves, with a cap alone the two readings cost as
 // much), 16 columns at a time (1135).
@@ -621,6 +621,10 @@ __device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job&
   constexpr int kBlocks = D / 64 * 2 * kPart / Smem<D>::kUnpackers;  // 64-channel blocks of a thread
   const int t = threadIdx.x - (384 - Smem<D>::kUnpackers), lane = t & 31, row = t % kPart, part = t / kPart & 1;
   const int block0 = t / (2 * kPart) * kBlocks;
+  // The stage is handed back before this one of the thread's 16-byte chunks is unpacked: early, and what was loaded last has
+  // arrived. us for 2048 tokens behind 14336 with heads of 128, and of 256, before the first 405, 972; the second 410, 906; the last but
+  // one 414, 874; the last 411, 887; after all of them 408, 930; with all loaded before the slot is waited for 410, 978.
+  constexpr int kHandBack = Smem<D>::kOne ? 2 * kBlocks - 2 : 0;
   uint32_t chunk_at[8];  // where the row's eight 16-byte chunks lie in a swizzled 128-byte row
 #pragma unroll
   for (int c = 0; c < 8; ++c) chunk_at[c] = lt::smem_u32(smem + Smem<D>::kKv) + row * 128 + ((c ^ (row & 7)) << 4);
@@ -638,7 +642,7 @@ __device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job&
       const bool there = (valid >> lane) & 1u;
       const uint8_t* from = smem + Smem<D>::kPacked + (stage * kPart + row) * kRow;
       // scales, fp16 pairs; a position that is not there counts as zeros, and so does a NaN value
-      uint32_t sc[kBlocks], seen = 0;  // seen: a word of every load
+      uint32_t sc[kBlocks], seen = 0;  // seen: made of every word
 #pragma unroll
       for (int g = 0; g < kBlocks; ++g) {
         sc[g] = there ? reinterpret_cast<const uint32_t*>(from + D + part * (D / 16))[block0 + g] : 0u;
@@ -661,13 +665,8 @@ __device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job&
       uint4 codes[2 * kBlocks];
 #pragma unroll
       for (int c = 0; c < 2 * kBlocks; ++c) {
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(codes[c].x), "=r"(codes[c].y), "=r"(codes[c].z), "=r"(codes[c].w)
-                     : "r"(lt::smem_u32(from + part * (D / 2) + (2 * block0 + c) * 16)) : "memory");
-        seen ^= codes[c].x;
+        codes[c] = reinterpret_cast<const uint4*>(from + part * (D / 2))[2 * block0 + c];
       }
-      const uint32_t here = zero_of(seen, p.zero);  // every lane has read the stage
-      if (lane == 0) arrive(&sh->packed_empty[stage] + here);
       if (half == 0) {
         wait_warp(&sh->kv_empty[slot], slot_parity, sh);
         // (until then the queries are in the last slots)
@@ -679,6 +678,13 @@ __device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job&
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const uint32_t w[4] = {codes[2 * c + g].x, codes[2 * c + g].y, codes[2 * c + g].z, codes[2 * c + g].w};
+          if (2 * c + g < kHandBack) seen ^= w[0] ^ w[1] ^ w[2] ^ w[3];
+          if (2 * c + g == kHandBack) {
+#pragma unroll
+            for (int u = kHandBack; u < 2 * kBlocks; ++u) seen ^= codes[u].x ^ codes[u].y ^ codes[u].z ^ codes[u].w;
+            const uint32_t here = zero_of(seen, p.zero);  // every lane has read the stage
+            if (lane == 0) arrive(&sh->packed_empty[stage] + here);
+          }
           const uint32_t scale = __byte_perm(sc[c], 0, g ? 0x3232 : 0x1010);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
