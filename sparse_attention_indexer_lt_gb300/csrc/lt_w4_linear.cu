@@ -14,7 +14,7 @@
 // further where there are few rows. The parts join in shared memory and over distributed shared memory, in one order
 // whatever the timing.
 //
-// What bounds it: issue and the ALU pipe (66% and 52% of their rates): 16 rows by 128 inputs take some 180 warp
+// What bounds it: issue and the ALU pipe (67% and 53% of their rates): 16 rows by 128 inputs take some 195 warp
 // instructions, 64 of them conversions and scalings. One token through 8192 x 28672 (132 MB): 29 us, 4.5 TB/s, where
 // the copy rate allows 19.5. On the way: a CTA for each row block 40 us; CTAs that stay 34; scales of two groups a load
 // 33; tensor maps and rings of two stages 30 (with three stages, and a CTA less an SM, 33); fewer steps a join 28 to
