@@ -52,13 +52,15 @@ struct Shared {
 };
 
 // A warp waits for a phase, kWaitPolls polls at most; a wait that gives up marks the CTA, whose outputs are NaN
-// then, and the warp goes on: the roles keep their steps, so nobody waits for one that has left.
+// then, and the warp goes on: the roles keep their steps, so nobody waits for one that has left. In a marked CTA nothing more
+// is brought, and nobody waits any more (beyond some 64 polls) but for what has to be over before it ends (kOver).
 __device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
                : "=r"(ok) : "r"(lt::smem_u32(bar)), "r"(parity) : "memory");
   return ok != 0;
 }
+template <bool kOver = false>
 __device__ __forceinline__ void wait_warp(uint64_t* bar, uint32_t parity, Shared* sh) {
   bool done = ready(bar, parity);
   if (__all_sync(~0u, done)) return;
@@ -66,6 +68,7 @@ __device__ __forceinline__ void wait_warp(uint64_t* bar, uint32_t parity, Shared
   for (uint32_t i = 0; i < lt::kWaitPolls; ++i) {
     done = done | lt::mbar_try_wait(bar, parity);
     if (__all_sync(~0u, done)) return;
+    if (!kOver && i % 64 == 63 && __any_sync(~0u, *(volatile int*)&sh->gave_up != 0)) return;
   }
   *(volatile int*)&sh->gave_up = 1;
 }
@@ -112,6 +115,12 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_kernel(ManyParams p) {
     if (tid + i * kLayoutThreads < pieces) write(tid + i * kLayoutThreads, held[i]);
   for (int q = tid + kHeld * kLayoutThreads; q < pieces; q += kLayoutThreads)
     write(q, q < there ? __ldg(x + q) : make_uint4(0u, 0u, 0u, 0u));
+}
+
+// What lane 0 has asked for into a ring is on its way no more, also where somebody gave up.
+__device__ __forceinline__ void wait_for_asked(uint64_t* full, int asked, int ring, Shared* sh) {
+  asked = __shfl_sync(~0u, asked, 0);
+  for (int i = max(asked - ring, 0); i < asked; ++i) wait_warp<true>(&full[i % ring], i / ring & 1, sh);
 }
 
 // A place in a ring: its index and the parity of its round.
@@ -274,42 +283,43 @@ __global__ void __launch_bounds__(Many<kTiles>::kCta, 3 - kTiles) many_kernel(Ma
     mma_commit(&sh->done, lead);
   } else if (warp == kUnpackWarps + 1) {
     Turn code(1);
+    int asked = 0;
 #pragma unroll 1
     for (int u = from; u < to; ++u) {
       wait_warp(&sh->codes_empty[code.at], code.parity, sh);
-      if (lane == 0) {
+      if (lane == 0 && *(volatile int*)&sh->gave_up == 0) {
         uint64_t* bar = &sh->codes_full[code.at];
         const uint32_t at = packed + code.at * Many<kTiles>::kPacked;
         lt::mbar_arrive_tx(bar, Many<kTiles>::kPacked);
         tensor_in(at, &codes, u * 128, row0, bar);
         tensor_in(at + kRows * 64, &codes, u * 128 + 64, row0, bar);
+        ++asked;
       }
       __syncwarp();
       code.next(p.code_ring);
     }
-    // nothing is on its way any more, also where somebody gave up
-    const int left = min(to - from, p.code_ring);
-    for (int i = to - from - left; i < to - from; ++i) wait_warp(&sh->codes_full[i % p.code_ring], i / p.code_ring & 1, sh);
+    wait_for_asked(sh->codes_full, asked, p.code_ring, sh);
   } else {
     dependency_wait();  // the launch that lays the tokens out
     for (int t = lane; t < tokens; t += 32) sh->inverse[t] = p.inverse[token0 + t];
     const uint8_t* src = p.tiles_at + (int64_t)blockIdx.y * p.steps * token_bytes;
     Turn token(1);
+    int asked = 0;
 #pragma unroll 1
     for (int b = first; b < last; ++b) {
       wait_warp(&sh->tokens_empty[token.at], token.parity, sh);
-      if (lane == 0) {
+      if (lane == 0 && *(volatile int*)&sh->gave_up == 0) {
         lt::mbar_arrive_tx(&sh->tokens_full[token.at], token_bytes);
         lt::bulk_g2s(smem + (tokens_at - packed) + token.at * token_bytes, src + (int64_t)b * token_bytes, token_bytes, &sh->tokens_full[token.at]);
+        ++asked;
       }
       __syncwarp();
       token.next(p.token_ring);
     }
-    const int left = min(last - first, p.token_ring);
-    for (int i = last - first - left; i < last - first; ++i) wait_warp(&sh->tokens_full[i % p.token_ring], i / p.token_ring & 1, sh);
+    wait_for_asked(sh->tokens_full, asked, p.token_ring, sh);
   }
   __syncwarp();
-  wait_warp(&sh->done, 0, sh);  // every product is done: the sums are there, and the rings are free
+  wait_warp<true>(&sh->done, 0, sh);  // every product is done: the sums are there, and the rings are free
   fence_after();
   __syncthreads();
   const bool bad = *(volatile int*)&sh->gave_up != 0;
