@@ -303,8 +303,8 @@ __device__ __forceinline__ float tanh_over_x(float u) {
 // cap tanh(s / cap) in units of log 2, as cap - 2 cap r with r = 1 / (1 + e^2x). In units of 2^-24, absolute: the
 // reciprocal is off by 2 of itself and so counts for 4 r, the sum before it for 2 r, the exponential (4 of itself) for 8 r (1 - r),
 // its argument's two roundings for 2 x / cosh(x)^2, the last step for |1 - 2 r|: less than 8 together, the most near
-// r = 7 / 8. So the capped logit is off by 2^-21 of the cap: for caps to 64 about what 32-bit sums of the products are off by. With larger caps,
-// logits up to the cap go by the polynomial. An infinity gives the cap, NaN stays NaN.
+// r = 7 / 8. So the capped logit is off by 2^-21 of the cap: for caps to 64 about what 32-bit sums of the products are off
+// by. With larger caps, logits up to the cap go by the polynomial. An infinity gives the cap, NaN stays NaN.
 __device__ __forceinline__ float capped_by_exp(const AttentionParams& p, float s) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_fast(s * p.two_over_cap)));

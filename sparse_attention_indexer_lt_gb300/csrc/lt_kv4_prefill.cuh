@@ -34,17 +34,18 @@
 // behind 14336 positions (32 query heads on 8 kv heads): 941 us with one lane issuing, 716
 // with the warp issuing and copies in a warp of their own, 650 with short loops and whole-line
 // queries and outputs, 511 without cutting requests that fill the SMs, 494 with four
-// products a statement, 424 with named barriers, 410 with the longest row tiles first (405 to 416 since packed stages are handed back by
-// what was loaded from them): 1.25 PFLOP/s, 65% of cuBLAS's burst; 84% is the most that two waves of 256 CTAs on 152 SMs
-// allow. Measured and dropped: a quarter, a third or half of the exponentials on the FMA
+// products a statement, 424 with named barriers, 410 with the longest row tiles first (405 to 416 since
+// packed stages are handed back by what was loaded from them): 1.25 PFLOP/s, 65% of cuBLAS's burst; 84% is the most
+// that two waves of 256 CTAs on 152 SMs allow. Measured and dropped: a quarter, a third or half of the exponentials on the FMA
 // pipes (541, 557, 621 us against 511), two threads a row (541), the first half's weights taken
 // before the tile's maximum is known (804 against 716).
 //
 // Heads of 256, the same chunk: 5063 us with the kernel for few rows; here 1586 with queries
 // in shared memory and a key and a value tile, 1238 with the queries in tensor memory and three tiles, 1100 with
 // eight warps unpacking, 854 with tiles of 64, logits a tile ahead and five packed stages in place of three
-// of 32 positions (1160 with those), 877 since packed stages are handed back by what was loaded from them: 1.18 PFLOP/s, 61% of
-// cuBLAS's burst, where four waves of 512 CTAs on 152 SMs allow 84%. The unpacked tile's way, read, write and fence, is what is left: 748 us without its writes.
+// of 32 positions (1160 with those), 877 since packed stages are handed back by what was loaded from them: 1.18
+// PFLOP/s, 61% of cuBLAS's burst, where four waves of 512 CTAs on 152 SMs allow 84%. The unpacked tile's way, read,
+// write and fence, is what is left: 748 us without its writes.
 //
 // Shaped logits (caps, slopes, prefixes) pass once more through tensor memory: shaped, hidden and their maximum taken
 // 32 columns at a time. A cap is a polynomial while the logits are below it (12 instructions a logit in all; by
@@ -278,8 +279,8 @@ __device__ __forceinline__ void softmax_role(const AttentionParams& p, const Job
 #pragma unroll
   for (int i = 0; i < 7; ++i) term[i] = tanh_term(i) * shaped_factor;
   const float to_cap = shaped_factor * p.one_over_cap;
-  // Whether the row's slope goes by each column's distance: where rows see what lies after them, too, and where a slope is so steep that
-  // the rounding of its part at a tile's first column (2^-24 of up to 64 slopes beside the row's own position) would show.
+  // Whether the row's slope goes by each column's distance: where rows see what lies after them, too, and where a slope is
+  // so steep that the rounding of its part at a tile's first column (2^-24 of up to 64 slopes beside the row's own position) would show.
   // (then its start_slope is 0, which for a slope of 0 is all the same)
   const bool steep = kShaped && (p.prefix != nullptr || fabsf(slope) > 4.0f);
   const bool by_distance = __any_sync(~0u, steep);  // some row of the warp
@@ -621,9 +622,9 @@ __device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job&
   constexpr int kBlocks = D / 64 * 2 * kPart / Smem<D>::kUnpackers;  // 64-channel blocks of a thread
   const int t = threadIdx.x - (384 - Smem<D>::kUnpackers), lane = t & 31, row = t % kPart, part = t / kPart & 1;
   const int block0 = t / (2 * kPart) * kBlocks;
-  // The stage is handed back before this one of the thread's 16-byte chunks is unpacked: early, and what was loaded last has
-  // arrived. us for 2048 tokens behind 14336 with heads of 128, and of 256, before the first 405, 972; the second 410, 906; the last but
-  // one 414, 874; the last 411, 887; after all of them 408, 930; with all loaded before the slot is waited for 410, 978.
+  // The stage is handed back before this one of the thread's 16-byte chunks is unpacked: early, but when what was loaded
+  // last has arrived. us for 2048 tokens behind 14336 with heads of 128, and of 256: before the first chunk 405, 972; the
+  // second 410, 906; the last but one 414, 874; the last 411, 887; after all of them 408, 930; before the wait for the slot 410, 978.
   constexpr int kHandBack = Smem<D>::kOne ? 2 * kBlocks - 2 : 0;
   uint32_t chunk_at[8];  // where the row's eight 16-byte chunks lie in a swizzled 128-byte row
 #pragma unroll
@@ -664,9 +665,7 @@ __device__ __forceinline__ void unpack_role(const AttentionParams& p, const Job&
       }
       uint4 codes[2 * kBlocks];
 #pragma unroll
-      for (int c = 0; c < 2 * kBlocks; ++c) {
-        codes[c] = reinterpret_cast<const uint4*>(from + part * (D / 2))[2 * block0 + c];
-      }
+      for (int c = 0; c < 2 * kBlocks; ++c) codes[c] = reinterpret_cast<const uint4*>(from + part * (D / 2))[2 * block0 + c];
       if (half == 0) {
         wait_warp(&sh->kv_empty[slot], slot_parity, sh);
         // (until then the queries are in the last slots)

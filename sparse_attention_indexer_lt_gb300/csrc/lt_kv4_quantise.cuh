@@ -133,7 +133,7 @@ struct Eight<float> {
   __device__ __forceinline__ uint32_t codes_by_borders(float s) const {
     uint32_t w = 0;
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {  // (seldom, but for inputs of zero, which take it too: a short loop, its input picked out of the registers)
+    for (int i = 0; i < 8; ++i) {  // (seldom, but for zeros: a short loop, its input picked out of the registers)
       float v = x[0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) v = i == j ? x[j] : v;

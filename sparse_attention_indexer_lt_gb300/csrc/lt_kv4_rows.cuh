@@ -36,8 +36,9 @@
 // 64 rows, do not fit the registers: they spill 404 bytes a thread with heads of 128, 308 with 64, 224 with 256.
 //
 // Shaped logits cost a lane some 5 instructions a logit with a cap and 2 with a slope, of 8 a tile and row tile: 64 ragged requests
-// with slopes take 281 us (252 plain), with 128 registers a thread (124 without). A stage is handed back by the second product's sums: a word of
-// each load of values takes 12 instructions more (288 and 254).
+// with slopes take 281 us (252 plain), with 128 registers a thread (124 without).
+//
+// A stage is handed back by the second product's sums; by a word of each load of values it takes 288 and 254.
 //
 // The running maximum moves for all rows of a tile at once, so a row's roundings go by when its neighbours' logits rise.
 

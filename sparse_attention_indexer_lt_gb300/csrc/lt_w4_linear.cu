@@ -411,18 +411,23 @@ constexpr int kFewInputs = 96 * 1024;  // bytes of inputs in shared memory at mo
 constexpr int kFewJoin = 2 * kWarps * 16 * kTokens * 4;  // at most
 constexpr int kFewSmem = 1024 + kRing + kFewInputs + kFewJoin;
 
-// Whether a call takes the kernel for few tokens. us there and in the one for many, in a graph, with bf16 tokens and (after the
-// bar) fp16 ones, which the former need not scale:
-//   n x k          1 token                   2                         4                         6                         8
-//   64 x 512       3.2, 4.7  | 2.7, 4.6      3.4, 4.5  | 2.8, 4.5      3.8, 4.6  | 2.8, 4.6      4.9, 4.6  | 3.5, 4.6      5.4, 4.6  | 3.6, 4.6
-//   4096 x 4096    6.7, 8.4  | 6.0, 8.4      7.3, 8.5  | 6.3, 8.4      8.5, 8.5  | 7.3, 8.5      9.5, 8.5  | 8.1, 8.5      10.0, 8.6 | 8.3, 8.5
-//   4099 x 5152    8.1, 10.1 | 7.3, 10.1     9.0, 10.3 | 8.0, 10.2     10.4, 10.3 | 9.2, 10.3    11.0, 10.4 | 9.5, 10.4    11.5, 10.4 | 9.6, 10.4
-//   14336 x 4096   11.9, 14.2 | 10.9, 14.3   12.7, 14.6 | 11.4, 14.4   15.1, 14.6 | 13.7, 14.6   16.6, 14.8 | 14.6, 14.6   20.1, 14.7 | 17.9, 14.7
-//   10240 x 8192   15.8, 17.3 | 14.7, 17.4   17.7, 17.6 | 16.7, 17.6   24.9, 17.7 | 23.3, 17.4   25.2, 17.8 | 23.3, 17.7   30.2, 17.7 | 28.0, 17.7
-//   28672 x 8192   30.8, 36.4 | 29.7, 36.2   33.6, 36.5 | 32.4, 36.4   43.1, 36.5 | 41.6, 36.2   39.8, 36.6 | 37.1, 36.4   53.5, 36.5 | 51.3, 36.2
-// Eagerly the second launch of the latter costs the host 6 more, so that up to some 12 us this one is the faster there even where it is the
-// slower in a graph: bf16 tokens from 5 on (4096 x 4096 with 8: 10.0 against 8.6). Past that the rule is coarse: it takes the slower
-// side by 3% at 14336 x 4096 with 4 bf16 tokens and, the other way, by 7 to 12% at 28672 x 8192 with 3 (33.8 and 32.3 here).
+// Whether a call takes the kernel for few tokens. us there and in the one for many, in a graph:
+//   n x k                1 token     2           3           4           6           8
+//   64 x 512      bf16   3.2, 4.7    3.4, 4.5    3.6, 4.6    3.8, 4.6    4.9, 4.6    5.4, 4.6
+//                 fp16   2.7, 4.6    2.8, 4.5    2.8, 4.6    2.8, 4.6    3.5, 4.6    3.6, 4.6
+//   4096 x 4096   bf16   6.7, 8.4    7.3, 8.5    8.1, 8.5    8.5, 8.5    9.5, 8.5    10.0, 8.6
+//                 fp16   6.0, 8.4    6.3, 8.4    7.1, 8.4    7.3, 8.5    8.1, 8.5    8.3, 8.5
+//   4099 x 5152   bf16   8.1, 10.1   9.0, 10.3   10.1, 10.3  10.4, 10.3  11.0, 10.4  11.5, 10.4
+//                 fp16   7.3, 10.1   8.0, 10.2   9.1, 10.2   9.2, 10.3   9.5, 10.4   9.6, 10.4
+//   14336 x 4096  bf16   11.9, 14.2  12.7, 14.6  14.6, 14.6  15.1, 14.6  16.6, 14.8  20.1, 14.7
+//                 fp16   10.9, 14.3  11.4, 14.4  13.6, 14.6  13.7, 14.6  14.6, 14.6  17.9, 14.7
+//   10240 x 8192  bf16   15.8, 17.3  17.7, 17.6  21.6, 17.7  24.9, 17.7  25.2, 17.8  30.2, 17.7
+//                 fp16   14.7, 17.4  16.7, 17.6  20.3, 17.5  23.3, 17.4  23.3, 17.7  28.0, 17.7
+//   28672 x 8192  bf16   30.8, 36.4  33.6, 36.5  33.8, 36.3  43.1, 36.5  39.8, 36.6  53.5, 36.5
+//                 fp16   29.7, 36.2  32.4, 36.4  32.3, 36.4  41.6, 36.2  37.1, 36.4  51.3, 36.2
+// Eagerly the second launch of the latter costs the host 6 more, so that this one is taken up to some 12 us, also where it is
+// the slower in a graph: bf16 tokens from 5 on (4096 x 4096 with 8: 10.0 against 8.6). Past that the rule is coarse: it takes the
+// slower side by 3% at 14336 x 4096 with 4 bf16 tokens and, the other way, by 7 and 12% at 28672 x 8192 with 3.
 bool few(int64_t tokens, int64_t n, int64_t k) { return tokens <= 2 || (tokens <= 4 && n * k <= (int64_t)1 << 26) || (tokens <= 8 && n * k <= (int64_t)1 << 25); }
 
 constexpr int64_t kMostSize = (int64_t)1 << 30;
